@@ -8,6 +8,9 @@ fails to load, every call raises.
     o, hT = chunk_fwd(q, k, v, alpha, beta, h0=None, chunk=64)
     o = decode_step(q, k, v, alpha, beta, H)          # H updated in place
 
+    o, hT = linattn_fwd(q, k, v, g, h0=None)          # linear attention, a decay for each head
+    y = head_norm_fwd(o, w, b, gate=z)                # norm and output gate, token-major
+
 With fuse=FUSE_GATES | FUSE_NORM_K (| FUSE_NORM_Q) the kernels first apply the
 per-token prologue: alpha and beta are logits, keys (queries) are normalised.
 """
@@ -27,12 +30,16 @@ STATUS = {0: "CKDA_OK", 1: "CKDA_ERR_NULL", 2: "CKDA_ERR_DIM", 3: "CKDA_ERR_UNSU
 (ERR_NULL, ERR_DIM, ERR_UNSUPPORTED, ERR_ALIAS, ERR_HIP, ERR_WORKSPACE, ERR_FLAGS) = range(1, 8)
 FUSE_GATES, FUSE_NORM_K, FUSE_NORM_Q = 1, 2, 4       # CKDA_FUSE_*
 GATE_SCALAR = 8                                      # CKDA_GATE_SCALAR
+DECAY_HEAD = 16                                      # CKDA_DECAY_HEAD
+NORM_RMS, NORM_GATE_SILU, NORM_GATE_SIGMOID = 1, 2, 4   # CKDA_NORM_*
 EXPORTS = ("ckda_chunk_fwd_workspace_size", "ckda_chunk_fwd", "ckda_chunk_fwd_noalloc", "ckda_chunk_fwd_timed",
            "ckda_chunk_fwd_ex",
            "ckda_chunk_fwd_gather", "ckda_decode_step", "ckda_decode_step_ex", "ckda_decode_step_gather",
            "ckda_deltaproduct2_fwd", "ckda_deltaproduct2_decode_step", "ckda_chunk_bwd",
            "ckda_chunk_bwd_workspace_size", "ckda_chunk_bwd_ex", "ckda_chunk_bwd_ex_workspace_size",
            "ckda_deltaproduct2_bwd", "ckda_deltaproduct2_bwd_workspace_size",
+           "ckda_linattn_fwd", "ckda_linattn_fwd_workspace_size", "ckda_linattn_bwd", "ckda_linattn_bwd_workspace_size",
+           "ckda_linattn_decode_step", "ckda_head_norm_fwd", "ckda_head_norm_bwd", "ckda_head_norm_bwd_workspace_size",
            "ckda_status_string", "ckda_last_error", "ckda_abi_version")
 
 _lib = None
@@ -87,6 +94,23 @@ def lib() -> ctypes.CDLL:
         L.ckda_decode_step.restype = i
         L.ckda_decode_step_ex.argtypes = [vp] * 7 + [i] * 6 + [vp]
         L.ckda_decode_step_ex.restype = i
+        f = ctypes.c_float
+        L.ckda_linattn_fwd_workspace_size.argtypes = [i] * 6
+        L.ckda_linattn_fwd_workspace_size.restype = sz
+        L.ckda_linattn_fwd.argtypes = [vp] * 8 + [i] * 8 + [vp, sz, vp]
+        L.ckda_linattn_fwd.restype = i
+        L.ckda_linattn_bwd_workspace_size.argtypes = [i] * 7
+        L.ckda_linattn_bwd_workspace_size.restype = sz
+        L.ckda_linattn_bwd.argtypes = [vp] * 13 + [i] * 8 + [vp, sz, vp]
+        L.ckda_linattn_bwd.restype = i
+        L.ckda_linattn_decode_step.argtypes = [vp] * 6 + [i] * 7 + [vp]
+        L.ckda_linattn_decode_step.restype = i
+        L.ckda_head_norm_fwd.argtypes = [vp] * 5 + [i] * 7 + [f, vp]
+        L.ckda_head_norm_fwd.restype = i
+        L.ckda_head_norm_bwd_workspace_size.argtypes = [i] * 6
+        L.ckda_head_norm_bwd_workspace_size.restype = sz
+        L.ckda_head_norm_bwd.argtypes = [vp] * 9 + [i] * 7 + [f, vp, sz, vp]
+        L.ckda_head_norm_bwd.restype = i
         L.ckda_status_string.argtypes = [i]
         L.ckda_status_string.restype = ctypes.c_char_p
         L.ckda_last_error.argtypes = []
@@ -421,3 +445,223 @@ def deltaproduct2_bwd(q, k, v, alpha, beta, do, h0=None, dhT=None, want_dh0=True
                                         B, H, T, dk, dv, code, _ptr(workspace),
                                         workspace.numel() * workspace.element_size(), _stream(stream)))
     return gq, gk, gv, galpha, gbeta, gh0
+
+
+# ---------------------------------------------------------------- linear attention, head norm
+
+def _tensors(device, expect):
+    """Checks of shape, dtype, contiguity and device for `expect`, a list of
+    (name, tensor or None, shape, dtype); all tensors must be on `device`.
+    Shapes first: the C ABI cannot see them."""
+    for name, t, shape, _ in expect:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    for name, t, _, dtype in expect:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _run(device, stream, fn, *args):
+    """fn(*args, stream handle) with `device` current: on `stream`, or on the
+    device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def _workspace_arg(workspace, need, device, stream):
+    """The caller's workspace, or a temporary one of `need` bytes, and its
+    (pointer, bytes); the tensor is to be kept until the call is made."""
+    if workspace is None:
+        workspace = _fresh((need,), torch.uint8, device, stream)
+    elif not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous GPU tensor on {device}")
+    return workspace, (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def _fresh(shape, dtype, device, stream, zero=False):
+    """A new tensor for one call, made (and zeroed) on the stream the kernels
+    run on, so that its memory cannot still be in use by earlier work of
+    another stream; also tied to the current stream, where the caller may use
+    it before it is freed."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream == current:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
+def _linattn_dims(q, v, g, lead):
+    """(B, H, Hk, T, dk, dv, flags) of q [B,Hk,T,dk] and v [B,H,T,dv] (lead 2),
+    or of a decode step's q [N,Hk,dk] and v [N,H,dv] (lead 1, T = 1)."""
+    sq, sv = _dims(q, lead + 2, "q"), _dims(v, lead + 2, "v")
+    H, Hk = sv[1], sq[1]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"q has {Hk} heads, which do not divide the {H} heads of v")
+    return sv[0], H, Hk, sv[2] if lead == 2 else 1, sq[-1], sv[-1], DECAY_HEAD if g.dim() == 1 else 0
+
+
+def linattn_workspace_size(B, H, T, dk, dv, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else _dtype_code(torch.empty(0, dtype=dtype))
+    return int(lib().ckda_linattn_fwd_workspace_size(B, H, T, dk, dv, code))
+
+
+def linattn_bwd_workspace_size(B, H, Hk, T, dk, dv, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else _dtype_code(torch.empty(0, dtype=dtype))
+    return int(lib().ckda_linattn_bwd_workspace_size(B, H, Hk, T, dk, dv, code))
+
+
+def linattn_fwd(q, k, v, g, h0=None, lens=None, workspace=None, o=None, hT=None, want_state=True, stream=None):
+    """Linear attention with a decay for each head (ckda_linattn_fwd):
+    H_t = exp(g_t) H_{t-1} + k_t v_t^T, o_t = H_t^T q_t.
+
+    q, k [B,Hk,T,dk]; v [B,H,T,dv], Hk dividing H (head h uses query and key
+    head h // (H / Hk)); g [B,H,T] log decays, or [H] constants; h0
+    [B,H,dk,dv] fp32 or None; lens [B] int32 GPU tensor of sequence lengths or
+    None.  Returns (o [B,H,T,dv], hT [B,H,dk,dv] fp32 or None).  Rows of o at
+    or past a sequence's length are left as they were (zero if o is not given).
+    `workspace` (uint8, linattn_workspace_size() bytes), `o` and `hT` may be
+    passed in to avoid allocations; hT may be h0."""
+    B, H, Hk, T, dk, dv, flags = _linattn_dims(q, v, g, 2)
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    _tensors(dev, [("q", q, (B, Hk, T, dk), dt), ("k", k, (B, Hk, T, dk), dt), ("v", v, (B, H, T, dv), dt),
+                   ("g", g, (H,) if flags else (B, H, T), dt), ("h0", h0, (B, H, dk, dv), f32),
+                   ("lens", lens, (B,), torch.int32), ("o", o, (B, H, T, dv), dt), ("hT", hT, (B, H, dk, dv), f32)])
+    code = _dtype_code(q)
+    L = lib()
+    need = L.ckda_linattn_fwd_workspace_size(B, H, T, dk, dv, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    if o is None:
+        o = _fresh((B, H, T, dv), dt, dev, stream, zero=lens is not None)
+    if hT is None and want_state:
+        hT = _fresh((B, H, dk, dv), f32, dev, stream)
+    _run(dev, stream, L.ckda_linattn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(lens),
+         o.data_ptr(), _ptr(hT), B, H, Hk, T, dk, dv, code, flags, *ws)
+    return o, hT
+
+
+def linattn_bwd(q, k, v, g, do, h0=None, dhT=None, lens=None, want_dh0=True, workspace=None, stream=None):
+    """Backward of linattn_fwd (ckda_linattn_bwd): given do = dL/do [B,H,T,dv]
+    and dhT = dL/dH_T [B,H,dk,dv] fp32 or None, returns (dq, dk, dv, dg, dh0 or
+    None): dq, dk [B,Hk,T,dk], dv [B,H,T,dv] and dg (the shape of g, with
+    respect to the log decays) in the inputs' dtype, dh0 fp32.  Rows at or past
+    a sequence's length have zero gradients."""
+    B, H, Hk, T, dk, dv, flags = _linattn_dims(q, v, g, 2)
+    dev, dt, f32 = q.device, q.dtype, torch.float32
+    _tensors(dev, [("q", q, (B, Hk, T, dk), dt), ("k", k, (B, Hk, T, dk), dt), ("v", v, (B, H, T, dv), dt),
+                   ("g", g, (H,) if flags else (B, H, T), dt), ("do", do, (B, H, T, dv), dt),
+                   ("h0", h0, (B, H, dk, dv), f32), ("dhT", dhT, (B, H, dk, dv), f32),
+                   ("lens", lens, (B,), torch.int32)])
+    code = _dtype_code(q)
+    L = lib()
+    need = L.ckda_linattn_bwd_workspace_size(B, H, Hk, T, dk, dv, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    zero = lens is not None
+    gq, gk = (_fresh((B, Hk, T, dk), dt, dev, stream, zero) for _ in range(2))
+    gv = _fresh((B, H, T, dv), dt, dev, stream, zero)
+    gg = _fresh(g.shape, dt, dev, stream, zero)
+    gh0 = _fresh((B, H, dk, dv), f32, dev, stream) if want_dh0 else None
+    _run(dev, stream, L.ckda_linattn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(lens),
+         do.data_ptr(), _ptr(dhT), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), _ptr(gh0), B, H, Hk, T, dk,
+         dv, code, flags, *ws)
+    return gq, gk, gv, gg, gh0
+
+
+def linattn_decode_step(q, k, v, g, H, o=None, stream=None):
+    """One token of linattn_fwd (ckda_linattn_decode_step): q, k [N,Hk,dk];
+    v [N,Hh,dv]; g [N,Hh] or [Hh]; H [N,Hh,dk,dv] fp32 updated in place.
+    Returns o [N,Hh,dv]."""
+    N, Hh, Hk, _, dk, dv, flags = _linattn_dims(q, v, g, 1)
+    dev, dt = q.device, q.dtype
+    _tensors(dev, [("q", q, (N, Hk, dk), dt), ("k", k, (N, Hk, dk), dt), ("v", v, (N, Hh, dv), dt),
+                   ("g", g, (Hh,) if flags else (N, Hh), dt), ("H", H, (N, Hh, dk, dv), torch.float32),
+                   ("o", o, (N, Hh, dv), dt)])
+    code = _dtype_code(q)
+    if o is None:
+        o = _fresh((N, Hh, dv), dt, dev, stream)
+    _run(dev, stream, lib().ckda_linattn_decode_step, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+         H.data_ptr(), o.data_ptr(), N, Hh, Hk, dk, dv, code, flags)
+    return o
+
+
+_ACTS = {"silu": NORM_GATE_SILU, "sigmoid": NORM_GATE_SIGMOID}
+
+
+def _norm_args(x, w, b, gate, act, rms):
+    """(B, H, T, D, wheads, flags) of head_norm_fwd's arguments."""
+    B, H, T, D = _dims(x, 4, "x")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    wheads = None
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            if t.dim() != 2 or t.shape[0] not in (1, H) or (wheads or t.shape[0]) != t.shape[0]:
+                raise ValueError(f"{name} must be [H, D] or [1, D] (w and b alike), got shape {tuple(t.shape)}")
+            wheads = t.shape[0]
+    return B, H, T, D, wheads or 1, (NORM_RMS if rms else 0) | (_ACTS[act] if gate is not None else 0)
+
+
+def head_norm_fwd(x, w=None, b=None, gate=None, act="silu", rms=False, eps=1e-5, y=None, stream=None):
+    """Norm of the attention's output rows with an output gate
+    (ckda_head_norm_fwd): y = (n w + b) act(gate), n the layer norm of each row
+    of x (rms: without the mean).
+
+    x [B,H,T,D], head-major; gate [B,T,H,D], token-major, or None; w, b [H,D],
+    or [1,D] for all heads, fp32, or None; act "silu" or "sigmoid" (of the
+    gate).  Returns y [B,T,H,D], token-major."""
+    B, H, T, D, wheads, flags = _norm_args(x, w, b, gate, act, rms)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("x", x, (B, H, T, D), dt), ("gate", gate, (B, T, H, D), dt), ("w", w, (wheads, D), f32),
+                   ("b", b, (wheads, D), f32), ("y", y, (B, T, H, D), dt)])
+    code = _dtype_code(x)
+    if y is None:
+        y = _fresh((B, T, H, D), dt, dev, stream)
+    _run(dev, stream, lib().ckda_head_norm_fwd, x.data_ptr(), _ptr(gate), _ptr(w), _ptr(b), y.data_ptr(), B, H, T, D,
+         wheads, code, flags, eps)
+    return y
+
+
+def head_norm_bwd(x, dy, w=None, b=None, gate=None, act="silu", rms=False, eps=1e-5, workspace=None, stream=None):
+    """Backward of head_norm_fwd (ckda_head_norm_bwd): given dy [B,T,H,D],
+    returns (dx [B,H,T,D], dgate [B,T,H,D] or None, dw, db): dx and dgate in
+    x's dtype, dw and db fp32 in the shape of w and b ([1,D] without either:
+    the gradients at w = 1, b = 0)."""
+    B, H, T, D, wheads, flags = _norm_args(x, w, b, gate, act, rms)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("x", x, (B, H, T, D), dt), ("dy", dy, (B, T, H, D), dt), ("gate", gate, (B, T, H, D), dt),
+                   ("w", w, (wheads, D), f32), ("b", b, (wheads, D), f32)])
+    code = _dtype_code(x)
+    L = lib()
+    need = L.ckda_head_norm_bwd_workspace_size(B, H, T, D, wheads, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes D={D}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    dx = _fresh((B, H, T, D), dt, dev, stream)
+    dz = _fresh((B, T, H, D), dt, dev, stream) if gate is not None else None
+    dw, db = (_fresh((wheads, D), f32, dev, stream) for _ in range(2))
+    _run(dev, stream, L.ckda_head_norm_bwd, x.data_ptr(), _ptr(gate), _ptr(w), _ptr(b), dy.data_ptr(), dx.data_ptr(),
+         _ptr(dz), dw.data_ptr(), db.data_ptr(), B, H, T, D, wheads, code, flags, eps, *ws)
+    return dx, dz, dw, db

@@ -10,13 +10,15 @@
 
 #include <string>
 
+#include "ckda_checks.hpp"
 #include "ckda_internal.hpp"
 
+namespace ckda {
+
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-int fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 int fail(int status, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -32,26 +34,13 @@ int ok() {
   return CKDA_OK;
 }
 
-bool supported_dim(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-bool supported_chunk(int c) { return c == 16 || c == 32 || c == 64; }
-bool supported_dtype(int t) { return t == CKDA_DTYPE_F32 || t == CKDA_DTYPE_BF16; }
-size_t dtype_bytes(int t) { return t == CKDA_DTYPE_BF16 ? 2 : 4; }
+const char* last_error() { return g_last_error.c_str(); }
 
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;  // [lo, hi)
-};
+}  // namespace ckda
 
-Range range(const char* name, const void* p, size_t bytes) {
-  uintptr_t a = (uintptr_t)p;
-  return Range{name, a, a + bytes};
-}
+using namespace ckda;
 
-bool overlap(const Range& a, const Range& b) {
-  return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool misaligned(const void* p) { return ((uintptr_t)p & 15u) != 0; }
+namespace {
 
 constexpr int kFuseAll = CKDA_FUSE_GATES | CKDA_FUSE_NORM_K | CKDA_FUSE_NORM_Q;
 constexpr int kFlagsAll = kFuseAll | CKDA_GATE_SCALAR;
@@ -70,12 +59,12 @@ const char* ckda_status_string(int status) {
     case CKDA_ERR_ALIAS: return "an output overlaps an input";
     case CKDA_ERR_WORKSPACE: return "workspace missing, too small or misaligned";
     case CKDA_ERR_HIP: return "HIP runtime error";
-    case CKDA_ERR_FLAGS: return "unknown prologue flag bits";
+    case CKDA_ERR_FLAGS: return "unknown flag bits or combination of flags";
   }
   return "unknown status";
 }
 
-const char* ckda_last_error(void) { return g_last_error.c_str(); }
+const char* ckda_last_error(void) { return last_error(); }
 
 int ckda_abi_version(void) { return CKDA_ABI_VERSION; }
 

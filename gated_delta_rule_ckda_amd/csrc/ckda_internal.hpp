@@ -72,6 +72,79 @@ hipError_t launch_dp2_bwd(const BwdArgs& a);
 hipError_t launch_decode(const DecodeArgs& a);
 hipError_t launch_chunk_fwd(const ChunkArgs& a);
 
+// ---- linear attention with a decay for each head (linattn.hip)
+constexpr int kLaChunk = 64;   // rows of a chunk
+
+struct LinAttnArgs {
+  const void *q, *k, *v, *g;
+  const float* h0;
+  const void* dout;          // backward: dL/do, dL/dH_T, gradients
+  const float* dhT;
+  void* o;                   // forward: outputs, final state
+  float* hT;
+  void *dq, *dk_out, *dv_out, *dg;
+  float* dh0;
+  const int* lens;           // [B] or NULL
+  int B, H, Hk, T, dk, dv, dtype, head_decay;
+  void* workspace;
+  hipStream_t stream;
+};
+struct LinAttnDecodeArgs {
+  const void *q, *k, *v, *g;
+  float* H_inout;
+  void* o;
+  int N, H, Hk, dk, dv, dtype, head_decay;
+  hipStream_t stream;
+};
+
+// One sweep: out_t = S_t^T x_t with S_t = a_t S_{t-1} + y_t z_t^T, S [d1, d2].
+// An operand that is `shared` has one head for the group's heads.
+struct SweepRole {
+  const void *x, *y, *z;
+  const void* w;             // dot[slice][bh][row] = w_row . out_row over the slice (or NULL)
+  float* dot;
+  void* out;
+  const float* init;         // first state (or NULL: zero)
+  float* fin;                // last state (or NULL)
+  float* seg_states;         // start state of every segment (with more than one)
+  float *seg_out, *seg_decay;   // states-only launches: the segments' own states and decays
+  int x_shared, y_shared, z_shared, w_shared;
+  int d2;
+  int reverse;               // from the last row to the first
+  int turned;                // init, fin and segment states are stored [d2, d1]
+  int out_f32;               // out is fp32
+  int exact_state;           // state products with three bf16 terms (a state is returned), else two
+  int parts;                 // workgroups per unit: segments x heads of the group x slices
+};
+struct SweepLaunch {
+  SweepRole role[3];
+  const void* g;
+  const int* lens;
+  long long seg_stride;      // floats between two segments' states
+  int nroles, units, group, heads, rows, parts, seg_rows, nseg, head_decay;
+};
+
+size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv);
+size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv);
+hipError_t launch_linattn_fwd(const LinAttnArgs& a);
+hipError_t launch_linattn_bwd(const LinAttnArgs& a);
+hipError_t launch_linattn_decode(const LinAttnDecodeArgs& a);
+
+// ---- norm of the attention output by head, with an output gate (head_norm.hip)
+struct HeadNormArgs {
+  const void *x, *z, *dy;
+  const float *w, *b;
+  void *y, *dx, *dz;
+  float *dw, *db;
+  int B, H, T, D, wheads, dtype, flags;
+  float eps;
+  void* workspace;
+  hipStream_t stream;
+};
+size_t head_norm_bwd_workspace_bytes(int B, int H, int T, int D, int wheads, int dtype);
+hipError_t launch_head_norm_fwd(const HeadNormArgs& a);
+hipError_t launch_head_norm_bwd(const HeadNormArgs& a);
+
 // Size of the fixed device scratch of ckda_chunk_fwd_noalloc (noalloc.hip),
 // and its device address on the current device (looked up on first use).
 constexpr size_t kNoallocScratchBytes = (size_t)64 << 20;

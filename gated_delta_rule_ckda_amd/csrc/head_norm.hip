@@ -1,0 +1,389 @@
+// head_norm.hip -- the norm that follows the attention: layer norm (or root
+// mean square norm) of each head's output row with an optional output gate,
+// forward and backward.
+//
+//   n = (x - m) s,  m = mean x (0 for the rms norm),  s = (mean (x - m)^2 + eps)^-1/2
+//   y = (n w + b) act(z),   act = silu or sigmoid of the gate z (1 without)
+// and with u = dy act(z), dn = u w:
+//   dx = s (dn - mean dn - n mean(dn n))   (rms norm: without mean dn)
+//   dz = dy (n w + b) act'(z),   dw = sum u n,   db = sum u  (over batch and time).
+// x is head-major [B, H, T, D] as the attention writes it; z, y, dy and dz are
+// token-major [B, T, H, D], the rows a projection reads or writes: the
+// transposition between the two costs nothing here, where every row is
+// touched once anyway.
+//
+// HBM-bound: every tensor is read or written once.  LPR lanes hold one row in
+// registers (NV vectors of VEC elements each, 16 bytes where the width allows),
+// so the row's sums (mean, centred square sum, and in the backward the two
+// means of dn) are DPP sums over the lane group (over the workgroup for rows
+// of more than 64 x 4 vectors).  The statistics are recomputed in the backward
+// from x, which it reads anyway, instead of being stored by the forward.  A
+// workgroup keeps to one head and walks a slab of its rows, so that w and b
+// are loaded once and dw and db stay in registers; a slab's sums go to the
+// workspace and a second kernel adds the slabs in a fixed order.
+// All arithmetic is fp32; only y, dx and dz are rounded, once.
+#include <algorithm>
+
+#include "ckda_device.hpp"
+#include "ckda_internal.hpp"
+
+namespace ckda {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kActNone = 0, kActSilu = CKDA_NORM_GATE_SILU, kActSigmoid = CKDA_NORM_GATE_SIGMOID;
+
+// VEC consecutive elements, widened
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float* v) {
+  if constexpr (VEC == 1) {
+    v[0] = to_f32(*p);
+  } else if constexpr (sizeof(T) == 2) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo_half(w[i]);
+      v[2 * i + 1] = bf16_hi_half(w[i]);
+    }
+  } else {
+    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = w[i];
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float* v) {
+  if constexpr (VEC == 1) {
+    *p = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<u32x4*>(p) = w;
+  } else {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  }
+}
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+
+// Sum over the LPR lanes of a row; 256 lanes (the workgroup) go through LDS,
+// in one of two alternating buffers so that one barrier per sum is enough.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x, float (*s)[kNormThreads / 64], int& phase) {
+  if constexpr (LPR <= 64) {
+    return group_sum<LPR>(x);
+  } else {
+    x = group_sum<64>(x);
+    float* buf = s[phase];
+    phase ^= 1;
+    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+  }
+}
+
+struct RowGeom {
+  int H, T, D, rows, slab_rows;   // rows = B T of one head
+};
+
+template <typename T, int VEC, int LPR, int NV, bool BWD>
+__global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, const T* z, const T* dy, const float* w,
+                                                                 const float* b, T* out, T* dz, float* part,
+                                                                 RowGeom G, int w_shared, int act, int rms, float eps) {
+  constexpr int GPW = kNormThreads / LPR;   // rows in flight per workgroup
+  constexpr int N = NV * VEC;
+  __shared__ float s_sum[2][kNormThreads / 64];
+  const int tid = threadIdx.x, lane = tid % LPR, grp = tid / LPR;
+  const int h = blockIdx.y;
+  const int row0 = blockIdx.x * G.slab_rows;
+  const int row1 = min(row0 + G.slab_rows, G.rows);
+  const int D = G.D;
+  const float inv_d = 1.f / (float)D;
+  int phase = 0;
+
+  float wv[N], bv[N];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int c = (v * LPR + lane) * VEC + e;
+      const int at = (w_shared ? 0 : h * D) + c;
+      wv[v * VEC + e] = c >= D ? 0.f : w ? w[at] : 1.f;
+      bv[v * VEC + e] = c < D && b ? b[at] : 0.f;
+    }
+  float dw[BWD ? N : 1], db[BWD ? N : 1];
+  if constexpr (BWD) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
+  }
+
+  for (int base = row0; base < row1; base += GPW) {   // the same trips for every lane of the workgroup
+    const int n = base + grp;
+    const bool live = n < row1;
+    const int bi = (live ? n : row0) / G.T, t = (live ? n : row0) % G.T;
+    const size_t xo = (((size_t)bi * G.H + h) * G.T + t) * D;   // head-major row
+    const size_t yo = (((size_t)bi * G.T + t) * G.H + h) * D;   // token-major row
+    float xv[N], zv[N], gv[BWD ? N : 1];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * VEC;
+      const bool in = live && c < D;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        xv[v * VEC + e] = zv[v * VEC + e] = 0.f;
+        if constexpr (BWD) gv[v * VEC + e] = 0.f;
+      }
+      if (in) {
+        load_vec<T, VEC>(x + xo + c, xv + v * VEC);
+        if (act) load_vec<T, VEC>(z + yo + c, zv + v * VEC);
+        if constexpr (BWD) load_vec<T, VEC>(dy + yo + c, gv + v * VEC);
+      }
+    }
+    float mean = 0.f;
+    if (!rms) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += xv[i];
+      mean = row_sum<LPR>(sum, s_sum, phase) * inv_d;
+    }
+    float sq = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int i = v * VEC + e;
+        xv[i] = (v * LPR + lane) * VEC + e < D ? xv[i] - mean : 0.f;
+        sq = __builtin_fmaf(xv[i], xv[i], sq);
+      }
+    const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, s_sum, phase) * inv_d + eps);
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float y = __builtin_fmaf(xv[i] * rstd, wv[i], bv[i]);
+        if (act) {
+          const float sg = sigmoid(zv[i]);
+          y *= act == kActSilu ? zv[i] * sg : sg;
+        }
+        xv[i] = y;
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * LPR + lane) * VEC;
+        if (live && c < D) store_vec<T, VEC>(out + yo + c, xv + v * VEC);
+      }
+    } else {
+      float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float nn = xv[i] * rstd;
+        float u = gv[i];
+        if (act) {
+          const float sg = sigmoid(zv[i]);
+          const float slope = act == kActSilu ? sg * __builtin_fmaf(zv[i], 1.f - sg, 1.f) : sg * (1.f - sg);
+          u *= act == kActSilu ? zv[i] * sg : sg;
+          zv[i] = gv[i] * __builtin_fmaf(nn, wv[i], bv[i]) * slope;   // dz
+        }
+        dw[i] = __builtin_fmaf(u, nn, dw[i]);
+        db[i] += u;
+        xv[i] = nn;
+        gv[i] = u * wv[i];   // dn
+        m1 += gv[i];
+        m2 = __builtin_fmaf(gv[i], nn, m2);
+      }
+      m1 = rms ? 0.f : row_sum<LPR>(m1, s_sum, phase) * inv_d;
+      m2 = row_sum<LPR>(m2, s_sum, phase) * inv_d;
+#pragma unroll
+      for (int i = 0; i < N; ++i) xv[i] = rstd * (gv[i] - m1 - xv[i] * m2);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * LPR + lane) * VEC;
+        if (live && c < D) {
+          store_vec<T, VEC>(out + xo + c, xv + v * VEC);
+          if (act) store_vec<T, VEC>(dz + yo + c, zv + v * VEC);
+        }
+      }
+    }
+  }
+
+  if constexpr (BWD) {
+    // the workgroup's sums: over the lane groups of a wave, then over the waves
+    constexpr int WAVES = kNormThreads / 64;
+    constexpr int COLS = (LPR < 64 ? LPR : 64) * N;   // columns one wave holds
+    __shared__ float s_part[LPR <= 64 ? WAVES : 1][LPR <= 64 ? COLS : 1];
+    float* to = part + ((size_t)h * gridDim.x + blockIdx.x) * 2 * D;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float* acc = which ? db : dw;
+      if constexpr (LPR <= 64) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int off = LPR; off < 64; off <<= 1) acc[i] += __shfl_xor(acc[i], off, 64);
+        __syncthreads();
+        if ((tid & 63) < LPR) {
+#pragma unroll
+          for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s_part[tid >> 6][(v * LPR + lane) * VEC + e] = acc[v * VEC + e];
+        }
+        __syncthreads();
+        for (int c = tid; c < D; c += kNormThreads)
+          to[which * D + c] = (s_part[0][c] + s_part[1][c]) + (s_part[2][c] + s_part[3][c]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const int c = (v * LPR + lane) * VEC + e;
+            if (c < D) to[which * D + c] = acc[v * VEC + e];
+          }
+      }
+    }
+  }
+}
+
+// dw and db: the sums of the slabs' parts [nparts][2][D] of one weight head.
+// 16 columns per workgroup, 64 threads on each.
+constexpr int kRedCols = 16, kRedRows = 64;
+__global__ __launch_bounds__(kRedCols * kRedRows) void norm_weight_grad_kernel(const float* part, int nparts, int D,
+                                                                               float* dw, float* db) {
+  __shared__ float s[kRedRows][kRedCols + 1];
+  const int tid = threadIdx.x, c = blockIdx.x * kRedCols + tid % kRedCols, j = tid / kRedCols;
+  const int which = blockIdx.y, head = blockIdx.z;
+  const float* p = part + (size_t)head * nparts * 2 * D + (size_t)which * D;
+  float x = 0.f;
+  if (c < D) {
+#pragma unroll 4
+    for (int i = j; i < nparts; i += kRedRows) x += p[(size_t)i * 2 * D + c];
+  }
+  s[j][tid % kRedCols] = x;
+  __syncthreads();
+  for (int half = kRedRows / 2; half > 0; half >>= 1) {
+    if (j < half) s[j][tid % kRedCols] += s[j + half][tid % kRedCols];
+    __syncthreads();
+  }
+  float* out = which ? db : dw;
+  if (j == 0 && c < D && out) out[(size_t)head * D + c] = s[0][tid];
+}
+
+// lanes and vectors per row for width D (VEC elements per vector)
+struct NormShape {
+  int vec, lpr, nv;
+};
+NormShape norm_shape(int D, int dtype) {
+  const int full = dtype == CKDA_DTYPE_BF16 ? 8 : 4;
+  NormShape s;
+  s.vec = D % full == 0 ? full : 1;   // rows that are whole 16-byte vectors, else single elements
+  const int pieces = (D + s.vec - 1) / s.vec;
+  if (pieces <= 64) {
+    s.lpr = 2;
+    while (s.lpr < pieces) s.lpr *= 2;
+    s.nv = 1;
+    if (s.vec == 1 && s.lpr < 16) s.lpr = 16;
+  } else if (pieces <= 256) {
+    s.lpr = 64;
+    s.nv = pieces <= 128 ? 2 : 4;
+  } else {
+    s.lpr = 256;
+    s.nv = 2;
+    while (s.nv * 256 < pieces) s.nv *= 2;
+  }
+  return s;
+}
+
+// rows of one head per workgroup: at least four per lane group, and at most
+// about 4096 workgroups (2048 in the backward, whose slabs each leave a part)
+int slab_rows(int rows, int H, int lpr, bool bwd) {
+  const int gpw = kNormThreads / lpr;
+  const long long most = std::max(1, (bwd ? 2048 : 4096) / H);
+  long long per = 4LL * gpw;
+  const long long need = (rows + most - 1) / most;
+  if (per < need) per = (need + gpw - 1) / gpw * gpw;
+  return (int)per;
+}
+
+template <typename T, int VEC, int LPR, int NV>
+hipError_t launch_norm_t(const HeadNormArgs& a, bool bwd) {
+  RowGeom G{a.H, a.T, a.D, a.B * a.T, slab_rows(a.B * a.T, a.H, LPR, bwd)};
+  const dim3 grid((G.rows + G.slab_rows - 1) / G.slab_rows, a.H);
+  const int act = a.z ? a.flags & (kActSilu | kActSigmoid) : kActNone;
+  const int rms = (a.flags & CKDA_NORM_RMS) ? 1 : 0, shared = a.wheads == 1;
+  if (G.rows == 0)
+    ;   // nothing but the weights' gradients, which are then zero
+  else if (bwd)
+    hipLaunchKernelGGL((head_norm_kernel<T, VEC, LPR, NV, true>), grid, dim3(kNormThreads), 0, a.stream, (const T*)a.x,
+                       (const T*)a.z, (const T*)a.dy, a.w, a.b, (T*)a.dx, (T*)a.dz, (float*)a.workspace, G, shared, act,
+                       rms, a.eps);
+  else
+    hipLaunchKernelGGL((head_norm_kernel<T, VEC, LPR, NV, false>), grid, dim3(kNormThreads), 0, a.stream, (const T*)a.x,
+                       (const T*)a.z, (const T*)nullptr, a.w, a.b, (T*)a.y, (T*)nullptr, (float*)nullptr, G, shared, act,
+                       rms, a.eps);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !bwd || (!a.dw && !a.db)) return e;
+  // shared weights: the parts of all heads are one list
+  const int nparts = (int)grid.x * (shared ? a.H : 1);
+  hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((a.D + kRedCols - 1) / kRedCols, 2, a.wheads),
+                     dim3(kRedCols * kRedRows), 0, a.stream, (const float*)a.workspace, nparts, a.D, a.dw, a.db);
+  return hipGetLastError();
+}
+
+template <typename T, int VEC>
+hipError_t launch_norm_v(const HeadNormArgs& a, const NormShape& s, bool bwd) {
+  if (s.lpr == 256) {
+    switch (s.nv) {
+      case 2: return launch_norm_t<T, VEC, 256, 2>(a, bwd);
+      case 4: return launch_norm_t<T, VEC, 256, 4>(a, bwd);
+      case 8:
+        if constexpr (VEC * sizeof(T) <= 16 && (VEC == 1 || sizeof(T) == 4)) return launch_norm_t<T, VEC, 256, 8>(a, bwd);
+        break;
+      case 16:
+        if constexpr (VEC == 1) return launch_norm_t<T, VEC, 256, 16>(a, bwd);
+        break;
+      case 32:
+        if constexpr (VEC == 1) return launch_norm_t<T, VEC, 256, 32>(a, bwd);
+        break;
+    }
+    return hipErrorInvalidValue;
+  }
+  if (s.nv == 4) return launch_norm_t<T, VEC, 64, 4>(a, bwd);
+  if (s.nv == 2) return launch_norm_t<T, VEC, 64, 2>(a, bwd);
+  switch (s.lpr) {
+    case 2:
+      if constexpr (VEC > 1) return launch_norm_t<T, VEC, 2, 1>(a, bwd);
+      break;
+    case 4:
+      if constexpr (VEC > 1) return launch_norm_t<T, VEC, 4, 1>(a, bwd);
+      break;
+    case 8:
+      if constexpr (VEC > 1) return launch_norm_t<T, VEC, 8, 1>(a, bwd);
+      break;
+    case 16: return launch_norm_t<T, VEC, 16, 1>(a, bwd);
+    case 32: return launch_norm_t<T, VEC, 32, 1>(a, bwd);
+    case 64: return launch_norm_t<T, VEC, 64, 1>(a, bwd);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_norm(const HeadNormArgs& a, bool bwd) {
+  const NormShape s = norm_shape(a.D, a.dtype);
+  if (a.dtype == CKDA_DTYPE_BF16)
+    return s.vec == 1 ? launch_norm_v<bf16_t, 1>(a, s, bwd) : launch_norm_v<bf16_t, 8>(a, s, bwd);
+  return s.vec == 1 ? launch_norm_v<float, 1>(a, s, bwd) : launch_norm_v<float, 4>(a, s, bwd);
+}
+
+}  // namespace
+
+size_t head_norm_bwd_workspace_bytes(int B, int H, int T, int D, int wheads, int dtype) {
+  (void)wheads;
+  const long long rows = (long long)B * T;
+  if (rows == 0 || H == 0) return 0;
+  const int per = slab_rows((int)rows, H, norm_shape(D, dtype).lpr, true);
+  return (size_t)((rows + per - 1) / per) * H * 2 * D * 4;
+}
+
+hipError_t launch_head_norm_fwd(const HeadNormArgs& a) { return launch_norm(a, false); }
+hipError_t launch_head_norm_bwd(const HeadNormArgs& a) { return launch_norm(a, true); }
+
+}  // namespace ckda

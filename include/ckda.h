@@ -64,7 +64,7 @@ typedef enum {
   CKDA_ERR_ALIAS = 4,       /* an output overlaps an input it may not overlap */
   CKDA_ERR_HIP = 5,         /* the HIP runtime reported an error at launch */
   CKDA_ERR_WORKSPACE = 6,   /* workspace missing, too small or misaligned */
-  CKDA_ERR_FLAGS = 7        /* flags hold bits outside CKDA_FUSE_* / CKDA_GATE_SCALAR */
+  CKDA_ERR_FLAGS = 7        /* flags hold bits the entry point does not take, or a combination it refuses */
 } ckda_status_t;
 
 /* Per-token prologue steps of the *_ex entry points (bitwise OR; 0 = none,
@@ -389,6 +389,135 @@ int ckda_decode_step_gather(const void* q, const void* k, const void* v, const v
                             const void* beta, float* H_inout, void* o,
                             int N, int H, int dk_in, const int* idx, int dk, int dv, int dtype, int flags,
                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head
+ *
+ *   H_t = a_t H_{t-1} + k_t v_t^T,   o_t = H_t^T q_t,   a_t = exp(g_t)
+ *
+ * one independent state H [dk, dv] per (batch, head): the recurrence of the
+ * entry points above without the delta rule's correction and with one scalar
+ * decay (no setting of theirs gives it: beta scales the correction as well as
+ * the write).  g holds LOG decays in `dtype`:
+ *   flags 0                [B, H, T] (decode: [N, H]), one per token and head;
+ *   CKDA_DECAY_HEAD        [H], one constant for each head.
+ * g <= 0; g = -inf (or anything below -166) resets the state.  Positive g is
+ * computed as given while the products stay in range.  A non-finite q, k, v or
+ * do makes the outputs of its 64-row chunk and of those after it (in the
+ * backward also before it) unspecified; rows at or past a sequence's length
+ * are never read.
+ *
+ * Shared heads: q and k have Hk heads, Hk dividing H, and head h uses theirs
+ * of index h / (H / Hk) (Hk = H: one each).  v, g, o and the states have H.
+ *
+ * lens: NULL, or [B] int32 (device), the number of rows of each batch entry
+ * that are part of its sequence (clamped into [0, T]); rows of o (and of the
+ * gradients) at or past it are left as they were, and the final state is that
+ * after the last row of the sequence.
+ *
+ * Supported: dtype F32 or BF16; dk, dv in {16, 32, 64, 128}; any T >= 0 with
+ * (T + 128) max(dk, dv) elements below 2 GiB (the backward: counted as fp32).
+ * States and their gradients are fp32.  bf16 inputs are multiplied on bf16
+ * matrix cores with every factor that bf16 does not hold exactly carried as a
+ * sum of two bf16 terms (three in the state itself), so that o and the
+ * gradients are rounded once; fp32 inputs on fp32 matrix cores. */
+#define CKDA_DECAY_HEAD 16
+
+/* Bytes of device workspace ckda_linattn_fwd needs, or 0 when the sizes are
+ * invalid or unsupported.  With few heads and many rows the sequence runs in
+ * segments, whose fp32 states and decays it holds; else 256. */
+size_t ckda_linattn_fwd_workspace_size(int B, int H, int T, int dk, int dv, int dtype);
+
+/* Forward over a whole sequence for every (batch, head).
+ *
+ *   q, k        : [B, Hk, T, dk] dtype
+ *   v           : [B, H, T, dv]  dtype
+ *   g           : [B, H, T] or [H] dtype
+ *   h0          : [B, H, dk, dv] fp32 initial states, or NULL for zeros
+ *   lens        : [B] int32, or NULL (every sequence has T rows)
+ *   o           : [B, H, T, dv]  dtype
+ *   hT          : [B, H, dk, dv] fp32 final states, or NULL to skip
+ *   workspace   : as ckda_chunk_fwd
+ * Aliasing as ckda_chunk_fwd (hT may equal h0 exactly). */
+int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g, const float* h0, const int* lens,
+                     void* o, float* hT, int B, int H, int Hk, int T, int dk, int dv, int dtype, int flags,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace ckda_linattn_bwd needs, or 0 for invalid or
+ * unsupported sizes: two fp32 numbers per row, head and 32 key channels, the
+ * final states, segment states as the forward's for both directions and, with
+ * shared heads, the heads' fp32 parts of dq and dk. */
+size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+
+/* Backward: the gradients of a loss L given dout = dL/do [B, H, T, dv] (dtype)
+ * and dhT = dL/dH_T [B, H, dk, dv] fp32 (or NULL for zero).
+ *   dq, dk : [B, Hk, T, dk] dtype (of shared heads: summed over the heads that
+ *            use them, in fp32);  dv : [B, H, T, dv] dtype
+ *   dg     : dtype, the shape of g: with respect to the log decays (of a
+ *            constant decay: summed over batch and time)
+ *   dh0    : [B, H, dk, dv] fp32, or NULL to skip
+ * With R_t = dL/dH_t (R_t = a_{t+1} R_{t+1} + q_t do_t^T, R_T = dhT + q_T
+ * do_T^T): dq_t = H_t do_t, dk_t = R_t v_t, dv_t = R_t^T k_t, dh0 = a_1 R_1 and
+ * dg_t = a_t <R_t, H_{t-1}>.  Nothing of the forward is needed but its inputs.
+ * Outputs must not overlap each other, any input or the workspace. */
+int ckda_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* h0, const int* lens,
+                     const void* dout, const float* dhT, void* dq, void* dk, void* dv, void* dg, float* dh0, int B,
+                     int H, int Hk, int T, int dk_, int dv_, int dtype, int flags, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* One token for N sequences x H heads, state in place:
+ *   q, k [N, Hk, dk], v [N, H, dv], g [N, H] or [H], H_inout [N, H, dk, dv]
+ *   fp32, o [N, H, dv];  H <- a H + k v^T, o = H^T q.
+ * One read and one write of the state, all arithmetic fp32.  Aliasing as
+ * ckda_decode_step. */
+int ckda_linattn_decode_step(const void* q, const void* k, const void* v, const void* g, float* H_inout, void* o, int N,
+                             int H, int Hk, int dk, int dv, int dtype, int flags, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Head norm: what follows the attention (and any of the entry points above
+ * that return o) before the output projection
+ *
+ *   n = (x - mean x) / sqrt(var x + eps)      over the D elements of a row
+ *   y = (n w + b) act(z)
+ *
+ * flags: CKDA_NORM_RMS           no mean: n = x / sqrt(mean x^2 + eps)
+ *        CKDA_NORM_GATE_SILU     act(z) = z sigmoid(z)
+ *        CKDA_NORM_GATE_SIGMOID  act(z) = sigmoid(z)
+ * With z NULL there is no gate and no act flag may be set; with z one of the
+ * two must be.
+ *
+ *   x           : [B, H, T, D] dtype, head-major (o of the attention; a decode
+ *                 step's [N, H, D] is B = N, T = 1)
+ *   z           : [B, T, H, D] dtype, token-major (a projection's output)
+ *   w, b        : [wheads, D] fp32, wheads = H or 1 (shared by all heads); NULL
+ *                 for ones / zeros
+ *   y           : [B, T, H, D] dtype, token-major (a projection's input)
+ *   eps         : finite, > 0
+ * With H = 1 this is an ordinary layer norm of rows of width D.
+ * Supported: dtype F32 or BF16; 1 <= D <= 8192 (widths that are whole 16-byte
+ * vectors are read and written as such, others element by element); all
+ * arithmetic fp32, outputs rounded once.  y may not overlap an input. */
+#define CKDA_NORM_RMS 1
+#define CKDA_NORM_GATE_SILU 2
+#define CKDA_NORM_GATE_SIGMOID 4
+
+int ckda_head_norm_fwd(const void* x, const void* z, const float* w, const float* b, void* y, int B, int H, int T,
+                       int D, int wheads, int dtype, int flags, float eps, void* stream);
+
+/* Bytes of device workspace ckda_head_norm_bwd needs, or 0 for invalid or
+ * unsupported sizes: two fp32 rows of width D per workgroup (partial sums of
+ * dw and db). */
+size_t ckda_head_norm_bwd_workspace_size(int B, int H, int T, int D, int wheads, int dtype);
+
+/* Backward of ckda_head_norm_fwd given dy [B, T, H, D] (dtype):
+ *   dx [B, H, T, D] dtype, dz [B, T, H, D] dtype (with z), dw and db
+ *   [wheads, D] fp32 (either may be NULL to skip it; summed over batch, time
+ *   and, if shared, heads, in a fixed order).
+ * The row statistics are recomputed from x.  Outputs must not overlap each
+ * other, any input or the workspace. */
+int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float* b, const void* dy, void* dx, void* dz,
+                       float* dw, float* db, int B, int H, int T, int D, int wheads, int dtype, int flags, float eps,
+                       void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* ckda_status_string(int status);
