@@ -113,7 +113,6 @@ struct SweepRole {
   int reverse;               // from the last row to the first
   int turned;                // init, fin and segment states are stored [d2, d1]
   int out_f32;               // out is fp32
-  int exact_state;           // state products with three bf16 terms (a state is returned), else two
   int parts;                 // workgroups per unit: segments x heads of the group x slices
 };
 struct SweepLaunch {
@@ -122,6 +121,7 @@ struct SweepLaunch {
   const int* lens;
   long long seg_stride;      // floats between two segments' states
   int nroles, units, group, heads, rows, parts, seg_rows, nseg, head_decay;
+  int exact_state;           // state products with three bf16 terms (a state is returned), else two
 };
 
 size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv);

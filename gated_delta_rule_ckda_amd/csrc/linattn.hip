@@ -35,6 +35,8 @@
 // matrix cores throughout.
 // Log decays are summed as two parts, whole multiples of 1/64 (whose sums are
 // exact) and the rest, so that differences of large sums keep fp32 accuracy.
+#include <type_traits>
+
 #include "ckda_device.hpp"
 #include "ckda_internal.hpp"
 
@@ -61,7 +63,7 @@ struct SweepCfg {
   static constexpr int TPW = (RH + WPC - 1) / WPC;   // row tiles per wave
   static constexpr int Y_BYTES = C * YROW, Z_BYTES = C * ZROW, H_BYTES = DS * YROW;
   static constexpr int HSETS = BF ? 2 : 1;           // hi and lo
-  static constexpr int DEC_BYTES = 4 * C * 4;        // c (whole), c (rest), exp(c_t), G(C, t)
+  static constexpr int DEC_BYTES = 5 * C * 4;        // c (whole), c (rest), exp(c_t), G(C, t), G(tile end, t)
   static constexpr int SET = Y_BYTES + Z_BYTES + DEC_BYTES;
   static constexpr int SET_H = SET + HSETS * H_BYTES;
   // pieces of 16 bytes that the 256 threads of the state waves copy
@@ -70,14 +72,17 @@ struct SweepCfg {
 };
 
 // Byte offset of the 16-byte piece `piece` of row `row` in an LDS array of
-// ROWB-byte rows.  The piece index is xor-ed with a row-dependent value chosen
-// so that both a 16-byte read of 16 consecutive rows and a transposing read of
-// 32 bytes of 8 consecutive rows touch every bank once.
+// ROWB-byte rows.  The piece index is xor-ed with twice the number of the
+// row's 256-byte line, so that neither kind of operand read has bank conflicts
+// (SQ_LDS_BANK_CONFLICT 0): a transposing 8-byte read takes 32 bytes of 8 rows
+// at a time, a 16-byte read of 16 rows takes rows 0-3 and 12-15 of one piece
+// with rows 4-11 of the next.  (Telling rows r and r + 8 apart as well costs
+// the 16-byte reads a two-way conflict.)
 template <int ROWB>
 __device__ __forceinline__ int lds_piece(int row, int piece) {
   constexpr int NCH = ROWB / 16 < 16 ? ROWB / 16 : 16;
   const int i = row / (16 / NCH);
-  const int s = ((i & (NCH / 2 - 1)) << 1) | ((i / (NCH / 2)) & 1);
+  const int s = (i & (NCH / 2 - 1)) << 1;
   return row * ROWB + ((piece ^ s) << 4);
 }
 
@@ -126,6 +131,11 @@ __device__ __forceinline__ float wave_prefix(float x) {
   return x;
 }
 
+// the value of lane 15 of this lane's row of 16 (DPP row_newbcast)
+__device__ __forceinline__ float row_last(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x15F, 0xF, 0xF, false));
+}
+
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kDecayFloor = -240.f;   // 2^-240 is 0 in fp32, and 64 such steps keep their sum's parts exact
 
@@ -145,10 +155,9 @@ __device__ __forceinline__ void split3_bf16(const float* v, Frag& fh, Frag& fm, 
   }
 }
 
-template <typename T> __device__ __forceinline__ float load_elem(const T* p) { return to_f32(*p); }
-
 // OUT: with output waves (512 threads); without, only the states (256).
-template <typename T, int D1, int DS, bool OUT>
+// EXACT: states with three bf16 terms (one is returned), else two.
+template <typename T, int D1, int DS, bool OUT, bool EXACT>
 __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
   using S = SweepCfg<T, D1, DS>;
   constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TPW = S::TPW;
@@ -174,7 +183,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
   }
   int role = 0;
   while (role + 1 < L.nroles && part >= L.role[role].parts) part -= L.role[role++].parts;
-  const SweepRole& A = L.role[role];
+  const SweepRole A = L.role[role];
   const int slices = A.d2 / DS;
   const int slice = part % slices;
   const int bh = unit * L.group + (part / slices) % L.group;
@@ -183,7 +192,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
   const int len = L.lens ? min(max(L.lens[bh / L.heads], 0), L.rows) : L.rows;
   const int row0 = seg * L.seg_rows;
   const int nrows = min(max(len - row0, 0), L.seg_rows);
-  const int nch = (nrows + C - 1) / C;
+  const int nch = (nrows + C - 1) / C, last = max(nch - 1, 0);
   // LDS row j of chunk c is row row0 + 64 c + j of the sweep: that row of the
   // sequence, or the len - 1 - that one.  Rows outside [0, len) fall outside
   // the buffers below: they read as zero and are not stored.
@@ -227,85 +236,123 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
     };
     load_x(0, xf, wv);
     lds_barrier();   // set 0 is filled
-    for (int c = 0; c < nch; ++c) {
-      const unsigned char* set = set_of(c);
-      const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
-      if (c + 1 < nch) load_x(c + 1, xn, wn);
-      // O^T = exp(c_t) H^T X^T
-      f32x4 oacc[NDV];
+    // One copy of the loop per wave: W, the wave's row tile, fixes how many
+    // tiles of P it has, so the body is straight-line code.
+    auto run = [&](auto wconst) __attribute__((always_inline)) {
+      constexpr int W = decltype(wconst)::value;
+      constexpr int NPB = (16 * W) / S::KB + 1;      // K blocks of P^T it multiplies
+      constexpr int NF = S::HSETS * NDV + W + 1;     // operand fragments per K block of D1
+      for (int c = 0; c < nch; ++c) {
+        const unsigned char* set = set_of(c);
+        const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
+        load_x(min(c + 1, last), xn, wn);
+        // H^T X^T and the tiles of Y X^T up to this wave's own, one K block's
+        // fragments read ahead of the products
+        Frag f[2][NF];
+        auto read = [&](int kb) __attribute__((always_inline)) {
+          Frag* d = f[kb & 1];
 #pragma unroll
-      for (int d = 0; d < NDV; ++d) {
-        oacc[d] = zero4();
+          for (int i = 0; i < S::HSETS * NDV; ++i)
+            d[i] = row_frag<S::YROW>(set + H_OFF + (i / NDV) * S::H_BYTES, 16 * (i % NDV), kb, g, r);
+#pragma unroll
+          for (int i = 0; i <= W; ++i) d[S::HSETS * NDV + i] = row_frag<S::YROW>(set, 16 * i, kb, g, r);
+        };
+        f32x4 oacc[NDV], olo[NDV], p[RT];
+#pragma unroll
+        for (int d = 0; d < NDV; ++d) oacc[d] = olo[d] = zero4();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) p[i] = zero4();
+        read(0);
 #pragma unroll
         for (int kb = 0; kb < KBN; ++kb) {
-          if constexpr (BF)
-            oacc[d] = mma<T>(oacc[d], row_frag<S::YROW>(set + H_OFF + S::H_BYTES, 16 * d, kb, g, r), xf[kb]);
-          oacc[d] = mma<T>(oacc[d], row_frag<S::YROW>(set + H_OFF, 16 * d, kb, g, r), xf[kb]);
+          if (kb + 1 < KBN) read(kb + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          const Frag* d = f[kb & 1];
+#pragma unroll
+          for (int i = 0; i < NDV; ++i) oacc[i] = mma<T>(oacc[i], d[i], xf[kb]);
+          if constexpr (BF) {
+#pragma unroll
+            for (int i = 0; i < NDV; ++i) olo[i] = mma<T>(olo[i], d[NDV + i], xf[kb]);
+          }
+#pragma unroll
+          for (int i = 0; i <= W; ++i) p[i] = mma<T>(p[i], d[S::HSETS * NDV + i], xf[kb]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        oacc[d] *= dec[2 * C + t];
-      }
-      // P^T = G . (Y X^T) for the row tiles up to this wave's own
-      const float ch = dec[t], cl = dec[C + t];
-      f32x4 p[RT];
+        Frag zf[NPB][NDV];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        p[i] = zero4();
-        if (i <= wave) {
+        for (int kb = 0; kb < NPB; ++kb)
 #pragma unroll
-          for (int kb = 0; kb < KBN; ++kb) p[i] = mma<T>(p[i], row_frag<S::YROW>(set, 16 * i, kb, g, r), xf[kb]);
-          const f32x4 sh = *reinterpret_cast<const f32x4*>(dec + 16 * i + 4 * g);
-          const f32x4 sl = *reinterpret_cast<const f32x4*>(dec + C + 16 * i + 4 * g);
+          for (int d = 0; d < NDV; ++d) zf[kb][d] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
+        // P^T = G . (Y X^T).  Below the diagonal G(t, s) is G(t, e) G(e, s)
+        // with e the last row of the tile of s: both at most 1 for decays, one
+        // exponential a tile here and one a row of the chunk (state waves).
+        const float ch = dec[t], cl = dec[C + t];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const float row = __builtin_amdgcn_exp2f((ch - dec[16 * i + 15]) + (cl - dec[C + 16 * i + 15]));
+          const f32x4 tail = *reinterpret_cast<const f32x4*>(dec + 4 * C + 16 * i + 4 * g);
+          p[i] *= tail * row;
+        }
+        {
+          const f32x4 sh = *reinterpret_cast<const f32x4*>(dec + 16 * W + 4 * g);
+          const f32x4 sl = *reinterpret_cast<const f32x4*>(dec + C + 16 * W + 4 * g);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float x = p[i][j] * __builtin_amdgcn_exp2f((ch - sh[j]) + (cl - sl[j]));
-            p[i][j] = i < wave || 4 * g + j <= r ? x : 0.f;
+            const float x = p[W][j] * __builtin_amdgcn_exp2f((ch - sh[j]) + (cl - sl[j]));
+            p[W][j] = 4 * g + j <= r ? x : 0.f;
           }
         }
-      }
-      // O^T += Z^T P^T
+        const float gam = dec[2 * C + t];
 #pragma unroll
-      for (int kb = 0; kb < KBC; ++kb) {
-        if (kb * S::KB <= 16 * wave) {
+        for (int d = 0; d < NDV; ++d) oacc[d] = (oacc[d] + olo[d]) * gam;
+        // O^T += Z^T P^T
+#pragma unroll
+        for (int kb = 0; kb < NPB; ++kb) {
           Frag ph, pl;
           if constexpr (BF) frags_from_acc_bf16_split(p[2 * kb], p[2 * kb + 1], ph, pl);
           else ph = frag_from_acc_f32(p[kb]);
 #pragma unroll
           for (int d = 0; d < NDV; ++d) {
-            const Frag zf = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
-            if constexpr (BF) oacc[d] = mma<T>(oacc[d], zf, pl);
-            oacc[d] = mma<T>(oacc[d], zf, ph);
+            if constexpr (BF) oacc[d] = mma<T>(oacc[d], zf[kb][d], pl);
+            oacc[d] = mma<T>(oacc[d], zf[kb][d], ph);
           }
         }
+        // this lane holds four consecutive columns of row t
+        const int row = first + dir * (C * c + t);
+#pragma unroll
+        for (int d = 0; d < NDV; ++d) {
+          const int col = slice * DS + 16 * d + 4 * g;
+          if (A.out_f32) store4<float>(outr, (row * A.d2 + col) * 4, oacc[d]);
+          else store4<T>(outr, (row * A.d2 + col) * E, oacc[d]);
+        }
+        if (A.dot) {   // this slice's part of w_t . out_t
+          float x = 0.f;
+#pragma unroll
+          for (int d = 0; d < NDV; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float w;
+              if constexpr (BF) w = (j & 1) ? bf16_hi_half(wv[d][j >> 1]) : bf16_lo_half(wv[d][j >> 1]);
+              else w = __uint_as_float(wv[d][j]);
+              x = __builtin_fmaf(w, oacc[d][j], x);
+            }
+          x += __shfl_xor(x, 16, 64);
+          x += __shfl_xor(x, 32, 64);
+          if (g == 0 && (unsigned)row < (unsigned)len)
+            A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
+        }
+#pragma unroll
+        for (int kb = 0; kb < KBN; ++kb) xf[kb] = xn[kb];
+#pragma unroll
+        for (int d = 0; d < NDV; ++d) wv[d] = wn[d];
+        lds_barrier();
       }
-      // this lane holds four consecutive columns of row t
-      const int row = first + dir * (C * c + t);
-#pragma unroll
-      for (int d = 0; d < NDV; ++d) {
-        const int col = slice * DS + 16 * d + 4 * g;
-        if (A.out_f32) store4<float>(outr, (row * A.d2 + col) * 4, oacc[d]);
-        else store4<T>(outr, (row * A.d2 + col) * E, oacc[d]);
-      }
-      if (A.dot) {   // this slice's part of w_t . out_t
-        float x = 0.f;
-#pragma unroll
-        for (int d = 0; d < NDV; ++d)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float w;
-            if constexpr (BF) w = (j & 1) ? bf16_hi_half(wv[d][j >> 1]) : bf16_lo_half(wv[d][j >> 1]);
-            else w = __uint_as_float(wv[d][j]);
-            x = __builtin_fmaf(w, oacc[d][j], x);
-          }
-        x += __shfl_xor(x, 16, 64);
-        x += __shfl_xor(x, 32, 64);
-        if (g == 0 && (unsigned)row < (unsigned)len)
-          A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
-      }
-#pragma unroll
-      for (int kb = 0; kb < KBN; ++kb) xf[kb] = xn[kb];
-#pragma unroll
-      for (int d = 0; d < NDV; ++d) wv[d] = wn[d];
-      lds_barrier();
+    };
+    switch (wave) {
+      case 0: run(std::integral_constant<int, 0>{}); break;
+      case 1: run(std::integral_constant<int, 1>{}); break;
+      case 2: run(std::integral_constant<int, 2>{}); break;
+      default: run(std::integral_constant<int, 3>{}); break;
     }
   } else {
     // ============================================================ state waves
@@ -313,12 +360,17 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
     const int dvt = sw % NDV, rt0 = (sw / NDV) * TPW;   // column tile, first row tile
     const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared, D1, E);
     const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared, A.d2, E);
-    const T* gp = (const T*)L.g;
-    const float g_head = L.head_decay ? load_elem(gp + bh % L.heads) : 0.f;
-    gp += (size_t)bh * L.rows;
+    const T* gp = (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
+    const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
     Frag yv[S::NY], zv[S::NZ];
-    float gv = 0.f;
+    T gv = from_f32<T>(0.f);   // as stored: widened when placed, so that loading does not wait
     auto load = [&](int c) __attribute__((always_inline)) {
+      {   // the decay of the chunk's row `lane`: reversed row j carries that of the row after it
+        const int j = row0 + C * c + lane, at = A.reverse ? len - j : j;
+        const int off = j < len && at < len ? (L.head_decay ? 0 : at * E) : 0x7FFFFFF0;   // out of range: 0
+        if constexpr (BF) gv.bits = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
+        else gv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
+      }
 #pragma unroll
       for (int j = 0; j < S::NY; ++j) {
         const int p = ct + 256 * j;
@@ -330,12 +382,6 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         const int p = ct + 256 * j;
         const int row = first + dir * (C * c + p / S::ZPR);
         zv[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, (row * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
-      }
-      if (sw == 0) {   // the decay of the chunk's row `lane`
-        const int j = row0 + C * c + lane;
-        const int at = A.reverse ? len - j : j;   // reversed row j carries the decay of the row after it
-        const bool live = j < len && at < len;
-        gv = !live ? 0.f : L.head_decay ? g_head : load_elem(gp + at);
       }
     };
     auto place = [&](int c) __attribute__((always_inline)) {
@@ -352,7 +398,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
           store_frag(set + Z_OFF + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), zv[j]);
       }
       if (sw == 0) {
-        float x = gv * kLog2E;
+        float x = to_f32(gv) * kLog2E;
         x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
         const float whole = rintf(x * 64.f) * (1.f / 64.f);
         const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
@@ -363,6 +409,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         dec[C + lane] = cl;
         dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
         dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
+        dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
       }
     };
     // the state slice: lane (g, r) holds rows 4 g .. 4 g + 3 of column r of each of its tiles
@@ -405,6 +452,9 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         }
       }
     };
+    // Loads, copies to LDS and state writes run on past the last chunk (the
+    // last one again, into sets nobody reads): a conditional load would make
+    // every wait for an older one wait for all loads in flight.
     load(0);
     if constexpr (S::D1P != D1) {
       // half K blocks: the columns behind D1 are zero for good
@@ -420,52 +470,56 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
     }
     place(0);
     put_state(0);
-    if (nch > 1) load(1);
+    load(min(1, last));
     lds_barrier();
     float decay = 1.f;   // product of the chunks' decays
     for (int c = 0; c < nch; ++c) {
       const unsigned char* set = set_of(c);
       const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
-      if (c + 1 < nch) place(c + 1);
-      if (c + 2 < nch) load(c + 2);
-      // B operand: G(C, s) z_s for this wave's column tile
-      Frag zh[KBC], zm[BF ? KBC : 1], zl[BF ? KBC : 1];
+      place(c + 1);
+      load(min(c + 2, last));
+      // A operand: the columns of Y this wave's row tiles are; B operand:
+      // G(C, s) z_s for its column tile
+      Frag zf[KBC], yf[KBC][TPW];
+#pragma unroll
+      for (int kb = 0; kb < KBC; ++kb) zf[kb] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * dvt, kb, g, r);
+#pragma unroll
+      for (int kb = 0; kb < KBC; ++kb)
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) yf[kb][i] = col_frag<T, S::YROW>(set, 16 * min(rt0 + i, S::RH - 1), kb, g, r);
+      const float end = dec[2 * C + C - 1];
+      decay *= end;
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) h[i] *= end;
 #pragma unroll
       for (int kb = 0; kb < KBC; ++kb) {
-        const Frag zf = col_frag<T, S::ZROW>(set + Z_OFF, 16 * dvt, kb, g, r);
+        Frag zh, zm, zl;
         if constexpr (BF) {
           const f32x4 e0 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 32 * kb + 4 * g);
           const f32x4 e1 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 32 * kb + 16 + 4 * g);
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float x = (e & 1) ? bf16_hi_half(zf.w[e >> 1]) : bf16_lo_half(zf.w[e >> 1]);
+            const float x = (e & 1) ? bf16_hi_half(zf[kb].w[e >> 1]) : bf16_lo_half(zf[kb].w[e >> 1]);
             v[e] = x * (e < 4 ? e0[e & 3] : e1[e & 3]);
           }
-          split3_bf16(v, zh[kb], zm[kb], zl[kb]);
+          split3_bf16(v, zh, zm, zl);
         } else {
           const f32x4 e0 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 16 * kb + 4 * g);
-          zh[kb] = frag_from_acc_f32(__builtin_bit_cast(f32x4, zf.w) * e0);
+          zh = frag_from_acc_f32(__builtin_bit_cast(f32x4, zf[kb].w) * e0);
         }
-      }
-      const float end = dec[2 * C + C - 1];
-      decay *= end;
+        if constexpr (BF && EXACT) {
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        if (!own(i)) continue;
-        f32x4 acc = h[i] * end;
-#pragma unroll
-        for (int kb = 0; kb < KBC; ++kb) {
-          const Frag yf = col_frag<T, S::YROW>(set, 16 * (rt0 + i), kb, g, r);
-          if constexpr (BF) {
-            if (A.exact_state) acc = mma<T>(acc, yf, zl[kb]);
-            acc = mma<T>(acc, yf, zm[kb]);
-          }
-          acc = mma<T>(acc, yf, zh[kb]);
+          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zl);
         }
-        h[i] = acc;
+        if constexpr (BF) {
+#pragma unroll
+          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zm);
+        }
+#pragma unroll
+        for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zh);
       }
-      if (c + 1 < nch) put_state(c + 1);
+      put_state(c + 1);
       lds_barrier();
     }
     // the final state (of the last segment), or this segment's own state
@@ -474,7 +528,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
       // dh0 = a_1 R_1: the first row's own decay, which a reversed sweep has not applied
       float scale = 1.f;
       if (A.reverse && len > 0 && OUT) {
-        const float x = (L.head_decay ? g_head : load_elem(gp)) * kLog2E;
+        const float x = to_f32(*gp) * kLog2E;
         scale = __builtin_amdgcn_exp2f(x < kDecayFloor ? kDecayFloor : x);
       }
 #pragma unroll
@@ -510,19 +564,25 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(float* states, const 
   }
 }
 
-template <typename T, int D1, int DS, bool OUT>
+template <typename T, int D1, int DS, bool OUT, bool EXACT>
 hipError_t launch_sweep_t(const SweepLaunch& L, hipStream_t stream) {
   const long long wgs = (long long)L.units * L.parts;
   if (wgs == 0) return hipSuccess;
-  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, OUT>), dim3((unsigned)wgs), dim3(OUT ? 512 : 256), 0, stream, L);
+  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, OUT, EXACT>), dim3((unsigned)wgs), dim3(OUT ? 512 : 256), 0, stream, L);
   return hipGetLastError();
+}
+
+template <typename T, int D1, int DS>
+hipError_t launch_sweep_o(const SweepLaunch& L, bool out, hipStream_t stream) {
+  if (!out) return launch_sweep_t<T, D1, DS, false, true>(L, stream);
+  // (fp32 products have one term: one instantiation)
+  return L.exact_state || sizeof(T) == 4 ? launch_sweep_t<T, D1, DS, true, true>(L, stream)
+                                         : launch_sweep_t<T, D1, DS, true, sizeof(T) == 4>(L, stream);
 }
 
 template <typename T, int D1>
 hipError_t launch_sweep_d(const SweepLaunch& L, int ds, bool out, hipStream_t stream) {
-  if (ds == 32)
-    return out ? launch_sweep_t<T, D1, 32, true>(L, stream) : launch_sweep_t<T, D1, 32, false>(L, stream);
-  return out ? launch_sweep_t<T, D1, 16, true>(L, stream) : launch_sweep_t<T, D1, 16, false>(L, stream);
+  return ds == 32 ? launch_sweep_o<T, D1, 32>(L, out, stream) : launch_sweep_o<T, D1, 16>(L, out, stream);
 }
 
 template <typename T>
@@ -819,7 +879,6 @@ static hipError_t segment_starts(const LinAttnArgs& a, bool reverse, int seg_row
   R.y_shared = 1;
   R.z = reverse ? a.dout : a.v;
   R.reverse = reverse;
-  R.exact_state = 1;
   R.d2 = a.dv;
   R.seg_out = states;
   R.seg_decay = decay;
@@ -856,7 +915,7 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
   R.init = a.h0;
   R.fin = a.hT;
   R.seg_states = states;
-  R.exact_state = a.hT != nullptr;
+  L.exact_state = a.hT != nullptr;
   R.parts = L.parts = p.nseg * L.group * (a.dv / ds);
   return launch_sweep(L, a.dtype, a.dk, ds, true, a.stream);
 }
@@ -947,7 +1006,6 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dv.out = a.dv_out;
   dv.init = a.dhT;
   dv.fin = a.dh0;
-  dv.exact_state = a.dh0 != nullptr;
   dv.seg_states = rstates;
   dk.x = a.v;
   dk.y = a.dout;
@@ -968,12 +1026,12 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dq.dot = (float*)(ws + p.dotq);
   dq.init = a.h0;
   dq.fin = a.dhT ? (float*)(ws + p.hT) : nullptr;   // <dhT, H_T> of the decay gradient
-  dq.exact_state = a.dhT != nullptr;
   dq.seg_states = states;
   SweepLaunch L = sweep_base(a);
   L.seg_rows = p.seg_rows;
   L.nseg = p.nseg;
   L.seg_stride = (long long)a.B * a.H * a.dk * a.dv;
+  L.exact_state = a.dh0 || a.dhT;
   const int per = p.nseg * L.group;
   dv.parts = per * (a.dv / dsv);
   dk.parts = dq.parts = per * (a.dk / dsk);
