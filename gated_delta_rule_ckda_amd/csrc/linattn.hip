@@ -155,10 +155,10 @@ __device__ __forceinline__ void split3_bf16(const float* v, Frag& fh, Frag& fm, 
   }
 }
 
-// OUT: with output waves (512 threads); without, only the states (256).
+// OUT: with output waves (768 threads); without, only the states (512).
 // EXACT: states with three bf16 terms (one is returned), else two.
 template <typename T, int D1, int DS, bool OUT, bool EXACT>
-__global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
+__global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
   using S = SweepCfg<T, D1, DS>;
   constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TPW = S::TPW;
   constexpr bool BF = S::BF;
@@ -202,6 +202,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
   auto rows_rsrc = [&](const void* p, int shared, int width, int es) __attribute__((always_inline)) {
     return make_rsrc((const unsigned char*)p + head(shared) * L.rows * width * es, (uint32_t)(len * width * es));
   };
+  // this head's log decays
+  const T* gp = (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
   auto set_of = [&](int c) __attribute__((always_inline)) { return lds + (c & 1) * (OUT ? S::SET_H : S::SET); };
   constexpr int Z_OFF = S::Y_BYTES, DEC_OFF = Z_OFF + S::Z_BYTES, H_OFF = DEC_OFF + S::DEC_BYTES;
 
@@ -212,8 +214,8 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
     const __amdgpu_buffer_rsrc_t outr = rows_rsrc(A.out, 0, A.d2, oes);
     const __amdgpu_buffer_rsrc_t wr = rows_rsrc(A.w, A.w_shared, A.d2, A.w ? E : 0);
     const int t = 16 * wave + r;      // this lane's row of the chunk
-    Frag xf[KBN], xn[KBN];
-    u32x4 wv[NDV], wn[NDV];           // four elements each
+    Frag x0[KBN], x1[KBN];            // this chunk's rows and the next one's
+    u32x4 w0[NDV], w1[NDV];           // four elements each
     auto load_x = [&](int c, Frag* d, u32x4* w) __attribute__((always_inline)) {
       const int row = first + dir * (C * c + t);
 #pragma unroll
@@ -234,7 +236,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         }
       }
     };
-    load_x(0, xf, wv);
+    load_x(0, x0, w0);
     lds_barrier();   // set 0 is filled
     // One copy of the loop per wave: W, the wave's row tile, fixes how many
     // tiles of P it has, so the body is straight-line code.
@@ -242,15 +244,16 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
       constexpr int W = decltype(wconst)::value;
       constexpr int NPB = (16 * W) / S::KB + 1;      // K blocks of P^T it multiplies
       constexpr int NF = S::HSETS * NDV + W + 1;     // operand fragments per K block of D1
-      for (int c = 0; c < nch; ++c) {
+      auto chunk = [&](int c, Frag* xf, u32x4* wv, Frag* xn, u32x4* wn) __attribute__((always_inline)) {
         const unsigned char* set = set_of(c);
         const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
         load_x(min(c + 1, last), xn, wn);
         // H^T X^T and the tiles of Y X^T up to this wave's own, one K block's
         // fragments read ahead of the products
-        Frag f[2][NF];
+        constexpr int AHEAD = BF ? 1 : 0;   // (fp32 fragments are twice as many: none, for the registers)
+        Frag f[AHEAD + 1][NF];
         auto read = [&](int kb) __attribute__((always_inline)) {
-          Frag* d = f[kb & 1];
+          Frag* d = f[kb & AHEAD];
 #pragma unroll
           for (int i = 0; i < S::HSETS * NDV; ++i)
             d[i] = row_frag<S::YROW>(set + H_OFF + (i / NDV) * S::H_BYTES, 16 * (i % NDV), kb, g, r);
@@ -262,12 +265,12 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         for (int d = 0; d < NDV; ++d) oacc[d] = olo[d] = zero4();
 #pragma unroll
         for (int i = 0; i < RT; ++i) p[i] = zero4();
-        read(0);
+        if constexpr (AHEAD) read(0);
 #pragma unroll
         for (int kb = 0; kb < KBN; ++kb) {
-          if (kb + 1 < KBN) read(kb + 1);
+          if (kb + AHEAD < KBN) read(kb + AHEAD);
           __builtin_amdgcn_sched_barrier(0);
-          const Frag* d = f[kb & 1];
+          const Frag* d = f[kb & AHEAD];
 #pragma unroll
           for (int i = 0; i < NDV; ++i) oacc[i] = mma<T>(oacc[i], d[i], xf[kb]);
           if constexpr (BF) {
@@ -341,11 +344,12 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
           if (g == 0 && (unsigned)row < (unsigned)len)
             A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
         }
-#pragma unroll
-        for (int kb = 0; kb < KBN; ++kb) xf[kb] = xn[kb];
-#pragma unroll
-        for (int d = 0; d < NDV; ++d) wv[d] = wn[d];
         lds_barrier();
+      };
+      for (int c = 0; c < nch; c += 2) {
+        chunk(c, x0, w0, x1, w1);
+        if (c + 1 >= nch) break;
+        chunk(c + 1, x1, w1, x0, w0);
       }
     };
     switch (wave) {
@@ -354,64 +358,10 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
       case 2: run(std::integral_constant<int, 2>{}); break;
       default: run(std::integral_constant<int, 3>{}); break;
     }
-  } else {
+  } else if (wave < (OUT ? 8 : 4)) {
     // ============================================================ state waves
-    const int sw = wave - (OUT ? 4 : 0), ct = tid - (OUT ? 256 : 0);
+    const int sw = wave - (OUT ? 4 : 0);
     const int dvt = sw % NDV, rt0 = (sw / NDV) * TPW;   // column tile, first row tile
-    const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared, D1, E);
-    const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared, A.d2, E);
-    const T* gp = (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
-    const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
-    Frag yv[S::NY], zv[S::NZ];
-    T gv = from_f32<T>(0.f);   // as stored: widened when placed, so that loading does not wait
-    auto load = [&](int c) __attribute__((always_inline)) {
-      {   // the decay of the chunk's row `lane`: reversed row j carries that of the row after it
-        const int j = row0 + C * c + lane, at = A.reverse ? len - j : j;
-        const int off = j < len && at < len ? (L.head_decay ? 0 : at * E) : 0x7FFFFFF0;   // out of range: 0
-        if constexpr (BF) gv.bits = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
-        else gv = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
-      }
-#pragma unroll
-      for (int j = 0; j < S::NY; ++j) {
-        const int p = ct + 256 * j;
-        const int row = first + dir * (C * c + p / S::YPR);
-        yv[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, row * D1 * E + (p % S::YPR) * 16, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < S::NZ; ++j) {
-        const int p = ct + 256 * j;
-        const int row = first + dir * (C * c + p / S::ZPR);
-        zv[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, (row * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
-      }
-    };
-    auto place = [&](int c) __attribute__((always_inline)) {
-      unsigned char* set = set_of(c);
-#pragma unroll
-      for (int j = 0; j < S::NY; ++j) {
-        const int p = ct + 256 * j;
-        if (C * S::YPR % 256 == 0 || p < C * S::YPR) store_frag(set + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), yv[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < S::NZ; ++j) {
-        const int p = ct + 256 * j;
-        if (C * S::ZPR % 256 == 0 || p < C * S::ZPR)
-          store_frag(set + Z_OFF + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), zv[j]);
-      }
-      if (sw == 0) {
-        float x = to_f32(gv) * kLog2E;
-        x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
-        const float whole = rintf(x * 64.f) * (1.f / 64.f);
-        const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
-        const float th = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ch), 63));
-        const float tl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cl), 63));
-        float* dec = reinterpret_cast<float*>(set + DEC_OFF);
-        dec[lane] = ch;
-        dec[C + lane] = cl;
-        dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
-        dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
-        dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
-      }
-    };
     // the state slice: lane (g, r) holds rows 4 g .. 4 g + 3 of column r of each of its tiles
     f32x4 h[TPW];
     const size_t sbase = (size_t)bh * D1 * A.d2;
@@ -452,32 +402,12 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         }
       }
     };
-    // Loads, copies to LDS and state writes run on past the last chunk (the
-    // last one again, into sets nobody reads): a conditional load would make
-    // every wait for an older one wait for all loads in flight.
-    load(0);
-    if constexpr (S::D1P != D1) {
-      // half K blocks: the columns behind D1 are zero for good
-      for (int p = ct; p < 2 * C * 2; p += 256) {
-        unsigned char* set = set_of(p & 1);
-        const int row = (p >> 1) >> 1, piece = 2 + ((p >> 1) & 1);
-        store_frag(set + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-        if (OUT && row < DS) {
-          store_frag(set + H_OFF + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-          store_frag(set + H_OFF + S::H_BYTES + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-        }
-      }
-    }
-    place(0);
     put_state(0);
-    load(min(1, last));
-    lds_barrier();
+    lds_barrier();   // set 0 is filled
     float decay = 1.f;   // product of the chunks' decays
     for (int c = 0; c < nch; ++c) {
       const unsigned char* set = set_of(c);
       const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
-      place(c + 1);
-      load(min(c + 2, last));
       // A operand: the columns of Y this wave's row tiles are; B operand:
       // G(C, s) z_s for its column tile
       Frag zf[KBC], yf[KBC][TPW];
@@ -538,7 +468,97 @@ __global__ __launch_bounds__(OUT ? 512 : 256) void sweep_kernel(SweepLaunch L) {
         for (int j = 0; j < 4; ++j) fin[sbase + state_at(i, j)] = h[i][j] * scale;
       }
     }
-    if (!OUT && slice == 0 && ct == 0) A.seg_decay[(size_t)seg * L.units * L.group + bh] = decay;
+    if (!OUT && slice == 0 && sw == 0 && lane == 0) A.seg_decay[(size_t)seg * L.units * L.group + bh] = decay;
+  } else {
+    // ============================================================ copy waves
+    const int cw = wave - (OUT ? 8 : 4), ct = tid - (OUT ? 512 : 256);
+    const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared, D1, E);
+    const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared, A.d2, E);
+    const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
+    struct Regs {
+      Frag y[S::NY], z[S::NZ];
+      T g;   // as stored: widened when placed, so that loading does not wait
+    };
+    auto load = [&](Regs& d, int c) __attribute__((always_inline)) {
+      {   // the decay of the chunk's row `lane`: reversed row j carries that of the row after it
+        const int j = row0 + C * c + lane, at = A.reverse ? len - j : j;
+        const int off = j < len && at < len ? (L.head_decay ? 0 : at * E) : 0x7FFFFFF0;   // out of range: 0
+        if constexpr (BF) d.g.bits = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
+        else d.g = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
+      }
+#pragma unroll
+      for (int j = 0; j < S::NY; ++j) {
+        const int p = ct + 256 * j;
+        const int row = first + dir * (C * c + p / S::YPR);
+        d.y[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, row * D1 * E + (p % S::YPR) * 16, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < S::NZ; ++j) {
+        const int p = ct + 256 * j;
+        const int row = first + dir * (C * c + p / S::ZPR);
+        d.z[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, (row * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
+      }
+    };
+    auto place = [&](const Regs& d, int c) __attribute__((always_inline)) {
+      unsigned char* set = set_of(c);
+      if (cw == 0) {
+        float x = to_f32(d.g) * kLog2E;
+        x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
+        const float whole = rintf(x * 64.f) * (1.f / 64.f);
+        const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
+        const float th = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ch), 63));
+        const float tl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cl), 63));
+        float* dec = reinterpret_cast<float*>(set + DEC_OFF);
+        dec[lane] = ch;
+        dec[C + lane] = cl;
+        dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
+        dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
+        dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
+      }
+#pragma unroll
+      for (int j = 0; j < S::NY; ++j) {
+        const int p = ct + 256 * j;
+        if (C * S::YPR % 256 == 0 || p < C * S::YPR)
+          store_frag(set + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), d.y[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < S::NZ; ++j) {
+        const int p = ct + 256 * j;
+        if (C * S::ZPR % 256 == 0 || p < C * S::ZPR)
+          store_frag(set + Z_OFF + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), d.z[j]);
+      }
+    };
+    if constexpr (S::D1P != D1) {
+      // half K blocks: the columns behind D1 are zero for good
+      for (int p = ct; p < 2 * C * 2; p += 256) {
+        unsigned char* set = set_of(p & 1);
+        const int row = (p >> 1) >> 1, piece = 2 + ((p >> 1) & 1);
+        store_frag(set + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+        if (OUT && row < DS) {
+          store_frag(set + H_OFF + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+          store_frag(set + H_OFF + S::H_BYTES + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+        }
+      }
+    }
+    // Chunk x is loaded into register set x % 2 two iterations before it is
+    // placed.  Loads and copies run on past the last chunk (the last one again,
+    // into sets nobody reads): a conditional load would make every wait for an
+    // older one wait for all loads in flight.
+    Regs r0, r1;
+    load(r0, 0);
+    load(r1, min(1, last));
+    place(r0, 0);
+    load(r0, min(2, last));
+    lds_barrier();   // set 0 is filled
+    for (int c = 0; c < nch; c += 2) {
+      place(r1, c + 1);
+      load(r1, min(c + 3, last));
+      lds_barrier();
+      if (c + 1 >= nch) break;
+      place(r0, c + 2);
+      load(r0, min(c + 4, last));
+      lds_barrier();
+    }
   }
 }
 
@@ -568,7 +588,7 @@ template <typename T, int D1, int DS, bool OUT, bool EXACT>
 hipError_t launch_sweep_t(const SweepLaunch& L, hipStream_t stream) {
   const long long wgs = (long long)L.units * L.parts;
   if (wgs == 0) return hipSuccess;
-  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, OUT, EXACT>), dim3((unsigned)wgs), dim3(OUT ? 512 : 256), 0, stream, L);
+  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, OUT, EXACT>), dim3((unsigned)wgs), dim3(OUT ? 768 : 512), 0, stream, L);
   return hipGetLastError();
 }
 
