@@ -27,7 +27,9 @@
 //                  in fp32 on the accumulators, which are then, in the K order
 //                  of ckda_device.hpp, the B operand of Z^T P^T; exp(c_t)
 //                  scales the accumulators of H^T X^T (a factor of the column);
-//   state waves:   H <- exp(c_C) H + Y^T (G(C, .) Z), then the new H^T to LDS.
+//   state waves:   H <- exp(c_C) H + Y^T (G(C, .) Z), then the new H^T to LDS;
+//   copy waves:    Y, Z and the terms of G(C, .) Z of the next chunk, the decay
+//                  factors of the one after it.
 // Precision: the inputs are exact in bf16; every factor that is not (P, H and
 // the scaled Z) is carried as a sum of bf16 terms: two (16 bits) where the
 // product ends in a rounded output, three (24 bits) for the state itself,
@@ -47,7 +49,7 @@ namespace {
 constexpr int C = kLaChunk;    // rows of a chunk
 constexpr int RT = C / 16;     // row tiles
 
-template <typename T, int D1, int DS>
+template <typename T, int D1, int DS, bool OUT, bool EXACT>
 struct SweepCfg {
   static constexpr int E = (int)sizeof(T);
   static constexpr bool BF = E == 2;
@@ -62,10 +64,14 @@ struct SweepCfg {
   static constexpr int WPC = 4 / NDV;                // waves on one column tile
   static constexpr int TPW = (RH + WPC - 1) / WPC;   // row tiles per wave
   static constexpr int Y_BYTES = C * YROW, Z_BYTES = C * ZROW, H_BYTES = DS * YROW;
-  static constexpr int HSETS = BF ? 2 : 1;           // hi and lo
-  static constexpr int DEC_BYTES = 5 * C * 4;        // c (whole), c (rest), exp(c_t), G(C, t), G(tile end, t)
-  static constexpr int SET = Y_BYTES + Z_BYTES + DEC_BYTES;
-  static constexpr int SET_H = SET + HSETS * H_BYTES;
+  static constexpr int HSETS = BF ? 2 : 1;           // terms of H: hi and lo
+  static constexpr int ZSETS = BF ? (EXACT ? 3 : 2) : 1;   // terms of the scaled Z
+  // one of two operand sets: Y, Z, the terms of G(C, .) Z, the terms of H^T
+  static constexpr int Z_OFF = Y_BYTES, ZS_OFF = Z_OFF + Z_BYTES, H_OFF = ZS_OFF + ZSETS * Z_BYTES;
+  static constexpr int SET = H_OFF + (OUT ? HSETS * H_BYTES : 0);
+  // one of four sets of decay factors: c (whole), c (rest), exp(c_t), G(C, t), G(tile end, t)
+  static constexpr int DEC_BYTES = 5 * C * 4, DEC_OFF = 2 * SET;
+  static constexpr int LDS_BYTES = DEC_OFF + 4 * DEC_BYTES;
   // pieces of 16 bytes that the 256 threads of the state waves copy
   static constexpr int YPR = D1 * E / 16, ZPR = ZROW / 16;
   static constexpr int NY = (C * YPR + 255) / 256, NZ = (C * ZPR + 255) / 256;
@@ -84,6 +90,15 @@ __device__ __forceinline__ int lds_piece(int row, int piece) {
   const int i = row / (16 / NCH);
   const int s = (i & (NCH / 2 - 1)) << 1;
   return row * ROWB + ((piece ^ s) << 4);
+}
+
+// The same for the H^T arrays, which are read as rows like Y but written in
+// 8-byte halves of one piece of 16 rows: with 256-byte rows these then fall on
+// different banks too.
+template <int ROWB>
+__device__ __forceinline__ int state_piece(int row, int piece) {
+  if constexpr (ROWB == 256) return row * ROWB + ((piece ^ ((row & 15) ^ (((row >> 2) ^ (row >> 3)) & 1))) << 4);
+  else return lds_piece<ROWB>(row, piece);
 }
 
 // rows row0 + r, K block kb along the row
@@ -159,10 +174,10 @@ __device__ __forceinline__ void split3_bf16(const float* v, Frag& fh, Frag& fm, 
 // EXACT: states with three bf16 terms (one is returned), else two.
 template <typename T, int D1, int DS, bool OUT, bool EXACT>
 __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
-  using S = SweepCfg<T, D1, DS>;
+  using S = SweepCfg<T, D1, DS, OUT, EXACT>;
   constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TPW = S::TPW;
   constexpr bool BF = S::BF;
-  __shared__ __attribute__((aligned(16))) unsigned char lds[2 * (OUT ? S::SET_H : S::SET)];
+  __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS_BYTES];
 
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int g = lane / 16, r = lane % 16;
@@ -204,8 +219,11 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
   };
   // this head's log decays
   const T* gp = (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
-  auto set_of = [&](int c) __attribute__((always_inline)) { return lds + (c & 1) * (OUT ? S::SET_H : S::SET); };
-  constexpr int Z_OFF = S::Y_BYTES, DEC_OFF = Z_OFF + S::Z_BYTES, H_OFF = DEC_OFF + S::DEC_BYTES;
+  auto set_of = [&](int c) __attribute__((always_inline)) { return lds + (c & 1) * S::SET; };
+  auto dec_of = [&](int c) __attribute__((always_inline)) {
+    return reinterpret_cast<float*>(lds + S::DEC_OFF + (c & 3) * S::DEC_BYTES);
+  };
+  constexpr int Z_OFF = S::Z_OFF, ZS_OFF = S::ZS_OFF, H_OFF = S::H_OFF;
 
   if (OUT && wave < 4) {
     // ============================================================ output waves
@@ -237,6 +255,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
       }
     };
     load_x(0, x0, w0);
+    lds_barrier();   // the first decay factors are there
     lds_barrier();   // set 0 is filled
     // One copy of the loop per wave: W, the wave's row tile, fixes how many
     // tiles of P it has, so the body is straight-line code.
@@ -246,7 +265,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
       constexpr int NF = S::HSETS * NDV + W + 1;     // operand fragments per K block of D1
       auto chunk = [&](int c, Frag* xf, u32x4* wv, Frag* xn, u32x4* wn) __attribute__((always_inline)) {
         const unsigned char* set = set_of(c);
-        const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
+        const float* dec = dec_of(c);
         load_x(min(c + 1, last), xn, wn);
         // H^T X^T and the tiles of Y X^T up to this wave's own, one K block's
         // fragments read ahead of the products
@@ -256,7 +275,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
           Frag* d = f[kb & AHEAD];
 #pragma unroll
           for (int i = 0; i < S::HSETS * NDV; ++i)
-            d[i] = row_frag<S::YROW>(set + H_OFF + (i / NDV) * S::H_BYTES, 16 * (i % NDV), kb, g, r);
+            d[i] = load_frag(set + H_OFF + (i / NDV) * S::H_BYTES + state_piece<S::YROW>(16 * (i % NDV) + r, kb * 4 + g));
 #pragma unroll
           for (int i = 0; i <= W; ++i) d[S::HSETS * NDV + i] = row_frag<S::YROW>(set, 16 * i, kb, g, r);
         };
@@ -281,9 +300,9 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
           for (int i = 0; i <= W; ++i) p[i] = mma<T>(p[i], d[S::HSETS * NDV + i], xf[kb]);
           __builtin_amdgcn_sched_barrier(0);
         }
-        Frag zf[NPB][NDV];
+        Frag zf[AHEAD ? NPB : 1][NDV];
 #pragma unroll
-        for (int kb = 0; kb < NPB; ++kb)
+        for (int kb = 0; kb < (AHEAD ? NPB : 0); ++kb)
 #pragma unroll
           for (int d = 0; d < NDV; ++d) zf[kb][d] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
         // P^T = G . (Y X^T).  Below the diagonal G(t, s) is G(t, e) G(e, s)
@@ -316,8 +335,10 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
           else ph = frag_from_acc_f32(p[kb]);
 #pragma unroll
           for (int d = 0; d < NDV; ++d) {
-            if constexpr (BF) oacc[d] = mma<T>(oacc[d], zf[kb][d], pl);
-            oacc[d] = mma<T>(oacc[d], zf[kb][d], ph);
+            if constexpr (!AHEAD) zf[0][d] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
+            const Frag z = zf[AHEAD ? kb : 0][d];
+            if constexpr (BF) oacc[d] = mma<T>(oacc[d], z, pl);
+            oacc[d] = mma<T>(oacc[d], z, ph);
           }
         }
         // this lane holds four consecutive columns of row t
@@ -386,7 +407,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
         for (int i = 0; i < TPW; ++i) {
           if (!own(i)) continue;
           if constexpr (BF) {
-            const int off = lds_piece<S::YROW>(16 * dvt + r, 2 * (rt0 + i) + (g >> 1)) + (g & 1) * 8;
+            const int off = state_piece<S::YROW>(16 * dvt + r, 2 * (rt0 + i) + (g >> 1)) + (g & 1) * 8;
             u32x2 a, b;
             uint32_t ha, la, hb, lb;
             split_pair_bf16(h[i][0], h[i][1], ha, la);
@@ -396,61 +417,46 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
             *reinterpret_cast<u32x2*>(hs + off) = a;
             *reinterpret_cast<u32x2*>(hs + S::H_BYTES + off) = b;
           } else {
-            const int off = lds_piece<S::YROW>(16 * dvt + r, 4 * (rt0 + i) + g);
+            const int off = state_piece<S::YROW>(16 * dvt + r, 4 * (rt0 + i) + g);
             *reinterpret_cast<f32x4*>(hs + off) = h[i];
           }
         }
       }
     };
     put_state(0);
+    lds_barrier();   // the first decay factors are there
     lds_barrier();   // set 0 is filled
     float decay = 1.f;   // product of the chunks' decays
-    for (int c = 0; c < nch; ++c) {
-      const unsigned char* set = set_of(c);
-      const float* dec = reinterpret_cast<const float*>(set + DEC_OFF);
-      // A operand: the columns of Y this wave's row tiles are; B operand:
-      // G(C, s) z_s for its column tile
-      Frag zf[KBC], yf[KBC][TPW];
+    auto chunk = [&](int c, const unsigned char* set) __attribute__((always_inline)) {
+      const float* dec = dec_of(c);
+      // A operand: the columns of Y this wave's row tiles are; B operand: the
+      // terms of G(C, s) z_s for its column tile
+      Frag zf[KBC][S::ZSETS], yf[KBC][TPW];
 #pragma unroll
-      for (int kb = 0; kb < KBC; ++kb) zf[kb] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * dvt, kb, g, r);
-#pragma unroll
-      for (int kb = 0; kb < KBC; ++kb)
+      for (int kb = 0; kb < KBC; ++kb) {
 #pragma unroll
         for (int i = 0; i < TPW; ++i) yf[kb][i] = col_frag<T, S::YROW>(set, 16 * min(rt0 + i, S::RH - 1), kb, g, r);
+#pragma unroll
+        for (int n = 0; n < S::ZSETS; ++n)
+          zf[kb][n] = col_frag<T, S::ZROW>(set + ZS_OFF + n * S::Z_BYTES, 16 * dvt, kb, g, r);
+      }
       const float end = dec[2 * C + C - 1];
       decay *= end;
 #pragma unroll
       for (int i = 0; i < TPW; ++i) h[i] *= end;
 #pragma unroll
-      for (int kb = 0; kb < KBC; ++kb) {
-        Frag zh, zm, zl;
-        if constexpr (BF) {
-          const f32x4 e0 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 32 * kb + 4 * g);
-          const f32x4 e1 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 32 * kb + 16 + 4 * g);
-          float v[8];
+      for (int kb = 0; kb < KBC; ++kb)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float x = (e & 1) ? bf16_hi_half(zf[kb].w[e >> 1]) : bf16_lo_half(zf[kb].w[e >> 1]);
-            v[e] = x * (e < 4 ? e0[e & 3] : e1[e & 3]);
-          }
-          split3_bf16(v, zh, zm, zl);
-        } else {
-          const f32x4 e0 = *reinterpret_cast<const f32x4*>(dec + 3 * C + 16 * kb + 4 * g);
-          zh = frag_from_acc_f32(__builtin_bit_cast(f32x4, zf[kb].w) * e0);
-        }
-        if constexpr (BF && EXACT) {
+        for (int n = S::ZSETS - 1; n >= 0; --n)
 #pragma unroll
-          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zl);
-        }
-        if constexpr (BF) {
-#pragma unroll
-          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zm);
-        }
-#pragma unroll
-        for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zh);
-      }
+          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zf[kb][n]);
       put_state(c + 1);
       lds_barrier();
+    };
+    for (int c = 0; c < nch; c += 2) {
+      chunk(c, set_of(0));
+      if (c + 1 >= nch) break;
+      chunk(c + 1, set_of(1));
     }
     // the final state (of the last segment), or this segment's own state
     float* fin = OUT ? (seg == L.nseg - 1 ? A.fin : nullptr) : A.seg_out + (size_t)seg * L.seg_stride;
@@ -499,8 +505,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
         d.z[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, (row * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
       }
     };
-    auto place = [&](const Regs& d, int c) __attribute__((always_inline)) {
-      unsigned char* set = set_of(c);
+    auto factors = [&](const Regs& d, int c) __attribute__((always_inline)) {
       if (cw == 0) {
         float x = to_f32(d.g) * kLog2E;
         x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
@@ -508,13 +513,17 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
         const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
         const float th = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ch), 63));
         const float tl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cl), 63));
-        float* dec = reinterpret_cast<float*>(set + DEC_OFF);
+        float* dec = dec_of(c);
         dec[lane] = ch;
         dec[C + lane] = cl;
         dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
         dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
         dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
       }
+    };
+    auto place = [&](const Regs& d, int c) __attribute__((always_inline)) {
+      unsigned char* set = set_of(c);
+      const float* dec = dec_of(c);
 #pragma unroll
       for (int j = 0; j < S::NY; ++j) {
         const int p = ct + 256 * j;
@@ -524,8 +533,23 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
 #pragma unroll
       for (int j = 0; j < S::NZ; ++j) {
         const int p = ct + 256 * j;
-        if (C * S::ZPR % 256 == 0 || p < C * S::ZPR)
-          store_frag(set + Z_OFF + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), d.z[j]);
+        if (C * S::ZPR % 256 == 0 || p < C * S::ZPR) {
+          const int off = lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR);
+          store_frag(set + Z_OFF + off, d.z[j]);
+          const float wt = dec[3 * C + p / S::ZPR];   // G(C, row)
+          if constexpr (BF) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] = wt * ((e & 1) ? bf16_hi_half(d.z[j].w[e >> 1]) : bf16_lo_half(d.z[j].w[e >> 1]));
+            Frag t[3];
+            split3_bf16(v, t[0], t[1], t[2]);
+#pragma unroll
+            for (int n = 0; n < S::ZSETS; ++n) store_frag(set + ZS_OFF + n * S::Z_BYTES + off, t[n]);
+          } else {
+            store_frag(set + ZS_OFF + off, frag_from_acc_f32(__builtin_bit_cast(f32x4, d.z[j].w) * wt));
+          }
+        }
       }
     };
     if constexpr (S::D1P != D1) {
@@ -535,8 +559,8 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
         const int row = (p >> 1) >> 1, piece = 2 + ((p >> 1) & 1);
         store_frag(set + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
         if (OUT && row < DS) {
-          store_frag(set + H_OFF + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-          store_frag(set + H_OFF + S::H_BYTES + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+          store_frag(set + H_OFF + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+          store_frag(set + H_OFF + S::H_BYTES + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
         }
       }
     }
@@ -544,18 +568,24 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
     // placed.  Loads and copies run on past the last chunk (the last one again,
     // into sets nobody reads): a conditional load would make every wait for an
     // older one wait for all loads in flight.
+    // The decay factors are a chunk ahead of the copies that use them.
     Regs r0, r1;
     load(r0, 0);
     load(r1, min(1, last));
+    factors(r0, 0);
+    lds_barrier();   // the first decay factors are there
     place(r0, 0);
+    factors(r1, 1);
     load(r0, min(2, last));
     lds_barrier();   // set 0 is filled
     for (int c = 0; c < nch; c += 2) {
       place(r1, c + 1);
+      factors(r0, c + 2);
       load(r1, min(c + 3, last));
       lds_barrier();
       if (c + 1 >= nch) break;
       place(r0, c + 2);
+      factors(r1, c + 3);
       load(r0, min(c + 4, last));
       lds_barrier();
     }
