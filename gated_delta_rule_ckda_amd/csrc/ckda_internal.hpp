@@ -106,8 +106,8 @@ struct SweepRole {
   void* out;
   const float* init;         // first state (or NULL: zero)
   float* fin;                // last state (or NULL)
-  float* seg_states;         // start state of every segment (with more than one)
-  float *seg_out, *seg_decay;   // states-only launches: the segments' own states and decays
+  float* seg_states;         // start state of every sub-segment (with more than one segment)
+  float *seg_out, *seg_decay;   // own-state launches: the sub-segments' own states and decays
   int x_shared, y_shared, z_shared, w_shared;
   int d2;
   int reverse;               // from the last row to the first
@@ -120,12 +120,12 @@ struct SweepLaunch {
   const void* g;
   const int* lens;
   long long seg_stride;      // floats between two segments' states
-  int nroles, units, group, heads, rows, parts, seg_rows, nseg, head_decay;
+  int nroles, units, group, heads, rows, parts, seg_rows, nseg, seg_subs, head_decay;
   int exact_state;           // state products with three bf16 terms (a state is returned), else two
 };
 
-size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv);
-size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv);
+size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
+size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 hipError_t launch_linattn_fwd(const LinAttnArgs& a);
 hipError_t launch_linattn_bwd(const LinAttnArgs& a);
 hipError_t launch_linattn_decode(const LinAttnDecodeArgs& a);

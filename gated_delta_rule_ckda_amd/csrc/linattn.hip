@@ -21,15 +21,18 @@
 // one segment of rows; the columns of the state evolve independently, and the
 // state slice never leaves the workgroup.  Eight waves: four "output waves",
 // each with 16 of the chunk's 64 rows, and four "state waves" that carry the
-// state slice in their accumulators and copy the next chunk's operands into
-// LDS.  Everything is double buffered, one barrier a chunk:
-//   output waves:  S^T = Y X^T tile by tile (rows s, columns t), P^T = G . S^T
-//                  in fp32 on the accumulators, which are then, in the K order
-//                  of ckda_device.hpp, the B operand of Z^T P^T; exp(c_t)
-//                  scales the accumulators of H^T X^T (a factor of the column);
-//   state waves:   H <- exp(c_C) H + Y^T (G(C, .) Z), then the new H^T to LDS;
-//   copy waves:    Y, Z and the terms of G(C, .) Z of the next chunk, the decay
-//                  factors of the one after it.
+// state slice in their accumulators and bring the next chunk's operands into
+// LDS.  A chunk has two phases with a barrier after each:
+//   1  output waves read H, Y and Z from LDS and multiply: S^T = Y X^T tile by
+//      tile (rows s, columns t) and H^T X^T; state waves read the columns of Y
+//      and of G(C, .) Z and form the next chunk's decay factors;
+//   2  output waves: P^T = G . S^T in fp32 on the accumulators, which are then,
+//      in the K order of ckda_device.hpp, the B operand of Z^T P^T; exp(c_t)
+//      scales the accumulators of H^T X^T (a factor of the column); outputs.
+//      State waves: H <- exp(c_C) H + Y^T (G(C, .) Z); the new H^T, and Y, Z
+//      and the terms of G(C, .) Z of the next chunk into the same LDS buffers.
+// One copy of each operand is all it takes in LDS, so two workgroups run on
+// every CU, each in the other's gaps.
 // Precision: the inputs are exact in bf16; every factor that is not (P, H and
 // the scaled Z) is carried as a sum of bf16 terms: two (16 bits) where the
 // product ends in a rounded output, three (24 bits) for the state itself,
@@ -37,6 +40,7 @@
 // matrix cores throughout.
 // Log decays are summed as two parts, whole multiples of 1/64 (whose sums are
 // exact) and the rest, so that differences of large sums keep fp32 accuracy.
+#include <algorithm>
 #include <type_traits>
 
 #include "ckda_device.hpp"
@@ -48,8 +52,11 @@ namespace {
 
 constexpr int C = kLaChunk;    // rows of a chunk
 constexpr int RT = C / 16;     // row tiles
+// decay factors of a chunk's rows: c (whole part), c (rest), exp(c_t), G(C, t),
+// G(e, t) with e the last row of t's tile
+constexpr int kDecSets = 5;
 
-template <typename T, int D1, int DS, bool OUT, bool EXACT>
+template <typename T, int D1, int DS, bool EXACT>
 struct SweepCfg {
   static constexpr int E = (int)sizeof(T);
   static constexpr bool BF = E == 2;
@@ -60,21 +67,19 @@ struct SweepCfg {
   static constexpr int RH = D1 / 16;                 // state row tiles
   static constexpr int NDV = DS / 16;                // state column tiles of the slice
   static constexpr int YROW = D1P * E, ZROW = DS * E;   // bytes of a row in LDS
-  // four state waves: wave w owns column tile w % NDV, row tiles (w / NDV) TPW ..
-  static constexpr int WPC = 4 / NDV;                // waves on one column tile
-  static constexpr int TPW = (RH + WPC - 1) / WPC;   // row tiles per wave
+  // four state waves on WR x WC blocks of TR x TC state tiles
+  static constexpr int WC = RH == 1 ? (NDV < 4 ? NDV : 4) : (NDV == 1 ? 1 : 2), WR = 4 / WC;
+  static constexpr int TR = (RH + WR - 1) / WR, TC = NDV / WC;
   static constexpr int Y_BYTES = C * YROW, Z_BYTES = C * ZROW, H_BYTES = DS * YROW;
   static constexpr int HSETS = BF ? 2 : 1;           // terms of H: hi and lo
   static constexpr int ZSETS = BF ? (EXACT ? 3 : 2) : 1;   // terms of the scaled Z
-  // one of two operand sets: Y, Z, the terms of G(C, .) Z, the terms of H^T
+  // LDS: Y, Z, the terms of G(C, .) Z, the terms of H^T, two sets of decay factors
   static constexpr int Z_OFF = Y_BYTES, ZS_OFF = Z_OFF + Z_BYTES, H_OFF = ZS_OFF + ZSETS * Z_BYTES;
-  static constexpr int SET = H_OFF + (OUT ? HSETS * H_BYTES : 0);
-  // one of four sets of decay factors: c (whole), c (rest), exp(c_t), G(C, t), G(tile end, t)
-  static constexpr int DEC_BYTES = 5 * C * 4, DEC_OFF = 2 * SET;
-  static constexpr int LDS_BYTES = DEC_OFF + 4 * DEC_BYTES;
-  // pieces of 16 bytes that the 256 threads of the state waves copy
+  static constexpr int DEC_OFF = H_OFF + HSETS * H_BYTES, DEC_BYTES = kDecSets * C * 4;
+  static constexpr int LDS_BYTES = DEC_OFF + 2 * DEC_BYTES;
+  // pieces of 16 bytes that the 512 threads copy
   static constexpr int YPR = D1 * E / 16, ZPR = ZROW / 16;
-  static constexpr int NY = (C * YPR + 255) / 256, NZ = (C * ZPR + 255) / 256;
+  static constexpr int NY = (C * YPR + 511) / 512, NZ = (C * ZPR + 511) / 512;
 };
 
 // Byte offset of the 16-byte piece `piece` of row `row` in an LDS array of
@@ -101,35 +106,62 @@ __device__ __forceinline__ int state_piece(int row, int piece) {
   else return lds_piece<ROWB>(row, piece);
 }
 
-// rows row0 + r, K block kb along the row
-template <int ROWB>
-__device__ __forceinline__ Frag row_frag(const unsigned char* m, int row0, int kb, int g, int r) {
-  return load_frag(m + lds_piece<ROWB>(row0 + r, kb * 4 + g));
-}
+// Operand reads.  A lane's address is kept as one offset for each piece or
+// column tile, opaque to the compiler (it would otherwise keep one for every
+// read, as the constants beside it pass the 16-bit offsets of LDS
+// instructions); row tiles, K blocks and terms are constant distances from it.
+// 16-byte pieces of row r of a row tile, K block kb along the row; base: the array's offset
+template <int ROWB, int KBN, bool STATE>
+struct RowFrags {
+  int off[KBN];
+  __device__ __forceinline__ RowFrags(int base, int g, int r) {
+#pragma unroll
+    for (int kb = 0; kb < KBN; ++kb) {
+      off[kb] = base + (STATE ? state_piece<ROWB>(r, kb * 4 + g) : lds_piece<ROWB>(r, kb * 4 + g));
+      asm("" : "+v"(off[kb]));
+    }
+  }
+  __device__ __forceinline__ Frag read(const unsigned char* lds, int tile, int kb, int beyond = 0) const {
+    return load_frag(lds + off[kb] + tile * 16 * ROWB + beyond);
+  }
+};
 
 // column col0 + r, rows of K block kb in the K order kappa
 template <typename T, int ROWB>
-__device__ __forceinline__ Frag col_frag(const unsigned char* m, int col0, int kb, int g, int r) {
-  Frag f;
-  if constexpr (sizeof(T) == 2) {
-    // two transposing reads (ds_read_b64_tr_b16): within 16 lanes, lane i gets
-    // as element j the element i % 4 of the 8 bytes lane 4 j + i / 4 addresses
-    typedef short v4s __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) v4s lds_v4s;
-    const int row = kb * 32 + 4 * g + (r >> 2), piece = col0 / 8 + ((r & 3) >> 1), half = (r & 1) * 8;
-    const u32x2 a = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(m + lds_piece<ROWB>(row, piece) + half)));
-    const u32x2 b = __builtin_bit_cast(
-        u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(m + lds_piece<ROWB>(row + 16, piece) + half)));
-    f.w = u32x4{a[0], a[1], b[0], b[1]};
-  } else {
+struct ColFrags {
+  static constexpr bool BF = sizeof(T) == 2;
+  int off[BF ? 1 : 4];
+  __device__ __forceinline__ void set(int base, int col0, int g, int r) {
+    if constexpr (BF) {
+      // two transposing reads (ds_read_b64_tr_b16): within 16 lanes, lane i gets
+      // as element j the element i % 4 of the 8 bytes lane 4 j + i / 4 addresses
+      off[0] = base + lds_piece<ROWB>(4 * g + (r >> 2), col0 / 8 + ((r & 3) >> 1)) + (r & 1) * 8;
+      asm("" : "+v"(off[0]));
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      f.w[e] = *reinterpret_cast<const uint32_t*>(m + lds_piece<ROWB>(kb * 16 + 4 * g + e, (col0 + r) / 4) +
-                                                  ((col0 + r) % 4) * 4);
+      for (int e = 0; e < 4; ++e) {
+        off[e] = base + lds_piece<ROWB>(4 * g + e, (col0 + r) / 4) + ((col0 + r) % 4) * 4;
+        asm("" : "+v"(off[e]));
+      }
+    }
   }
-  return f;
-}
+  __device__ __forceinline__ Frag read(const unsigned char* lds, int kb, int beyond = 0) const {
+    Frag f;
+    if constexpr (BF) {
+      typedef short v4s __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4s lds_v4s;
+      const unsigned char* p = lds + off[0] + kb * 32 * ROWB + beyond;   // (16 rows on: the same piece order)
+      const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p));
+      const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * ROWB)));
+      f.w = u32x4{a[0], a[1], b[0], b[1]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        f.w[e] = *reinterpret_cast<const uint32_t*>(lds + off[e] + kb * 16 * ROWB + beyond);
+    }
+    return f;
+  }
+};
 
 // inclusive prefix sum over the wave's 64 lanes (DPP row shifts, then the
 // last lane of each row into the rows after it)
@@ -170,150 +202,266 @@ __device__ __forceinline__ void split3_bf16(const float* v, Frag& fh, Frag& fm, 
   }
 }
 
-// OUT: with output waves (768 threads); without, only the states (512).
+// Decay factors of a chunk from the log decays g (one row a lane) into dec.
+__device__ __forceinline__ void decay_factors(float g, float* dec, int lane) {
+  float x = g * kLog2E;
+  x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
+  const float whole = rintf(x * 64.f) * (1.f / 64.f);
+  const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
+  const float th = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ch), 63));
+  const float tl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cl), 63));
+  dec[lane] = ch;
+  dec[C + lane] = cl;
+  dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
+  dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
+  dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
+}
+
+// The rows a workgroup works on: chunk row j of a segment is row row0 + j of
+// the sweep, which is that row of the sequence, or the len - 1 - that one.
+// Rows outside [0, len) fall outside the buffers: they read as zero and are
+// not stored.
+struct Rows {
+  int len, row0, nch, last, dir, first;
+  __device__ __forceinline__ Rows(const SweepLaunch& L, int bh, int seg, int seg_rows, int reverse) {
+    len = L.lens ? min(max(L.lens[bh / L.heads], 0), L.rows) : L.rows;
+    row0 = seg * seg_rows;
+    nch = (min(max(len - row0, 0), seg_rows) + C - 1) / C;
+    last = max(nch - 1, 0);
+    dir = reverse ? -1 : 1;
+    first = reverse ? len - 1 - row0 : row0;
+  }
+  __device__ __forceinline__ int row(int j) const { return first + dir * j; }
+};
+// A head's rows of `width` elements of `es` bytes as a range-checked buffer.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, size_t head, int rows, int len, int width,
+                                                            int es) {
+  return make_rsrc((const unsigned char*)p + head * rows * width * es, (uint32_t)(len * width * es));
+}
+// The log decay of row j of a sweep: reversed row j carries that of the row after it (the first has none).
+template <typename T>
+__device__ __forceinline__ T load_decay(__amdgpu_buffer_rsrc_t gr, const Rows& R, int j, int reverse, int head_decay) {
+  const int at = reverse ? R.len - j : j;
+  const int off = j < R.len && at < R.len ? (head_decay ? 0 : at * (int)sizeof(T)) : 0x7FFFFFF0;   // out of range: 0
+  if constexpr (sizeof(T) == 2) return T{(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0)};
+  else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
+}
+template <typename T>
+__device__ __forceinline__ const T* decays_of(const SweepLaunch& L, int bh) {
+  return (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
+}
+// N terms of wt z for the eight (four) elements of a piece, stored at p, p + stride, ..
+template <typename T, int N>
+__device__ __forceinline__ void store_scaled(unsigned char* p, int stride, Frag z, float wt) {
+  if constexpr (sizeof(T) == 2) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = wt * ((e & 1) ? bf16_hi_half(z.w[e >> 1]) : bf16_lo_half(z.w[e >> 1]));
+    Frag t[3];
+    split3_bf16(v, t[0], t[1], t[2]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) store_frag(p + n * stride, t[n]);
+  } else {
+    store_frag(p, frag_from_acc_f32(__builtin_bit_cast(f32x4, z.w) * wt));
+  }
+}
+// workgroup -> unit (key head of a batch entry) and its part of the unit's
+// work.  A unit's parts get ids equal modulo 8 where the units allow it, so
+// that they share an XCD's L2.
+__device__ __forceinline__ void unit_of(int units, int parts, int& unit, int& part) {
+  const int id = blockIdx.x;
+  if (units % 8 == 0) {
+    unit = (id / 8) / parts * 8 + id % 8;
+    part = (id / 8) % parts;
+  } else {
+    unit = id / parts;
+    part = id % parts;
+  }
+}
+
+// Four consecutive elements of a row, as loaded.
+template <typename T> struct Quad;
+template <> struct Quad<bf16_t> {
+  typedef u32x2 Raw;
+  static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t b, int off) {
+    return __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0);
+  }
+  static __device__ __forceinline__ float get(Raw w, int j) {
+    return (j & 1) ? bf16_hi_half(w[j >> 1]) : bf16_lo_half(w[j >> 1]);
+  }
+};
+template <> struct Quad<float> {
+  typedef u32x4 Raw;
+  static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t b, int off) {
+    return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
+  }
+  static __device__ __forceinline__ float get(Raw w, int j) { return __uint_as_float(w[j]); }
+};
+
 // EXACT: states with three bf16 terms (one is returned), else two.
-template <typename T, int D1, int DS, bool OUT, bool EXACT>
-__global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
-  using S = SweepCfg<T, D1, DS, OUT, EXACT>;
-  constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TPW = S::TPW;
+template <typename T, int D1, int DS, bool EXACT>
+__global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
+  using S = SweepCfg<T, D1, DS, EXACT>;
+  constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TR = S::TR, TC = S::TC;
   constexpr bool BF = S::BF;
   __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS_BYTES];
 
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int g = lane / 16, r = lane % 16;
-
-  // workgroup -> unit (key head of a batch entry) and its part of it: role,
-  // segment, head of the group, slice.  A unit's parts get ids equal modulo 8
-  // where the units allow it, so that they share an XCD's L2.
-  int unit, part;
-  {
-    const int id = blockIdx.x;
-    if (L.units % 8 == 0) {
-      unit = (id / 8) / L.parts * 8 + id % 8;
-      part = (id / 8) % L.parts;
-    } else {
-      unit = id / L.parts;
-      part = id % L.parts;
-    }
-  }
-  int role = 0;
+  int unit, part, role = 0;
+  unit_of(L.units, L.parts, unit, part);
   while (role + 1 < L.nroles && part >= L.role[role].parts) part -= L.role[role++].parts;
   const SweepRole A = L.role[role];
   const int slices = A.d2 / DS;
   const int slice = part % slices;
   const int bh = unit * L.group + (part / slices) % L.group;
   const int seg = part / slices / L.group;
-
-  const int len = L.lens ? min(max(L.lens[bh / L.heads], 0), L.rows) : L.rows;
-  const int row0 = seg * L.seg_rows;
-  const int nrows = min(max(len - row0, 0), L.seg_rows);
-  const int nch = (nrows + C - 1) / C, last = max(nch - 1, 0);
-  // LDS row j of chunk c is row row0 + 64 c + j of the sweep: that row of the
-  // sequence, or the len - 1 - that one.  Rows outside [0, len) fall outside
-  // the buffers below: they read as zero and are not stored.
-  const int dir = A.reverse ? -1 : 1;
-  const int first = A.reverse ? len - 1 - row0 : row0;
-  auto head = [&](int shared) __attribute__((always_inline)) { return (size_t)(shared ? unit : bh); };
-  auto rows_rsrc = [&](const void* p, int shared, int width, int es) __attribute__((always_inline)) {
-    return make_rsrc((const unsigned char*)p + head(shared) * L.rows * width * es, (uint32_t)(len * width * es));
-  };
-  // this head's log decays
-  const T* gp = (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
-  auto set_of = [&](int c) __attribute__((always_inline)) { return lds + (c & 1) * S::SET; };
+  const Rows R(L, bh, seg, L.seg_rows, A.reverse);
+  const int len = R.len, nch = R.nch;
   auto dec_of = [&](int c) __attribute__((always_inline)) {
-    return reinterpret_cast<float*>(lds + S::DEC_OFF + (c & 3) * S::DEC_BYTES);
+    return reinterpret_cast<float*>(lds + S::DEC_OFF + (c & 1) * S::DEC_BYTES);
   };
-  constexpr int Z_OFF = S::Z_OFF, ZS_OFF = S::ZS_OFF, H_OFF = S::H_OFF;
+  unsigned char *ly = lds, *lz = lds + S::Z_OFF, *lzs = lds + S::ZS_OFF, *lh = lds + S::H_OFF;
 
-  if (OUT && wave < 4) {
+  // All waves copy Y, Z and the scaled Z to LDS, a chunk ahead in registers.
+  // Loads and copies run on past the last chunk (the last one again, into
+  // buffers nobody reads): a conditional load would make every wait for an
+  // older one wait for all loads in flight.
+  const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared ? unit : bh, L.rows, len, D1, E);
+  const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared ? unit : bh, L.rows, len, A.d2, E);
+  Frag yv[S::NY], zv[S::NZ];
+  auto load = [&](int c) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < S::NY; ++j) {
+      const int p = tid + 512 * j;
+      yv[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, R.row(C * c + p / S::YPR) * D1 * E + (p % S::YPR) * 16, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) {
+      const int p = tid + 512 * j;
+      zv[j].w = __builtin_amdgcn_raw_buffer_load_b128(
+          zr, (R.row(C * c + p / S::ZPR) * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
+    }
+  };
+  auto place = [&](int c) __attribute__((always_inline)) {
+    const float* dec = dec_of(c);
+#pragma unroll
+    for (int j = 0; j < S::NY; ++j) {
+      const int p = tid + 512 * j;
+      if (C * S::YPR % 512 == 0 || p < C * S::YPR) store_frag(ly + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), yv[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) {
+      const int p = tid + 512 * j;
+      if (C * S::ZPR % 512 == 0 || p < C * S::ZPR) {
+        const int off = lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR);
+        store_frag(lz + off, zv[j]);
+        store_scaled<T, S::ZSETS>(lzs + off, S::Z_BYTES, zv[j], dec[3 * C + p / S::ZPR]);
+      }
+    }
+  };
+  load(0);
+
+  if (wave < 4) {
     // ============================================================ output waves
-    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(A.x, A.x_shared, D1, E);
-    const int oes = A.out_f32 ? 4 : E;
-    const __amdgpu_buffer_rsrc_t outr = rows_rsrc(A.out, 0, A.d2, oes);
-    const __amdgpu_buffer_rsrc_t wr = rows_rsrc(A.w, A.w_shared, A.d2, A.w ? E : 0);
+    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(A.x, A.x_shared ? unit : bh, L.rows, len, D1, E);
+    const __amdgpu_buffer_rsrc_t outr = rows_rsrc(A.out, bh, L.rows, len, A.d2, A.out_f32 ? 4 : E);
+    const __amdgpu_buffer_rsrc_t wr = rows_rsrc(A.w, A.w_shared ? unit : bh, L.rows, len, A.d2, A.w ? E : 0);
     const int t = 16 * wave + r;      // this lane's row of the chunk
-    Frag x0[KBN], x1[KBN];            // this chunk's rows and the next one's
-    u32x4 w0[NDV], w1[NDV];           // four elements each
-    auto load_x = [&](int c, Frag* d, u32x4* w) __attribute__((always_inline)) {
-      const int row = first + dir * (C * c + t);
+    const RowFrags<S::YROW, KBN, false> yrow(0, g, r);
+    const RowFrags<S::YROW, KBN, true> hrow(S::H_OFF, g, r);
+    ColFrags<T, S::ZROW> zcol[NDV];
+#pragma unroll
+    for (int d = 0; d < NDV; ++d) zcol[d].set(S::Z_OFF, 16 * d, g, r);
+    Frag xf[KBN];                     // this lane's row of X
+    auto load_x = [&](int c) __attribute__((always_inline)) {
+      const int row = R.row(C * c + t);
 #pragma unroll
       for (int kb = 0; kb < KBN; ++kb) {
         const int off = row * D1 * E + kb * 64 + g * 16;
-        d[kb].w = __builtin_amdgcn_raw_buffer_load_b128(xr, D1 < S::KB && g * 16 >= D1 * E ? 0x7FFFFFF0 : off, 0, 0);
-      }
-      if (A.w) {
-#pragma unroll
-        for (int d2 = 0; d2 < NDV; ++d2) {
-          const int off = (row * A.d2 + slice * DS + 16 * d2 + 4 * g) * E;
-          if constexpr (BF) {
-            const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(wr, off, 0, 0);
-            w[d2] = u32x4{a[0], a[1], 0, 0};
-          } else {
-            w[d2] = __builtin_amdgcn_raw_buffer_load_b128(wr, off, 0, 0);
-          }
-        }
+        xf[kb].w = __builtin_amdgcn_raw_buffer_load_b128(xr, D1 < S::KB && g * 16 >= D1 * E ? 0x7FFFFFF0 : off, 0, 0);
       }
     };
-    load_x(0, x0, w0);
+    load_x(0);
     lds_barrier();   // the first decay factors are there
-    lds_barrier();   // set 0 is filled
+    place(0);
+    load(min(1, R.last));
+    lds_barrier();   // the first operands are there
     // One copy of the loop per wave: W, the wave's row tile, fixes how many
-    // tiles of P it has, so the body is straight-line code.
-    auto run = [&](auto wconst) __attribute__((always_inline)) {
+    // tiles of P it has, and DOT whether it forms the dots, so that the body is
+    // straight-line code and every wait counts the loads in flight exactly.
+    auto run = [&](auto wconst, auto dotconst) __attribute__((always_inline)) {
       constexpr int W = decltype(wconst)::value;
+      constexpr bool DOT = decltype(dotconst)::value;
       constexpr int NPB = (16 * W) / S::KB + 1;      // K blocks of P^T it multiplies
-      constexpr int NF = S::HSETS * NDV + W + 1;     // operand fragments per K block of D1
-      auto chunk = [&](int c, Frag* xf, u32x4* wv, Frag* xn, u32x4* wn) __attribute__((always_inline)) {
-        const unsigned char* set = set_of(c);
+      for (int c = 0; c < nch; ++c) {
         const float* dec = dec_of(c);
-        load_x(min(c + 1, last), xn, wn);
-        // H^T X^T and the tiles of Y X^T up to this wave's own, one K block's
-        // fragments read ahead of the products
-        constexpr int AHEAD = BF ? 1 : 0;   // (fp32 fragments are twice as many: none, for the registers)
-        Frag f[AHEAD + 1][NF];
-        auto read = [&](int kb) __attribute__((always_inline)) {
-          Frag* d = f[kb & AHEAD];
+        const int row = R.row(C * c + t);
+        typename Quad<T>::Raw wv[NDV];   // four elements of w each
+        if constexpr (DOT) {
 #pragma unroll
-          for (int i = 0; i < S::HSETS * NDV; ++i)
-            d[i] = load_frag(set + H_OFF + (i / NDV) * S::H_BYTES + state_piece<S::YROW>(16 * (i % NDV) + r, kb * 4 + g));
+          for (int d = 0; d < NDV; ++d) wv[d] = Quad<T>::load(wr, (row * A.d2 + slice * DS + 16 * d + 4 * g) * E);
+        }
+        // ---- phase 1: H^T X^T, and the tiles of Y X^T up to this wave's own
+        f32x4 oacc[NDV], p[RT];
 #pragma unroll
-          for (int i = 0; i <= W; ++i) d[S::HSETS * NDV + i] = row_frag<S::YROW>(set, 16 * i, kb, g, r);
-        };
-        f32x4 oacc[NDV], olo[NDV], p[RT];
-#pragma unroll
-        for (int d = 0; d < NDV; ++d) oacc[d] = olo[d] = zero4();
+        for (int d = 0; d < NDV; ++d) oacc[d] = zero4();
 #pragma unroll
         for (int i = 0; i < RT; ++i) p[i] = zero4();
-        if constexpr (AHEAD) read(0);
+        // Operand fragments are read one step ahead of the products that take
+        // them; a step is one K block of up to four state column tiles, or of
+        // the tiles of Y.
+        constexpr int DG = NDV < 4 ? NDV : 4, NG = NDV / DG;
+        constexpr int NF = S::HSETS * DG > W + 1 ? S::HSETS * DG : W + 1;
+        Frag f[2][NF];
+        auto read = [&](int step) __attribute__((always_inline)) {
+          Frag* to = f[step & 1];
+          const int kb = step / (NG + 1), grp = step % (NG + 1);
+          if (grp < NG) {
 #pragma unroll
-        for (int kb = 0; kb < KBN; ++kb) {
-          if (kb + AHEAD < KBN) read(kb + AHEAD);
-          __builtin_amdgcn_sched_barrier(0);
-          const Frag* d = f[kb & AHEAD];
+            for (int i = 0; i < S::HSETS * DG; ++i)
+              to[i] = hrow.read(lds, grp * DG + i % DG, kb, (i / DG) * S::H_BYTES);
+          } else {
 #pragma unroll
-          for (int i = 0; i < NDV; ++i) oacc[i] = mma<T>(oacc[i], d[i], xf[kb]);
-          if constexpr (BF) {
-#pragma unroll
-            for (int i = 0; i < NDV; ++i) olo[i] = mma<T>(olo[i], d[NDV + i], xf[kb]);
+            for (int i = 0; i <= W; ++i) to[i] = yrow.read(lds, i, kb);
           }
+        };
+        read(0);
 #pragma unroll
-          for (int i = 0; i <= W; ++i) p[i] = mma<T>(p[i], d[S::HSETS * NDV + i], xf[kb]);
+        for (int step = 0; step < KBN * (NG + 1); ++step) {
+          if (step + 1 < KBN * (NG + 1)) read(step + 1);
+          __builtin_amdgcn_sched_barrier(0);
+          const Frag* from = f[step & 1];
+          const int kb = step / (NG + 1), grp = step % (NG + 1);
+          if (grp < NG) {
+#pragma unroll
+            for (int i = S::HSETS * DG - 1; i >= 0; --i) {
+              f32x4& o = oacc[grp * DG + i % DG];
+              o = mma<T>(o, from[i], xf[kb]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i <= W; ++i) p[i] = mma<T>(p[i], from[i], xf[kb]);
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
-        Frag zf[AHEAD ? NPB : 1][NDV];
+        Frag zf[NPB][NDV];
 #pragma unroll
-        for (int kb = 0; kb < (AHEAD ? NPB : 0); ++kb)
+        for (int kb = 0; kb < NPB; ++kb)
 #pragma unroll
-          for (int d = 0; d < NDV; ++d) zf[kb][d] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
-        // P^T = G . (Y X^T).  Below the diagonal G(t, s) is G(t, e) G(e, s)
-        // with e the last row of the tile of s: both at most 1 for decays, one
-        // exponential a tile here and one a row of the chunk (state waves).
+          for (int d = 0; d < NDV; ++d) zf[kb][d] = zcol[d].read(lds, kb);
+        load_x(min(c + 1, R.last));
+        lds_barrier();
+        // ---- phase 2: P^T = G . (Y X^T).  Below the diagonal G(t, s) is
+        // G(t, e) G(e, s) with e the last row of the tile of s: both at most 1
+        // for decays, one exponential a tile here and one a row of the chunk
+        // (decay_factors).
         const float ch = dec[t], cl = dec[C + t];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const float row = __builtin_amdgcn_exp2f((ch - dec[16 * i + 15]) + (cl - dec[C + 16 * i + 15]));
+          const float rowf = __builtin_amdgcn_exp2f((ch - dec[16 * i + 15]) + (cl - dec[C + 16 * i + 15]));
           const f32x4 tail = *reinterpret_cast<const f32x4*>(dec + 4 * C + 16 * i + 4 * g);
-          p[i] *= tail * row;
+          p[i] *= tail * rowf;
         }
         {
           const f32x4 sh = *reinterpret_cast<const f32x4*>(dec + 16 * W + 4 * g);
@@ -326,7 +474,7 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
         }
         const float gam = dec[2 * C + t];
 #pragma unroll
-        for (int d = 0; d < NDV; ++d) oacc[d] = (oacc[d] + olo[d]) * gam;
+        for (int d = 0; d < NDV; ++d) oacc[d] *= gam;
         // O^T += Z^T P^T
 #pragma unroll
         for (int kb = 0; kb < NPB; ++kb) {
@@ -335,261 +483,306 @@ __global__ __launch_bounds__(OUT ? 768 : 512) void sweep_kernel(SweepLaunch L) {
           else ph = frag_from_acc_f32(p[kb]);
 #pragma unroll
           for (int d = 0; d < NDV; ++d) {
-            if constexpr (!AHEAD) zf[0][d] = col_frag<T, S::ZROW>(set + Z_OFF, 16 * d, kb, g, r);
-            const Frag z = zf[AHEAD ? kb : 0][d];
-            if constexpr (BF) oacc[d] = mma<T>(oacc[d], z, pl);
-            oacc[d] = mma<T>(oacc[d], z, ph);
+            if constexpr (BF) oacc[d] = mma<T>(oacc[d], zf[kb][d], pl);
+            oacc[d] = mma<T>(oacc[d], zf[kb][d], ph);
           }
         }
         // this lane holds four consecutive columns of row t
-        const int row = first + dir * (C * c + t);
 #pragma unroll
         for (int d = 0; d < NDV; ++d) {
           const int col = slice * DS + 16 * d + 4 * g;
           if (A.out_f32) store4<float>(outr, (row * A.d2 + col) * 4, oacc[d]);
           else store4<T>(outr, (row * A.d2 + col) * E, oacc[d]);
         }
-        if (A.dot) {   // this slice's part of w_t . out_t
+        if constexpr (DOT) {   // this slice's part of w_t . out_t
           float x = 0.f;
 #pragma unroll
           for (int d = 0; d < NDV; ++d)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float w;
-              if constexpr (BF) w = (j & 1) ? bf16_hi_half(wv[d][j >> 1]) : bf16_lo_half(wv[d][j >> 1]);
-              else w = __uint_as_float(wv[d][j]);
-              x = __builtin_fmaf(w, oacc[d][j], x);
-            }
+            for (int j = 0; j < 4; ++j) x = __builtin_fmaf(Quad<T>::get(wv[d], j), oacc[d][j], x);
           x += __shfl_xor(x, 16, 64);
           x += __shfl_xor(x, 32, 64);
           if (g == 0 && (unsigned)row < (unsigned)len)
             A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
         }
+        place(c + 1);
+        load(min(c + 2, R.last));
         lds_barrier();
-      };
-      for (int c = 0; c < nch; c += 2) {
-        chunk(c, x0, w0, x1, w1);
-        if (c + 1 >= nch) break;
-        chunk(c + 1, x1, w1, x0, w0);
       }
     };
-    switch (wave) {
-      case 0: run(std::integral_constant<int, 0>{}); break;
-      case 1: run(std::integral_constant<int, 1>{}); break;
-      case 2: run(std::integral_constant<int, 2>{}); break;
-      default: run(std::integral_constant<int, 3>{}); break;
-    }
-  } else if (wave < (OUT ? 8 : 4)) {
+    auto run_wave = [&](auto dotconst) __attribute__((always_inline)) {
+      switch (wave) {
+        case 0: run(std::integral_constant<int, 0>{}, dotconst); break;
+        case 1: run(std::integral_constant<int, 1>{}, dotconst); break;
+        case 2: run(std::integral_constant<int, 2>{}, dotconst); break;
+        default: run(std::integral_constant<int, 3>{}, dotconst); break;
+      }
+    };
+    if (A.w) run_wave(std::true_type{});
+    else run_wave(std::false_type{});
+  } else {
     // ============================================================ state waves
-    const int sw = wave - (OUT ? 4 : 0);
-    const int dvt = sw % NDV, rt0 = (sw / NDV) * TPW;   // column tile, first row tile
+    const int sw = wave - 4;
+    const int ct0 = (sw % S::WC) * TC, rt0 = (sw / S::WC) * TR;   // this wave's first column and row tile
+    const T* gp = decays_of<T>(L, bh);
+    const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
+    T gv;   // the next chunk's log decays as stored: widened when used, so that loading does not wait
+    auto load_g = [&](int c) __attribute__((always_inline)) {
+      gv = load_decay<T>(gr, R, R.row0 + C * c + lane, A.reverse, L.head_decay);
+    };
+    ColFrags<T, S::YROW> ycol[TR];
+    ColFrags<T, S::ZROW> zcol[TC];
+#pragma unroll
+    for (int i = 0; i < TR; ++i) ycol[i].set(0, 16 * min(rt0 + i, S::RH - 1), g, r);
+#pragma unroll
+    for (int j = 0; j < TC; ++j) zcol[j].set(S::ZS_OFF, 16 * (ct0 + j), g, r);
     // the state slice: lane (g, r) holds rows 4 g .. 4 g + 3 of column r of each of its tiles
-    f32x4 h[TPW];
+    f32x4 h[TR][TC];
     const size_t sbase = (size_t)bh * D1 * A.d2;
-    auto state_at = [&](int i, int j) __attribute__((always_inline)) {   // element offset inside one head's state
-      const int row = 16 * (rt0 + i) + 4 * g + j, col = slice * DS + 16 * dvt + r;
+    auto state_at = [&](int i, int j, int e) __attribute__((always_inline)) {   // element offset inside one head's state
+      const int row = 16 * (rt0 + i) + 4 * g + e, col = slice * DS + 16 * (ct0 + j) + r;
       return A.turned ? col * D1 + row : row * A.d2 + col;
     };
-    auto own = [&](int i) __attribute__((always_inline)) { return TPW * S::WPC == S::RH || rt0 + i < S::RH; };
-    const float* init = L.nseg > 1 ? (A.seg_states ? A.seg_states + (size_t)seg * L.seg_stride : nullptr) : A.init;
+    auto own = [&](int i) __attribute__((always_inline)) { return S::WR * TR == S::RH || rt0 + i < S::RH; };
+    const float* init = L.nseg > 1 ? A.seg_states + (size_t)seg * L.seg_subs * L.seg_stride : A.init;
 #pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      h[i] = zero4();
-      if (init && own(i)) {
+    for (int i = 0; i < TR; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[i][j] = init[sbase + state_at(i, j)];
-      }
-    }
-    auto put_state = [&](int c) __attribute__((always_inline)) {   // H^T [column][row] as the A operand of H^T X^T
-      if constexpr (OUT) {
-        unsigned char* hs = set_of(c) + H_OFF;
+      for (int j = 0; j < TC; ++j) {
+        h[i][j] = zero4();
+        if (init && own(i)) {
 #pragma unroll
-        for (int i = 0; i < TPW; ++i) {
-          if (!own(i)) continue;
-          if constexpr (BF) {
-            const int off = state_piece<S::YROW>(16 * dvt + r, 2 * (rt0 + i) + (g >> 1)) + (g & 1) * 8;
-            u32x2 a, b;
-            uint32_t ha, la, hb, lb;
-            split_pair_bf16(h[i][0], h[i][1], ha, la);
-            split_pair_bf16(h[i][2], h[i][3], hb, lb);
-            a = u32x2{ha, hb};
-            b = u32x2{la, lb};
-            *reinterpret_cast<u32x2*>(hs + off) = a;
-            *reinterpret_cast<u32x2*>(hs + S::H_BYTES + off) = b;
-          } else {
-            const int off = state_piece<S::YROW>(16 * dvt + r, 4 * (rt0 + i) + g);
-            *reinterpret_cast<f32x4*>(hs + off) = h[i];
-          }
+          for (int e = 0; e < 4; ++e) h[i][j][e] = init[sbase + state_at(i, j, e)];
         }
       }
+    int hput[TR];   // offsets of this lane's rows of H^T, by row tile
+#pragma unroll
+    for (int i = 0; i < TR; ++i) {
+      hput[i] = S::H_OFF + (BF ? state_piece<S::YROW>(16 * ct0 + r, 2 * (rt0 + i) + (g >> 1)) + (g & 1) * 8
+                               : state_piece<S::YROW>(16 * ct0 + r, 4 * (rt0 + i) + g));
+      asm("" : "+v"(hput[i]));
+    }
+    auto put_state = [&]() __attribute__((always_inline)) {   // H^T [column][row] as the A operand of H^T X^T
+#pragma unroll
+      for (int i = 0; i < TR; ++i)
+#pragma unroll
+        for (int j = 0; j < TC; ++j) {
+          if (!own(i)) continue;
+          const f32x4 x = h[i][j];
+          if constexpr (BF) {
+            unsigned char* to = lds + hput[i] + j * 16 * S::YROW;
+            uint32_t ha, la, hb, lb;
+            split_pair_bf16(x[0], x[1], ha, la);
+            split_pair_bf16(x[2], x[3], hb, lb);
+            *reinterpret_cast<u32x2*>(to) = u32x2{ha, hb};
+            *reinterpret_cast<u32x2*>(to + S::H_BYTES) = u32x2{la, lb};
+          } else {
+            *reinterpret_cast<f32x4*>(lds + hput[i] + j * 16 * S::YROW) = x;
+          }
+        }
     };
-    put_state(0);
+    load_g(0);
+    if constexpr (S::D1P != D1) {
+      // half K blocks: the columns behind D1 are zero for good
+      for (int p = tid - 256; p < 2 * (C > DS ? C : DS); p += 256) {
+        const int row = p >> 1, piece = 2 + (p & 1);
+        if (row < C) store_frag(ly + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+        if (row < DS) {
+          store_frag(lh + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+          store_frag(lh + S::H_BYTES + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
+        }
+      }
+    }
+    if (sw == 0) decay_factors(to_f32(gv), dec_of(0), lane);
+    put_state();
     lds_barrier();   // the first decay factors are there
-    lds_barrier();   // set 0 is filled
-    float decay = 1.f;   // product of the chunks' decays
-    auto chunk = [&](int c, const unsigned char* set) __attribute__((always_inline)) {
-      const float* dec = dec_of(c);
-      // A operand: the columns of Y this wave's row tiles are; B operand: the
-      // terms of G(C, s) z_s for its column tile
-      Frag zf[KBC][S::ZSETS], yf[KBC][TPW];
+    place(0);
+    load_g(min(1, R.last));
+    load(min(1, R.last));
+    lds_barrier();   // the first operands are there
+    for (int c = 0; c < nch; ++c) {
+      // ---- phase 1.  A operand: the columns of Y this wave's row tiles are;
+      // B operand: the terms of G(C, s) z_s for its column tile
+      const float end = dec_of(c)[2 * C + C - 1];
+      if (sw == 0) decay_factors(to_f32(gv), dec_of(c + 1), lane);
+#pragma unroll
+      for (int i = 0; i < TR; ++i)
+#pragma unroll
+        for (int j = 0; j < TC; ++j) h[i][j] *= end;
 #pragma unroll
       for (int kb = 0; kb < KBC; ++kb) {
+        Frag zf[TC][S::ZSETS], yf[TR];
 #pragma unroll
-        for (int i = 0; i < TPW; ++i) yf[kb][i] = col_frag<T, S::YROW>(set, 16 * min(rt0 + i, S::RH - 1), kb, g, r);
+        for (int i = 0; i < TR; ++i) yf[i] = ycol[i].read(lds, kb);
 #pragma unroll
-        for (int n = 0; n < S::ZSETS; ++n)
-          zf[kb][n] = col_frag<T, S::ZROW>(set + ZS_OFF + n * S::Z_BYTES, 16 * dvt, kb, g, r);
-      }
-      const float end = dec[2 * C + C - 1];
-      decay *= end;
+        for (int j = 0; j < TC; ++j)
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) h[i] *= end;
-#pragma unroll
-      for (int kb = 0; kb < KBC; ++kb)
+          for (int n = 0; n < S::ZSETS; ++n)
+            zf[j][n] = zcol[j].read(lds, kb, n * S::Z_BYTES);
+        if (kb == KBC - 1) lds_barrier();   // everything is read: the rest is phase 2
 #pragma unroll
         for (int n = S::ZSETS - 1; n >= 0; --n)
 #pragma unroll
-          for (int i = 0; i < TPW; ++i) h[i] = mma<T>(h[i], yf[kb][i], zf[kb][n]);
-      put_state(c + 1);
+          for (int j = 0; j < TC; ++j)
+#pragma unroll
+            for (int i = 0; i < TR; ++i) h[i][j] = mma<T>(h[i][j], yf[i], zf[j][n]);
+      }
+      // ---- phase 2
+      place(c + 1);
+      load_g(min(c + 2, R.last));
+      load(min(c + 2, R.last));
+      put_state();
       lds_barrier();
-    };
-    for (int c = 0; c < nch; c += 2) {
-      chunk(c, set_of(0));
-      if (c + 1 >= nch) break;
-      chunk(c + 1, set_of(1));
     }
-    // the final state (of the last segment), or this segment's own state
-    float* fin = OUT ? (seg == L.nseg - 1 ? A.fin : nullptr) : A.seg_out + (size_t)seg * L.seg_stride;
-    if (fin) {
+    // the final state, of the last segment
+    if (A.fin && seg == L.nseg - 1) {
       // dh0 = a_1 R_1: the first row's own decay, which a reversed sweep has not applied
       float scale = 1.f;
-      if (A.reverse && len > 0 && OUT) {
+      if (A.reverse && len > 0) {
         const float x = to_f32(*gp) * kLog2E;
         scale = __builtin_amdgcn_exp2f(x < kDecayFloor ? kDecayFloor : x);
       }
 #pragma unroll
-      for (int i = 0; i < TPW; ++i) {
-        if (!own(i)) continue;
+      for (int i = 0; i < TR; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fin[sbase + state_at(i, j)] = h[i][j] * scale;
-      }
-    }
-    if (!OUT && slice == 0 && sw == 0 && lane == 0) A.seg_decay[(size_t)seg * L.units * L.group + bh] = decay;
-  } else {
-    // ============================================================ copy waves
-    const int cw = wave - (OUT ? 8 : 4), ct = tid - (OUT ? 512 : 256);
-    const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared, D1, E);
-    const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared, A.d2, E);
-    const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
-    struct Regs {
-      Frag y[S::NY], z[S::NZ];
-      T g;   // as stored: widened when placed, so that loading does not wait
-    };
-    auto load = [&](Regs& d, int c) __attribute__((always_inline)) {
-      {   // the decay of the chunk's row `lane`: reversed row j carries that of the row after it
-        const int j = row0 + C * c + lane, at = A.reverse ? len - j : j;
-        const int off = j < len && at < len ? (L.head_decay ? 0 : at * E) : 0x7FFFFFF0;   // out of range: 0
-        if constexpr (BF) d.g.bits = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
-        else d.g = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
-      }
+        for (int j = 0; j < TC; ++j) {
+          if (!own(i)) continue;
 #pragma unroll
-      for (int j = 0; j < S::NY; ++j) {
-        const int p = ct + 256 * j;
-        const int row = first + dir * (C * c + p / S::YPR);
-        d.y[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, row * D1 * E + (p % S::YPR) * 16, 0, 0);
-      }
-#pragma unroll
-      for (int j = 0; j < S::NZ; ++j) {
-        const int p = ct + 256 * j;
-        const int row = first + dir * (C * c + p / S::ZPR);
-        d.z[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, (row * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
-      }
-    };
-    auto factors = [&](const Regs& d, int c) __attribute__((always_inline)) {
-      if (cw == 0) {
-        float x = to_f32(d.g) * kLog2E;
-        x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
-        const float whole = rintf(x * 64.f) * (1.f / 64.f);
-        const float ch = wave_prefix(whole), cl = wave_prefix(x - whole);
-        const float th = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ch), 63));
-        const float tl = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, cl), 63));
-        float* dec = dec_of(c);
-        dec[lane] = ch;
-        dec[C + lane] = cl;
-        dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
-        dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
-        dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
-      }
-    };
-    auto place = [&](const Regs& d, int c) __attribute__((always_inline)) {
-      unsigned char* set = set_of(c);
-      const float* dec = dec_of(c);
-#pragma unroll
-      for (int j = 0; j < S::NY; ++j) {
-        const int p = ct + 256 * j;
-        if (C * S::YPR % 256 == 0 || p < C * S::YPR)
-          store_frag(set + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), d.y[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < S::NZ; ++j) {
-        const int p = ct + 256 * j;
-        if (C * S::ZPR % 256 == 0 || p < C * S::ZPR) {
-          const int off = lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR);
-          store_frag(set + Z_OFF + off, d.z[j]);
-          const float wt = dec[3 * C + p / S::ZPR];   // G(C, row)
-          if constexpr (BF) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              v[e] = wt * ((e & 1) ? bf16_hi_half(d.z[j].w[e >> 1]) : bf16_lo_half(d.z[j].w[e >> 1]));
-            Frag t[3];
-            split3_bf16(v, t[0], t[1], t[2]);
-#pragma unroll
-            for (int n = 0; n < S::ZSETS; ++n) store_frag(set + ZS_OFF + n * S::Z_BYTES + off, t[n]);
-          } else {
-            store_frag(set + ZS_OFF + off, frag_from_acc_f32(__builtin_bit_cast(f32x4, d.z[j].w) * wt));
-          }
+          for (int e = 0; e < 4; ++e) A.fin[sbase + state_at(i, j, e)] = h[i][j][e] * scale;
         }
-      }
-    };
-    if constexpr (S::D1P != D1) {
-      // half K blocks: the columns behind D1 are zero for good
-      for (int p = ct; p < 2 * C * 2; p += 256) {
-        unsigned char* set = set_of(p & 1);
-        const int row = (p >> 1) >> 1, piece = 2 + ((p >> 1) & 1);
-        store_frag(set + lds_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-        if (OUT && row < DS) {
-          store_frag(set + H_OFF + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-          store_frag(set + H_OFF + S::H_BYTES + state_piece<S::YROW>(row, piece), Frag{u32x4{0, 0, 0, 0}});
-        }
-      }
-    }
-    // Chunk x is loaded into register set x % 2 two iterations before it is
-    // placed.  Loads and copies run on past the last chunk (the last one again,
-    // into sets nobody reads): a conditional load would make every wait for an
-    // older one wait for all loads in flight.
-    // The decay factors are a chunk ahead of the copies that use them.
-    Regs r0, r1;
-    load(r0, 0);
-    load(r1, min(1, last));
-    factors(r0, 0);
-    lds_barrier();   // the first decay factors are there
-    place(r0, 0);
-    factors(r1, 1);
-    load(r0, min(2, last));
-    lds_barrier();   // set 0 is filled
-    for (int c = 0; c < nch; c += 2) {
-      place(r1, c + 1);
-      factors(r0, c + 2);
-      load(r1, min(c + 3, last));
-      lds_barrier();
-      if (c + 1 >= nch) break;
-      place(r0, c + 2);
-      factors(r1, c + 3);
-      load(r0, min(c + 4, last));
-      lds_barrier();
     }
   }
+}
+
+// A segment's own state, from zero: sum_s G(end, s) y_s z_s^T, and its whole
+// decay.  One workgroup holds the whole [D1, D2] state of one (batch, head) in
+// the accumulators of its eight waves (two rows of waves, four columns), so
+// that every row of Y and Z is read once; per chunk it copies Y and the terms
+// of the scaled Z to LDS and multiplies Y^T (G(C, .) Z), in two phases with a
+// barrier each as above.  What bounds it is the matrix products.
+template <typename T, int D1, int D2>
+struct OwnCfg {
+  static constexpr int E = (int)sizeof(T);
+  static constexpr int KBC = C / FragTraits<T>::KB;
+  static constexpr int YROW = D1 * E < 32 ? 32 : D1 * E, ZROW = D2 * E < 32 ? 32 : D2 * E;
+  static constexpr int ZSETS = E == 2 ? 3 : 1;
+  static constexpr int RH = D1 / 16, RD = D2 / 16;
+  static constexpr int TR = (RH + 1) / 2, TC = (RD + 3) / 4;   // tiles of one wave
+  static constexpr int Y_BYTES = C * YROW, Z_BYTES = C * ZROW;
+  static constexpr int DEC_OFF = Y_BYTES + ZSETS * Z_BYTES, DEC_BYTES = kDecSets * C * 4;
+  static constexpr int LDS_BYTES = DEC_OFF + 2 * DEC_BYTES;
+  static constexpr int YPR = D1 * E / 16, ZPR = D2 * E / 16;
+  static constexpr int NY = (C * YPR + 511) / 512, NZ = (C * ZPR + 511) / 512;
+};
+
+template <typename T, int D1, int D2>
+__global__ __launch_bounds__(512) void own_state_kernel(SweepLaunch L) {
+  using S = OwnCfg<T, D1, D2>;
+  constexpr int E = S::E;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS_BYTES];
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
+  const int g = lane / 16, r = lane % 16;
+  int unit, part;
+  unit_of(L.units, L.parts, unit, part);
+  const SweepRole A = L.role[0];
+  const int bh = unit * L.group + part % L.group;
+  const int seg = part / L.group;
+  const Rows R(L, bh, seg, L.seg_rows, A.reverse);
+  auto dec_of = [&](int c) __attribute__((always_inline)) {
+    return reinterpret_cast<float*>(lds + S::DEC_OFF + (c & 1) * S::DEC_BYTES);
+  };
+  unsigned char *ly = lds, *lzs = lds + S::Y_BYTES;
+  const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared ? unit : bh, L.rows, R.len, D1, E);
+  const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared ? unit : bh, L.rows, R.len, D2, E);
+  const __amdgpu_buffer_rsrc_t gr = make_rsrc(decays_of<T>(L, bh), (uint32_t)((L.head_decay ? 1 : R.len) * E));
+  Frag yv[S::NY], zv[S::NZ];
+  T gv;
+  auto load = [&](int c) __attribute__((always_inline)) {
+    gv = load_decay<T>(gr, R, R.row0 + C * c + lane, A.reverse, L.head_decay);
+#pragma unroll
+    for (int j = 0; j < S::NY; ++j) {
+      const int p = tid + 512 * j;
+      yv[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, R.row(C * c + p / S::YPR) * D1 * E + (p % S::YPR) * 16, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) {
+      const int p = tid + 512 * j;
+      zv[j].w = __builtin_amdgcn_raw_buffer_load_b128(zr, R.row(C * c + p / S::ZPR) * D2 * E + (p % S::ZPR) * 16, 0, 0);
+    }
+  };
+  auto place = [&](int c) __attribute__((always_inline)) {
+    const float* dec = dec_of(c);
+#pragma unroll
+    for (int j = 0; j < S::NY; ++j) {
+      const int p = tid + 512 * j;
+      if (C * S::YPR % 512 == 0 || p < C * S::YPR) store_frag(ly + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), yv[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) {
+      const int p = tid + 512 * j;
+      if (C * S::ZPR % 512 == 0 || p < C * S::ZPR)
+        store_scaled<T, S::ZSETS>(lzs + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), S::Z_BYTES, zv[j],
+                                  dec[3 * C + p / S::ZPR]);
+    }
+  };
+  const int rt0 = (wave / 4) * S::TR, ct0 = (wave % 4) * S::TC;
+  auto rt = [&](int i) __attribute__((always_inline)) { return min(rt0 + i, S::RH - 1); };   // (spare waves repeat the last tile)
+  auto ctl = [&](int j) __attribute__((always_inline)) { return min(ct0 + j, S::RD - 1); };
+  ColFrags<T, S::YROW> ycol[S::TR];
+  ColFrags<T, S::ZROW> zcol[S::TC];
+#pragma unroll
+  for (int i = 0; i < S::TR; ++i) ycol[i].set(0, 16 * rt(i), g, r);
+#pragma unroll
+  for (int j = 0; j < S::TC; ++j) zcol[j].set(S::Y_BYTES, 16 * ctl(j), g, r);
+  f32x4 h[S::TR][S::TC];
+#pragma unroll
+  for (int i = 0; i < S::TR; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TC; ++j) h[i][j] = zero4();
+  load(0);
+  if (wave == 0) decay_factors(to_f32(gv), dec_of(0), lane);
+  lds_barrier();
+  place(0);
+  load(min(1, R.last));
+  lds_barrier();
+  float decay = 1.f;   // product of the chunks' decays
+  for (int c = 0; c < R.nch; ++c) {
+    if (wave == 0) decay_factors(to_f32(gv), dec_of(c + 1), lane);
+    const float end = dec_of(c)[2 * C + C - 1];
+    decay *= end;
+#pragma unroll
+    for (int i = 0; i < S::TR; ++i)
+#pragma unroll
+      for (int j = 0; j < S::TC; ++j) h[i][j] *= end;
+#pragma unroll
+    for (int kb = 0; kb < S::KBC; ++kb) {
+      Frag yf[S::TR];
+#pragma unroll
+      for (int i = 0; i < S::TR; ++i) yf[i] = ycol[i].read(lds, kb);
+#pragma unroll
+      for (int n = S::ZSETS - 1; n >= 0; --n)
+#pragma unroll
+        for (int j = 0; j < S::TC; ++j) {
+          const Frag zf = zcol[j].read(lds, kb, n * S::Z_BYTES);
+#pragma unroll
+          for (int i = 0; i < S::TR; ++i) h[i][j] = mma<T>(h[i][j], yf[i], zf);
+        }
+    }
+    lds_barrier();
+    place(c + 1);
+    load(min(c + 2, R.last));
+    lds_barrier();
+  }
+  float* out = A.seg_out + (size_t)seg * L.seg_stride + (size_t)bh * D1 * D2;
+#pragma unroll
+  for (int i = 0; i < S::TR; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TC; ++j)
+      if (rt0 + i < S::RH && ct0 + j < S::RD) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(16 * (rt0 + i) + 4 * g + e) * D2 + 16 * (ct0 + j) + r] = h[i][j][e];
+      }
+  if (tid == 0) A.seg_decay[(size_t)seg * L.units * L.group + bh] = decay;
 }
 
 // Segment states, in place: segment i holds its own state (from zero) on entry
@@ -614,34 +807,70 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(float* states, const 
   }
 }
 
-template <typename T, int D1, int DS, bool OUT, bool EXACT>
+template <typename T, int D1, int DS, bool EXACT>
 hipError_t launch_sweep_t(const SweepLaunch& L, hipStream_t stream) {
   const long long wgs = (long long)L.units * L.parts;
   if (wgs == 0) return hipSuccess;
-  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, OUT, EXACT>), dim3((unsigned)wgs), dim3(OUT ? 768 : 512), 0, stream, L);
+  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, EXACT>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
   return hipGetLastError();
 }
 
 template <typename T, int D1, int DS>
-hipError_t launch_sweep_o(const SweepLaunch& L, bool out, hipStream_t stream) {
-  if (!out) return launch_sweep_t<T, D1, DS, false, true>(L, stream);
-  // (fp32 products have one term: one instantiation)
-  return L.exact_state || sizeof(T) == 4 ? launch_sweep_t<T, D1, DS, true, true>(L, stream)
-                                         : launch_sweep_t<T, D1, DS, true, sizeof(T) == 4>(L, stream);
+hipError_t launch_sweep_x(const SweepLaunch& L, hipStream_t stream) {
+  constexpr bool F = sizeof(T) == 4;   // fp32 states have one term: one instantiation
+  return L.exact_state || F ? launch_sweep_t<T, D1, DS, true>(L, stream) : launch_sweep_t<T, D1, DS, F>(L, stream);
 }
 
 template <typename T, int D1>
-hipError_t launch_sweep_d(const SweepLaunch& L, int ds, bool out, hipStream_t stream) {
-  return ds == 32 ? launch_sweep_o<T, D1, 32>(L, out, stream) : launch_sweep_o<T, D1, 16>(L, out, stream);
+hipError_t launch_sweep_d(const SweepLaunch& L, int ds, hipStream_t stream) {
+  switch (ds) {
+    case 16: return launch_sweep_x<T, D1, 16>(L, stream);
+    case 32: return launch_sweep_x<T, D1, 32>(L, stream);
+    case 64: return launch_sweep_x<T, D1, 64>(L, stream);
+    case 128:
+      if constexpr (sizeof(T) == 2) return launch_sweep_x<T, D1, 128>(L, stream);
+      break;
+  }
+  return hipErrorInvalidValue;
 }
 
 template <typename T>
-hipError_t launch_sweep_e(const SweepLaunch& L, int d1, int ds, bool out, hipStream_t stream) {
+hipError_t launch_sweep_e(const SweepLaunch& L, int d1, int ds, hipStream_t stream) {
   switch (d1) {
-    case 16: return launch_sweep_d<T, 16>(L, ds, out, stream);
-    case 32: return launch_sweep_d<T, 32>(L, ds, out, stream);
-    case 64: return launch_sweep_d<T, 64>(L, ds, out, stream);
-    case 128: return launch_sweep_d<T, 128>(L, ds, out, stream);
+    case 16: return launch_sweep_d<T, 16>(L, ds, stream);
+    case 32: return launch_sweep_d<T, 32>(L, ds, stream);
+    case 64: return launch_sweep_d<T, 64>(L, ds, stream);
+    case 128: return launch_sweep_d<T, 128>(L, ds, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <typename T, int D1, int D2>
+hipError_t launch_own_t(const SweepLaunch& L, hipStream_t stream) {
+  const long long wgs = (long long)L.units * L.parts;
+  if (wgs == 0) return hipSuccess;
+  hipLaunchKernelGGL((own_state_kernel<T, D1, D2>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
+  return hipGetLastError();
+}
+
+template <typename T, int D1>
+hipError_t launch_own_d(const SweepLaunch& L, hipStream_t stream) {
+  switch (L.role[0].d2) {
+    case 16: return launch_own_t<T, D1, 16>(L, stream);
+    case 32: return launch_own_t<T, D1, 32>(L, stream);
+    case 64: return launch_own_t<T, D1, 64>(L, stream);
+    case 128: return launch_own_t<T, D1, 128>(L, stream);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
+  switch (d1) {
+    case 16: return launch_own_d<T, 16>(L, stream);
+    case 32: return launch_own_d<T, 32>(L, stream);
+    case 64: return launch_own_d<T, 64>(L, stream);
+    case 128: return launch_own_d<T, 128>(L, stream);
   }
   return hipErrorInvalidValue;
 }
@@ -863,44 +1092,61 @@ hipError_t launch_linattn_decode(const LinAttnDecodeArgs& a) {
 
 // ---------------------------------------------------------------- host side
 
-static hipError_t launch_sweep(const SweepLaunch& L, int dtype, int d1, int ds, bool out, hipStream_t stream) {
-  return dtype == 1 ? launch_sweep_e<bf16_t>(L, d1, ds, out, stream) : launch_sweep_e<float>(L, d1, ds, out, stream);
+static hipError_t launch_sweep(const SweepLaunch& L, int dtype, int d1, int ds, hipStream_t stream) {
+  return dtype == 1 ? launch_sweep_e<bf16_t>(L, d1, ds, stream) : launch_sweep_e<float>(L, d1, ds, stream);
 }
 
-static int slice_width(int d2) { return d2 >= 32 ? 32 : 16; }
+// Value columns of a slice: all of them in bf16 (the state and three terms of
+// the values fit in LDS), at most 64 in fp32.
+static int slice_width(int d2, int dtype) { return dtype == CKDA_DTYPE_BF16 ? d2 : std::min(d2, 64); }
 
-// Rows of a segment: one segment when the (batch, head, slice) workgroups of
-// one sweep fill the CUs, else enough segments to give every CU one, of at
-// least eight chunks each (every further segment re-reads its rows once more,
-// for its own state).
-static int segment_rows(long long wgs, int T) {
-  constexpr int kCUs = 256, kMinChunks = 8;
-  const int nch = (T + C - 1) / C;
+// How a sweep's rows are split.  `wgs` workgroups of (batch, head, slice) leave
+// CUs idle below 256; the rows are then split into segments, and the states between them come from the
+// segments' own states (own_state_kernel, which reads y and z once more) joined
+// in order.  The own states are formed over sub-segments, short enough to
+// occupy the CUs as well.
+struct Split {
+  int seg_rows, nseg, sub_rows, subs, nsub;   // subs: sub-segments per segment; nsub: of the whole sequence
+};
+static Split split_rows(long long wgs, long long heads, int T) {
+  constexpr long long kCUs = 256;
+  constexpr int kMinChunks = 4;   // of a segment
+  const int nch = std::max(1, (T + C - 1) / C);
+  Split p;
   long long nseg = wgs > 0 ? kCUs / wgs : 1;
-  if (nseg > nch / kMinChunks) nseg = nch / kMinChunks;
-  if (nseg < 1) nseg = 1;
-  return (int)((nch + nseg - 1) / nseg) * C;
+  nseg = std::max(1LL, std::min(nseg, (long long)nch / kMinChunks));
+  const int per = (int)((nch + nseg - 1) / nseg);
+  p.nseg = std::max(1, (nch + per - 1) / per);
+  long long subs = heads > 0 && p.nseg > 1 ? (kCUs + heads * (p.nseg - 1) - 1) / (heads * (p.nseg - 1)) : 1;
+  subs = std::max(1LL, std::min(subs, (long long)per / 4));
+  const int sub = (int)((per + subs - 1) / subs);
+  p.subs = (per + sub - 1) / sub;
+  p.sub_rows = sub * C;
+  p.seg_rows = p.subs * p.sub_rows;   // whole sub-segments
+  p.nseg = std::max(1, (nch + p.subs * sub - 1) / (p.subs * sub));
+  p.nsub = (p.nseg - 1) * p.subs + 1;   // the last segment's start is the last one needed
+  return p;
 }
-static int segment_count(int T, int rows) { return T <= rows ? 1 : (T + rows - 1) / rows; }
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// workspace of the forward: the segments' states and decays
+// workspace of the forward: the sub-segments' states and decays
 struct FwdPlan {
-  int seg_rows, nseg;
+  Split sp;
   size_t states, decay, bytes;
 };
-static FwdPlan fwd_plan(int B, int H, int T, int dk, int dv) {
+static FwdPlan fwd_plan(int B, int H, int T, int dk, int dv, int dtype) {
   FwdPlan p;
   const size_t bh = (size_t)B * H;
-  p.seg_rows = segment_rows((long long)bh * (dv / slice_width(dv)), T);
-  p.nseg = segment_count(T, p.seg_rows);
+  p.sp = split_rows((long long)bh * (dv / slice_width(dv, dtype)), (long long)bh, T);
   p.states = 0;
-  p.decay = p.nseg > 1 ? up256((size_t)p.nseg * bh * dk * dv * 4) : 0;
-  p.bytes = p.nseg > 1 ? p.decay + up256((size_t)p.nseg * bh * 4) : 0;
+  p.decay = p.sp.nseg > 1 ? up256((size_t)p.sp.nsub * bh * dk * dv * 4) : 0;
+  p.bytes = p.sp.nseg > 1 ? p.decay + up256((size_t)p.sp.nsub * bh * 4) : 0;
   return p;
 }
-size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv) { return fwd_plan(B, H, T, dk, dv).bytes; }
+size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
+  return fwd_plan(B, H, T, dk, dv, dtype).bytes;
+}
 
 static SweepLaunch sweep_base(const LinAttnArgs& a) {
   SweepLaunch L = {};
@@ -914,15 +1160,19 @@ static SweepLaunch sweep_base(const LinAttnArgs& a) {
   return L;
 }
 
-// states of the segments of one direction: own states, then their starts
-static hipError_t segment_starts(const LinAttnArgs& a, bool reverse, int seg_rows, int nseg, float* states, float* decay,
+static void set_split(SweepLaunch& L, const LinAttnArgs& a, const Split& sp) {
+  L.seg_rows = sp.seg_rows;
+  L.nseg = sp.nseg;
+  L.seg_subs = sp.subs;
+  L.seg_stride = (long long)a.B * a.H * a.dk * a.dv;
+}
+
+// the states at the starts of all sub-segments of one direction
+static hipError_t segment_starts(const LinAttnArgs& a, bool reverse, const Split& sp, float* states, float* decay,
                                  const float* init) {
   SweepLaunch L = sweep_base(a);
-  const int ds = slice_width(a.dv);
-  const size_t bh = (size_t)a.B * a.H, elems = (size_t)a.dk * a.dv;
-  L.seg_rows = seg_rows;
-  L.nseg = nseg;
-  L.seg_stride = (long long)(bh * elems);
+  set_split(L, a, sp);
+  L.seg_rows = sp.sub_rows;
   L.nroles = 1;
   SweepRole& R = L.role[0];
   R.y = reverse ? a.q : a.k;
@@ -932,28 +1182,26 @@ static hipError_t segment_starts(const LinAttnArgs& a, bool reverse, int seg_row
   R.d2 = a.dv;
   R.seg_out = states;
   R.seg_decay = decay;
-  R.parts = L.parts = (nseg - 1) * L.group * (a.dv / ds);
-  hipError_t e = launch_sweep(L, a.dtype, a.dk, ds, false, a.stream);
+  R.parts = L.parts = (sp.nsub - 1) * L.group;
+  hipError_t e = a.dtype == 1 ? launch_own_e<bf16_t>(L, a.dk, a.stream) : launch_own_e<float>(L, a.dk, a.stream);
   if (e != hipSuccess) return e;
-  const long long threads = (long long)(bh * elems / 4);
+  const long long threads = L.seg_stride / 4;
   hipLaunchKernelGGL(segment_scan_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, a.stream, states, decay,
-                     init, nseg, (int)bh, (long long)elems, L.seg_stride);
+                     init, sp.nsub, a.B * a.H, (long long)a.dk * a.dv, L.seg_stride);
   return hipGetLastError();
 }
 
 hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
-  const FwdPlan p = fwd_plan(a.B, a.H, a.T, a.dk, a.dv);
+  const FwdPlan p = fwd_plan(a.B, a.H, a.T, a.dk, a.dv, a.dtype);
   unsigned char* ws = (unsigned char*)a.workspace;
   float* states = (float*)(ws + p.states);
-  if (p.nseg > 1) {
-    hipError_t e = segment_starts(a, false, p.seg_rows, p.nseg, states, (float*)(ws + p.decay), a.h0);
+  if (p.sp.nseg > 1) {
+    hipError_t e = segment_starts(a, false, p.sp, states, (float*)(ws + p.decay), a.h0);
     if (e != hipSuccess) return e;
   }
   SweepLaunch L = sweep_base(a);
-  const int ds = slice_width(a.dv);
-  L.seg_rows = p.seg_rows;
-  L.nseg = p.nseg;
-  L.seg_stride = (long long)a.B * a.H * a.dk * a.dv;
+  const int ds = slice_width(a.dv, a.dtype);
+  set_split(L, a, p.sp);
   L.nroles = 1;
   SweepRole& R = L.role[0];
   R.x = a.q;
@@ -966,23 +1214,23 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
   R.fin = a.hT;
   R.seg_states = states;
   L.exact_state = a.hT != nullptr;
-  R.parts = L.parts = p.nseg * L.group * (a.dv / ds);
-  return launch_sweep(L, a.dtype, a.dk, ds, true, a.stream);
+  R.parts = L.parts = p.sp.nseg * L.group * (a.dv / ds);
+  return launch_sweep(L, a.dtype, a.dk, ds, a.stream);
 }
 
 // workspace of the backward: dots of queries and keys with their gradients,
 // the final state, segment states of both directions, and the heads' parts of
 // shared gradients
 struct BwdPlan {
-  int seg_rows, nseg;
+  Split sp;
   size_t dotq, dotk, hT, head_sum, states, rstates, decay, dq, dk, bytes;
 };
-static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv) {
+static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   BwdPlan p;
   const size_t bh = (size_t)B * H, elems = (size_t)dk * dv;
-  const int sk = dk / slice_width(dk), sv = dv / slice_width(dv);
-  p.seg_rows = segment_rows((long long)bh * (2 * sk + sv), T);
-  p.nseg = segment_count(T, p.seg_rows);
+  const int sk = dk / slice_width(dk, dtype), sv = dv / slice_width(dv, dtype);
+  p.sp = split_rows((long long)bh * (2 * sk + sv), (long long)bh, T);
+  const size_t nsub = p.sp.nseg > 1 ? (size_t)p.sp.nsub : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -993,22 +1241,22 @@ static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv) {
   p.dotk = take((size_t)sk * bh * T * 4);
   p.hT = take(bh * elems * 4);
   p.head_sum = take(bh * 8);
-  p.states = take(p.nseg > 1 ? (size_t)p.nseg * bh * elems * 4 : 0);
-  p.rstates = take(p.nseg > 1 ? (size_t)p.nseg * bh * elems * 4 : 0);
-  p.decay = take(p.nseg > 1 ? (size_t)p.nseg * bh * 4 : 0);
+  p.states = take(nsub * bh * elems * 4);
+  p.rstates = take(nsub * bh * elems * 4);
+  p.decay = take(nsub * bh * 4);
   const bool grouped = H != Hk;
   p.dq = take(grouped ? bh * T * dk * 4 : 0);
   p.dk = take(grouped ? bh * T * dk * 4 : 0);
   p.bytes = at;
   return p;
 }
-size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv) {
-  return bwd_plan(B, H, Hk, T, dk, dv).bytes;
+size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
+  return bwd_plan(B, H, Hk, T, dk, dv, dtype).bytes;
 }
 
 template <typename T>
 static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsigned char* ws) {
-  const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk);
+  const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, a.dtype);
   double* sums = a.head_decay ? (double*)(ws + p.head_sum) : nullptr;
   hipError_t e = hipSuccess;
   if (bh > 0)
@@ -1035,17 +1283,17 @@ static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsign
 }
 
 hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
-  const BwdPlan p = bwd_plan(a.B, a.H, a.Hk, a.T, a.dk, a.dv);
+  const BwdPlan p = bwd_plan(a.B, a.H, a.Hk, a.T, a.dk, a.dv, a.dtype);
   unsigned char* ws = (unsigned char*)a.workspace;
   float *states = (float*)(ws + p.states), *rstates = (float*)(ws + p.rstates);
   hipError_t e;
-  if (p.nseg > 1) {
+  if (p.sp.nseg > 1) {
     float* decay = (float*)(ws + p.decay);
-    if ((e = segment_starts(a, false, p.seg_rows, p.nseg, states, decay, a.h0)) != hipSuccess) return e;
-    if ((e = segment_starts(a, true, p.seg_rows, p.nseg, rstates, decay, a.dhT)) != hipSuccess) return e;
+    if ((e = segment_starts(a, false, p.sp, states, decay, a.h0)) != hipSuccess) return e;
+    if ((e = segment_starts(a, true, p.sp, rstates, decay, a.dhT)) != hipSuccess) return e;
   }
   const bool grouped = a.H != a.Hk;
-  const int dsk = slice_width(a.dk), dsv = slice_width(a.dv);
+  const int dsk = slice_width(a.dk, a.dtype), dsv = slice_width(a.dv, a.dtype);
   SweepRole dv = {}, dk = {}, dq = {};
   dv.x = a.k;
   dv.y = a.q;
@@ -1078,11 +1326,9 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dq.fin = a.dhT ? (float*)(ws + p.hT) : nullptr;   // <dhT, H_T> of the decay gradient
   dq.seg_states = states;
   SweepLaunch L = sweep_base(a);
-  L.seg_rows = p.seg_rows;
-  L.nseg = p.nseg;
-  L.seg_stride = (long long)a.B * a.H * a.dk * a.dv;
+  set_split(L, a, p.sp);
   L.exact_state = a.dh0 || a.dhT;
-  const int per = p.nseg * L.group;
+  const int per = p.sp.nseg * L.group;
   dv.parts = per * (a.dv / dsv);
   dk.parts = dq.parts = per * (a.dk / dsk);
   // one launch where the sweeps have the same widths, else the two that
@@ -1093,17 +1339,17 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
     L.role[2] = dq;
     L.nroles = 3;
     L.parts = dv.parts + dk.parts + dq.parts;
-    if ((e = launch_sweep(L, a.dtype, a.dk, dsk, true, a.stream)) != hipSuccess) return e;
+    if ((e = launch_sweep(L, a.dtype, a.dk, dsk, a.stream)) != hipSuccess) return e;
   } else {
     L.role[0] = dv;
     L.nroles = 1;
     L.parts = dv.parts;
-    if ((e = launch_sweep(L, a.dtype, a.dk, dsv, true, a.stream)) != hipSuccess) return e;
+    if ((e = launch_sweep(L, a.dtype, a.dk, dsv, a.stream)) != hipSuccess) return e;
     L.role[0] = dk;
     L.role[1] = dq;
     L.nroles = 2;
     L.parts = dk.parts + dq.parts;
-    if ((e = launch_sweep(L, a.dtype, a.dv, dsk, true, a.stream)) != hipSuccess) return e;
+    if ((e = launch_sweep(L, a.dtype, a.dv, dsk, a.stream)) != hipSuccess) return e;
   }
   return a.dtype == 1 ? launch_bwd_tail<bf16_t>(a, p, ws) : launch_bwd_tail<float>(a, p, ws);
 }

@@ -70,7 +70,7 @@ static LinAttnSizes linattn_bytes(int B, int H, int Hk, int T, int dk, int dv, i
 size_t ckda_linattn_fwd_workspace_size(int B, int H, int T, int dk, int dv, int dtype) {
   if (B < 0 || H < 0 || T < 0) return 0;
   if (!supported_dim(dk) || !supported_dim(dv) || !supported_dtype(dtype)) return 0;
-  const size_t bytes = ckda::linattn_fwd_workspace_bytes(B, H, T, dk, dv);
+  const size_t bytes = ckda::linattn_fwd_workspace_bytes(B, H, T, dk, dv, dtype);
   return bytes == 0 ? 256 : bytes;
 }
 
@@ -109,7 +109,7 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
 size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (B < 0 || H < 0 || T < 0 || (H > 0 && (Hk < 1 || H % Hk != 0))) return 0;
   if (!supported_dim(dk) || !supported_dim(dv) || !supported_dtype(dtype)) return 0;
-  const size_t bytes = ckda::linattn_bwd_workspace_bytes(B, H, Hk, T, dk, dv);
+  const size_t bytes = ckda::linattn_bwd_workspace_bytes(B, H, Hk, T, dk, dv, dtype);
   return bytes == 0 ? 256 : bytes;
 }
 
