@@ -609,24 +609,34 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       for (int i = 0; i < TR; ++i)
 #pragma unroll
         for (int j = 0; j < TC; ++j) h[i][j] *= end;
+      constexpr int KA = BF ? KBC : 1;   // K blocks read ahead of the products (fp32: one, for the registers)
+      Frag zf[KA][TC][S::ZSETS], yf[KA][TR];
+      auto read = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
-      for (int kb = 0; kb < KBC; ++kb) {
-        Frag zf[TC][S::ZSETS], yf[TR];
-#pragma unroll
-        for (int i = 0; i < TR; ++i) yf[i] = ycol[i].read(lds, kb);
+        for (int i = 0; i < TR; ++i) yf[kb % KA][i] = ycol[i].read(lds, kb);
 #pragma unroll
         for (int j = 0; j < TC; ++j)
 #pragma unroll
-          for (int n = 0; n < S::ZSETS; ++n)
-            zf[j][n] = zcol[j].read(lds, kb, n * S::Z_BYTES);
-        if (kb == KBC - 1) lds_barrier();   // everything is read: the rest is phase 2
+          for (int n = 0; n < S::ZSETS; ++n) zf[kb % KA][j][n] = zcol[j].read(lds, kb, n * S::Z_BYTES);
+      };
+      auto multiply = [&](int kb) __attribute__((always_inline)) {
 #pragma unroll
         for (int n = S::ZSETS - 1; n >= 0; --n)
 #pragma unroll
           for (int j = 0; j < TC; ++j)
 #pragma unroll
-            for (int i = 0; i < TR; ++i) h[i][j] = mma<T>(h[i][j], yf[i], zf[j][n]);
+            for (int i = 0; i < TR; ++i) h[i][j] = mma<T>(h[i][j], yf[kb % KA][i], zf[kb % KA][j][n]);
+      };
+#pragma unroll
+      for (int kb = 0; kb < KA; ++kb) read(kb);
+#pragma unroll
+      for (int kb = KA; kb < KBC; ++kb) {
+        multiply(kb - KA);
+        read(kb);
       }
+      lds_barrier();   // everything is read; the products run on into phase 2
+#pragma unroll
+      for (int kb = KBC - KA; kb < KBC; ++kb) multiply(kb);
       // ---- phase 2
       place(c + 1);
       load_g(min(c + 2, R.last));
@@ -676,7 +686,7 @@ struct OwnCfg {
 };
 
 template <typename T, int D1, int D2>
-__global__ __launch_bounds__(512) void own_state_kernel(SweepLaunch L) {
+__global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(SweepLaunch L) {
   using S = OwnCfg<T, D1, D2>;
   constexpr int E = S::E;
   __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS_BYTES];
@@ -794,15 +804,21 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(float* states, const 
   if (i >= heads * elems) return;
   const int bh = (int)(i / elems);
   f32x4 h = init ? *reinterpret_cast<const f32x4*>(init + i) : zero4();
-  for (int s = 0; s < nseg; ++s) {
-    f32x4* p = reinterpret_cast<f32x4*>(states + s * seg_stride + i);
-    if (s + 1 < nseg) {
-      const f32x4 mine = *p;
-      const float d = decay[(size_t)s * heads + bh];
-      *p = h;
-      h = d * h + mine;
-    } else {
-      *p = h;
+  constexpr int AHEAD = 8;   // segments whose loads are in flight together
+  for (int s0 = 0; s0 < nseg; s0 += AHEAD) {
+    f32x4 mine[AHEAD];
+    float d[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int s = min(s0 + j, nseg - 2);   // (the last segment's own state is not formed)
+      mine[j] = *reinterpret_cast<const f32x4*>(states + s * seg_stride + i);
+      d[j] = decay[(size_t)s * heads + bh];
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (s0 + j >= nseg) break;
+      *reinterpret_cast<f32x4*>(states + (s0 + j) * seg_stride + i) = h;
+      h = d[j] * h + mine[j];
     }
   }
 }
@@ -1096,36 +1112,86 @@ static hipError_t launch_sweep(const SweepLaunch& L, int dtype, int d1, int ds, 
   return dtype == 1 ? launch_sweep_e<bf16_t>(L, d1, ds, stream) : launch_sweep_e<float>(L, d1, ds, stream);
 }
 
-// Value columns of a slice: all of them in bf16 (the state and three terms of
-// the values fit in LDS), at most 64 in fp32.
-static int slice_width(int d2, int dtype) { return dtype == CKDA_DTYPE_BF16 ? d2 : std::min(d2, 64); }
-
-// How a sweep's rows are split.  `wgs` workgroups of (batch, head, slice) leave
-// CUs idle below 256; the rows are then split into segments, and the states between them come from the
-// segments' own states (own_state_kernel, which reads y and z once more) joined
-// in order.  The own states are formed over sub-segments, short enough to
-// occupy the CUs as well.
+// How a call is split over workgroups: slices of `ds` value columns (of the
+// widths that has more), and segments of rows, whose start states come from
+// the segments' own states (own_state_kernel reads y and z once more) joined in
+// order; the own states are formed over sub-segments, short enough to occupy
+// the CUs as well.
+//
+// Wide slices do the work that does not depend on the columns (Y X^T, its
+// decays, the copies of Y) fewer times, narrow ones and segments give a call
+// of few heads more workgroups.  The split is the one of least time by the
+// measured time of a chunk (MI355X, 256 workgroups, us; d2 = 128):
+//   bf16, d1 128:  1.39, 1.77, 2.82, 4.97 for slices of 16, 32, 64, 128 columns
+//         d1 64:   1.17, 1.46, 1.92, 3.69      d1 32:  1.00, 1.26, 1.64, 3.53
+//   fp32, d1 128:  4.10, 5.43, 8.50 (16, 32, 64; wider ones do not fit in LDS)
+//         d1 64:   2.52, 3.24, 4.87            d1 32:  1.73, 2.34, 3.45
+// to which chunk_us() is fitted.
 struct Split {
+  int ds;
   int seg_rows, nseg, sub_rows, subs, nsub;   // subs: sub-segments per segment; nsub: of the whole sequence
 };
-static Split split_rows(long long wgs, long long heads, int T) {
+static double chunk_us(int d1, int ds, int dtype) {
+  return dtype == CKDA_DTYPE_BF16 ? 0.8 + ds * (0.009 + 0.00018 * d1) : 0.7 + 0.015 * d1 + ds * (0.017 + 0.00059 * d1);
+}
+// a segment's first loads and its start state
+static double segment_us(int d1, int ds) { return 2.5 + 0.00015 * d1 * ds; }
+static double own_chunk_us(int d1, int d2, int dtype) {
+  return dtype == CKDA_DTYPE_BF16 ? 0.5 + 0.00006 * d1 * d2 : 0.6 + 0.0003 * d1 * d2;
+}
+static int slice_width(int d2, int ds) { return std::min(d2, ds); }
+
+// dk, dv: widths; backward: the three gradient sweeps (and both directions'
+// segment states) instead of the forward one
+static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool backward) {
   constexpr long long kCUs = 256;
-  constexpr int kMinChunks = 4;   // of a segment
   const int nch = std::max(1, (T + C - 1) / C);
-  Split p;
-  long long nseg = wgs > 0 ? kCUs / wgs : 1;
-  nseg = std::max(1LL, std::min(nseg, (long long)nch / kMinChunks));
-  const int per = (int)((nch + nseg - 1) / nseg);
-  p.nseg = std::max(1, (nch + per - 1) / per);
-  long long subs = heads > 0 && p.nseg > 1 ? (kCUs + heads * (p.nseg - 1) - 1) / (heads * (p.nseg - 1)) : 1;
-  subs = std::max(1LL, std::min(subs, (long long)per / 4));
-  const int sub = (int)((per + subs - 1) / subs);
-  p.subs = (per + sub - 1) / sub;
-  p.sub_rows = sub * C;
-  p.seg_rows = p.subs * p.sub_rows;   // whole sub-segments
-  p.nseg = std::max(1, (nch + p.subs * sub - 1) / (p.subs * sub));
-  p.nsub = (p.nseg - 1) * p.subs + 1;   // the last segment's start is the last one needed
-  return p;
+  Split best = {};
+  double least = 0.0;
+  for (int ds = 16; ds <= (dtype == CKDA_DTYPE_BF16 ? 128 : 64); ds *= 2) {
+    if (ds > 16 && ds > std::max(dk, dv)) break;
+    const long long sk = dk / slice_width(dk, ds), sv = dv / slice_width(dv, ds);
+    const long long wgs = heads * (backward ? 2 * sk + sv : sv);
+    // segments: none, two, three, or as many as fill the CUs once to four times
+    for (int i = 0; i < 7; ++i) {
+      const long long n = i < 3 ? i + 1 : kCUs * (i - 2) / std::max(1LL, wgs);
+      if (n < 1) continue;
+      Split p;
+      p.ds = ds;
+      int per = (int)((nch + n - 1) / n);   // chunks of a segment
+      if (n > 1 && per < 2) break;
+      p.nseg = (nch + per - 1) / per;
+      // sub-segments: two workgroups per CU, at least two chunks each
+      long long subs = 1;
+      if (p.nseg > 1 && heads > 0)
+        subs = std::max(1LL, std::min(2 * kCUs / std::max(1LL, heads * (p.nseg - 1)), (long long)per / 2));
+      const int sub = (int)((per + subs - 1) / subs);
+      p.subs = (per + sub - 1) / sub;
+      per = p.subs * sub;   // whole sub-segments
+      p.nseg = (nch + per - 1) / per;
+      p.sub_rows = sub * C;
+      p.seg_rows = per * C;
+      p.nsub = (p.nseg - 1) * p.subs + 1;   // the last segment's start is the last one needed
+      auto rounds = [&](long long wgs, long long at_once) { return (double)((wgs + at_once - 1) / at_once); };
+      auto sweep = [&](long long slices, int d1, int d2) {
+        return rounds(heads * slices * p.nseg, kCUs) *
+               (segment_us(d1, slice_width(d2, ds)) + per * chunk_us(d1, slice_width(d2, ds), dtype));
+      };
+      double us = !backward ? sweep(sv, dk, dv) : dk == dv ? sweep(2 * sk + sv, dk, dv) : sweep(sv, dk, dv) + sweep(2 * sk, dv, dk);
+      if (p.nseg > 1) {
+        // two launches more, the own states (two workgroups a CU take some 1.6
+        // times as long as one), and one pass over the states
+        const double own = rounds(heads * (p.nsub - 1), 2 * kCUs) * sub * own_chunk_us(dk, dv, dtype) * 1.6;
+        const double join = 3.0 + (double)heads * p.nsub * dk * dv * 8 / 4e6;
+        us += (backward ? 2 : 1) * (5.0 + own + join);
+      }
+      if (best.ds == 0 || us < least) {
+        best = p;
+        least = us;
+      }
+    }
+  }
+  return best;
 }
 
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -1138,7 +1204,7 @@ struct FwdPlan {
 static FwdPlan fwd_plan(int B, int H, int T, int dk, int dv, int dtype) {
   FwdPlan p;
   const size_t bh = (size_t)B * H;
-  p.sp = split_rows((long long)bh * (dv / slice_width(dv, dtype)), (long long)bh, T);
+  p.sp = plan_split((long long)bh, T, dk, dv, dtype, false);
   p.states = 0;
   p.decay = p.sp.nseg > 1 ? up256((size_t)p.sp.nsub * bh * dk * dv * 4) : 0;
   p.bytes = p.sp.nseg > 1 ? p.decay + up256((size_t)p.sp.nsub * bh * 4) : 0;
@@ -1200,7 +1266,7 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
     if (e != hipSuccess) return e;
   }
   SweepLaunch L = sweep_base(a);
-  const int ds = slice_width(a.dv, a.dtype);
+  const int ds = slice_width(a.dv, p.sp.ds);
   set_split(L, a, p.sp);
   L.nroles = 1;
   SweepRole& R = L.role[0];
@@ -1228,8 +1294,8 @@ struct BwdPlan {
 static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   BwdPlan p;
   const size_t bh = (size_t)B * H, elems = (size_t)dk * dv;
-  const int sk = dk / slice_width(dk, dtype), sv = dv / slice_width(dv, dtype);
-  p.sp = split_rows((long long)bh * (2 * sk + sv), (long long)bh, T);
+  p.sp = plan_split((long long)bh, T, dk, dv, dtype, true);
+  const int sk = dk / slice_width(dk, p.sp.ds);
   const size_t nsub = p.sp.nseg > 1 ? (size_t)p.sp.nsub : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -1256,7 +1322,7 @@ size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, 
 
 template <typename T>
 static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsigned char* ws) {
-  const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, a.dtype);
+  const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, p.sp.ds);
   double* sums = a.head_decay ? (double*)(ws + p.head_sum) : nullptr;
   hipError_t e = hipSuccess;
   if (bh > 0)
@@ -1293,7 +1359,7 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
     if ((e = segment_starts(a, true, p.sp, rstates, decay, a.dhT)) != hipSuccess) return e;
   }
   const bool grouped = a.H != a.Hk;
-  const int dsk = slice_width(a.dk, a.dtype), dsv = slice_width(a.dv, a.dtype);
+  const int dsk = slice_width(a.dk, p.sp.ds), dsv = slice_width(a.dv, p.sp.ds);
   SweepRole dv = {}, dk = {}, dq = {};
   dv.x = a.k;
   dv.y = a.q;
