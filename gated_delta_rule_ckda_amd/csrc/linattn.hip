@@ -77,9 +77,15 @@ struct SweepCfg {
   static constexpr int Z_OFF = Y_BYTES, ZS_OFF = Z_OFF + Z_BYTES, H_OFF = ZS_OFF + ZSETS * Z_BYTES;
   static constexpr int DEC_OFF = H_OFF + HSETS * H_BYTES, DEC_BYTES = kDecSets * C * 4;
   static constexpr int LDS_BYTES = DEC_OFF + 2 * DEC_BYTES;
-  // pieces of 16 bytes that the 512 threads copy
+  // Pieces of 16 bytes to copy, in units of one piece for each of 256 threads:
+  // by the state waves, but for the first YO units of Y and ZO of Z of the
+  // widest slices, which the output waves copy (a unit of Z costs some ten
+  // times one of Y, for its scaled terms).  Units are loaded NR chunks before
+  // they are copied; a chunk of a narrow slice takes less time than a load.
   static constexpr int YPR = D1 * E / 16, ZPR = ZROW / 16;
-  static constexpr int NY = (C * YPR + 511) / 512, NZ = (C * ZPR + 511) / 512;
+  static constexpr int NY = (C * YPR + 255) / 256, NZ = (C * ZPR + 255) / 256;
+  static constexpr int YO = DS == 128 ? NY / 2 : 0, ZO = DS == 128 ? NZ / 4 : 0;
+  static constexpr int NR = DS == 128 ? 1 : 2;
 };
 
 // Byte offset of the 16-byte piece `piece` of row `row` in an LDS array of
@@ -239,17 +245,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, size_
   return make_rsrc((const unsigned char*)p + head * rows * width * es, (uint32_t)(len * width * es));
 }
 // The log decay of row j of a sweep: reversed row j carries that of the row after it (the first has none).
+// As stored, in 32 bits; decay_of() widens it.
 template <typename T>
-__device__ __forceinline__ T load_decay(__amdgpu_buffer_rsrc_t gr, const Rows& R, int j, int reverse, int head_decay) {
+__device__ __forceinline__ uint32_t load_decay(__amdgpu_buffer_rsrc_t gr, const Rows& R, int j, int reverse, int head_decay) {
   const int at = reverse ? R.len - j : j;
   const int off = j < R.len && at < R.len ? (head_decay ? 0 : at * (int)sizeof(T)) : 0x7FFFFFF0;   // out of range: 0
-  if constexpr (sizeof(T) == 2) return T{(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0)};
-  else return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0));
+  if constexpr (sizeof(T) == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0);
+}
+template <typename T>
+__device__ __forceinline__ float decay_of(uint32_t w) {
+  pin(w);   // not widened before: that would wait for the load
+  return __uint_as_float(sizeof(T) == 2 ? w << 16 : w);
 }
 template <typename T>
 __device__ __forceinline__ const T* decays_of(const SweepLaunch& L, int bh) {
   return (const T*)L.g + (L.head_decay ? (size_t)(bh % L.heads) : (size_t)bh * L.rows);
 }
+__device__ __forceinline__ void pin4(u32x4& x) { asm volatile("" : "+v"(x)); }
+
 // N terms of wt z for the eight (four) elements of a piece, stored at p, p + stride, ..
 template <typename T, int N>
 __device__ __forceinline__ void store_scaled(unsigned char* p, int stride, Frag z, float wt) {
@@ -291,11 +305,11 @@ template <> struct Quad<bf16_t> {
   }
 };
 template <> struct Quad<float> {
-  typedef u32x4 Raw;
+  typedef f32x4 Raw;
   static __device__ __forceinline__ Raw load(__amdgpu_buffer_rsrc_t b, int off) {
-    return __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
   }
-  static __device__ __forceinline__ float get(Raw w, int j) { return __uint_as_float(w[j]); }
+  static __device__ __forceinline__ float get(Raw w, int j) { return w[j]; }
 };
 
 // EXACT: states with three bf16 terms (one is returned), else two.
@@ -323,44 +337,57 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
   };
   unsigned char *ly = lds, *lz = lds + S::Z_OFF, *lzs = lds + S::ZS_OFF, *lh = lds + S::H_OFF;
 
-  // All waves copy Y, Z and the scaled Z to LDS, a chunk ahead in registers.
-  // Loads and copies run on past the last chunk (the last one again, into
-  // buffers nobody reads): a conditional load would make every wait for an
-  // older one wait for all loads in flight.
+  // Copies of Y, Z and the scaled Z to LDS, a chunk ahead in registers: units
+  // y0 .. y1 - 1 of Y and z0 .. z1 - 1 of Z.  Loads and copies run on past the
+  // last chunk (the last one again, into buffers nobody reads): a conditional
+  // load would make every wait for an older one wait for all loads in flight.
   const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared ? unit : bh, L.rows, len, D1, E);
   const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared ? unit : bh, L.rows, len, A.d2, E);
-  Frag yv[S::NY], zv[S::NZ];
-  auto load = [&](int c) __attribute__((always_inline)) {
+  const int ct = tid & 255;
+  constexpr int YM = S::NY - S::YO, ZM = S::NZ - S::ZO;   // (the state waves have the most)
+  struct Units {
+    Frag y[YM], z[ZM];
+  };
+  auto load = [&](Units& u, int c, auto state) __attribute__((always_inline)) {
+    constexpr bool ST = decltype(state)::value;
+    constexpr int y0 = ST ? S::YO : 0, ny = ST ? YM : S::YO, z0 = ST ? S::ZO : 0, nz = ST ? ZM : S::ZO;
 #pragma unroll
-    for (int j = 0; j < S::NY; ++j) {
-      const int p = tid + 512 * j;
-      yv[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, R.row(C * c + p / S::YPR) * D1 * E + (p % S::YPR) * 16, 0, 0);
+    for (int j = 0; j < ny; ++j) {
+      const int p = ct + 256 * (y0 + j);
+      u.y[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, R.row(C * c + p / S::YPR) * D1 * E + (p % S::YPR) * 16, 0, 0);
     }
 #pragma unroll
-    for (int j = 0; j < S::NZ; ++j) {
-      const int p = tid + 512 * j;
-      zv[j].w = __builtin_amdgcn_raw_buffer_load_b128(
+    for (int j = 0; j < nz; ++j) {
+      const int p = ct + 256 * (z0 + j);
+      u.z[j].w = __builtin_amdgcn_raw_buffer_load_b128(
           zr, (R.row(C * c + p / S::ZPR) * A.d2 + slice * DS) * E + (p % S::ZPR) * 16, 0, 0);
     }
   };
-  auto place = [&](int c) __attribute__((always_inline)) {
+  auto place = [&](Units& u, int c, auto state) __attribute__((always_inline)) {
+    constexpr bool ST = decltype(state)::value;
+    constexpr int y0 = ST ? S::YO : 0, ny = ST ? YM : S::YO, z0 = ST ? S::ZO : 0, nz = ST ? ZM : S::ZO;
     const float* dec = dec_of(c);
+    // the copies' uses of the loads are tied to here: moved up into an earlier
+    // phase they would make it wait for them
 #pragma unroll
-    for (int j = 0; j < S::NY; ++j) {
-      const int p = tid + 512 * j;
-      if (C * S::YPR % 512 == 0 || p < C * S::YPR) store_frag(ly + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), yv[j]);
+    for (int j = 0; j < ny; ++j) pin4(u.y[j].w);
+#pragma unroll
+    for (int j = 0; j < nz; ++j) pin4(u.z[j].w);
+#pragma unroll
+    for (int j = 0; j < ny; ++j) {
+      const int p = ct + 256 * (y0 + j);
+      if (C * S::YPR % 256 == 0 || p < C * S::YPR) store_frag(ly + lds_piece<S::YROW>(p / S::YPR, p % S::YPR), u.y[j]);
     }
 #pragma unroll
-    for (int j = 0; j < S::NZ; ++j) {
-      const int p = tid + 512 * j;
-      if (C * S::ZPR % 512 == 0 || p < C * S::ZPR) {
+    for (int j = 0; j < nz; ++j) {
+      const int p = ct + 256 * (z0 + j);
+      if (C * S::ZPR % 256 == 0 || p < C * S::ZPR) {
         const int off = lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR);
-        store_frag(lz + off, zv[j]);
-        store_scaled<T, S::ZSETS>(lzs + off, S::Z_BYTES, zv[j], dec[3 * C + p / S::ZPR]);
+        store_frag(lz + off, u.z[j]);
+        store_scaled<T, S::ZSETS>(lzs + off, S::Z_BYTES, u.z[j], dec[3 * C + p / S::ZPR]);
       }
     }
   };
-  load(0);
 
   if (wave < 4) {
     // ============================================================ output waves
@@ -382,10 +409,13 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         xf[kb].w = __builtin_amdgcn_raw_buffer_load_b128(xr, D1 < S::KB && g * 16 >= D1 * E ? 0x7FFFFFF0 : off, 0, 0);
       }
     };
+    constexpr std::false_type OUTPUT{};
+    Units u0;
+    load(u0, 0, OUTPUT);
     load_x(0);
     lds_barrier();   // the first decay factors are there
-    place(0);
-    load(min(1, R.last));
+    place(u0, 0, OUTPUT);
+    load(u0, min(1, R.last), OUTPUT);
     lds_barrier();   // the first operands are there
     // One copy of the loop per wave: W, the wave's row tile, fixes how many
     // tiles of P it has, and DOT whether it forms the dots, so that the body is
@@ -497,6 +527,8 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         if constexpr (DOT) {   // this slice's part of w_t . out_t
           float x = 0.f;
 #pragma unroll
+          for (int d = 0; d < NDV; ++d) pin(wv[d]);
+#pragma unroll
           for (int d = 0; d < NDV; ++d)
 #pragma unroll
             for (int j = 0; j < 4; ++j) x = __builtin_fmaf(Quad<T>::get(wv[d], j), oacc[d][j], x);
@@ -505,8 +537,8 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
           if (g == 0 && (unsigned)row < (unsigned)len)
             A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
         }
-        place(c + 1);
-        load(min(c + 2, R.last));
+        place(u0, c + 1, OUTPUT);
+        load(u0, min(c + 2, R.last), OUTPUT);
         lds_barrier();
       }
     };
@@ -526,7 +558,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
     const int ct0 = (sw % S::WC) * TC, rt0 = (sw / S::WC) * TR;   // this wave's first column and row tile
     const T* gp = decays_of<T>(L, bh);
     const __amdgpu_buffer_rsrc_t gr = make_rsrc(gp, (uint32_t)((L.head_decay ? 1 : len) * E));
-    T gv;   // the next chunk's log decays as stored: widened when used, so that loading does not wait
+    uint32_t gv;   // the next chunk's log decay of row `lane`
     auto load_g = [&](int c) __attribute__((always_inline)) {
       gv = load_decay<T>(gr, R, R.row0 + C * c + lane, A.reverse, L.head_decay);
     };
@@ -581,7 +613,11 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
           }
         }
     };
+    constexpr std::true_type STATE{};
+    Units u0, u1;   // of even chunks and of odd ones (NR == 1: u0 of all)
     load_g(0);
+    load(u0, 0, STATE);
+    if constexpr (S::NR == 2) load(u1, min(1, R.last), STATE);
     if constexpr (S::D1P != D1) {
       // half K blocks: the columns behind D1 are zero for good
       for (int p = tid - 256; p < 2 * (C > DS ? C : DS); p += 256) {
@@ -593,18 +629,18 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         }
       }
     }
-    if (sw == 0) decay_factors(to_f32(gv), dec_of(0), lane);
+    if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane);
     put_state();
     lds_barrier();   // the first decay factors are there
-    place(0);
+    place(u0, 0, STATE);
     load_g(min(1, R.last));
-    load(min(1, R.last));
+    load(u0, min(S::NR, R.last), STATE);
     lds_barrier();   // the first operands are there
-    for (int c = 0; c < nch; ++c) {
+    auto chunk = [&](int c, Units& next) __attribute__((always_inline)) {
       // ---- phase 1.  A operand: the columns of Y this wave's row tiles are;
       // B operand: the terms of G(C, s) z_s for its column tile
       const float end = dec_of(c)[2 * C + C - 1];
-      if (sw == 0) decay_factors(to_f32(gv), dec_of(c + 1), lane);
+      if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane);
 #pragma unroll
       for (int i = 0; i < TR; ++i)
 #pragma unroll
@@ -634,15 +670,20 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         multiply(kb - KA);
         read(kb);
       }
-      lds_barrier();   // everything is read; the products run on into phase 2
 #pragma unroll
       for (int kb = KBC - KA; kb < KBC; ++kb) multiply(kb);
+      lds_barrier();
       // ---- phase 2
-      place(c + 1);
+      place(next, c + 1, STATE);
       load_g(min(c + 2, R.last));
-      load(min(c + 2, R.last));
+      load(next, min(c + 1 + S::NR, R.last), STATE);
       put_state();
       lds_barrier();
+    };
+    for (int c = 0; c < nch; c += 2) {
+      chunk(c, S::NR == 2 ? u1 : u0);
+      if (c + 1 >= nch) break;
+      chunk(c + 1, u0);
     }
     // the final state, of the last segment
     if (A.fin && seg == L.nseg - 1) {
@@ -706,7 +747,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
   const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared ? unit : bh, L.rows, R.len, D2, E);
   const __amdgpu_buffer_rsrc_t gr = make_rsrc(decays_of<T>(L, bh), (uint32_t)((L.head_decay ? 1 : R.len) * E));
   Frag yv[S::NY], zv[S::NZ];
-  T gv;
+  uint32_t gv;
   auto load = [&](int c) __attribute__((always_inline)) {
     gv = load_decay<T>(gr, R, R.row0 + C * c + lane, A.reverse, L.head_decay);
 #pragma unroll
@@ -722,6 +763,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
   };
   auto place = [&](int c) __attribute__((always_inline)) {
     const float* dec = dec_of(c);
+#pragma unroll
+    for (int j = 0; j < S::NY; ++j) pin4(yv[j].w);
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) pin4(zv[j].w);
 #pragma unroll
     for (int j = 0; j < S::NY; ++j) {
       const int p = tid + 512 * j;
@@ -750,14 +795,14 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
 #pragma unroll
     for (int j = 0; j < S::TC; ++j) h[i][j] = zero4();
   load(0);
-  if (wave == 0) decay_factors(to_f32(gv), dec_of(0), lane);
+  if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane);
   lds_barrier();
   place(0);
   load(min(1, R.last));
   lds_barrier();
   float decay = 1.f;   // product of the chunks' decays
   for (int c = 0; c < R.nch; ++c) {
-    if (wave == 0) decay_factors(to_f32(gv), dec_of(c + 1), lane);
+    if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane);
     const float end = dec_of(c)[2 * C + C - 1];
     decay *= end;
 #pragma unroll
