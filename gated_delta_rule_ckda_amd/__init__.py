@@ -451,9 +451,15 @@ def deltaproduct2_bwd(q, k, v, alpha, beta, do, h0=None, dhT=None, want_dh0=True
 
 def _tensors(device, expect):
     """Checks of shape, dtype, contiguity and device for `expect`, a list of
-    (name, tensor or None, shape, dtype); all tensors must be on `device`.
-    Shapes first: the C ABI cannot see them."""
-    for name, t, shape, _ in expect:
+    (name, tensor or None, shape, dtype); all tensors must be on `device`, a
+    GPU.  The C ABI cannot see any of these."""
+    index = device.index if device.type == "cuda" else -2
+    for _, t, shape, dtype in expect:
+        if t is not None and (t.shape != shape or t.dtype != dtype or t.get_device() != index or not t.is_contiguous()):
+            break
+    else:
+        return
+    for name, t, shape, _ in expect:   # shapes first
         if t is not None and t.shape != shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     for name, t, _, dtype in expect:
@@ -477,10 +483,12 @@ def _run(device, stream, fn, *args):
     elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
     if device.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream))
+        status = fn(*args, stream.cuda_stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+            status = fn(*args, stream.cuda_stream)
+    if status:
+        _check(status)
 
 
 def _workspace_arg(workspace, need, device, stream):
@@ -493,21 +501,29 @@ def _workspace_arg(workspace, need, device, stream):
     return workspace, (workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
-def _fresh(shape, dtype, device, stream, zero=False):
-    """A new tensor for one call, made (and zeroed) on the stream the kernels
-    run on, so that its memory cannot still be in use by earlier work of
-    another stream; also tied to the current stream, where the caller may use
-    it before it is freed."""
-    make = torch.zeros if zero else torch.empty
+def _fresh(shape, dtype, device, stream):
+    """A new tensor for one call, made on the stream the kernels run on, so
+    that its memory cannot still be in use by earlier work of another stream;
+    also tied to the current stream, where the caller may use it before it is
+    freed."""
     if stream is None:
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     current = torch.cuda.current_stream(device)
     if stream == current:
-        return make(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = make(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(current)
     return t
+
+
+def _zero(tensors, stream):
+    """Zeroes the tensors in one launch, on the stream the kernels run on."""
+    if stream is None:
+        torch._foreach_zero_(tensors)
+    else:
+        with torch.cuda.stream(stream):
+            torch._foreach_zero_(tensors)
 
 
 def _linattn_dims(q, v, g, lead):
@@ -553,7 +569,9 @@ def linattn_fwd(q, k, v, g, h0=None, lens=None, workspace=None, o=None, hT=None,
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     if o is None:
-        o = _fresh((B, H, T, dv), dt, dev, stream, zero=lens is not None)
+        o = _fresh((B, H, T, dv), dt, dev, stream)
+        if lens is not None:
+            _zero([o], stream)
     if hT is None and want_state:
         hT = _fresh((B, H, dk, dv), f32, dev, stream)
     _run(dev, stream, L.ckda_linattn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(lens),
@@ -579,10 +597,11 @@ def linattn_bwd(q, k, v, g, do, h0=None, dhT=None, lens=None, want_dh0=True, wor
     if need == 0:
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
-    zero = lens is not None
-    gq, gk = (_fresh((B, Hk, T, dk), dt, dev, stream, zero) for _ in range(2))
-    gv = _fresh((B, H, T, dv), dt, dev, stream, zero)
-    gg = _fresh(g.shape, dt, dev, stream, zero)
+    gq, gk = (_fresh((B, Hk, T, dk), dt, dev, stream) for _ in range(2))
+    gv = _fresh((B, H, T, dv), dt, dev, stream)
+    gg = _fresh(g.shape, dt, dev, stream)
+    if lens is not None:
+        _zero([gq, gk, gv, gg], stream)
     gh0 = _fresh((B, H, dk, dv), f32, dev, stream) if want_dh0 else None
     _run(dev, stream, L.ckda_linattn_bwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(h0), _ptr(lens),
          do.data_ptr(), _ptr(dhT), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), gg.data_ptr(), _ptr(gh0), B, H, Hk, T, dk,

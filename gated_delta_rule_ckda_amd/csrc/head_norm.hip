@@ -34,24 +34,30 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kActNone = 0, kActSilu = CKDA_NORM_GATE_SILU, kActSigmoid = CKDA_NORM_GATE_SIGMOID;
 
-// VEC consecutive elements, widened
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float* v) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f32(*p);
-  } else if constexpr (sizeof(T) == 2) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+// VEC consecutive elements (16 bytes, or one element): as loaded, and widened
+template <typename T, int VEC> struct Vec {
+  u32x4 w;
+  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void clear() { w = u32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ void widen(float* v) const {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo_half(w[i]);
-      v[2 * i + 1] = bf16_hi_half(w[i]);
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_lo_half(w[i]);
+        v[2 * i + 1] = bf16_hi_half(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
     }
-  } else {
-    const f32x4 w = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = w[i];
   }
-}
+};
+template <typename T> struct Vec<T, 1> {
+  T w;
+  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void clear() { w = from_f32<T>(0.f); }
+  __device__ __forceinline__ void widen(float* v) const { v[0] = to_f32(w); }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void store_vec(T* p, const float* v) {
   if constexpr (VEC == 1) {
@@ -66,7 +72,14 @@ __device__ __forceinline__ void store_vec(T* p, const float* v) {
   }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + expf(-z)); }
+// sigmoid(z).  With bf16 outputs by the hardware's exp2 and reciprocal (a few
+// 2^-23, against an output rounding of 2^-8): the library's exponential and
+// division are half of the backward's vector instructions, which then bound it.
+template <typename T> __device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (sizeof(T) == 2)
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.4426950408889634f));
+  else return 1.f / (1.f + expf(-z));
+}
 
 // Sum over the LPR lanes of a row; 256 lanes (the workgroup) go through LDS,
 // in one of two alternating buffers so that one barrier per sum is enough.
@@ -84,6 +97,9 @@ __device__ __forceinline__ float row_sum(float x, float (*s)[kNormThreads / 64],
   }
 }
 
+// Rows of one lane group whose loads are in flight together.
+constexpr int rows_in_flight(int n, bool bwd) { return n <= 8 ? (bwd ? 2 : 4) : 1; }
+
 struct RowGeom {
   int H, T, D, rows, slab_rows;   // rows = B T of one head
 };
@@ -94,6 +110,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
                                                                  RowGeom G, int w_shared, int act, int rms, float eps) {
   constexpr int GPW = kNormThreads / LPR;   // rows in flight per workgroup
   constexpr int N = NV * VEC;
+  constexpr int U = rows_in_flight(N, BWD);
   __shared__ float s_sum[2][kNormThreads / 64];
   const int tid = threadIdx.x, lane = tid % LPR, grp = tid / LPR;
   const int h = blockIdx.y;
@@ -119,89 +136,102 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
     for (int i = 0; i < N; ++i) dw[i] = db[i] = 0.f;
   }
 
-  for (int base = row0; base < row1; base += GPW) {   // the same trips for every lane of the workgroup
-    const int n = base + grp;
-    const bool live = n < row1;
-    const int bi = (live ? n : row0) / G.T, t = (live ? n : row0) % G.T;
-    const size_t xo = (((size_t)bi * G.H + h) * G.T + t) * D;   // head-major row
-    const size_t yo = (((size_t)bi * G.T + t) * G.H + h) * D;   // token-major row
-    float xv[N], zv[N], gv[BWD ? N : 1];
+  for (int base = row0; base < row1; base += U * GPW) {   // the same trips for every lane of the workgroup
+    // the loads of U rows first
+    Vec<T, VEC> xr[U][NV], zr[U][NV], gr[U][BWD ? NV : 1];
+    bool live[U];
+    size_t xo[U], yo[U];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * VEC;
-      const bool in = live && c < D;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        xv[v * VEC + e] = zv[v * VEC + e] = 0.f;
-        if constexpr (BWD) gv[v * VEC + e] = 0.f;
-      }
-      if (in) {
-        load_vec<T, VEC>(x + xo + c, xv + v * VEC);
-        if (act) load_vec<T, VEC>(z + yo + c, zv + v * VEC);
-        if constexpr (BWD) load_vec<T, VEC>(dy + yo + c, gv + v * VEC);
-      }
-    }
-    float mean = 0.f;
-    if (!rms) {
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum += xv[i];
-      mean = row_sum<LPR>(sum, s_sum, phase) * inv_d;
-    }
-    float sq = 0.f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const int i = v * VEC + e;
-        xv[i] = (v * LPR + lane) * VEC + e < D ? xv[i] - mean : 0.f;
-        sq = __builtin_fmaf(xv[i], xv[i], sq);
-      }
-    const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, s_sum, phase) * inv_d + eps);
-    if constexpr (!BWD) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float y = __builtin_fmaf(xv[i] * rstd, wv[i], bv[i]);
-        if (act) {
-          const float sg = sigmoid(zv[i]);
-          y *= act == kActSilu ? zv[i] * sg : sg;
-        }
-        xv[i] = y;
-      }
+    for (int u = 0; u < U; ++u) {
+      const int n = base + u * GPW + grp;
+      live[u] = n < row1;
+      const int bi = (live[u] ? n : row0) / G.T, t = (live[u] ? n : row0) - bi * G.T;
+      xo[u] = (((size_t)bi * G.H + h) * G.T + t) * D;   // head-major row
+      yo[u] = (((size_t)bi * G.T + t) * G.H + h) * D;   // token-major row
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * LPR + lane) * VEC;
-        if (live && c < D) store_vec<T, VEC>(out + yo + c, xv + v * VEC);
-      }
-    } else {
-      float m1 = 0.f, m2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float nn = xv[i] * rstd;
-        float u = gv[i];
-        if (act) {
-          const float sg = sigmoid(zv[i]);
-          const float slope = act == kActSilu ? sg * __builtin_fmaf(zv[i], 1.f - sg, 1.f) : sg * (1.f - sg);
-          u *= act == kActSilu ? zv[i] * sg : sg;
-          zv[i] = gv[i] * __builtin_fmaf(nn, wv[i], bv[i]) * slope;   // dz
+        xr[u][v].clear();
+        zr[u][v].clear();
+        if constexpr (BWD) gr[u][v].clear();
+        if (live[u] && c < D) {
+          xr[u][v].load(x + xo[u] + c);
+          if (act) zr[u][v].load(z + yo[u] + c);
+          if constexpr (BWD) gr[u][v].load(dy + yo[u] + c);
         }
-        dw[i] = __builtin_fmaf(u, nn, dw[i]);
-        db[i] += u;
-        xv[i] = nn;
-        gv[i] = u * wv[i];   // dn
-        m1 += gv[i];
-        m2 = __builtin_fmaf(gv[i], nn, m2);
       }
-      m1 = rms ? 0.f : row_sum<LPR>(m1, s_sum, phase) * inv_d;
-      m2 = row_sum<LPR>(m2, s_sum, phase) * inv_d;
+    }
 #pragma unroll
-      for (int i = 0; i < N; ++i) xv[i] = rstd * (gv[i] - m1 - xv[i] * m2);
+    for (int u = 0; u < U; ++u) {
+      float xv[N], zv[N], gv[BWD ? N : 1];
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        const int c = (v * LPR + lane) * VEC;
-        if (live && c < D) {
-          store_vec<T, VEC>(out + xo + c, xv + v * VEC);
-          if (act) store_vec<T, VEC>(dz + yo + c, zv + v * VEC);
+        xr[u][v].widen(xv + v * VEC);
+        zr[u][v].widen(zv + v * VEC);
+        if constexpr (BWD) gr[u][v].widen(gv + v * VEC);
+      }
+      float mean = 0.f;
+      if (!rms) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum += xv[i];
+        mean = row_sum<LPR>(sum, s_sum, phase) * inv_d;
+      }
+      float sq = 0.f;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const int i = v * VEC + e;
+          xv[i] = (v * LPR + lane) * VEC + e < D ? xv[i] - mean : 0.f;
+          sq = __builtin_fmaf(xv[i], xv[i], sq);
+        }
+      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, s_sum, phase) * inv_d + eps);
+      if constexpr (!BWD) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float y = __builtin_fmaf(xv[i] * rstd, wv[i], bv[i]);
+          if (act) {
+            const float sg = sigmoid<T>(zv[i]);
+            y *= act == kActSilu ? zv[i] * sg : sg;
+          }
+          xv[i] = y;
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = (v * LPR + lane) * VEC;
+          if (live[u] && c < D) store_vec<T, VEC>(out + yo[u] + c, xv + v * VEC);
+        }
+      } else {
+        float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float nn = xv[i] * rstd;
+          float u = gv[i];
+          if (act) {
+            const float sg = sigmoid<T>(zv[i]);
+            const float slope = act == kActSilu ? sg * __builtin_fmaf(zv[i], 1.f - sg, 1.f) : sg * (1.f - sg);
+            u *= act == kActSilu ? zv[i] * sg : sg;
+            zv[i] = gv[i] * __builtin_fmaf(nn, wv[i], bv[i]) * slope;   // dz
+          }
+          dw[i] = __builtin_fmaf(u, nn, dw[i]);
+          db[i] += u;
+          xv[i] = nn;
+          gv[i] = u * wv[i];   // dn
+          m1 += gv[i];
+          m2 = __builtin_fmaf(gv[i], nn, m2);
+        }
+        m1 = rms ? 0.f : row_sum<LPR>(m1, s_sum, phase) * inv_d;
+        m2 = row_sum<LPR>(m2, s_sum, phase) * inv_d;
+#pragma unroll
+        for (int i = 0; i < N; ++i) xv[i] = rstd * (gv[i] - m1 - xv[i] * m2);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = (v * LPR + lane) * VEC;
+          if (live[u] && c < D) {
+            store_vec<T, VEC>(out + xo[u] + c, xv + v * VEC);
+            if (act) store_vec<T, VEC>(dz + yo[u] + c, zv + v * VEC);
+          }
         }
       }
     }
@@ -298,10 +328,9 @@ NormShape norm_shape(int D, int dtype) {
 int slab_rows(int rows, int H, int lpr, bool bwd) {
   const int gpw = kNormThreads / lpr;
   const long long most = std::max(1, (bwd ? 2048 : 4096) / H);
-  long long per = 4LL * gpw;
+  const long long unit = 4LL * gpw;
   const long long need = (rows + most - 1) / most;
-  if (per < need) per = (need + gpw - 1) / gpw * gpw;
-  return (int)per;
+  return (int)std::max(unit, (need + unit - 1) / unit * unit);
 }
 
 template <typename T, int VEC, int LPR, int NV>

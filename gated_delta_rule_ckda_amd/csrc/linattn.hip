@@ -946,7 +946,10 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 //   dg_t = <dhT, H_T> + sum_{u >= t} (a_u - b_u),
 // a running sum from the sequence's end.  The sweeps leave the parts of a and b
 // per slice, taken from their unrounded outputs; the sum runs in fp64.
-// One workgroup per (batch, head), four rows per thread.
+// One workgroup per (batch, head), four rows per thread; of a constant decay,
+// whose gradient is the sum over rows and batch, either each (batch, head)
+// leaves its sum for a second kernel, or, where a batch holds few rows, one
+// workgroup per head takes the batch entries in turn (`batches` of them).
 constexpr int kDgThreads = 1024;
 
 __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
@@ -961,11 +964,10 @@ __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
 template <typename T>
 __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dotq, const float* dotk, int slices,
                                                                 const float* dhT, const float* hT, int elems,
-                                                                const int* lens, int rows, int heads, int nbh, T* dg,
-                                                                double* head_sum) {
+                                                                const int* lens, int rows, int heads, int nbh, int batches,
+                                                                T* dg, double* head_sum, int head_decay) {
   __shared__ double s_wave[kDgThreads / 64], s_total;
-  const int bh = blockIdx.x, tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int len = lens ? min(max(lens[bh / heads], 0), rows) : rows;
+  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   // sum over the workgroup, and the exclusive prefix of this thread
   auto scan = [&](double x, double& total) __attribute__((always_inline)) {
     const double inc = wave_prefix_f64(x, lane);
@@ -983,42 +985,50 @@ __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dot
     __syncthreads();
     return before;
   };
-  double carry = 0.0;
-  if (dhT) {
-    double x = 0.0;
-    for (int i = tid; i < elems; i += kDgThreads) x += (double)dhT[(size_t)bh * elems + i] * hT[(size_t)bh * elems + i];
-    scan(x, carry);
-  }
   double sum = 0.0;
-  for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
-    double d[4], mine = 0.0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = len - 1 - (base + 4 * tid + j);
+  for (int b = 0; b < batches; ++b) {
+    const int bh = b * heads + blockIdx.x;
+    const int len = lens ? min(max(lens[bh / heads], 0), rows) : rows;
+    double carry = 0.0;
+    if (dhT) {
       double x = 0.0;
-      if (row >= 0)
-        for (int s = 0; s < slices; ++s) {
-          const size_t at = ((size_t)s * nbh + bh) * rows + row;
-          x += (double)dotq[at] - (double)dotk[at];
-        }
-      mine += x;
-      d[j] = mine;
+      for (int i = tid; i < elems; i += kDgThreads)
+        x += (double)dhT[(size_t)bh * elems + i] * hT[(size_t)bh * elems + i];
+      scan(x, carry);
     }
-    double total;
-    const double before = carry + scan(mine, total);
+    for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
+      double d[4], mine = 0.0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = len - 1 - (base + 4 * tid + j);
-      if (row < 0) continue;
-      if (head_sum) sum += before + d[j];
-      else dg[(size_t)bh * rows + row] = from_f32<T>((float)(before + d[j]));
+      for (int j = 0; j < 4; ++j) {
+        const int row = len - 1 - (base + 4 * tid + j);
+        double x = 0.0;
+        if (row >= 0)
+          for (int s = 0; s < slices; ++s) {
+            const size_t at = ((size_t)s * nbh + bh) * rows + row;
+            x += (double)dotq[at] - (double)dotk[at];
+          }
+        mine += x;
+        d[j] = mine;
+      }
+      double total;
+      const double before = carry + scan(mine, total);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = len - 1 - (base + 4 * tid + j);
+        if (row < 0) continue;
+        if (head_decay) sum += before + d[j];
+        else dg[(size_t)bh * rows + row] = from_f32<T>((float)(before + d[j]));
+      }
+      carry += total;
     }
-    carry += total;
   }
-  if (head_sum) {
+  if (head_decay) {
     double total;
     scan(sum, total);
-    if (tid == 0) head_sum[bh] = total;
+    if (tid == 0) {
+      if (head_sum) head_sum[blockIdx.x] = total;
+      else dg[blockIdx.x] = from_f32<T>((float)total);
+    }
   }
 }
 
@@ -1034,8 +1044,11 @@ __global__ __launch_bounds__(64) void head_decay_grad_kernel(const double* head_
 // Gradients of a query or key shared by `group` heads: the sum of the heads'
 // fp32 parts [units, group, rows, d], rounded once.  Four elements per thread.
 template <typename T>
-__global__ __launch_bounds__(256) void fold_heads_kernel(const float* parts, int units, int group, int rows, int d,
-                                                         const int* lens, int units_per_batch, T* out) {
+__global__ __launch_bounds__(256) void fold_heads_kernel(const float* qparts, const float* kparts, int units, int group,
+                                                         int rows, int d, const int* lens, int units_per_batch, T* dq,
+                                                         T* dk) {
+  const float* parts = blockIdx.y ? kparts : qparts;
+  T* out = blockIdx.y ? dk : dq;
   const long long per = (long long)rows * d;
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= units * per) return;
@@ -1368,14 +1381,18 @@ size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, 
 template <typename T>
 static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsigned char* ws) {
   const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, p.sp.ds);
-  double* sums = a.head_decay ? (double*)(ws + p.head_sum) : nullptr;
+  // (a workgroup takes 4 rows per thread at a time)
+  const bool in_turn = a.head_decay && (long long)a.B * a.T <= 2 * 4 * kDgThreads;
+  double* sums = a.head_decay && !in_turn ? (double*)(ws + p.head_sum) : nullptr;
   hipError_t e = hipSuccess;
-  if (bh > 0)
-    hipLaunchKernelGGL((decay_grad_kernel<T>), dim3(bh), dim3(kDgThreads), 0, a.stream, (const float*)(ws + p.dotq),
-                       (const float*)(ws + p.dotk), slices, a.dhT, (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T,
-                       a.H, bh, (T*)a.dg, sums);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (a.head_decay) {
+  if (bh > 0 || in_turn) {
+    hipLaunchKernelGGL((decay_grad_kernel<T>), dim3(in_turn ? a.H : bh), dim3(kDgThreads), 0, a.stream,
+                       (const float*)(ws + p.dotq), (const float*)(ws + p.dotk), slices, a.dhT,
+                       (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T, a.H, bh, in_turn ? a.B : 1, (T*)a.dg, sums,
+                       a.head_decay);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (sums) {
     hipLaunchKernelGGL((head_decay_grad_kernel<T>), dim3((a.H + 63) / 64), dim3(64), 0, a.stream, sums, a.B, a.H,
                        (T*)a.dg);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1383,12 +1400,10 @@ static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsign
   if (a.H != a.Hk && bh > 0 && a.T > 0) {
     const int units = a.B * a.Hk;
     const long long threads = (long long)units * a.T * a.dk / 4;
-    for (int i = 0; i < 2; ++i) {
-      hipLaunchKernelGGL((fold_heads_kernel<T>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, a.stream,
-                         (const float*)(ws + (i ? p.dk : p.dq)), units, a.H / a.Hk, a.T, a.dk, a.lens, a.Hk,
-                         (T*)(i ? a.dk_out : a.dq));
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    hipLaunchKernelGGL((fold_heads_kernel<T>), dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, a.stream,
+                       (const float*)(ws + p.dq), (const float*)(ws + p.dk), units, a.H / a.Hk, a.T, a.dk, a.lens, a.Hk,
+                       (T*)a.dq, (T*)a.dk_out);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
 }
