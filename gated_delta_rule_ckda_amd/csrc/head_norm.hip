@@ -13,7 +13,7 @@
 // touched once anyway.
 //
 // HBM-bound: every tensor is read or written once.  LPR lanes hold one row in
-// registers (NV vectors of VEC elements each, 16 bytes where the width allows),
+// registers (NV vectors of VEC elements each, 16 bytes but for odd bf16 widths),
 // so the row's sums (mean, centred square sum, and in the backward the two
 // means of dn) are DPP sums over the lane group (over the workgroup for rows
 // of more than 64 x 4 vectors).  The statistics are recomputed in the backward
@@ -34,10 +34,22 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kActNone = 0, kActSilu = CKDA_NORM_GATE_SILU, kActSigmoid = CKDA_NORM_GATE_SIGMOID;
 
-// VEC consecutive elements (16 bytes, or one element): as loaded, and widened
+// 16 bytes at a 4-byte boundary (global memory takes these at full width)
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4), aligned(4)));
+
+// VEC consecutive elements (16 bytes, or one element): as loaded, and widened.
+// `left` is how many of them the row still has: a row's last vector may be short.
 template <typename T, int VEC> struct Vec {
   u32x4 w;
-  __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const u32x4*>(p); }
+  __device__ __forceinline__ void load(const T* p, int left) {
+    if (left >= VEC) {
+      w = *reinterpret_cast<const u32x4a*>(p);
+    } else {
+      const uint32_t* d = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = i * VEC / 4 < left ? d[i] : 0u;
+    }
+  }
   __device__ __forceinline__ void clear() { w = u32x4{0, 0, 0, 0}; }
   __device__ __forceinline__ void widen(float* v) const {
     if constexpr (sizeof(T) == 2) {
@@ -54,21 +66,29 @@ template <typename T, int VEC> struct Vec {
 };
 template <typename T> struct Vec<T, 1> {
   T w;
-  __device__ __forceinline__ void load(const T* p) { w = *p; }
+  __device__ __forceinline__ void load(const T* p, int) { w = *p; }
   __device__ __forceinline__ void clear() { w = from_f32<T>(0.f); }
   __device__ __forceinline__ void widen(float* v) const { v[0] = to_f32(w); }
 };
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float* v) {
+__device__ __forceinline__ void store_vec(T* p, const float* v, int left) {
   if constexpr (VEC == 1) {
     *p = from_f32<T>(v[0]);
-  } else if constexpr (sizeof(T) == 2) {
+  } else {
     u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<u32x4*>(p) = w;
-  } else {
-    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 2) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      else w[i] = __float_as_uint(v[i]);
+    }
+    if (left >= VEC) {
+      *reinterpret_cast<u32x4a*>(p) = w;
+    } else {
+      uint32_t* d = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i * VEC / 4 < left) d[i] = w[i];
+    }
   }
 }
 
@@ -81,19 +101,24 @@ template <typename T> __device__ __forceinline__ float sigmoid(float z) {
   else return 1.f / (1.f + expf(-z));
 }
 
-// Sum over the LPR lanes of a row; 256 lanes (the workgroup) go through LDS,
-// in one of two alternating buffers so that one barrier per sum is enough.
-template <int LPR>
-__device__ __forceinline__ float row_sum(float x, float (*s)[kNormThreads / 64], int& phase) {
-  if constexpr (LPR <= 64) {
-    return group_sum<LPR>(x);
-  } else {
-    x = group_sum<64>(x);
-    float* buf = s[phase];
+// K sums at once over the LPR lanes of a row; 256 lanes (the workgroup) go
+// through LDS, in one of two alternating buffers so that one barrier is enough.
+constexpr int kMostSums = 8;
+template <int LPR, int K>
+__device__ __forceinline__ void row_sums(float (&x)[K], float (*s)[kMostSums][kNormThreads / 64], int& phase) {
+  static_assert(K <= kMostSums, "sums at once");
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = group_sum<(LPR < 64 ? LPR : 64)>(x[k]);
+  if constexpr (LPR > 64) {
+    float(*buf)[kNormThreads / 64] = s[phase];
     phase ^= 1;
-    if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = x;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) buf[k][threadIdx.x >> 6] = x[k];
+    }
     __syncthreads();
-    return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = (buf[k][0] + buf[k][1]) + (buf[k][2] + buf[k][3]);
   }
 }
 
@@ -111,7 +136,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
   constexpr int GPW = kNormThreads / LPR;   // rows in flight per workgroup
   constexpr int N = NV * VEC;
   constexpr int U = rows_in_flight(N, BWD);
-  __shared__ float s_sum[2][kNormThreads / 64];
+  __shared__ float s_sum[LPR > 64 ? 2 : 1][kMostSums][kNormThreads / 64];
   const int tid = threadIdx.x, lane = tid % LPR, grp = tid / LPR;
   const int h = blockIdx.y;
   const int row0 = blockIdx.x * G.slab_rows;
@@ -155,83 +180,104 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
         zr[u][v].clear();
         if constexpr (BWD) gr[u][v].clear();
         if (live[u] && c < D) {
-          xr[u][v].load(x + xo[u] + c);
-          if (act) zr[u][v].load(z + yo[u] + c);
-          if constexpr (BWD) gr[u][v].load(dy + yo[u] + c);
+          xr[u][v].load(x + xo[u] + c, D - c);
+          if (act) zr[u][v].load(z + yo[u] + c, D - c);
+          if constexpr (BWD) gr[u][v].load(dy + yo[u] + c, D - c);
         }
       }
     }
+    float xv[U][N], mean[U], sq[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float xv[N], zv[N], gv[BWD ? N : 1];
+      mean[u] = 0.f;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        xr[u][v].widen(xv + v * VEC);
-        zr[u][v].widen(zv + v * VEC);
-        if constexpr (BWD) gr[u][v].widen(gv + v * VEC);
-      }
-      float mean = 0.f;
-      if (!rms) {
-        float sum = 0.f;
+      for (int v = 0; v < NV; ++v) xr[u][v].widen(xv[u] + v * VEC);
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum += xv[i];
-        mean = row_sum<LPR>(sum, s_sum, phase) * inv_d;
-      }
-      float sq = 0.f;
+      for (int i = 0; i < N; ++i) mean[u] += xv[u][i];
+    }
+    if (!rms) row_sums<LPR>(mean, s_sum, phase);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      mean[u] = rms ? 0.f : mean[u] * inv_d;
+      sq[u] = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const int i = v * VEC + e;
-          xv[i] = (v * LPR + lane) * VEC + e < D ? xv[i] - mean : 0.f;
-          sq = __builtin_fmaf(xv[i], xv[i], sq);
+          xv[u][i] = (v * LPR + lane) * VEC + e < D ? xv[u][i] - mean[u] : 0.f;
+          sq[u] = __builtin_fmaf(xv[u][i], xv[u][i], sq[u]);
         }
-      const float rstd = 1.f / sqrtf(row_sum<LPR>(sq, s_sum, phase) * inv_d + eps);
-      if constexpr (!BWD) {
+    }
+    row_sums<LPR>(sq, s_sum, phase);
+    float rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) rstd[u] = 1.f / sqrtf(sq[u] * inv_d + eps);
+    if constexpr (!BWD) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float zv[N];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) zr[u][v].widen(zv + v * VEC);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          float y = __builtin_fmaf(xv[i] * rstd, wv[i], bv[i]);
+          float y = __builtin_fmaf(xv[u][i] * rstd[u], wv[i], bv[i]);
           if (act) {
             const float sg = sigmoid<T>(zv[i]);
             y *= act == kActSilu ? zv[i] * sg : sg;
           }
-          xv[i] = y;
+          xv[u][i] = y;
         }
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int c = (v * LPR + lane) * VEC;
-          if (live[u] && c < D) store_vec<T, VEC>(out + yo[u] + c, xv + v * VEC);
+          if (live[u] && c < D) store_vec<T, VEC>(out + yo[u] + c, xv[u] + v * VEC, D - c);
         }
-      } else {
-        float m1 = 0.f, m2 = 0.f;
+      }
+    } else {
+      float gv[U][N], m[2 * U];   // dn; its sum and that of dn n
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float zv[N];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          zr[u][v].widen(zv + v * VEC);
+          gr[u][v].widen(gv[u] + v * VEC);
+        }
+        m[u] = m[U + u] = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float nn = xv[i] * rstd;
-          float u = gv[i];
+          const float nn = xv[u][i] * rstd[u];
+          float f = gv[u][i];
           if (act) {
             const float sg = sigmoid<T>(zv[i]);
             const float slope = act == kActSilu ? sg * __builtin_fmaf(zv[i], 1.f - sg, 1.f) : sg * (1.f - sg);
-            u *= act == kActSilu ? zv[i] * sg : sg;
-            zv[i] = gv[i] * __builtin_fmaf(nn, wv[i], bv[i]) * slope;   // dz
+            f *= act == kActSilu ? zv[i] * sg : sg;
+            zv[i] = gv[u][i] * __builtin_fmaf(nn, wv[i], bv[i]) * slope;   // dz
           }
-          dw[i] = __builtin_fmaf(u, nn, dw[i]);
-          db[i] += u;
-          xv[i] = nn;
-          gv[i] = u * wv[i];   // dn
-          m1 += gv[i];
-          m2 = __builtin_fmaf(gv[i], nn, m2);
+          dw[i] = __builtin_fmaf(f, nn, dw[i]);
+          db[i] += f;
+          xv[u][i] = nn;
+          gv[u][i] = f * wv[i];
+          m[u] += gv[u][i];
+          m[U + u] = __builtin_fmaf(gv[u][i], nn, m[U + u]);
         }
-        m1 = rms ? 0.f : row_sum<LPR>(m1, s_sum, phase) * inv_d;
-        m2 = row_sum<LPR>(m2, s_sum, phase) * inv_d;
-#pragma unroll
-        for (int i = 0; i < N; ++i) xv[i] = rstd * (gv[i] - m1 - xv[i] * m2);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
           const int c = (v * LPR + lane) * VEC;
-          if (live[u] && c < D) {
-            store_vec<T, VEC>(out + xo[u] + c, xv + v * VEC);
-            if (act) store_vec<T, VEC>(dz + yo[u] + c, zv + v * VEC);
-          }
+          if (live[u] && c < D && act) store_vec<T, VEC>(dz + yo[u] + c, zv + v * VEC, D - c);
+        }
+      }
+      row_sums<LPR>(m, s_sum, phase);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float m1 = rms ? 0.f : m[u] * inv_d, m2 = m[U + u] * inv_d;
+#pragma unroll
+        for (int i = 0; i < N; ++i) xv[u][i] = rstd[u] * (gv[u][i] - m1 - xv[u][i] * m2);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = (v * LPR + lane) * VEC;
+          if (live[u] && c < D) store_vec<T, VEC>(out + xo[u] + c, xv[u] + v * VEC, D - c);
         }
       }
     }
@@ -305,7 +351,7 @@ struct NormShape {
 NormShape norm_shape(int D, int dtype) {
   const int full = dtype == CKDA_DTYPE_BF16 ? 8 : 4;
   NormShape s;
-  s.vec = D % full == 0 ? full : 1;   // rows that are whole 16-byte vectors, else single elements
+  s.vec = D * (dtype == CKDA_DTYPE_BF16 ? 2 : 4) % 4 == 0 ? full : 1;   // rows of whole 4-byte words, else single elements
   const int pieces = (D + s.vec - 1) / s.vec;
   if (pieces <= 64) {
     s.lpr = 2;
@@ -399,7 +445,7 @@ hipError_t launch_norm(const HeadNormArgs& a, bool bwd) {
   const NormShape s = norm_shape(a.D, a.dtype);
   if (a.dtype == CKDA_DTYPE_BF16)
     return s.vec == 1 ? launch_norm_v<bf16_t, 1>(a, s, bwd) : launch_norm_v<bf16_t, 8>(a, s, bwd);
-  return s.vec == 1 ? launch_norm_v<float, 1>(a, s, bwd) : launch_norm_v<float, 4>(a, s, bwd);
+  return launch_norm_v<float, 4>(a, s, bwd);
 }
 
 }  // namespace

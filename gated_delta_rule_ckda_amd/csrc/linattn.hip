@@ -1211,7 +1211,8 @@ static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool 
     const long long sk = dk / slice_width(dk, ds), sv = dv / slice_width(dv, ds);
     const long long wgs = heads * (backward ? 2 * sk + sv : sv);
     // segments: none, two, three, or as many as fill the CUs once to four times
-    for (int i = 0; i < 7; ++i) {
+    // (short sequences and full grids: none)
+    for (int i = 0; i < (nch < 4 || wgs >= 2 * kCUs ? 1 : 7); ++i) {
       const long long n = i < 3 ? i + 1 : kCUs * (i - 2) / std::max(1LL, wgs);
       if (n < 1) continue;
       Split p;

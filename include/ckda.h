@@ -494,9 +494,9 @@ int ckda_linattn_decode_step(const void* q, const void* k, const void* v, const 
  *   y           : [B, T, H, D] dtype, token-major (a projection's input)
  *   eps         : finite, > 0
  * With H = 1 this is an ordinary layer norm of rows of width D.
- * Supported: dtype F32 or BF16; 1 <= D <= 8192 (widths that are whole 16-byte
- * vectors are read and written as such, others element by element); all
- * arithmetic fp32, outputs rounded once.  y may not overlap an input. */
+ * Supported: dtype F32 or BF16; 1 <= D <= 8192 (odd bf16 widths are read and
+ * written element by element, others in 16-byte vectors); all arithmetic fp32,
+ * outputs rounded once.  y may not overlap an input. */
 #define CKDA_NORM_RMS 1
 #define CKDA_NORM_GATE_SILU 2
 #define CKDA_NORM_GATE_SIGMOID 4
