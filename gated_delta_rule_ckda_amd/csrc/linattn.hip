@@ -192,19 +192,39 @@ __device__ __forceinline__ float row_last(float x) {
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kDecayFloor = -240.f;   // 2^-240 is 0 in fp32, and 64 such steps keep their sum's parts exact
 
-// three bf16 terms of x: hi + mid + lo = x to 2^-25 of |x|
-__device__ __forceinline__ void split3_bf16(const float* v, Frag& fh, Frag& fm, Frag& fl) {
+// x less the low / high half of a packed bf16 pair, exact where x - half is a
+// float (a residual always is): one dot product with (-1, 0) / (0, -1) instead
+// of widening the half and subtracting it.  (The constant sits in a register:
+// as a literal of the packed instruction it gave wrong sums.)
+__device__ __forceinline__ float less_half(float x, uint32_t pair, uint32_t minus_one) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  asm("" : "+s"(minus_one));
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, minus_one), x, false);
+}
+constexpr uint32_t kMinusLo = 0x0000BF80u, kMinusHi = 0xBF800000u;   // (-1, 0), (0, -1) in bf16
+
+// the two terms of the pair (a, b), packed: hi + lo = x to 2^-16 of |x|
+__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& l) {
+  h = pack_bf16x2(a, b);
+  asm("" : "+v"(h));
+  l = pack_bf16x2(less_half(a, h, kMinusLo), less_half(b, h, kMinusHi));
+}
+// N = 2 or 3 terms of eight values: their sum is x to 2^-16 or 2^-25 of |x|
+template <int N>
+__device__ __forceinline__ void split_terms(const float* v, Frag* f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = v[2 * i], b = v[2 * i + 1];
-    uint32_t h = pack_bf16x2(a, b);
-    asm("" : "+v"(h));
-    const float ra = a - bf16_lo_half(h), rb = b - bf16_hi_half(h);
-    uint32_t m = pack_bf16x2(ra, rb);
-    asm("" : "+v"(m));
-    fh.w[i] = h;
-    fm.w[i] = m;
-    fl.w[i] = pack_bf16x2(ra - bf16_lo_half(m), rb - bf16_hi_half(m));
+    float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      uint32_t h = pack_bf16x2(a, b);
+      asm("" : "+v"(h));
+      f[n].w[i] = h;
+      if (n + 1 < N) {
+        a = less_half(a, h, kMinusLo);
+        b = less_half(b, h, kMinusHi);
+      }
+    }
   }
 }
 
@@ -271,8 +291,8 @@ __device__ __forceinline__ void store_scaled(unsigned char* p, int stride, Frag 
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = wt * ((e & 1) ? bf16_hi_half(z.w[e >> 1]) : bf16_lo_half(z.w[e >> 1]));
-    Frag t[3];
-    split3_bf16(v, t[0], t[1], t[2]);
+    Frag t[N];
+    split_terms<N>(v, t);
 #pragma unroll
     for (int n = 0; n < N; ++n) store_frag(p + n * stride, t[n]);
   } else {
@@ -509,7 +529,13 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 #pragma unroll
         for (int kb = 0; kb < NPB; ++kb) {
           Frag ph, pl;
-          if constexpr (BF) frags_from_acc_bf16_split(p[2 * kb], p[2 * kb + 1], ph, pl);
+          if constexpr (BF) {
+            const f32x4 u = p[2 * kb], v = p[2 * kb + 1];
+            const float w[8] = {u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]};
+            Frag two[2];
+            split_terms<2>(w, two);
+            ph = two[0], pl = two[1];
+          }
           else ph = frag_from_acc_f32(p[kb]);
 #pragma unroll
           for (int d = 0; d < NDV; ++d) {
@@ -604,8 +630,8 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
           if constexpr (BF) {
             unsigned char* to = lds + hput[i] + j * 16 * S::YROW;
             uint32_t ha, la, hb, lb;
-            split_pair_bf16(x[0], x[1], ha, la);
-            split_pair_bf16(x[2], x[3], hb, lb);
+            split2(x[0], x[1], ha, la);
+            split2(x[2], x[3], hb, lb);
             *reinterpret_cast<u32x2*>(to) = u32x2{ha, hb};
             *reinterpret_cast<u32x2*>(to + S::H_BYTES) = u32x2{la, lb};
           } else {
@@ -992,8 +1018,13 @@ __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dot
     double carry = 0.0;
     if (dhT) {
       double x = 0.0;
-      for (int i = tid; i < elems; i += kDgThreads)
-        x += (double)dhT[(size_t)bh * elems + i] * hT[(size_t)bh * elems + i];
+      const f32x4 *p = reinterpret_cast<const f32x4*>(dhT + (size_t)bh * elems),
+                  *q = reinterpret_cast<const f32x4*>(hT + (size_t)bh * elems);
+#pragma unroll 4
+      for (int i = tid; i < elems / 4; i += kDgThreads) {
+        const f32x4 u = p[i], v = q[i];
+        x += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
+      }
       scan(x, carry);
     }
     for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
