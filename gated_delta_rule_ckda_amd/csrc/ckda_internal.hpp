@@ -113,7 +113,7 @@ struct SweepRole {
   int reverse;               // from the last row to the first
   int turned;                // init, fin and segment states are stored [d2, d1]
   int out_f32;               // out is fp32
-  int parts;                 // workgroups per unit: segments x heads of the group x slices
+  int parts;                 // workgroups per unit and segment: heads of the group x slices
 };
 struct SweepLaunch {
   SweepRole role[3];

@@ -299,18 +299,28 @@ __device__ __forceinline__ void store_scaled(unsigned char* p, int stride, Frag 
     store_frag(p, frag_from_acc_f32(__builtin_bit_cast(f32x4, z.w) * wt));
   }
 }
-// workgroup -> unit (key head of a batch entry) and its part of the unit's
-// work.  A unit's parts get ids equal modulo 8 where the units allow it, so
-// that they share an XCD's L2.
-__device__ __forceinline__ void unit_of(int units, int parts, int& unit, int& part) {
+// A cell is one segment of one unit (key head of a batch entry); its parts
+// (role, head of the group, slice) read the same rows of x and y.  Workgroups
+// go to the 8 XCDs in turn, so the parts of a cell get ids equal modulo 8 and
+// find each other's rows in their XCD's L2 -- where there are cells for every
+// XCD; a few cells are spread over all of them instead.  (A whole
+// unit in turn instead of a cell, with 4 units: every XCD read every key.)
+constexpr int kXcds = 8;
+__host__ __device__ inline bool cells_by_xcd(long long cells) { return cells % kXcds == 0 || cells >= 4 * kXcds; }
+inline long long cell_workgroups(long long cells, int parts) {
+  return (cells_by_xcd(cells) ? (cells + kXcds - 1) / kXcds * kXcds : cells) * parts;
+}
+// false: no cell (the ids are filled up to whole rounds of XCDs)
+__device__ __forceinline__ bool cell_of(int cells, int parts, int& cell, int& part) {
   const int id = blockIdx.x;
-  if (units % 8 == 0) {
-    unit = (id / 8) / parts * 8 + id % 8;
-    part = (id / 8) % parts;
+  if (cells_by_xcd(cells)) {
+    cell = (id / kXcds) / parts * kXcds + id % kXcds;
+    part = (id / kXcds) % parts;
   } else {
-    unit = id / parts;
+    cell = id / parts;
     part = id % parts;
   }
+  return cell < cells;
 }
 
 // Four consecutive elements of a row, as loaded.
@@ -342,14 +352,14 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int g = lane / 16, r = lane % 16;
-  int unit, part, role = 0;
-  unit_of(L.units, L.parts, unit, part);
+  int cell, part, role = 0;
+  if (!cell_of(L.units * L.nseg, L.parts, cell, part)) return;
+  const int unit = cell / L.nseg, seg = cell % L.nseg;
   while (role + 1 < L.nroles && part >= L.role[role].parts) part -= L.role[role++].parts;
   const SweepRole A = L.role[role];
   const int slices = A.d2 / DS;
   const int slice = part % slices;
-  const int bh = unit * L.group + (part / slices) % L.group;
-  const int seg = part / slices / L.group;
+  const int bh = unit * L.group + part / slices;
   const Rows R(L, bh, seg, L.seg_rows, A.reverse);
   const int len = R.len, nch = R.nch;
   auto dec_of = [&](int c) __attribute__((always_inline)) {
@@ -759,11 +769,11 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
   __shared__ __attribute__((aligned(16))) unsigned char lds[S::LDS_BYTES];
   const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
   const int g = lane / 16, r = lane % 16;
-  int unit, part;
-  unit_of(L.units, L.parts, unit, part);
+  int cell, part;
+  if (!cell_of(L.units * L.nseg, L.parts, cell, part)) return;
+  const int unit = cell / L.nseg, seg = cell % L.nseg;
   const SweepRole A = L.role[0];
-  const int bh = unit * L.group + part % L.group;
-  const int seg = part / L.group;
+  const int bh = unit * L.group + part;
   const Rows R(L, bh, seg, L.seg_rows, A.reverse);
   auto dec_of = [&](int c) __attribute__((always_inline)) {
     return reinterpret_cast<float*>(lds + S::DEC_OFF + (c & 1) * S::DEC_BYTES);
@@ -896,7 +906,7 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(float* states, const 
 
 template <typename T, int D1, int DS, bool EXACT>
 hipError_t launch_sweep_t(const SweepLaunch& L, hipStream_t stream) {
-  const long long wgs = (long long)L.units * L.parts;
+  const long long wgs = cell_workgroups((long long)L.units * L.nseg, L.parts);
   if (wgs == 0) return hipSuccess;
   hipLaunchKernelGGL((sweep_kernel<T, D1, DS, EXACT>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
   return hipGetLastError();
@@ -934,7 +944,7 @@ hipError_t launch_sweep_e(const SweepLaunch& L, int d1, int ds, hipStream_t stre
 
 template <typename T, int D1, int D2>
 hipError_t launch_own_t(const SweepLaunch& L, hipStream_t stream) {
-  const long long wgs = (long long)L.units * L.parts;
+  const long long wgs = cell_workgroups((long long)L.units * L.nseg, L.parts);
   if (wgs == 0) return hipSuccess;
   hipLaunchKernelGGL((own_state_kernel<T, D1, D2>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
   return hipGetLastError();
@@ -1338,7 +1348,8 @@ static hipError_t segment_starts(const LinAttnArgs& a, bool reverse, const Split
   R.d2 = a.dv;
   R.seg_out = states;
   R.seg_decay = decay;
-  R.parts = L.parts = (sp.nsub - 1) * L.group;
+  L.nseg = sp.nsub - 1;   // (the last one's own state is not needed)
+  R.parts = L.parts = L.group;
   hipError_t e = a.dtype == 1 ? launch_own_e<bf16_t>(L, a.dk, a.stream) : launch_own_e<float>(L, a.dk, a.stream);
   if (e != hipSuccess) return e;
   const long long threads = L.seg_stride / 4;
@@ -1370,7 +1381,7 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
   R.fin = a.hT;
   R.seg_states = states;
   L.exact_state = a.hT != nullptr;
-  R.parts = L.parts = p.sp.nseg * L.group * (a.dv / ds);
+  R.parts = L.parts = L.group * (a.dv / ds);
   return launch_sweep(L, a.dtype, a.dk, ds, a.stream);
 }
 
@@ -1486,9 +1497,8 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   SweepLaunch L = sweep_base(a);
   set_split(L, a, p.sp);
   L.exact_state = a.dh0 || a.dhT;
-  const int per = p.sp.nseg * L.group;
-  dv.parts = per * (a.dv / dsv);
-  dk.parts = dq.parts = per * (a.dk / dsk);
+  dv.parts = L.group * (a.dv / dsv);
+  dk.parts = dq.parts = L.group * (a.dk / dsk);
   // one launch where the sweeps have the same widths, else the two that
   // contract over dv apart from the one over dk
   if (a.dk == a.dv) {
