@@ -403,6 +403,10 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
     for (int j = 0; j < ny; ++j) pin4(u.y[j].w);
 #pragma unroll
     for (int j = 0; j < nz; ++j) pin4(u.z[j].w);
+    // (read before anything is written: a wait for them then waits for no write)
+    float wt[nz > 0 ? nz : 1];   // G(C, row)
+#pragma unroll
+    for (int j = 0; j < nz; ++j) wt[j] = dec[3 * C + min(ct + 256 * (z0 + j), C * S::ZPR - 1) / S::ZPR];
 #pragma unroll
     for (int j = 0; j < ny; ++j) {
       const int p = ct + 256 * (y0 + j);
@@ -414,7 +418,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       if (C * S::ZPR % 256 == 0 || p < C * S::ZPR) {
         const int off = lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR);
         store_frag(lz + off, u.z[j]);
-        store_scaled<T, S::ZSETS>(lzs + off, S::Z_BYTES, u.z[j], dec[3 * C + p / S::ZPR]);
+        store_scaled<T, S::ZSETS>(lzs + off, S::Z_BYTES, u.z[j], wt[j]);
       }
     }
   };
@@ -803,6 +807,9 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
     for (int j = 0; j < S::NY; ++j) pin4(yv[j].w);
 #pragma unroll
     for (int j = 0; j < S::NZ; ++j) pin4(zv[j].w);
+    float wt[S::NZ];
+#pragma unroll
+    for (int j = 0; j < S::NZ; ++j) wt[j] = dec[3 * C + min(tid + 512 * j, C * S::ZPR - 1) / S::ZPR];
 #pragma unroll
     for (int j = 0; j < S::NY; ++j) {
       const int p = tid + 512 * j;
@@ -812,8 +819,7 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
     for (int j = 0; j < S::NZ; ++j) {
       const int p = tid + 512 * j;
       if (C * S::ZPR % 512 == 0 || p < C * S::ZPR)
-        store_scaled<T, S::ZSETS>(lzs + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), S::Z_BYTES, zv[j],
-                                  dec[3 * C + p / S::ZPR]);
+        store_scaled<T, S::ZSETS>(lzs + lds_piece<S::ZROW>(p / S::ZPR, p % S::ZPR), S::Z_BYTES, zv[j], wt[j]);
     }
   };
   const int rt0 = (wave / 4) * S::TR, ct0 = (wave % 4) * S::TC;
