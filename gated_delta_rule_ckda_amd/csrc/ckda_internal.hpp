@@ -126,6 +126,7 @@ struct SweepLaunch {
 
 size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
 size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, int dtype);
+bool linattn_fits_grid(int B, int H, int Hk, int T, int dk, int dv, int dtype, bool backward);
 hipError_t launch_linattn_fwd(const LinAttnArgs& a);
 hipError_t launch_linattn_bwd(const LinAttnArgs& a);
 hipError_t launch_linattn_decode(const LinAttnDecodeArgs& a);

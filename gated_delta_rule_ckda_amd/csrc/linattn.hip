@@ -1427,6 +1427,20 @@ size_t linattn_bwd_workspace_bytes(int B, int H, int Hk, int T, int dk, int dv, 
   return bwd_plan(B, H, Hk, T, dk, dv, dtype).bytes;
 }
 
+// A launch takes fewer than 2^32 threads.
+bool linattn_fits_grid(int B, int H, int Hk, int T, int dk, int dv, int dtype, bool backward) {
+  const long long bh = (long long)B * H, units = (long long)B * Hk;
+  long long most = 0;
+  if (bh > 65536) {   // (fewer heads have at most 24 slices each, or some 2000 segments among them)
+    const Split sp = plan_split(bh, T, dk, dv, dtype, backward);
+    const long long sk = dk / slice_width(dk, sp.ds), sv = dv / slice_width(dv, sp.ds);
+    const long long slices = !backward ? sv : dk == dv ? sv + 2 * sk : std::max(sv, 2 * sk);
+    most = std::max(512 * cell_workgroups(units * sp.nseg, (int)(H / Hk * slices)), backward ? kDgThreads * bh : 0);
+  }
+  if (backward && H != Hk) most = std::max(most, units * T * (dk / 4));   // fold_heads_kernel
+  return most + 255 <= (long long)UINT32_MAX;
+}
+
 template <typename T>
 static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsigned char* ws) {
   const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, p.sp.ds);

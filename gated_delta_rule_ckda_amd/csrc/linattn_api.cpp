@@ -86,6 +86,8 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
   if (BH * (size_t)(dv / 16) > (size_t)INT32_MAX) return fail(CKDA_ERR_DIM, "%s: B*H too large", fn);
   if (!linattn_rows_fit(T, dk, dv, dtype_bytes(dtype)))
     return fail(CKDA_ERR_DIM, "%s: T=%d too long: one head's rows must stay below 2 GiB", fn, T);
+  if (!ckda::linattn_fits_grid(B, H, Hk, T, dk, dv, dtype, false))
+    return fail(CKDA_ERR_DIM, "%s: B*H exceeds the launch grid", fn);
   const size_t need = ckda_linattn_fwd_workspace_size(B, H, T, dk, dv, dtype);
   if (T > 0 && (st = check_workspace(fn, workspace, workspace_bytes, need)) != CKDA_OK) return st;
   const LinAttnSizes n = linattn_bytes(B, H, Hk, T, dk, dv, dtype, flags);
@@ -126,10 +128,11 @@ int ckda_linattn_bwd(const void* q, const void* k, const void* v, const void* g,
   if (H == 0 || (BH == 0 && !head)) return ok();
   if ((T > 0 && BH > 0 && (!q || !k || !v || !dout || !dq || !dk_out || !dv_out)) || ((T > 0 || head) && (!g || !dg)))
     return fail(CKDA_ERR_NULL, "%s: inputs, do and the gradients of q, k, v and g are required", fn);
-  if (BH * 24 > (size_t)INT32_MAX || ((size_t)T * BH + 1023) / 1024 * dk > (size_t)INT32_MAX)
-    return fail(CKDA_ERR_DIM, "%s: sizes exceed the launch grid", fn);
+  if (BH * 24 > (size_t)INT32_MAX) return fail(CKDA_ERR_DIM, "%s: B*H too large", fn);
   if (!linattn_rows_fit(T, dk, dv, 4))
     return fail(CKDA_ERR_DIM, "%s: T=%d too long: one head's rows must stay below 2 GiB (as fp32)", fn, T);
+  if (!ckda::linattn_fits_grid(B, H, Hk, T, dk, dv, dtype, true))
+    return fail(CKDA_ERR_DIM, "%s: sizes exceed the launch grid", fn);
   const size_t need = ckda_linattn_bwd_workspace_size(B, H, Hk, T, dk, dv, dtype);
   if ((st = check_workspace(fn, workspace, workspace_bytes, need)) != CKDA_OK) return st;
   const LinAttnSizes n = linattn_bytes(B, H, Hk, T, dk, dv, dtype, flags);
@@ -160,7 +163,7 @@ int ckda_linattn_decode_step(const void* q, const void* k, const void* v, const 
   if (st != CKDA_OK) return st;
   const size_t NH = (size_t)N * H;
   if (NH == 0) return ok();
-  if (NH * (size_t)(dv / 16) > (size_t)INT32_MAX) return fail(CKDA_ERR_DIM, "%s: N*H exceeds the launch grid", fn);
+  if (NH >= 1u << 24) return fail(CKDA_ERR_DIM, "%s: N*H exceeds the launch grid", fn);   // 256 threads each, of 2^32
   if (!q || !k || !v || !g || !H_inout || !o) return fail(CKDA_ERR_NULL, "%s: every pointer is required", fn);
   const LinAttnSizes n = linattn_bytes(N, H, Hk, 1, dk, dv, dtype, flags);
   const Range in[] = {range("q", q, n.qk), range("k", k, n.qk), range("v", v, n.v), range("g", g, n.g)};

@@ -101,6 +101,16 @@ def test_decode_refusals(status, kw):
     assert b"ckda_linattn_decode_step" in ck.lib().ckda_last_error()
 
 
+@pytest.mark.parametrize("call,kw", [
+    (fwd, dict(B=1 << 16, H=1 << 8, Hk=1, T=1)), (bwd, dict(B=1 << 14, H=1 << 8, Hk=1 << 8, T=1)),
+    (bwd, dict(B=1 << 10, H=1 << 4, Hk=1 << 3, T=1 << 16)), (dec, dict(N=1 << 14, H=1 << 10, Hk=1)),
+])
+def test_launch_grid(call, kw):
+    """Sizes whose launches would have 2^32 threads or more are refused before any of them."""
+    assert call(**kw, ws_bytes=1 << 50) == ck.ERR_DIM if call is not dec else call(**kw) == ck.ERR_DIM
+    assert b"launch grid" in ck.lib().ckda_last_error()
+
+
 NORM = [(ck.ERR_DIM, dict(B=-1)), (ck.ERR_DIM, dict(D=0)), (ck.ERR_UNSUPPORTED, dict(D=8193)),
         (ck.ERR_DIM, dict(wheads=2)), (ck.ERR_DIM, dict(wheads=0)), (ck.ERR_UNSUPPORTED, dict(dtype=5)),
         (ck.ERR_FLAGS, dict(flags=8)), (ck.ERR_FLAGS, dict(flags=6)), (ck.ERR_FLAGS, dict(flags=0)),
