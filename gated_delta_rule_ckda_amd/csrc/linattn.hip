@@ -31,8 +31,6 @@
 //      scales the accumulators of H^T X^T (a factor of the column); outputs.
 //      State waves: H <- exp(c_C) H + Y^T (G(C, .) Z); the new H^T, and Y, Z
 //      and the terms of G(C, .) Z of the next chunk into the same LDS buffers.
-// One copy of each operand is all it takes in LDS, so two workgroups run on
-// every CU, each in the other's gaps.
 // Precision: the inputs are exact in bf16; every factor that is not (P, H and
 // the scaled Z) is carried as a sum of bf16 terms: two (16 bits) where the
 // product ends in a rounded output, three (24 bits) for the state itself,
@@ -989,9 +987,13 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 // a running sum from the sequence's end.  The sweeps leave the parts of a and b
 // per slice, taken from their unrounded outputs; the sum runs in fp64.
 // One workgroup per (batch, head), four rows per thread; of a constant decay,
-// whose gradient is the sum over rows and batch, either each (batch, head)
-// leaves its sum for a second kernel, or, where a batch holds few rows, one
-// workgroup per head takes the batch entries in turn (`batches` of them).
+// whose gradient is the sum over rows and batch, each leaves its sum for a
+// second kernel, but for a single batch entry.  (One workgroup per head over
+// the batch entries in turn saves that launch of some 2 us, and loses from two
+// entries on: 8 heads, 100 rows, the whole backward in us, 19.0 and 18.3 for
+// one entry, 18.3 and 19.6 for two, 19.3 and 27.8 for eight.)
+// Bound by the latency of its loads and of the scan's barriers: 5.4 us for
+// B4 H16 T4096, 13.6 us for the eight slices of B2 H12 T777.
 constexpr int kDgThreads = 1024;
 
 __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
@@ -1006,8 +1008,8 @@ __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
 template <typename T>
 __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dotq, const float* dotk, int slices,
                                                                 const float* dhT, const float* hT, int elems,
-                                                                const int* lens, int rows, int heads, int nbh, int batches,
-                                                                T* dg, double* head_sum, int head_decay) {
+                                                                const int* lens, int rows, int heads, T* dg,
+                                                                double* head_sum, int head_decay) {
   __shared__ double s_wave[kDgThreads / 64], s_total;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   // sum over the workgroup, and the exclusive prefix of this thread
@@ -1028,46 +1030,44 @@ __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dot
     return before;
   };
   double sum = 0.0;
-  for (int b = 0; b < batches; ++b) {
-    const int bh = b * heads + blockIdx.x;
-    const int len = lens ? min(max(lens[bh / heads], 0), rows) : rows;
-    double carry = 0.0;
-    if (dhT) {
-      double x = 0.0;
-      const f32x4 *p = reinterpret_cast<const f32x4*>(dhT + (size_t)bh * elems),
-                  *q = reinterpret_cast<const f32x4*>(hT + (size_t)bh * elems);
+  const int bh = blockIdx.x;
+  const int len = lens ? min(max(lens[bh / heads], 0), rows) : rows;
+  double carry = 0.0;
+  if (dhT) {
+    double x = 0.0;
+    const f32x4 *p = reinterpret_cast<const f32x4*>(dhT + (size_t)bh * elems),
+                *q = reinterpret_cast<const f32x4*>(hT + (size_t)bh * elems);
 #pragma unroll 4
-      for (int i = tid; i < elems / 4; i += kDgThreads) {
-        const f32x4 u = p[i], v = q[i];
-        x += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
-      }
-      scan(x, carry);
+    for (int i = tid; i < elems / 4; i += kDgThreads) {
+      const f32x4 u = p[i], v = q[i];
+      x += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
     }
-    for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
-      double d[4], mine = 0.0;
+    scan(x, carry);
+  }
+  for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
+    double d[4] = {0.0, 0.0, 0.0, 0.0}, mine = 0.0;
+#pragma unroll 4   // the loads of four slices in flight
+    for (int s = 0; s < slices; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = len - 1 - (base + 4 * tid + j);
-        double x = 0.0;
-        if (row >= 0)
-          for (int s = 0; s < slices; ++s) {
-            const size_t at = ((size_t)s * nbh + bh) * rows + row;
-            x += (double)dotq[at] - (double)dotk[at];
-          }
-        mine += x;
-        d[j] = mine;
+      for (int j = 0; j < 4; ++j) {   // (rows before the first: that one, dropped below)
+        const size_t at = ((size_t)s * gridDim.x + bh) * rows + max(len - 1 - (base + 4 * tid + j), 0);
+        d[j] += (double)dotq[at] - (double)dotk[at];
       }
-      double total;
-      const double before = carry + scan(mine, total);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = len - 1 - (base + 4 * tid + j);
-        if (row < 0) continue;
-        if (head_decay) sum += before + d[j];
-        else dg[(size_t)bh * rows + row] = from_f32<T>((float)(before + d[j]));
-      }
-      carry += total;
+    for (int j = 0; j < 4; ++j) {
+      mine += base + 4 * tid + j < len ? d[j] : 0.0;
+      d[j] = mine;
     }
+    double total;
+    const double before = carry + scan(mine, total);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = len - 1 - (base + 4 * tid + j);
+      if (row < 0) continue;
+      if (head_decay) sum += before + d[j];
+      else dg[(size_t)bh * rows + row] = from_f32<T>((float)(before + d[j]));
+    }
+    carry += total;
   }
   if (head_decay) {
     double total;
@@ -1444,14 +1444,12 @@ bool linattn_fits_grid(int B, int H, int Hk, int T, int dk, int dv, int dtype, b
 template <typename T>
 static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsigned char* ws) {
   const int bh = a.B * a.H, slices = a.dk / slice_width(a.dk, p.sp.ds);
-  // (a workgroup takes 4 rows per thread at a time)
-  const bool in_turn = a.head_decay && (long long)a.B * a.T <= 2 * 4 * kDgThreads;
-  double* sums = a.head_decay && !in_turn ? (double*)(ws + p.head_sum) : nullptr;
+  double* sums = a.head_decay && a.B != 1 ? (double*)(ws + p.head_sum) : nullptr;
   hipError_t e = hipSuccess;
-  if (bh > 0 || in_turn) {
-    hipLaunchKernelGGL((decay_grad_kernel<T>), dim3(in_turn ? a.H : bh), dim3(kDgThreads), 0, a.stream,
+  if (bh > 0) {
+    hipLaunchKernelGGL((decay_grad_kernel<T>), dim3(bh), dim3(kDgThreads), 0, a.stream,
                        (const float*)(ws + p.dotq), (const float*)(ws + p.dotk), slices, a.dhT,
-                       (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T, a.H, bh, in_turn ? a.B : 1, (T*)a.dg, sums,
+                       (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T, a.H, (T*)a.dg, sums,
                        a.head_decay);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }

@@ -173,6 +173,67 @@ def test_backward_segments(dtype, state):
     run_bwd(inputs(33, B, H, Hk, T, 32, 32, dtype, state=state, lens=[2333]))
 
 
+def of_batches(x, keep):
+    """The batch entries `keep` of inputs or results: batch entries are independent."""
+    return {n: t if t is None or n in ("g", "dg") and t.dim() == 1 else t[keep] for n, t in x.items()}
+
+
+MANY = [(8, 8, 8), (16, 8, 8), (24, 8, 8), (41, 8, 1), (13, 16, 2)]   # 64 .. 328 heads, whole and broken rounds of units
+WIDE = [(16, 128), (128, 128), (64, 128), (128, 64), (32, 64), (64, 64), (128, 16)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", WIDE)
+@pytest.mark.parametrize("B,H,Hk", MANY)
+def test_many_heads(B, H, Hk, dk, dv, dtype):
+    """Calls of many heads take wide slices of the states; two batch entries of each are compared."""
+    keep = [0, B - 1]
+    x = inputs(B * 1000 + dk + dv, B, H, Hk, 150, dk, dv, dtype)
+    log(f"linattn q {tuple(x['q'].shape)} v {tuple(x['v'].shape)} {dtype}")
+    d, few = cuda(x), of_batches(x, keep)
+    o, hT, bo, bh = fwd_bounds(few)
+    want = bwd_bounds(few)
+    got_o, got_h = fwd(d)
+    only_o, none = fwd(d, want_state=False)
+    got = of_batches(dict(zip(("dq", "dk", "dv", "dg", "dh0"), bwd(d))), keep)
+    torch.cuda.synchronize()
+    assert none is None
+    check("o", got_o[keep], o, bo)
+    check("hT", got_h[keep], hT, bh)
+    check("o without a state", only_o[keep], o, bo)
+    for n, (w, b) in want.items():
+        check(n, got[n], w, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,H,Hk", [(1, 2, 2), (8, 8, 8), (13, 16, 2)])
+def test_gradients_without_states(B, H, Hk, dtype):
+    """Neither dhT nor dh0: the states of the sweeps are not returned."""
+    keep = [0, B - 1]
+    x = inputs(B + 61, B, H, Hk, 150, 64, 64, dtype, state=False)
+    want = bwd_bounds(of_batches(x, keep))
+    got = of_batches(dict(zip(("dq", "dk", "dv", "dg"), bwd(cuda(x), want_dh0=False))), keep)
+    torch.cuda.synchronize()
+    for n in ("dq", "dk", "dv", "dg"):
+        check(n, got[n], *want[n])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (16, 128), (128, 64)])
+@pytest.mark.parametrize("lens", [None, [1500, 600]])
+def test_segments_of_wide_states(dk, dv, lens, dtype):
+    x = inputs(dk + dv, 2, 2, 1, 1500, dk, dv, dtype, lens=lens)
+    assert ck.linattn_workspace_size(2, 2, 1500, dk, dv, dtype) > 256
+    run_fwd(x)
+    run_bwd(x)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,lens", [(1, 100, None), (1, 5000, None), (3, 5000, None), (40, 9, None), (3, 70, [70, 0, 5])])
+def test_gradient_of_a_constant_decay(B, T, lens, dtype):
+    run_bwd(inputs(B + T, B, 2, 2, T, 16, 16, dtype, decay="head", lens=lens))
+
+
 def test_backward_against_differences():
     """<gradient, direction> against central differences of the fp64 recurrence."""
     x = inputs(51, 2, 4, 2, 90, 32, 64, F32)
