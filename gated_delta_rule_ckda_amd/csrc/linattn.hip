@@ -986,14 +986,15 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 //   dg_t = <dhT, H_T> + sum_{u >= t} (a_u - b_u),
 // a running sum from the sequence's end.  The sweeps leave the parts of a and b
 // per slice, taken from their unrounded outputs; the sum runs in fp64.
-// One workgroup per (batch, head), four rows per thread; of a constant decay,
+// One workgroup per (batch, head), four rows per thread (one, where all fit); of a constant decay,
 // whose gradient is the sum over rows and batch, each leaves its sum for a
 // second kernel, but for a single batch entry.  (One workgroup per head over
 // the batch entries in turn saves that launch of some 2 us, and loses from two
 // entries on: 8 heads, 100 rows, the whole backward in us, 19.0 and 18.3 for
 // one entry, 18.3 and 19.6 for two, 19.3 and 27.8 for eight.)
-// Bound by the latency of its loads and of the scan's barriers: 5.4 us for
-// B4 H16 T4096, 13.6 us for the eight slices of B2 H12 T777.
+// Bound by the latency of its loads and of the scan's barriers: 5.8 us for
+// B4 H16 T4096, 4.0 us for the eight slices of B2 H12 T777 (13.6 us with four
+// rows to every thread and the slices' loads one after another).
 constexpr int kDgThreads = 1024;
 
 __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
@@ -1005,7 +1006,7 @@ __device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
   return x;
 }
 
-template <typename T>
+template <typename T, int RPT>
 __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dotq, const float* dotk, int slices,
                                                                 const float* dhT, const float* hT, int elems,
                                                                 const int* lens, int rows, int heads, T* dg,
@@ -1044,28 +1045,29 @@ __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dot
     }
     scan(x, carry);
   }
-  for (int base = 0; base < len; base += 4 * kDgThreads) {   // counted from the end
-    double d[4] = {0.0, 0.0, 0.0, 0.0}, mine = 0.0;
+  for (int base = 0; base < len; base += RPT * kDgThreads) {   // counted from the end
+    double d[RPT], mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < RPT; ++j) d[j] = 0.0;
+    const int first = len - 1 - (base + RPT * tid);
+    if (first >= 0) {
 #pragma unroll 4   // the loads of four slices in flight
-    for (int s = 0; s < slices; ++s)
+      for (int s = 0; s < slices; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {   // (rows before the first: that one, dropped below)
-        const size_t at = ((size_t)s * gridDim.x + bh) * rows + max(len - 1 - (base + 4 * tid + j), 0);
-        d[j] += (double)dotq[at] - (double)dotk[at];
-      }
+        for (int j = 0; j < RPT; ++j) {   // (a row before the first: that one again, dropped below)
+          const size_t at = ((size_t)s * gridDim.x + bh) * rows + max(first - j, 0);
+          d[j] += (double)dotq[at] - (double)dotk[at];
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mine += base + 4 * tid + j < len ? d[j] : 0.0;
-      d[j] = mine;
+      for (int j = 0; j < RPT; ++j) d[j] = mine += first - j >= 0 ? d[j] : 0.0;
     }
     double total;
     const double before = carry + scan(mine, total);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = len - 1 - (base + 4 * tid + j);
-      if (row < 0) continue;
+    for (int j = 0; j < RPT; ++j) {
+      if (first - j < 0) continue;
       if (head_decay) sum += before + d[j];
-      else dg[(size_t)bh * rows + row] = from_f32<T>((float)(before + d[j]));
+      else dg[(size_t)bh * rows + first - j] = from_f32<T>((float)(before + d[j]));
     }
     carry += total;
   }
@@ -1447,10 +1449,12 @@ static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsign
   double* sums = a.head_decay && a.B != 1 ? (double*)(ws + p.head_sum) : nullptr;
   hipError_t e = hipSuccess;
   if (bh > 0) {
-    hipLaunchKernelGGL((decay_grad_kernel<T>), dim3(bh), dim3(kDgThreads), 0, a.stream,
-                       (const float*)(ws + p.dotq), (const float*)(ws + p.dotk), slices, a.dhT,
-                       (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T, a.H, (T*)a.dg, sums,
-                       a.head_decay);
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(bh), dim3(kDgThreads), 0, a.stream, (const float*)(ws + p.dotq),
+                         (const float*)(ws + p.dotk), slices, a.dhT, (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T,
+                         a.H, (T*)a.dg, sums, a.head_decay);
+    };
+    a.T <= kDgThreads ? launch(decay_grad_kernel<T, 1>) : launch(decay_grad_kernel<T, 4>);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (sums) {
