@@ -569,7 +569,7 @@ def linattn_fwd(q, k, v, g, h0=None, lens=None, workspace=None, o=None, hT=None,
     L = lib()
     need = L.ckda_linattn_fwd_workspace_size(B, H, T, dk, dv, code)
     if need == 0:
-        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} H={H} T={T} dk={dk} dv={dv}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     if o is None:
         o = _fresh((B, H, T, dv), dt, dev, stream)
@@ -598,7 +598,7 @@ def linattn_bwd(q, k, v, g, do, h0=None, dhT=None, lens=None, want_dh0=True, wor
     L = lib()
     need = L.ckda_linattn_bwd_workspace_size(B, H, Hk, T, dk, dv, code)
     if need == 0:
-        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes dk={dk} dv={dv}")
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} H={H} T={T} dk={dk} dv={dv}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     gq, gk = (_fresh((B, Hk, T, dk), dt, dev, stream) for _ in range(2))
     gv = _fresh((B, H, T, dv), dt, dev, stream)

@@ -28,6 +28,11 @@ static bool linattn_rows_fit(int T, int dk, int dv, size_t es) {
   return ((size_t)T + 2 * ckda::kLaChunk) * (dk > dv ? dk : dv) * es <= (size_t)INT32_MAX;
 }
 
+// heads and rows whose products the host's arithmetic holds (wider calls are refused)
+static bool linattn_planned(int B, int H, int T, int dk, int dv, size_t es) {
+  return (size_t)B * H * 24 <= (size_t)INT32_MAX && linattn_rows_fit(T, dk, dv, es);
+}
+
 static int check_workspace(const char* fn, const void* workspace, size_t have, size_t need) {
   if (!workspace) return fail(CKDA_ERR_WORKSPACE, "%s: workspace is NULL", fn);
   if (have < need) return fail(CKDA_ERR_WORKSPACE, "%s: workspace of %zu bytes, need %zu", fn, have, need);
@@ -70,6 +75,7 @@ static LinAttnSizes linattn_bytes(int B, int H, int Hk, int T, int dk, int dv, i
 size_t ckda_linattn_fwd_workspace_size(int B, int H, int T, int dk, int dv, int dtype) {
   if (B < 0 || H < 0 || T < 0) return 0;
   if (!supported_dim(dk) || !supported_dim(dv) || !supported_dtype(dtype)) return 0;
+  if (!linattn_planned(B, H, T, dk, dv, dtype_bytes(dtype))) return 0;
   const size_t bytes = ckda::linattn_fwd_workspace_bytes(B, H, T, dk, dv, dtype);
   return bytes == 0 ? 256 : bytes;
 }
@@ -83,7 +89,7 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
   const size_t BH = (size_t)B * H;
   if (BH == 0 || (T == 0 && !hT)) return ok();
   if (T > 0 && (!q || !k || !v || !g || !o)) return fail(CKDA_ERR_NULL, "%s: q, k, v, g and o are required", fn);
-  if (BH * (size_t)(dv / 16) > (size_t)INT32_MAX) return fail(CKDA_ERR_DIM, "%s: B*H too large", fn);
+  if (BH * 24 > (size_t)INT32_MAX) return fail(CKDA_ERR_DIM, "%s: B*H too large", fn);
   if (!linattn_rows_fit(T, dk, dv, dtype_bytes(dtype)))
     return fail(CKDA_ERR_DIM, "%s: T=%d too long: one head's rows must stay below 2 GiB", fn, T);
   if (!ckda::linattn_fits_grid(B, H, Hk, T, dk, dv, dtype, false))
@@ -111,6 +117,7 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
 size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype) {
   if (B < 0 || H < 0 || T < 0 || (H > 0 && (Hk < 1 || H % Hk != 0))) return 0;
   if (!supported_dim(dk) || !supported_dim(dv) || !supported_dtype(dtype)) return 0;
+  if (!linattn_planned(B, H, T, dk, dv, 4)) return 0;
   const size_t bytes = ckda::linattn_bwd_workspace_bytes(B, H, Hk, T, dk, dv, dtype);
   return bytes == 0 ? 256 : bytes;
 }

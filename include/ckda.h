@@ -425,7 +425,8 @@ int ckda_decode_step_gather(const void* q, const void* k, const void* v, const v
 
 /* Bytes of device workspace ckda_linattn_fwd needs, or 0 when the sizes are
  * invalid or unsupported.  With few heads and many rows the sequence runs in
- * segments, whose fp32 states and decays it holds; else 256. */
+ * segments, whose fp32 states and decays it holds; else 256.  (It may be less
+ * for a longer sequence: ask for the sizes of each call.) */
 size_t ckda_linattn_fwd_workspace_size(int B, int H, int T, int dk, int dv, int dtype);
 
 /* Forward over a whole sequence for every (batch, head).
@@ -444,9 +445,9 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace ckda_linattn_bwd needs, or 0 for invalid or
- * unsupported sizes: two fp32 numbers per row, head and 32 key channels, the
- * final states, segment states as the forward's for both directions and, with
- * shared heads, the heads' fp32 parts of dq and dk. */
+ * unsupported sizes: two fp32 numbers per row, head and slice of key channels,
+ * the final states, segment states as the forward's for both directions and,
+ * with shared heads, the heads' fp32 parts of dq and dk. */
 size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 
 /* Backward: the gradients of a loss L given dout = dL/do [B, H, T, dv] (dtype)
