@@ -127,7 +127,20 @@ constexpr int rows_in_flight(int n, bool bwd) { return n <= 8 ? (bwd ? 2 : 4) : 
 
 struct RowGeom {
   int H, T, D, rows, slab_rows;   // rows = B T of one head
+  int heads_first;                // order of the workgroups
 };
+
+// Workgroups of all heads of one slab next to each other, so that the pieces
+// of a token-major row are touched at about the same time.  MI355X, cold
+// inputs, us, slabs first -> heads first:
+//   forward   bf16 B4 H16 T4096 D128 55 -> 48, B4 H8 T4096 D256 53 -> 45, B2 H8 T4096 D512 47.5 -> 46;
+//             fp32 B4 H16 T4096 D64 52 -> 41, B1 H32 T4096 D128 49 -> 41
+//   backward  bf16 B4 H16 T4096 D128 86 -> 81, B1 H64 T4096 D128 83 -> 77, B4 H8 T4096 D256 87 -> 77;
+//             fp32 B2 H8 T4096 D128 40 -> 34.5
+// but, in the backward, for rows of 512 bytes and more in token-major rows of
+// 8 KB and more:
+//             bf16 B2 H8 T4096 D512 75 -> 82; fp32 B2 H16 T4096 D128 68 -> 78, B1 H32 T4096 D128 70 -> 76
+bool heads_first(int H, int D, int es, bool bwd) { return !bwd || D * es < 512 || H * D * es < 8192; }
 
 template <typename T, int VEC, int LPR, int NV, bool BWD>
 __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, const T* z, const T* dy, const float* w,
@@ -138,8 +151,9 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
   constexpr int U = rows_in_flight(N, BWD);
   __shared__ float s_sum[LPR > 64 ? 2 : 1][kMostSums][kNormThreads / 64];
   const int tid = threadIdx.x, lane = tid % LPR, grp = tid / LPR;
-  const int h = blockIdx.y;
-  const int row0 = blockIdx.x * G.slab_rows;
+  const int h = G.heads_first ? blockIdx.x : blockIdx.y;
+  const int slab = G.heads_first ? blockIdx.y : blockIdx.x;
+  const int row0 = slab * G.slab_rows;
   const int row1 = min(row0 + G.slab_rows, G.rows);
   const int D = G.D;
   const float inv_d = 1.f / (float)D;
@@ -288,7 +302,7 @@ __global__ __launch_bounds__(kNormThreads) void head_norm_kernel(const T* x, con
     constexpr int WAVES = kNormThreads / 64;
     constexpr int COLS = (LPR < 64 ? LPR : 64) * N;   // columns one wave holds
     __shared__ float s_part[LPR <= 64 ? WAVES : 1][LPR <= 64 ? COLS : 1];
-    float* to = part + ((size_t)h * gridDim.x + blockIdx.x) * 2 * D;
+    float* to = part + ((size_t)h * (G.heads_first ? gridDim.y : gridDim.x) + slab) * 2 * D;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       float* acc = which ? db : dw;
@@ -381,8 +395,9 @@ int slab_rows(int rows, int H, int lpr, bool bwd) {
 
 template <typename T, int VEC, int LPR, int NV>
 hipError_t launch_norm_t(const HeadNormArgs& a, bool bwd) {
-  RowGeom G{a.H, a.T, a.D, a.B * a.T, slab_rows(a.B * a.T, a.H, LPR, bwd)};
-  const dim3 grid((G.rows + G.slab_rows - 1) / G.slab_rows, a.H);
+  RowGeom G{a.H, a.T, a.D, a.B * a.T, slab_rows(a.B * a.T, a.H, LPR, bwd), heads_first(a.H, a.D, (int)sizeof(T), bwd)};
+  const unsigned slabs = (G.rows + G.slab_rows - 1) / G.slab_rows;   // at most 4096
+  const dim3 grid = G.heads_first ? dim3(a.H, slabs) : dim3(slabs, a.H);
   const int act = a.z ? a.flags & (kActSilu | kActSigmoid) : kActNone;
   const int rms = (a.flags & CKDA_NORM_RMS) ? 1 : 0, shared = a.wheads == 1;
   if (G.rows == 0)
@@ -398,7 +413,7 @@ hipError_t launch_norm_t(const HeadNormArgs& a, bool bwd) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !bwd || (!a.dw && !a.db)) return e;
   // shared weights: the parts of all heads are one list
-  const int nparts = (int)grid.x * (shared ? a.H : 1);
+  const int nparts = (int)slabs * (shared ? a.H : 1);
   hipLaunchKernelGGL(norm_weight_grad_kernel, dim3((a.D + kRedCols - 1) / kRedCols, 2, a.wheads),
                      dim3(kRedCols * kRedRows), 0, a.stream, (const float*)a.workspace, nparts, a.D, a.dw, a.db);
   return hipGetLastError();

@@ -96,6 +96,13 @@ def test_sizes(B, H, T, D, dtype):
     run(B * 1000 + T, B, H, T, D, dtype, "sigmoid", False, H % 2 == 0)
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("B,H,T,D,dtype", [(2, 16, 90, 128, F32), (1, 8, 70, 512, BF), (1, 8, 70, 256, BF), (2, 3, 40, 1025, BF)])
+def test_several_slabs_of_several_heads(B, H, T, D, dtype, shared):
+    """Both orders of the workgroups (heads or slabs first)."""
+    run(D + T, B, H, T, D, dtype, "silu", False, shared)
+
+
 def test_large_mean_keeps_the_variance():
     """The variance is of centred values: rows far from zero lose nothing but the input's own rounding."""
     run(9, 1, 2, 16, 128, F32, None, False, False, offset=100.0)
