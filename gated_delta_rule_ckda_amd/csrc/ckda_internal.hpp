@@ -109,7 +109,7 @@ struct SweepRole {
   float* seg_states;         // start state of every sub-segment (with more than one segment)
   float *seg_out, *seg_decay;   // own-state launches: the sub-segments' own states and decays
   int x_shared, y_shared, z_shared, w_shared;
-  int d2;
+  int d1, d2;
   int reverse;               // from the last row to the first
   int turned;                // init, fin and segment states are stored [d2, d1]
   int out_f32;               // out is fp32

@@ -340,8 +340,9 @@ template <> struct Quad<float> {
   static __device__ __forceinline__ float get(Raw w, int j) { return w[j]; }
 };
 
-// EXACT: states with three bf16 terms (one is returned), else two.
-template <typename T, int D1, int DS, bool EXACT>
+// EXACT: states with three bf16 terms (one is returned), else two.  PAD: roles
+// of fewer than D1 state rows run among those of D1, with zeros in the rest.
+template <typename T, int D1, int DS, bool EXACT, bool PAD>
 __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
   using S = SweepCfg<T, D1, DS, EXACT>;
   constexpr int E = S::E, KBN = S::KBN, KBC = S::KBC, NDV = S::NDV, TR = S::TR, TC = S::TC;
@@ -355,6 +356,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
   const int unit = cell / L.nseg, seg = cell % L.nseg;
   while (role + 1 < L.nroles && part >= L.role[role].parts) part -= L.role[role++].parts;
   const SweepRole A = L.role[role];
+  const int d1 = PAD ? A.d1 : D1;
   const int slices = A.d2 / DS;
   const int slice = part % slices;
   const int bh = unit * L.group + part / slices;
@@ -369,9 +371,10 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
   // y0 .. y1 - 1 of Y and z0 .. z1 - 1 of Z.  Loads and copies run on past the
   // last chunk (the last one again, into buffers nobody reads): a conditional
   // load would make every wait for an older one wait for all loads in flight.
-  const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared ? unit : bh, L.rows, len, D1, E);
+  const __amdgpu_buffer_rsrc_t yr = rows_rsrc(A.y, A.y_shared ? unit : bh, L.rows, len, d1, E);
   const __amdgpu_buffer_rsrc_t zr = rows_rsrc(A.z, A.z_shared ? unit : bh, L.rows, len, A.d2, E);
   const int ct = tid & 255;
+  const bool ypad = PAD && ct % S::YPR * 16 >= d1 * E;   // (256 threads are whole rows of pieces)
   constexpr int YM = S::NY - S::YO, ZM = S::NZ - S::ZO;   // (the state waves have the most)
   struct Units {
     Frag y[YM], z[ZM];
@@ -382,7 +385,8 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 #pragma unroll
     for (int j = 0; j < ny; ++j) {
       const int p = ct + 256 * (y0 + j);
-      u.y[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, R.row(C * c + p / S::YPR) * D1 * E + (p % S::YPR) * 16, 0, 0);
+      const int off = R.row(C * c + p / S::YPR) * d1 * E + (p % S::YPR) * 16;
+      u.y[j].w = __builtin_amdgcn_raw_buffer_load_b128(yr, ypad ? 0x7FFFFFF0 : off, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < nz; ++j) {
@@ -423,7 +427,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 
   if (wave < 4) {
     // ============================================================ output waves
-    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(A.x, A.x_shared ? unit : bh, L.rows, len, D1, E);
+    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(A.x, A.x_shared ? unit : bh, L.rows, len, d1, E);
     const __amdgpu_buffer_rsrc_t outr = rows_rsrc(A.out, bh, L.rows, len, A.d2, A.out_f32 ? 4 : E);
     const __amdgpu_buffer_rsrc_t wr = rows_rsrc(A.w, A.w_shared ? unit : bh, L.rows, len, A.d2, A.w ? E : 0);
     const int t = 16 * wave + r;      // this lane's row of the chunk
@@ -437,8 +441,9 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       const int row = R.row(C * c + t);
 #pragma unroll
       for (int kb = 0; kb < KBN; ++kb) {
-        const int off = row * D1 * E + kb * 64 + g * 16;
-        xf[kb].w = __builtin_amdgcn_raw_buffer_load_b128(xr, D1 < S::KB && g * 16 >= D1 * E ? 0x7FFFFFF0 : off, 0, 0);
+        const int off = row * d1 * E + kb * 64 + g * 16;
+        const bool pad = (PAD || D1 < S::KB) && kb * 64 + g * 16 >= d1 * E;
+        xf[kb].w = __builtin_amdgcn_raw_buffer_load_b128(xr, pad ? 0x7FFFFFF0 : off, 0, 0);
       }
     };
     constexpr std::false_type OUTPUT{};
@@ -608,19 +613,20 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
     for (int j = 0; j < TC; ++j) zcol[j].set(S::ZS_OFF, 16 * (ct0 + j), g, r);
     // the state slice: lane (g, r) holds rows 4 g .. 4 g + 3 of column r of each of its tiles
     f32x4 h[TR][TC];
-    const size_t sbase = (size_t)bh * D1 * A.d2;
+    const size_t sbase = (size_t)bh * d1 * A.d2;
     auto state_at = [&](int i, int j, int e) __attribute__((always_inline)) {   // element offset inside one head's state
       const int row = 16 * (rt0 + i) + 4 * g + e, col = slice * DS + 16 * (ct0 + j) + r;
-      return A.turned ? col * D1 + row : row * A.d2 + col;
+      return A.turned ? col * d1 + row : row * A.d2 + col;
     };
     auto own = [&](int i) __attribute__((always_inline)) { return S::WR * TR == S::RH || rt0 + i < S::RH; };
+    auto stored = [&](int i) __attribute__((always_inline)) { return own(i) && (!PAD || 16 * (rt0 + i) < d1); };
     const float* init = L.nseg > 1 ? A.seg_states + (size_t)seg * L.seg_subs * L.seg_stride : A.init;
 #pragma unroll
     for (int i = 0; i < TR; ++i)
 #pragma unroll
       for (int j = 0; j < TC; ++j) {
         h[i][j] = zero4();
-        if (init && own(i)) {
+        if (init && stored(i)) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) h[i][j][e] = init[sbase + state_at(i, j, e)];
         }
@@ -735,7 +741,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       for (int i = 0; i < TR; ++i)
 #pragma unroll
         for (int j = 0; j < TC; ++j) {
-          if (!own(i)) continue;
+          if (!stored(i)) continue;
 #pragma unroll
           for (int e = 0; e < 4; ++e) A.fin[sbase + state_at(i, j, e)] = h[i][j][e] * scale;
         }
@@ -908,18 +914,28 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(float* states, const 
   }
 }
 
-template <typename T, int D1, int DS, bool EXACT>
+template <typename T, int D1, int DS, bool EXACT, bool PAD>
 hipError_t launch_sweep_t(const SweepLaunch& L, hipStream_t stream) {
   const long long wgs = cell_workgroups((long long)L.units * L.nseg, L.parts);
   if (wgs == 0) return hipSuccess;
-  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, EXACT>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
+  hipLaunchKernelGGL((sweep_kernel<T, D1, DS, EXACT, PAD>), dim3((unsigned)wgs), dim3(512), 0, stream, L);
   return hipGetLastError();
 }
 
+constexpr int kPadSlice = 32;   // widest slices of launches that pad roles
+template <typename T, int D1, int DS, bool PAD>
+hipError_t launch_sweep_p(const SweepLaunch& L, hipStream_t stream) {
+  constexpr bool F = sizeof(T) == 4;   // fp32 states have one term: one instantiation
+  return L.exact_state || F ? launch_sweep_t<T, D1, DS, true, PAD>(L, stream) : launch_sweep_t<T, D1, DS, F, PAD>(L, stream);
+}
 template <typename T, int D1, int DS>
 hipError_t launch_sweep_x(const SweepLaunch& L, hipStream_t stream) {
-  constexpr bool F = sizeof(T) == 4;   // fp32 states have one term: one instantiation
-  return L.exact_state || F ? launch_sweep_t<T, D1, DS, true>(L, stream) : launch_sweep_t<T, D1, DS, F>(L, stream);
+  for (int i = 0; i < L.nroles; ++i)
+    if (L.role[i].d1 != D1) {
+      if constexpr (DS <= kPadSlice && D1 > 16) return launch_sweep_p<T, D1, DS, true>(L, stream);
+      else return hipErrorInvalidValue;
+    }
+  return launch_sweep_p<T, D1, DS, false>(L, stream);
 }
 
 template <typename T, int D1>
@@ -1081,21 +1097,30 @@ __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dot
   }
 }
 
+// The second kernel of a constant decay's gradient: one thread per head.
 template <typename T>
-__global__ __launch_bounds__(64) void head_decay_grad_kernel(const double* head_sum, int B, int H, T* dg) {
-  const int h = blockIdx.x * 64 + threadIdx.x;
+__device__ __forceinline__ void add_batches(const double* head_sum, int B, int H, T* dg) {
+  const int h = blockIdx.x * 256 + threadIdx.x;
   if (h >= H) return;
   double x = 0.0;
+#pragma unroll 8
   for (int b = 0; b < B; ++b) x += head_sum[(size_t)b * H + h];
   dg[h] = from_f32<T>((float)x);
+}
+template <typename T>
+__global__ __launch_bounds__(256) void head_decay_grad_kernel(const double* head_sum, int B, int H, T* dg) {
+  add_batches(head_sum, B, H, dg);
 }
 
 // Gradients of a query or key shared by `group` heads: the sum of the heads'
 // fp32 parts [units, group, rows, d], rounded once.  Four elements per thread.
+// HBM-bound: 112 us for the 600 MB of B1 H16 Hk4 T32768 d128.  A third plane of
+// workgroups takes add_batches() along, which saves a launch (2 to 5 us).
 template <typename T>
 __global__ __launch_bounds__(256) void fold_heads_kernel(const float* qparts, const float* kparts, int units, int group,
                                                          int rows, int d, const int* lens, int units_per_batch, T* dq,
-                                                         T* dk) {
+                                                         T* dk, const double* head_sum, int B, int H, T* dg) {
+  if (blockIdx.y == 2) return add_batches(head_sum, B, H, dg);
   const float* parts = blockIdx.y ? kparts : qparts;
   T* out = blockIdx.y ? dk : dq;
   const long long per = (long long)rows * d;
@@ -1234,9 +1259,17 @@ static hipError_t launch_sweep(const SweepLaunch& L, int dtype, int d1, int ds, 
 //   fp32, d1 128:  4.10, 5.43, 8.50 (16, 32, 64; wider ones do not fit in LDS)
 //         d1 64:   2.52, 3.24, 4.87            d1 32:  1.73, 2.34, 3.45
 // to which chunk_us() is fitted.
+//
+// A backward of different widths has two launches, one contracting over dk and
+// two sweeps over dv; with few heads one launch of all three, the narrower
+// contraction padded with zeros, fills the CUs better (us, two launches -> one:
+// bf16 B2 H12 T777 dk64 dv128 40.0 -> 31.8, B1 H8 T2000 dk32 dv64 34.7 -> 31.4,
+// fp32 B3 H8 T1000 dk64 dv128 94.7 -> 83.8).  With slices wider than
+// kPadSlice the launches are full anyway.
 struct Split {
   int ds;
   int seg_rows, nseg, sub_rows, subs, nsub;   // subs: sub-segments per segment; nsub: of the whole sequence
+  bool together;   // backward of different widths: the sweeps in one launch, the narrower contraction padded
 };
 static double chunk_us(int d1, int ds, int dtype) {
   return dtype == CKDA_DTYPE_BF16 ? 0.8 + ds * (0.009 + 0.00018 * d1) : 0.7 + 0.015 * d1 + ds * (0.017 + 0.00059 * d1);
@@ -1277,6 +1310,7 @@ static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool 
       p.subs = (per + sub - 1) / sub;
       per = p.subs * sub;   // whole sub-segments
       p.nseg = (nch + per - 1) / per;
+      p.together = false;
       p.sub_rows = sub * C;
       p.seg_rows = per * C;
       p.nsub = (p.nseg - 1) * p.subs + 1;   // the last segment's start is the last one needed
@@ -1285,7 +1319,11 @@ static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool 
         return rounds(heads * slices * p.nseg, kCUs) *
                (segment_us(d1, slice_width(d2, ds)) + per * chunk_us(d1, slice_width(d2, ds), dtype));
       };
-      double us = !backward ? sweep(sv, dk, dv) : dk == dv ? sweep(2 * sk + sv, dk, dv) : sweep(sv, dk, dv) + sweep(2 * sk, dv, dk);
+      double us = !backward ? sweep(sv, dk, dv) : dk == dv ? sweep(2 * sk + sv, dk, dv) : sweep(sv, dk, dv) + sweep(2 * sk, dv, dk) + 2.0;
+      if (backward && dk != dv && ds <= kPadSlice && std::min(dk, dv) >= ds) {
+        const double one = sweep(2 * sk + sv, std::max(dk, dv), ds);   // (a slice's width counts, not d2)
+        if ((p.together = one < us)) us = one;
+      }
       if (p.nseg > 1) {
         // two launches more, the own states (two workgroups a CU take some 1.6
         // times as long as one), and one pass over the states
@@ -1383,6 +1421,7 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
   R.y = a.k;
   R.x_shared = R.y_shared = 1;
   R.z = a.v;
+  R.d1 = a.dk;
   R.d2 = a.dv;
   R.out = a.o;
   R.init = a.h0;
@@ -1436,7 +1475,7 @@ bool linattn_fits_grid(int B, int H, int Hk, int T, int dk, int dv, int dtype, b
   if (bh > 65536) {   // (fewer heads have at most 24 slices each, or some 2000 segments among them)
     const Split sp = plan_split(bh, T, dk, dv, dtype, backward);
     const long long sk = dk / slice_width(dk, sp.ds), sv = dv / slice_width(dv, sp.ds);
-    const long long slices = !backward ? sv : dk == dv ? sv + 2 * sk : std::max(sv, 2 * sk);
+    const long long slices = backward ? sv + 2 * sk : sv;
     most = std::max(512 * cell_workgroups(units * sp.nseg, (int)(H / Hk * slices)), backward ? kDgThreads * bh : 0);
   }
   if (backward && H != Hk) most = std::max(most, units * T * (dk / 4));   // fold_heads_kernel
@@ -1457,20 +1496,20 @@ static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsign
     a.T <= kDgThreads ? launch(decay_grad_kernel<T, 1>) : launch(decay_grad_kernel<T, 4>);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  if (sums) {
-    hipLaunchKernelGGL((head_decay_grad_kernel<T>), dim3((a.H + 63) / 64), dim3(64), 0, a.stream, sums, a.B, a.H,
-                       (T*)a.dg);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  const unsigned head_blocks = (a.H + 255) / 256;
   if (a.H != a.Hk && bh > 0 && a.T > 0) {
     const int units = a.B * a.Hk;
     const long long threads = (long long)units * a.T * a.dk / 4;
-    hipLaunchKernelGGL((fold_heads_kernel<T>), dim3((unsigned)((threads + 255) / 256), 2), dim3(256), 0, a.stream,
+    const unsigned blocks = std::max((unsigned)((threads + 255) / 256), sums ? head_blocks : 0u);
+    hipLaunchKernelGGL((fold_heads_kernel<T>), dim3(blocks, sums ? 3 : 2), dim3(256), 0, a.stream,
                        (const float*)(ws + p.dq), (const float*)(ws + p.dk), units, a.H / a.Hk, a.T, a.dk, a.lens, a.Hk,
-                       (T*)a.dq, (T*)a.dk_out);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+                       (T*)a.dq, (T*)a.dk_out, sums, a.B, a.H, (T*)a.dg);
+    e = hipGetLastError();
+  } else if (sums) {
+    hipLaunchKernelGGL((head_decay_grad_kernel<T>), dim3(head_blocks), dim3(256), 0, a.stream, sums, a.B, a.H, (T*)a.dg);
+    e = hipGetLastError();
   }
-  return hipSuccess;
+  return e;
 }
 
 hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
@@ -1490,6 +1529,7 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dv.y = a.q;
   dv.x_shared = dv.y_shared = 1;
   dv.z = a.dout;
+  dv.d1 = a.dk;
   dv.d2 = a.dv;
   dv.reverse = 1;
   dv.out = a.dv_out;
@@ -1501,6 +1541,7 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dk.z = dq.w = a.q;
   dk.w = dq.z = a.k;
   dk.z_shared = dk.w_shared = dq.z_shared = dq.w_shared = 1;
+  dk.d1 = dq.d1 = a.dv;
   dk.d2 = dq.d2 = a.dk;
   dk.turned = dq.turned = 1;
   dk.reverse = 1;
@@ -1521,15 +1562,15 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   L.exact_state = a.dh0 || a.dhT;
   dv.parts = L.group * (a.dv / dsv);
   dk.parts = dq.parts = L.group * (a.dk / dsk);
-  // one launch where the sweeps have the same widths, else the two that
-  // contract over dv apart from the one over dk
-  if (a.dk == a.dv) {
+  // one launch where the sweeps have the same widths or the split says so, else
+  // the two that contract over dv apart from the one over dk
+  if (a.dk == a.dv || p.sp.together) {
     L.role[0] = dv;
     L.role[1] = dk;
     L.role[2] = dq;
     L.nroles = 3;
     L.parts = dv.parts + dk.parts + dq.parts;
-    if ((e = launch_sweep(L, a.dtype, a.dk, dsk, a.stream)) != hipSuccess) return e;
+    if ((e = launch_sweep(L, a.dtype, std::max(a.dk, a.dv), dsk, a.stream)) != hipSuccess) return e;
   } else {
     L.role[0] = dv;
     L.nroles = 1;
