@@ -36,6 +36,14 @@
 // product ends in a rounded output, three (24 bits) for the state itself,
 // which is returned in fp32.  All sums are fp32.  fp32 inputs take the fp32
 // matrix cores throughout.
+// What bounds it (MI355X, bf16, d128): with slices of 16 and 32 columns each
+// CU's path to the L2, about 16 bytes a cycle for the chunk's x and y, which
+// every slice reads again (B4 H16 T4096, 256 workgroups of 32 columns: 102 us,
+// 256 MB of HBM traffic at 2.6 TB/s); with whole states of 128 columns HBM and
+// the phases' products alike (the backward's three sweeps of that size, 192
+// workgroups: 230 us cold, 680 MB); in short calls the latency of the first loads
+// and of a chunk's two phases (77 rows: 6.8 us).  fp32: the fp32 matrix cores,
+// at half their rate (B3 H8 T1000 dk64 dv128: 37 us).
 // Log decays are summed as two parts, whole multiples of 1/64 (whose sums are
 // exact) and the rest, so that differences of large sums keep fp32 accuracy.
 #include <algorithm>
@@ -754,7 +762,9 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 // the accumulators of its eight waves (two rows of waves, four columns), so
 // that every row of Y and Z is read once; per chunk it copies Y and the terms
 // of the scaled Z to LDS and multiplies Y^T (G(C, .) Z), in two phases with a
-// barrier each as above.  What bounds it is the matrix products.
+// barrier each as above.  Two workgroups a CU.  B1 H16 Hk4 T32768 d128, bf16:
+// 66 us, 2.4 TB/s: bound by the latency of a chunk's loads, its two barriers
+// and the forming of the terms; the products are a third of it.
 template <typename T, int D1, int D2>
 struct OwnCfg {
   static constexpr int E = (int)sizeof(T);
@@ -1150,7 +1160,9 @@ __global__ __launch_bounds__(256) void fold_heads_kernel(const float* qparts, co
 // H <- a H + k v^T, o = H^T q, one read and one write of the state.  A
 // workgroup holds DVS columns of one state: each thread 16-byte columns of
 // ITER rows in registers, stored as soon as they are updated; the column sums
-// of q_i H_i go through LDS.
+// of q_i H_i go through LDS.  HBM-bound: 220 us for 8192 states of 128 x 128
+// (4.9 TB/s, a large copy's rate; 159 us on one repeated set, which the
+// last-level cache holds half of).
 constexpr int kLaDecodeThreads = 256;
 
 template <typename T, int DK, int DVS>
@@ -1242,8 +1254,11 @@ static hipError_t la_decode_dk(const LinAttnDecodeArgs& a, int dvs) {
 hipError_t launch_linattn_decode(const LinAttnDecodeArgs& a) {
   const long long states = (long long)a.N * a.H;
   if (states == 0) return hipSuccess;
+  // Few states: their columns over more CUs, down to 32 (rows of 128 bytes).
+  // us on one repeated set of states, bf16 d128, whole | to 32 | to 16 columns:
+  // 16 states 3.7 | 3.2 | 3.8, 32 states 3.8 | 3.3 | 4.4, 64 states 4.1 | 3.6, 128 states 4.6 | 4.2
   int dvs = a.dv;
-  while (dvs > 16 && states * (a.dv / dvs) < 256) dvs /= 2;   // few states: their columns over more CUs
+  while (dvs > 32 && states * (a.dv / dvs) < 256) dvs /= 2;
   return a.dtype == 1 ? la_decode_dk<bf16_t>(a, dvs) : la_decode_dk<float>(a, dvs);
 }
 
@@ -1336,9 +1351,14 @@ static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool 
       }
       if (p.nseg > 1) {
         // two launches more: the own states (two workgroups a CU take some 1.6
-        // times as long as one), and one pass over the states
+        // times as long as one), and one pass over the states.
         const double own = rounds(dirs * heads * (p.nsub - 1), 2 * kCUs) * sub * own_chunk_us(dk, dv, dtype) * 1.6;
         us += 8.0 + own + (double)dirs * heads * p.nsub * dk * dv * 8 / 4e6;
+        // Segments have to promise a tenth less: chunks of a launch that leaves
+        // CUs idle take less than the times above (backward of B4 H16 T4096 d128,
+        // bf16: 192 workgroups of whole sequences, 3.6 us a chunk, 235 us in all;
+        // four segments, estimated at 98% of the former's time, 285 us)
+        us *= 1.1;
       }
       if (best.ds == 0 || us < least) {
         best = p;
