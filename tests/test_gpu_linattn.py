@@ -404,3 +404,46 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_graphs_that_share_a_workspace():
+    """Two graphs captured with one workspace, replayed in turn: nothing is kept in it between calls."""
+    d1, d2 = cuda(inputs(96, 2, 2, 1, 2048, 32, 64, BF)), cuda(inputs(97, 1, 4, 4, 1500, 64, 32, BF))
+    need = max(ck.linattn_bwd_workspace_size(2, 2, 1, 2048, 32, 64, BF), ck.linattn_bwd_workspace_size(1, 4, 4, 1500, 64, 32, BF),
+               ck.linattn_workspace_size(2, 2, 2048, 32, 64, BF), ck.linattn_workspace_size(1, 4, 1500, 64, 32, BF))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    both = lambda d: [*fwd(d, workspace=ws), *bwd(d, workspace=ws)]  # noqa: E731
+    want = [[t.clone() for t in both(d)] for d in (d1, d2)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for d in (d1, d2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(both(d))
+        graphs.append(g)
+    for rep in range(3):
+        for i in (0, 1):
+            for t in got[i]:
+                t.fill_(float("nan"))
+            ws.fill_(255)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got[i], want[i])), (rep, i)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_tensor_in_several_places(dtype):
+    """q is k, do is v, dhT is h0."""
+    x = inputs(98, 2, 3, 3, 150, 64, 64, dtype)
+    x["k"], x["do"], x["dhT"] = x["q"], x["v"], x["h0"]
+    d = cuda(x)
+    d["k"], d["do"], d["dhT"] = d["q"], d["v"], d["h0"]
+    o, hT, bo, bh = fwd_bounds(x)
+    want = bwd_bounds(x)
+    got_o, got_h = fwd(d)
+    got = dict(zip(("dq", "dk", "dv", "dg", "dh0"), bwd(d)))
+    torch.cuda.synchronize()
+    check("o", got_o, o, bo)
+    check("hT", got_h, hT, bh)
+    for n, (w, b) in want.items():
+        check(n, got[n], w, b)
