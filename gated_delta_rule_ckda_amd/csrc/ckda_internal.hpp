@@ -101,8 +101,8 @@ struct LinAttnDecodeArgs {
 // An operand that is `shared` has one head for the group's heads.
 struct SweepRole {
   const void *x, *y, *z;
-  const void* w;             // dot[slice][bh][row] = w_row . out_row over the slice (or NULL)
-  float* dot;
+  const void* w;             // dot[part][slice][bh][row] = w_row . out_row over the slice (or NULL), of
+  float* dot;                // the rows before the row's chunk (part 0) and of those in it before the row (1)
   void* out;
   const float* init;         // first state (or NULL: zero)
   float* fin;                // last state (or NULL)
@@ -113,6 +113,7 @@ struct SweepRole {
   int reverse;               // from the last row to the first
   int turned;                // init, fin and segment states are stored [d2, d1]
   int out_f32;               // out is fp32
+  int drop_end;              // states without the rows of a sequence's last chunk (its decay applied)
   int parts;                 // workgroups per unit and segment: heads of the group x slices
 };
 struct SweepLaunch {

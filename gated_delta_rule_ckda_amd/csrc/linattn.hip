@@ -190,9 +190,37 @@ __device__ __forceinline__ float wave_prefix(float x) {
   return x;
 }
 
+// sum over this lane and those after it (row_shl within rows, then the sums of the rows after)
+__device__ __forceinline__ float wave_suffix(float x, int lane) {
+#define CKDA_STEP(CTRL) \
+  x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false))
+  CKDA_STEP(0x101);
+  CKDA_STEP(0x102);
+  CKDA_STEP(0x104);
+  CKDA_STEP(0x108);
+#undef CKDA_STEP
+  auto first = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l)); };
+  const float s3 = first(48), s2 = first(32) + s3, s1 = first(16) + s2;
+  return x + (lane < 16 ? s1 : lane < 32 ? s2 : lane < 48 ? s3 : 0.f);
+}
+// the value of the lane before this one (DPP wave_shr), 0 for the first
+__device__ __forceinline__ float lane_before(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x138, 0xF, 0xF, false));
+}
+
 // the value of lane 15 of this lane's row of 16 (DPP row_newbcast)
 __device__ __forceinline__ float row_last(float x) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x15F, 0xF, 0xF, false));
+}
+
+// sum over the lanes r, r + 16, r + 32 and r + 48 (in pairs of rows, then of
+// halves: both operands of a swap the same register)
+__device__ __forceinline__ float row_groups_sum(float x) {
+  const uint32_t a = __float_as_uint(x);
+  const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+  const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
 constexpr float kLog2E = 1.4426950408889634f;
@@ -234,8 +262,9 @@ __device__ __forceinline__ void split_terms(const float* v, Frag* f) {
   }
 }
 
-// Decay factors of a chunk from the log decays g (one row a lane) into dec.
-__device__ __forceinline__ void decay_factors(float g, float* dec, int lane) {
+// Decay factors of a chunk from the log decays g (one row a lane) into dec;
+// drop: the chunk's rows are to have no part in the state after it.
+__device__ __forceinline__ void decay_factors(float g, float* dec, int lane, bool drop = false) {
   float x = g * kLog2E;
   x = x < kDecayFloor ? kDecayFloor : x;   // keeps NaN
   const float whole = rintf(x * 64.f) * (1.f / 64.f);
@@ -245,25 +274,30 @@ __device__ __forceinline__ void decay_factors(float g, float* dec, int lane) {
   dec[lane] = ch;
   dec[C + lane] = cl;
   dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
-  dec[3 * C + lane] = __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
+  dec[3 * C + lane] = drop ? 0.f : __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
   dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
 }
 
 // The rows a workgroup works on: chunk row j of a segment is row row0 + j of
-// the sweep, which is that row of the sequence, or the len - 1 - that one.
+// the sweep, which is that row of the sequence, or the up - 1 - that one, up
+// being len rounded up to whole chunks: the chunks of both directions are the
+// same rows (decay_grad_kernel adds what their sweeps leave chunk by chunk).
 // Rows outside [0, len) fall outside the buffers: they read as zero and are
 // not stored.
 struct Rows {
-  int len, row0, nch, last, dir, first;
+  int len, up, row0, nch, last, dir, first;
   __device__ __forceinline__ Rows(const SweepLaunch& L, int bh, int seg, int seg_rows, int reverse) {
     len = L.lens ? min(max(L.lens[bh / L.heads], 0), L.rows) : L.rows;
+    up = (len + C - 1) / C * C;
     row0 = seg * seg_rows;
     nch = (min(max(len - row0, 0), seg_rows) + C - 1) / C;
     last = max(nch - 1, 0);
     dir = reverse ? -1 : 1;
-    first = reverse ? len - 1 - row0 : row0;
+    first = reverse ? up - 1 - row0 : row0;
   }
   __device__ __forceinline__ int row(int j) const { return first + dir * j; }
+  // chunk c of the segment is the last one of a sweep forward in time
+  __device__ __forceinline__ bool at_end(int c) const { return row0 + C * c + C >= len; }
 };
 // A head's rows of `width` elements of `es` bytes as a range-checked buffer.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, size_t head, int rows, int len, int width,
@@ -274,8 +308,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, size_
 // As stored, in 32 bits; decay_of() widens it.
 template <typename T>
 __device__ __forceinline__ uint32_t load_decay(__amdgpu_buffer_rsrc_t gr, const Rows& R, int j, int reverse, int head_decay) {
-  const int at = reverse ? R.len - j : j;
-  const int off = j < R.len && at < R.len ? (head_decay ? 0 : at * (int)sizeof(T)) : 0x7FFFFFF0;   // out of range: 0
+  const int at = reverse ? R.up - j : j;
+  const int off = (unsigned)at < (unsigned)R.len ? (head_decay ? 0 : at * (int)sizeof(T)) : 0x7FFFFFF0;   // out of range: 0
   if constexpr (sizeof(T) == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(gr, off, 0, 0);
   else return __builtin_amdgcn_raw_buffer_load_b32(gr, off, 0, 0);
 }
@@ -532,6 +566,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         // for decays, one exponential a tile here and one a row of the chunk
         // (decay_factors).
         const float ch = dec[t], cl = dec[C + t];
+        f32x4 self = zero4();   // with dots: the row's pair with itself, which is not part of them
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           const float rowf = __builtin_amdgcn_exp2f((ch - dec[16 * i + 15]) + (cl - dec[C + 16 * i + 15]));
@@ -544,12 +579,28 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float x = p[W][j] * __builtin_amdgcn_exp2f((ch - sh[j]) + (cl - sl[j]));
-            p[W][j] = 4 * g + j <= r ? x : 0.f;
+            p[W][j] = (DOT ? 4 * g + j < r : 4 * g + j <= r) ? x : 0.f;
+            if constexpr (DOT) self[j] = 4 * g + j == r ? x : 0.f;
           }
         }
         const float gam = dec[2 * C + t];
 #pragma unroll
         for (int d = 0; d < NDV; ++d) oacc[d] *= gam;
+        // this slice's part of w_t . out_t, of what the accumulators hold
+        auto dot = [&]() __attribute__((always_inline)) {
+          float x = 0.f;
+#pragma unroll
+          for (int d = 0; d < NDV; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x = __builtin_fmaf(Quad<T>::get(wv[d], j), oacc[d][j], x);
+          return x;   // this lane's columns
+        };
+        float before = 0.f;   // of the rows before the chunk
+        if constexpr (DOT) {
+#pragma unroll
+          for (int d = 0; d < NDV; ++d) pin(wv[d]);
+          before = dot();
+        }
         // O^T += Z^T P^T
 #pragma unroll
         for (int kb = 0; kb < NPB; ++kb) {
@@ -568,25 +619,36 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
             oacc[d] = mma<T>(oacc[d], zf[kb][d], ph);
           }
         }
+        if constexpr (DOT) {
+          const float both = dot();
+          // (bf16: both terms in one product, the tile's rows of Z in both halves of the K block)
+          Frag f;
+          if constexpr (BF) {
+            uint32_t ha, la, hb, lb;
+            split2(self[0], self[1], ha, la);
+            split2(self[2], self[3], hb, lb);
+            f.w = u32x4{ha, hb, la, lb};
+          } else f = frag_from_acc_f32(self);
+#pragma unroll
+          for (int d = 0; d < NDV; ++d) {
+            const u32x4 z = zf[NPB - 1][d].w;
+            constexpr int at = W & 1 ? 2 : 0;
+            oacc[d] = mma<T>(oacc[d], BF ? Frag{u32x4{z[at], z[at + 1], z[at], z[at + 1]}} : zf[NPB - 1][d], f);
+          }
+          const float in = row_groups_sum(both - before);
+          before = row_groups_sum(before);
+          if (g == 0 && (unsigned)row < (unsigned)len) {
+            float* to = A.dot + ((size_t)slice * L.units * L.group + bh) * L.rows + row;
+            to[0] = before;
+            to[(size_t)slices * L.units * L.group * L.rows] = in;
+          }
+        }
         // this lane holds four consecutive columns of row t
 #pragma unroll
         for (int d = 0; d < NDV; ++d) {
           const int col = slice * DS + 16 * d + 4 * g;
           if (A.out_f32) store4<float>(outr, (row * A.d2 + col) * 4, oacc[d]);
           else store4<T>(outr, (row * A.d2 + col) * E, oacc[d]);
-        }
-        if constexpr (DOT) {   // this slice's part of w_t . out_t
-          float x = 0.f;
-#pragma unroll
-          for (int d = 0; d < NDV; ++d) pin(wv[d]);
-#pragma unroll
-          for (int d = 0; d < NDV; ++d)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x = __builtin_fmaf(Quad<T>::get(wv[d], j), oacc[d][j], x);
-          x += __shfl_xor(x, 16, 64);
-          x += __shfl_xor(x, 32, 64);
-          if (g == 0 && (unsigned)row < (unsigned)len)
-            A.dot[((size_t)slice * L.units * L.group + bh) * L.rows + row] = x;
         }
         place(u0, c + 1, OUTPUT);
         load(u0, min(c + 2, R.last), OUTPUT);
@@ -681,7 +743,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
         }
       }
     }
-    if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane);
+    if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane, A.drop_end && R.at_end(0));
     put_state();
     lds_barrier();   // the first decay factors are there
     place(u0, 0, STATE);
@@ -692,7 +754,7 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       // ---- phase 1.  A operand: the columns of Y this wave's row tiles are;
       // B operand: the terms of G(C, s) z_s for its column tile
       const float end = dec_of(c)[2 * C + C - 1];
-      if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane);
+      if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane, A.drop_end && R.at_end(c + 1));
 #pragma unroll
       for (int i = 0; i < TR; ++i)
 #pragma unroll
@@ -851,14 +913,14 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
 #pragma unroll
     for (int j = 0; j < S::TC; ++j) h[i][j] = zero4();
   load(0);
-  if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane);
+  if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(0), lane, A.drop_end && R.at_end(0));
   lds_barrier();
   place(0);
   load(min(1, R.last));
   lds_barrier();
   float decay = 1.f;   // product of the chunks' decays
   for (int c = 0; c < R.nch; ++c) {
-    if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane);
+    if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane, A.drop_end && R.at_end(c + 1));
     const float end = dec_of(c)[2 * C + C - 1];
     decay *= end;
 #pragma unroll
@@ -1015,103 +1077,191 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 
 // ---------------------------------------------------------------- decay gradient
 // dg_t = a_t <R_t, H_{t-1}> is everything that passes gate t: the pairs of a
-// key before t and a query from t on, with the initial state among the keys and
-// dhT among the queries.  With a_u = q_u . dq_u (every pair ending at query u)
-// and b_u = k_u . dk_u (every pair starting at key u)
-//   dg_t = <dhT, H_T> + sum_{u >= t} (a_u - b_u),
-// a running sum from the sequence's end.  The sweeps leave the parts of a and b
-// per slice, taken from their unrounded outputs; the sum runs in fp64.
-// One workgroup per (batch, head), four rows per thread (one, where all fit); of a constant decay,
-// whose gradient is the sum over rows and batch, each leaves its sum for a
-// second kernel, but for a single batch entry.  (One workgroup per head over
-// the batch entries in turn saves that launch of some 2 us, and loses from two
-// entries on: 8 heads, 100 rows, the whole backward in us, 19.0 and 18.3 for
-// one entry, 18.3 and 19.6 for two, 19.3 and 27.8 for eight.)
-// Bound by the latency of its loads and of the scan's barriers: 5.8 us for
-// B4 H16 T4096, 4.0 us for the eight slices of B2 H12 T777 (13.6 us with four
-// rows to every thread and the slices' loads one after another).
+// key s before t and a query u from t on, with the initial state among the keys
+// and dhT among the queries.  The dots q_u . dq_u (every pair ending at u) less
+// k_s . dk_s (every pair starting at s), summed over all rows from t on, give
+// it too, but with the rounding errors of the largest pairs anywhere behind t:
+// of strong decays nothing is left.  So pairs that pass no gate (a token with
+// itself, the last token with dhT) are never added, and the sum is taken chunk
+// by chunk.  For t in chunk c, rows u and s of that chunk only:
+//   dg_t = sum_{u >= t} (i_u - j_u) + sum_{u >= t} a_u + sum_{s < t} b_s + X_c
+// with q_u . dq_u = a_u (keys before the chunk) + i_u (in it, before u) and
+// k_s . dk_s = b_s (queries after the chunk) + j_s (in it, after s), which the
+// sweeps leave per slice from their unrounded outputs; X_c is what passes the
+// whole chunk.  Of the last chunk that is <dhT, H> with H its start state,
+// decayed; of the others a running sum again, but over chunks,
+//   X_c = X_{c+1} + sum_{u in c+1} a_u - sum_{s in c} b_s,
+// which starts anew, from 0, where the chunk lets less than 2^-16 pass and the
+// sum is not above its own rounding error: 2^-19 (fp32 inputs: 2^-23) of the sum
+// of |a| and |b| of one of the two chunks, the dots of bf16 inputs coming from
+// states and pairs of 16 bits.  A decay factor below 2^-126 counts as 0: dg_t is
+// 0 there, and no sum crosses it.
+// What is left: dg_t is off by some 2^-18 (2^-22) of the pairs in its own chunk
+// that pass any gate, and of what passes the chunk's ends.  A single gate much
+// stronger than those around it, with a gradient that much smaller than theirs,
+// keeps fewer digits of its own.
+//
+// One workgroup per (batch, head); a wave has CPW of the 16 CPW chunks of a
+// round, from the sequence's end, a lane a row: the sums inside a chunk are
+// fp32 prefix sums of the wave; one wave runs X over the round's chunks, in
+// fp64, as are the sums of dhT and of a constant decay.  Of a constant decay, whose gradient is the sum over rows and batch,
+// each workgroup leaves its sum for a second kernel, but for a single batch
+// entry.  (One workgroup per head over the batch entries in turn saves that
+// launch of some 2 us, and loses from two entries on.)
 constexpr int kDgThreads = 1024;
 
-__device__ __forceinline__ double wave_prefix_f64(double x, int lane) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const double y = __shfl_up(x, off, 64);
-    if (lane >= off) x += y;
-  }
-  return x;
+// x of another lane by a DPP move (0 where there is none), halves of a double
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_f64(double x) {
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+  w[0] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xF, false);
+  w[1] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, w);
 }
+__device__ __forceinline__ double lane_f64(double x, int lane) {
+  u32x2 w = __builtin_bit_cast(u32x2, x);
+  w[0] = (uint32_t)__builtin_amdgcn_readlane((int)w[0], lane);
+  w[1] = (uint32_t)__builtin_amdgcn_readlane((int)w[1], lane);
+  return __builtin_bit_cast(double, w);
+}
+// sum over the lanes up to this one
+__device__ __forceinline__ double wave_prefix_f64(double x) {
+  x += dpp_f64<0x111>(x);   // row_shr:1, 2, 4, 8, then the last lanes of rows into those after
+  x += dpp_f64<0x112>(x);
+  x += dpp_f64<0x114>(x);
+  x += dpp_f64<0x118>(x);
+  x += dpp_f64<0x142, 0xA>(x);
+  return x + dpp_f64<0x143, 0xC>(x);
+}
+__device__ __forceinline__ double lane_before_f64(double x) { return dpp_f64<0x138>(x); }   // wave_shr:1
 
-template <typename T, int RPT>
+template <typename T, int CPW>
 __global__ __launch_bounds__(kDgThreads) void decay_grad_kernel(const float* dotq, const float* dotk, int slices,
-                                                                const float* dhT, const float* hT, int elems,
-                                                                const int* lens, int rows, int heads, T* dg,
-                                                                double* head_sum, int head_decay) {
-  __shared__ double s_wave[kDgThreads / 64], s_total;
+                                                                const T* gate, const float* dhT, const float* hT,
+                                                                int elems, int has_h0, const int* lens, int rows, int heads,
+                                                                T* dg, double* head_sum, int head_decay) {
+  constexpr int WAVES = kDgThreads / 64, NC = WAVES * CPW;   // chunks of a round
+  static_assert(NC <= 64, "one lane of the wave that runs X per chunk");
+  __shared__ double s_wave[WAVES], s_x[NC];
+  __shared__ float s_a[NC], s_b[NC], s_size[NC], s_whole[NC];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  // sum over the workgroup, and the exclusive prefix of this thread
-  auto scan = [&](double x, double& total) __attribute__((always_inline)) {
-    const double inc = wave_prefix_f64(x, lane);
-    if (lane == 63) s_wave[wave] = inc;
+  // sum over the workgroup, for wave 0
+  auto total = [&](double x) __attribute__((always_inline)) {
+    x = wave_prefix_f64(x);
+    if (lane == 63) s_wave[wave] = x;
     __syncthreads();
-    if (wave == 0) {
-      const double w = lane < kDgThreads / 64 ? s_wave[lane] : 0.0;
-      const double winc = wave_prefix_f64(w, lane);
-      if (lane < kDgThreads / 64) s_wave[lane] = winc - w;
-      if (lane == 63) s_total = winc;
-    }
-    __syncthreads();
-    const double before = s_wave[wave] + (inc - x);
-    total = s_total;
-    __syncthreads();
-    return before;
+    x = 0.0;
+    if (wave == 0)
+      for (int w = 0; w < WAVES; ++w) x += s_wave[w];
+    return x;
   };
-  double sum = 0.0;
   const int bh = blockIdx.x;
   const int len = lens ? min(max(lens[bh / heads], 0), rows) : rows;
-  double carry = 0.0;
+  const int nch = (len + C - 1) / C;
+  const T* gp = gate + (head_decay ? (size_t)(bh % heads) : (size_t)bh * rows);
+  // wave 0: X of the chunk after a round's first, and that chunk's sum of a and size
+  double x_after = 0.0, a_after = 0.0, sum = 0.0;
+  float size_after = 0.f;
   if (dhT) {
-    double x = 0.0;
+    double y = 0.0;
     const f32x4 *p = reinterpret_cast<const f32x4*>(dhT + (size_t)bh * elems),
-                *q = reinterpret_cast<const f32x4*>(hT + (size_t)bh * elems);
+                *h = reinterpret_cast<const f32x4*>(hT + (size_t)bh * elems);
 #pragma unroll 4
     for (int i = tid; i < elems / 4; i += kDgThreads) {
-      const f32x4 u = p[i], v = q[i];
-      x += ((double)u[0] * v[0] + (double)u[1] * v[1]) + ((double)u[2] * v[2] + (double)u[3] * v[3]);
+      const f32x4 u = p[i], w = h[i];
+      y += ((double)u[0] * w[0] + (double)u[1] * w[1]) + ((double)u[2] * w[2] + (double)u[3] * w[3]);
     }
-    scan(x, carry);
+    x_after = total(y);
   }
-  for (int base = 0; base < len; base += RPT * kDgThreads) {   // counted from the end
-    double d[RPT], mine = 0.0;
+  const size_t half = (size_t)slices * gridDim.x * rows;   // from the dots before (after) the chunk to those in it
+  for (int end = nch; end > 0; end -= NC) {   // chunks end - 1, end - 2, ..
+    float mine[CPW];
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) d[j] = 0.0;
-    const int first = len - 1 - (base + RPT * tid);
-    if (first >= 0) {
+    for (int j = 0; j < CPW; ++j) {
+      const int i = j * WAVES + wave, c = end - 1 - i, row = C * c + lane;
+      float a = 0.f, b = 0.f, in = 0.f, x = 0.f;
+      if (c >= 0 && row < len) {
+        x = to_f32(head_decay ? *gp : gp[row]) * kLog2E;
 #pragma unroll 4   // the loads of four slices in flight
-      for (int s = 0; s < slices; ++s)
-#pragma unroll
-        for (int j = 0; j < RPT; ++j) {   // (a row before the first: that one again, dropped below)
-          const size_t at = ((size_t)s * gridDim.x + bh) * rows + max(first - j, 0);
-          d[j] += (double)dotq[at] - (double)dotk[at];
+        for (int s = 0; s < slices; ++s) {
+          const size_t at = ((size_t)s * gridDim.x + bh) * rows + row;
+          a += dotq[at];
+          b += dotk[at];
+          in += dotq[half + at] - dotk[half + at];
         }
+      }
+      const bool closed = x < -126.f;
+      const unsigned long long shut = __ballot(closed);
+      const float from = wave_suffix(a, lane), upto = wave_prefix(b), before = lane_before(upto);
+      float tail = wave_suffix(in, lane);
+      if (shut) {   // pairs in the chunk: of the rows up to the next closed gate
+        const unsigned long long later = lane < 63 ? shut >> (lane + 1) : 0;
+        // (summed again for that: a difference of tails would keep the rounding of what lies behind the gate)
+        tail = in;
 #pragma unroll
-      for (int j = 0; j < RPT; ++j) d[j] = mine += first - j >= 0 ? d[j] : 0.0;
+        for (int off = 1; off < 64; off <<= 1) {
+          const float y = __shfl_down(tail, off, 64);
+          if (lane + off < 64 && (later & ((1ull << off) - 1)) == 0) tail += y;
+        }
+      }
+      mine[j] = closed ? 0.f : from + before + tail;
+      const float size = group_sum<64>(fabsf(a) + fabsf(b));
+      const float whole = group_sum<64>(x < kDecayFloor ? kDecayFloor : x);   // log2 of the chunk's decay
+      if (lane == 0) {
+        s_a[i] = from;
+        s_size[i] = size;
+        s_whole[i] = shut ? kDecayFloor : whole;
+      }
+      if (lane == 63) s_b[i] = upto;
     }
-    double total;
-    const double before = carry + scan(mine, total);
+    __syncthreads();
+    if (wave == 0) {
+      constexpr float kNoise = sizeof(T) == 2 ? 0x1p-19f : 0x1p-23f;
+      const int n = min(end, NC), c = end - 1 - lane;   // a lane a chunk
+      const bool live = lane < n, last = c == nch - 1;
+      const double a = live ? s_a[lane] : 0.0, b = live ? s_b[lane] : 0.0;
+      const float size = live ? s_size[lane] : 0.f, whole = live ? s_whole[lane] : 0.f;
+      double a_prev = lane_before_f64(a);
+      float size_prev = __shfl_up(size, 1, 64);
+      if (lane == 0) a_prev = a_after, size_prev = size_after;
+      double x = live && !last ? a_prev - b : 0.0;
+      if (lane == 0) x += x_after;
+      x = wave_prefix_f64(x);
+      // the first chunk that starts anew, then the first one after it, ..
+      const bool zero = whole < -126.f || (c == 0 && !has_h0), faint = whole < -16.f && !last;
+      const double noise = (double)(kNoise * fmaxf(size, size_prev));
+      double base = 0.0;
+      int done = -1;
+      for (;;) {
+        const unsigned long long hit = __ballot(live && lane > done && (zero || (faint && fabs(x - base) <= noise)));
+        if (!hit) break;
+        done = __ffsll((long long)hit) - 1;
+        const double at = lane_f64(x, done);
+        if (lane >= done) base = at;
+      }
+      x -= base;
+      if (live) s_x[lane] = x;
+      x_after = lane_f64(x, n - 1);
+      a_after = lane_f64(a, n - 1);
+      size_after = __shfl(size, n - 1, 64);
+    }
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < RPT; ++j) {
-      if (first - j < 0) continue;
-      if (head_decay) sum += before + d[j];
-      else dg[(size_t)bh * rows + first - j] = from_f32<T>((float)(before + d[j]));
+    for (int j = 0; j < CPW; ++j) {
+      const int i = j * WAVES + wave, c = end - 1 - i, row = C * c + lane;
+      if (c < 0 || row >= len) continue;
+      const double d = mine[j] + s_x[i];
+      if (head_decay) sum += d;
+      else dg[(size_t)bh * rows + row] = from_f32<T>((float)d);
     }
-    carry += total;
+    __syncthreads();   // before the next round's sums
   }
   if (head_decay) {
-    double total;
-    scan(sum, total);
+    __syncthreads();
+    sum = total(sum);
     if (tid == 0) {
-      if (head_sum) head_sum[blockIdx.x] = total;
-      else dg[blockIdx.x] = from_f32<T>((float)total);
+      if (head_sum) head_sum[blockIdx.x] = sum;
+      else dg[blockIdx.x] = from_f32<T>((float)sum);
     }
   }
 }
@@ -1423,6 +1573,7 @@ static hipError_t segment_starts(const LinAttnArgs& a, const Split& sp, float* s
   F.z = a.v;
   F.seg_out = states;
   F.seg_decay = decay;
+  F.drop_end = rstates != nullptr;   // (the backward's dq sweep)
   R.y = a.q;
   R.z = a.dout;
   R.seg_out = rstates;
@@ -1470,8 +1621,9 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
 }
 
 // workspace of the backward: dots of queries and keys with their gradients,
-// the final state, segment states of both directions, and the heads' parts of
-// shared gradients
+// (of either, with the rows outside and inside their chunk), the last chunk's
+// decayed start state, segment states of both directions, and the heads' parts
+// of shared gradients
 struct BwdPlan {
   Split sp;
   size_t dotq, dotk, hT, head_sum, states, rstates, decay, dq, dk, bytes;
@@ -1488,8 +1640,8 @@ static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv, int dtype) 
     at += up256(bytes);
     return here;
   };
-  p.dotq = take((size_t)sk * bh * T * 4);
-  p.dotk = take((size_t)sk * bh * T * 4);
+  p.dotq = take((size_t)sk * bh * T * 8);
+  p.dotk = take((size_t)sk * bh * T * 8);
   p.hT = take(bh * elems * 4);
   p.head_sum = take(bh * 8);
   p.states = take(nsub * bh * elems * 4);
@@ -1527,8 +1679,8 @@ static hipError_t launch_bwd_tail(const LinAttnArgs& a, const BwdPlan& p, unsign
   if (bh > 0) {
     auto launch = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(bh), dim3(kDgThreads), 0, a.stream, (const float*)(ws + p.dotq),
-                         (const float*)(ws + p.dotk), slices, a.dhT, (const float*)(ws + p.hT), a.dk * a.dv, a.lens, a.T,
-                         a.H, (T*)a.dg, sums, a.head_decay);
+                         (const float*)(ws + p.dotk), slices, (const T*)a.g, a.dhT, (const float*)(ws + p.hT), a.dk * a.dv,
+                         a.h0 != nullptr, a.lens, a.T, a.H, (T*)a.dg, sums, a.head_decay);
     };
     a.T <= kDgThreads ? launch(decay_grad_kernel<T, 1>) : launch(decay_grad_kernel<T, 4>);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1591,7 +1743,8 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   dq.out = grouped ? (void*)(ws + p.dq) : a.dq;
   dq.dot = (float*)(ws + p.dotq);
   dq.init = a.h0;
-  dq.fin = a.dhT ? (float*)(ws + p.hT) : nullptr;   // <dhT, H_T> of the decay gradient
+  dq.fin = a.dhT ? (float*)(ws + p.hT) : nullptr;   // what of the last chunk's start state meets dhT
+  dq.drop_end = 1;
   dq.seg_states = states;
   SweepLaunch L = sweep_base(a);
   set_split(L, a, p.sp);

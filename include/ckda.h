@@ -445,9 +445,9 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace ckda_linattn_bwd needs, or 0 for invalid or
- * unsupported sizes: two fp32 numbers per row, head and slice of key channels,
- * the final states, segment states as the forward's for both directions and,
- * with shared heads, the heads' fp32 parts of dq and dk. */
+ * unsupported sizes: four fp32 numbers per row, head and slice of key channels,
+ * one state for each head, segment states as the forward's for both directions
+ * and, with shared heads, the heads' fp32 parts of dq and dk. */
 size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int dv, int dtype);
 
 /* Backward: the gradients of a loss L given dout = dL/do [B, H, T, dv] (dtype)
@@ -460,6 +460,12 @@ size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int 
  * With R_t = dL/dH_t (R_t = a_{t+1} R_{t+1} + q_t do_t^T, R_T = dhT + q_T
  * do_T^T): dq_t = H_t do_t, dk_t = R_t v_t, dv_t = R_t^T k_t, dh0 = a_1 R_1 and
  * dg_t = a_t <R_t, H_{t-1}>.  Nothing of the forward is needed but its inputs.
+ * Accuracy of dg (beside its rounding to dtype): some 2^-18 (F32: 2^-22) of the
+ * gradients of its 64-row chunk and of what passes that chunk's ends, whatever
+ * the decays' strength, as long as they are alike; a gate much stronger than
+ * those around it, with a gradient that much smaller, keeps fewer digits of its
+ * own.  A decay factor below 2^-126 (g < -87.4) counts as 0 in it: dg is 0 there
+ * and nothing crosses it.
  * Outputs must not overlap each other, any input or the workspace. */
 int ckda_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* h0, const int* lens,
                      const void* dout, const float* dhT, void* dq, void* dk, void* dv, void* dg, float* dh0, int B,
