@@ -47,9 +47,12 @@ static int check_aligned(const char* fn, const Range* r, int n) {
   return CKDA_OK;
 }
 
-// no output overlaps an input or another output; `same` may equal `with` exactly
-static int check_alias(const char* fn, const Range* in, int nin, const Range* out, int nout,
+// no output overlaps an input or another output, and the workspace (among the
+// inputs, or NULL) no input; `same` may equal `with` exactly
+static int check_alias(const char* fn, const Range* in, int nin, const Range* out, int nout, const Range* ws,
                        const Range* same = nullptr, const Range* with = nullptr) {
+  for (int j = 0; ws && j < nin; ++j)
+    if (&in[j] != ws && overlap(*ws, in[j])) return fail(CKDA_ERR_ALIAS, "%s: workspace overlaps %s", fn, in[j].name);
   for (int i = 0; i < nout; ++i) {
     for (int j = 0; j < nin; ++j) {
       if (&out[i] == same && &in[j] == with && same->lo == with->lo) continue;
@@ -103,7 +106,7 @@ int ckda_linattn_fwd(const void* q, const void* k, const void* v, const void* g,
   const Range out[] = {range("o", o, n.v), range("hT", hT, hT ? n.states : 0)};
   if ((st = check_aligned(fn, in, 6)) != CKDA_OK || (st = check_aligned(fn, out, 2)) != CKDA_OK) return st;
   if (lens && ((uintptr_t)lens & 3u) != 0) return fail(CKDA_ERR_DIM, "%s: lens is not 4-byte aligned", fn);
-  if ((st = check_alias(fn, in, 7, out, 2, &out[1], &in[4])) != CKDA_OK) return st;   // hT may be h0
+  if ((st = check_alias(fn, in, 7, out, 2, &in[5], &out[1], &in[4])) != CKDA_OK) return st;   // hT may be h0
   ckda::LinAttnArgs a = {};
   a.q = q, a.k = k, a.v = v, a.g = g, a.h0 = h0, a.o = o, a.hT = hT, a.lens = lens;
   a.B = B, a.H = H, a.Hk = Hk, a.T = T, a.dk = dk, a.dv = dv, a.dtype = dtype;
@@ -151,7 +154,7 @@ int ckda_linattn_bwd(const void* q, const void* k, const void* v, const void* g,
                        range("dg", dg, dg ? n.g : 0), range("dh0", dh0, dh0 ? n.states : 0)};
   if ((st = check_aligned(fn, in, 8)) != CKDA_OK || (st = check_aligned(fn, out, 5)) != CKDA_OK) return st;
   if (lens && ((uintptr_t)lens & 3u) != 0) return fail(CKDA_ERR_DIM, "%s: lens is not 4-byte aligned", fn);
-  if ((st = check_alias(fn, in, 9, out, 5)) != CKDA_OK) return st;
+  if ((st = check_alias(fn, in, 9, out, 5, &in[7])) != CKDA_OK) return st;
   ckda::LinAttnArgs a = {};
   a.q = q, a.k = k, a.v = v, a.g = g, a.h0 = h0, a.lens = lens, a.dout = dout, a.dhT = dhT;
   a.dq = dq, a.dk_out = dk_out, a.dv_out = dv_out, a.dg = dg, a.dh0 = dh0;
@@ -176,7 +179,7 @@ int ckda_linattn_decode_step(const void* q, const void* k, const void* v, const 
   const Range in[] = {range("q", q, n.qk), range("k", k, n.qk), range("v", v, n.v), range("g", g, n.g)};
   const Range out[] = {range("o", o, n.v), range("H_inout", H_inout, n.states)};
   if ((st = check_aligned(fn, in, 4)) != CKDA_OK || (st = check_aligned(fn, out, 2)) != CKDA_OK) return st;
-  if ((st = check_alias(fn, in, 4, out, 2)) != CKDA_OK) return st;
+  if ((st = check_alias(fn, in, 4, out, 2, nullptr)) != CKDA_OK) return st;
   const ckda::LinAttnDecodeArgs a{q,  k,  v,     g, H_inout, o, N, H, Hk, dk, dv, dtype, (flags & CKDA_DECAY_HEAD) != 0,
                                   (hipStream_t)stream};
   const hipError_t e = ckda::launch_linattn_decode(a);
@@ -222,7 +225,7 @@ int ckda_head_norm_fwd(const void* x, const void* z, const float* w, const float
                       range("b", b, b ? wb : 0)};
   const Range out[] = {range("y", y, bytes)};
   if ((st = check_aligned(fn, in, 4)) != CKDA_OK || (st = check_aligned(fn, out, 1)) != CKDA_OK) return st;
-  if ((st = check_alias(fn, in, 4, out, 1)) != CKDA_OK) return st;
+  if ((st = check_alias(fn, in, 4, out, 1, nullptr)) != CKDA_OK) return st;
   ckda::HeadNormArgs a = {};
   a.x = x, a.z = z, a.w = w, a.b = b, a.y = y;
   a.B = B, a.H = H, a.T = T, a.D = D, a.wheads = wheads, a.dtype = dtype, a.flags = flags, a.eps = eps;
@@ -258,7 +261,7 @@ int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float
   const Range out[] = {range("dx", dx, bytes), range("dz", dz, z ? bytes : 0), range("dw", dw, dw ? wb : 0),
                        range("db", db, db ? wb : 0)};
   if ((st = check_aligned(fn, in, 6)) != CKDA_OK || (st = check_aligned(fn, out, 4)) != CKDA_OK) return st;
-  if ((st = check_alias(fn, in, 6, out, 4)) != CKDA_OK) return st;
+  if ((st = check_alias(fn, in, 6, out, 4, &in[5])) != CKDA_OK) return st;
   ckda::HeadNormArgs a = {};
   a.x = x, a.z = z, a.w = w, a.b = b, a.dy = dy, a.dx = dx, a.dz = dz, a.dw = dw, a.db = db;
   a.B = B, a.H = H, a.T = T, a.D = D, a.wheads = wheads, a.dtype = dtype, a.flags = flags, a.eps = eps;

@@ -466,7 +466,8 @@ size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int 
  * those around it, with a gradient that much smaller, keeps fewer digits of its
  * own.  A decay factor below 2^-126 (g < -87.4) counts as 0 in it: dg is 0 there
  * and nothing crosses it.
- * Outputs must not overlap each other, any input or the workspace. */
+ * Outputs must not overlap each other, any input or the workspace, nor the
+ * workspace an input. */
 int ckda_linattn_bwd(const void* q, const void* k, const void* v, const void* g, const float* h0, const int* lens,
                      const void* dout, const float* dhT, void* dq, void* dk, void* dv, void* dg, float* dh0, int B,
                      int H, int Hk, int T, int dk_, int dv_, int dtype, int flags, void* workspace,
@@ -521,7 +522,7 @@ size_t ckda_head_norm_bwd_workspace_size(int B, int H, int T, int D, int wheads,
  *   [wheads, D] fp32 (either may be NULL to skip it; summed over batch, time
  *   and, if shared, heads, in a fixed order).
  * The row statistics are recomputed from x.  Outputs must not overlap each
- * other, any input or the workspace. */
+ * other, any input or the workspace, nor the workspace an input. */
 int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float* b, const void* dy, void* dx, void* dz,
                        float* dw, float* db, int B, int H, int T, int D, int wheads, int dtype, int flags, float eps,
                        void* workspace, size_t workspace_bytes, void* stream);
