@@ -640,10 +640,10 @@ def _norm_args(x, w, b, gate, act, rms):
     wheads = None
     for name, t in (("w", w), ("b", b)):
         if t is not None:
-            if t.dim() != 2 or t.shape[0] not in (1, H) or (wheads or t.shape[0]) != t.shape[0]:
+            if t.dim() != 2 or t.shape[0] not in (1, H) or wheads not in (None, t.shape[0]):
                 raise ValueError(f"{name} must be [H, D] or [1, D] (w and b alike), got shape {tuple(t.shape)}")
             wheads = t.shape[0]
-    return B, H, T, D, wheads or 1, (NORM_RMS if rms else 0) | (_ACTS[act] if gate is not None else 0)
+    return B, H, T, D, 1 if wheads is None else wheads, (NORM_RMS if rms else 0) | (_ACTS[act] if gate is not None else 0)
 
 
 def head_norm_fwd(x, w=None, b=None, gate=None, act="silu", rms=False, eps=1e-5, y=None, stream=None):

@@ -397,7 +397,8 @@ int slab_rows(int rows, int H, int lpr, bool bwd) {
 
 template <typename T, int VEC, int LPR, int NV>
 hipError_t launch_norm_t(const HeadNormArgs& a, bool bwd) {
-  RowGeom G{a.H, a.T, a.D, a.B * a.T, slab_rows(a.B * a.T, a.H, LPR, bwd), heads_first(a.H, a.D, (int)sizeof(T), bwd)};
+  const int rows = a.H > 0 ? a.B * a.T : 0;
+  RowGeom G{a.H, a.T, a.D, rows, slab_rows(rows, std::max(a.H, 1), LPR, bwd), heads_first(a.H, a.D, (int)sizeof(T), bwd)};
   const unsigned slabs = (G.rows + G.slab_rows - 1) / G.slab_rows;   // at most 4096
   const dim3 grid = G.heads_first ? dim3(a.H, slabs) : dim3(slabs, a.H);
   const int act = a.z ? a.flags & (kActSilu | kActSigmoid) : kActNone;

@@ -250,7 +250,8 @@ int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float
   int st = head_norm_sizes(fn, z, B, H, T, D, wheads, dtype, flags, eps);
   if (st != CKDA_OK) return st;
   const size_t rows = (size_t)B * T * H;
-  if (H == 0 || (rows == 0 && !dw && !db)) return ok();
+  // gradients of shared weights exist (as zeros) without rows or heads
+  if (wheads == 0 || (rows == 0 && !dw && !db)) return ok();
   if (rows > 0 && (!x || !dy || !dx || (z && !dz)))
     return fail(CKDA_ERR_NULL, "%s: x, dy and dx (dz with z) are required", fn);
   const size_t need = ckda_head_norm_bwd_workspace_size(B, H, T, D, wheads, dtype);
