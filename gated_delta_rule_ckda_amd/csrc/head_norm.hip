@@ -138,7 +138,7 @@ struct RowGeom {
 //   backward  bf16 B4 H16 T4096 D128 86 -> 81, B1 H64 T4096 D128 83 -> 77, B4 H8 T4096 D256 87 -> 77;
 //             fp32 B2 H8 T4096 D128 40 -> 34.5
 // but, in the backward, for rows of 512 bytes and more in token-major rows of
-// 8 KB and more:
+// 8 KB and more (as measured; why these differ is not known):
 //             bf16 B2 H8 T4096 D512 75 -> 82; fp32 B2 H16 T4096 D128 68 -> 78, B1 H32 T4096 D128 70 -> 76
 bool heads_first(int H, int D, int es, bool bwd) { return !bwd || D * es < 512 || H * D * es < 8192; }
 

@@ -34,18 +34,22 @@
 // Precision: the inputs are exact in bf16; every factor that is not (P, H and
 // the scaled Z) is carried as a sum of bf16 terms: two (16 bits) where the
 // product ends in a rounded output, three (24 bits) for the state itself,
-// which is returned in fp32.  All sums are fp32.  fp32 inputs take the fp32
-// matrix cores throughout.
-// What bounds it (MI355X, bf16, d128): with slices of 16 and 32 columns each
-// CU's path to the L2, about 16 bytes a cycle for the chunk's x and y, which
-// every slice reads again (B4 H16 T4096, 256 workgroups of 32 columns: 102 us,
-// 256 MB of HBM traffic at 2.6 TB/s); with whole states of 128 columns HBM and
-// the phases' products alike (the backward's three sweeps of that size, 192
-// workgroups: 230 us cold, 680 MB); in short calls the latency of the first loads
-// and of a chunk's two phases (77 rows: 6.8 us).  fp32: the fp32 matrix cores,
-// at half their rate (B3 H8 T1000 dk64 dv128: 37 us).
+// which is returned in fp32 (two where none is).  All sums are fp32.  fp32
+// inputs take the fp32 matrix cores throughout.
+// What bounds it (MI355X, bf16, d128): with slices of 32 columns each CU's
+// vector-memory return path, 84% busy (TD_TD_BUSY) at some 11 bytes a cycle, as
+// every slice reads the chunk's x and y again (B4 H16 T4096, 256 workgroups: 104
+// us, 260 MB of HBM traffic); with whole states of 128 columns no unit by itself
+// (the backward's three sweeps of that size, 192 workgroups: 250 us, 790 MB;
+// return path 57%, matrix cores 21%, LDS 27% busy): one workgroup to a CU waits at
+// two barriers a chunk; in short calls the latency of the first loads and of a
+// chunk's two phases (77 rows: 6.8 us).  fp32: that latency too (B3 H8 T1000 dk64
+// dv128: 38 us, matrix cores 19%, return path 25% busy).
 // Log decays are summed as two parts, whole multiples of 1/64 (whose sums are
 // exact) and the rest, so that differences of large sums keep fp32 accuracy.
+// (g log2 e itself is rounded once for each row, by 2^-24 of it: at most 4e-8 of
+// the norm of o over 1000 rows of constant decays, the products' own roundings
+// being 2e-7.)
 #include <algorithm>
 #include <type_traits>
 
@@ -97,7 +101,8 @@ struct SweepCfg {
 // Byte offset of the 16-byte piece `piece` of row `row` in an LDS array of
 // ROWB-byte rows.  The piece index is xor-ed with twice the number of the
 // row's 256-byte line, so that neither kind of operand read has bank conflicts
-// (SQ_LDS_BANK_CONFLICT 0): a transposing 8-byte read takes 32 bytes of 8 rows
+// (SQ_LDS_BANK_CONFLICT 0 in own_state_kernel; the sweeps' conflicts, 10 to 15% of
+// their LDS cycles at d128, are those of other accesses): a transposing 8-byte read takes 32 bytes of 8 rows
 // at a time, a 16-byte read of 16 rows takes rows 0-3 and 12-15 of one piece
 // with rows 4-11 of the next.  (Telling rows r and r + 8 apart as well costs
 // the 16-byte reads a two-way conflict.)
@@ -1108,6 +1113,9 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 // each workgroup leaves its sum for a second kernel, but for a single batch
 // entry.  (One workgroup per head over the batch entries in turn saves that
 // launch of some 2 us, and loses from two entries on.)
+// Bound by the latency of its loads, scans and barriers: 8.4 us for the one slice
+// of B4 H16 T4096, 6.5 for the four of B2 H12 T777, 50 for B1 H16 T32768, whose 16
+// workgroups take 4096 rows a round.
 constexpr int kDgThreads = 1024;
 
 // x of another lane by a DPP move (0 where there is none), halves of a double
@@ -1505,9 +1513,10 @@ static Split plan_split(long long heads, int T, int dk, int dv, int dtype, bool 
         const double own = rounds(dirs * heads * (p.nsub - 1), 2 * kCUs) * sub * own_chunk_us(dk, dv, dtype) * 1.6;
         us += 8.0 + own + (double)dirs * heads * p.nsub * dk * dv * 8 / 4e6;
         // Segments have to promise a tenth less: chunks of a launch that leaves
-        // CUs idle take less than the times above (backward of B4 H16 T4096 d128,
-        // bf16: 192 workgroups of whole sequences, 3.6 us a chunk, 235 us in all;
-        // four segments, estimated at 98% of the former's time, 285 us)
+        // CUs idle take less than the times above, which the model does not know.
+        // One call stands behind the tenth: the backward of B4 H16 T4096 d128, bf16
+        // (192 workgroups of whole sequences 235 us in all when this was measured,
+        // four segments, estimated at 98% of that, 285 us)
         us *= 1.1;
       }
       if (best.ds == 0 || us < least) {

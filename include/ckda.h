@@ -455,7 +455,7 @@ size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int 
  *   dq, dk : [B, Hk, T, dk] dtype (of shared heads: summed over the heads that
  *            use them, in fp32);  dv : [B, H, T, dv] dtype
  *   dg     : dtype, the shape of g: with respect to the log decays (of a
- *            constant decay: summed over batch and time)
+ *            constant decay: summed over batch and time in fp64, rounded once)
  *   dh0    : [B, H, dk, dv] fp32, or NULL to skip
  * With R_t = dL/dH_t (R_t = a_{t+1} R_{t+1} + q_t do_t^T, R_T = dhT + q_T
  * do_T^T): dq_t = H_t do_t, dk_t = R_t v_t, dv_t = R_t^T k_t, dh0 = a_1 R_1 and
