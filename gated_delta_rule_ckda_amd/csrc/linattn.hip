@@ -1101,18 +1101,19 @@ hipError_t launch_own_e(const SweepLaunch& L, int d1, hipStream_t stream) {
 // of |a| and |b| of one of the two chunks, the dots of bf16 inputs coming from
 // states and pairs of 16 bits.  A decay factor below 2^-126 counts as 0: dg_t is
 // 0 there, and no sum crosses it.
-// What is left: dg_t is off by some 2^-18 (2^-22) of the pairs in its own chunk
-// that pass any gate, and of what passes the chunk's ends.  A single gate much
+// What is left: dg_t is off by some 2^-18 (2^-22) of the pairs that pass any gate
+// of its own chunk or the next.  A single gate much
 // stronger than those around it, with a gradient that much smaller than theirs,
 // keeps fewer digits of its own.
 //
 // One workgroup per (batch, head); a wave has CPW of the 16 CPW chunks of a
 // round, from the sequence's end, a lane a row: the sums inside a chunk are
 // fp32 prefix sums of the wave; one wave runs X over the round's chunks, in
-// fp64, as are the sums of dhT and of a constant decay.  Of a constant decay, whose gradient is the sum over rows and batch,
-// each workgroup leaves its sum for a second kernel, but for a single batch
-// entry.  (One workgroup per head over the batch entries in turn saves that
-// launch of some 2 us, and loses from two entries on.)
+// fp64, as are the sums of dhT and of a constant decay.  Of the latter, whose
+// gradient is the sum over rows and batch, each workgroup leaves its sum for a
+// second kernel, but for a single batch entry.  (One workgroup per head over the
+// batch entries in turn saves that launch of some 2 us, and loses from two
+// entries on.)
 // Bound by the latency of its loads, scans and barriers: 8.4 us for the one slice
 // of B4 H16 T4096, 6.5 for the four of B2 H12 T777, 50 for B1 H16 T32768, whose 16
 // workgroups take 4096 rows a round.

@@ -461,10 +461,9 @@ size_t ckda_linattn_bwd_workspace_size(int B, int H, int Hk, int T, int dk, int 
  * do_T^T): dq_t = H_t do_t, dk_t = R_t v_t, dv_t = R_t^T k_t, dh0 = a_1 R_1 and
  * dg_t = a_t <R_t, H_{t-1}>.  Nothing of the forward is needed but its inputs.
  * Accuracy of dg (beside its rounding to dtype): some 2^-18 (F32: 2^-22) of the
- * gradients of its 64-row chunk and of what passes that chunk's ends, whatever
- * the decays' strength, as long as they are alike; a gate much stronger than
- * those around it, with a gradient that much smaller, keeps fewer digits of its
- * own.  A decay factor below 2^-126 (g < -87.4) counts as 0 in it: dg is 0 there
+ * gradients of its 64-row chunk and the next, whatever the decays' strength, as
+ * long as they are alike; a gate much stronger than those around it, with a
+ * gradient that much smaller, keeps fewer digits of its own.  A decay factor below 2^-126 (g < -87.4) counts as 0 in it: dg is 0 there
  * and nothing crosses it.
  * Outputs must not overlap each other, any input or the workspace, nor the
  * workspace an input. */
