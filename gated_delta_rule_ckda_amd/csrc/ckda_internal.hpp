@@ -107,7 +107,8 @@ struct SweepRole {
   const float* init;         // first state (or NULL: zero)
   float* fin;                // last state (or NULL)
   float* seg_states;         // start state of every sub-segment (with more than one segment)
-  float *seg_out, *seg_decay;   // own-state launches: the sub-segments' own states and decays
+  float* seg_out;            // own-state launches: the sub-segments' own states and decays (two floats each)
+  float2* seg_decay;
   int x_shared, y_shared, z_shared, w_shared;
   int d1, d2;
   int reverse;               // from the last row to the first

@@ -65,6 +65,7 @@ constexpr int RT = C / 16;     // row tiles
 // decay factors of a chunk's rows: c (whole part), c (rest), exp(c_t), G(C, t),
 // G(e, t) with e the last row of t's tile
 constexpr int kDecSets = 5;
+constexpr int kDecFloats = kDecSets * C + 4;   // and, behind them, the chunk's decay less 1 (or 0: decay_step)
 
 template <typename T, int D1, int DS, bool EXACT>
 struct SweepCfg {
@@ -85,7 +86,7 @@ struct SweepCfg {
   static constexpr int ZSETS = BF ? (EXACT ? 3 : 2) : 1;   // terms of the scaled Z
   // LDS: Y, Z, the terms of G(C, .) Z, the terms of H^T, two sets of decay factors
   static constexpr int Z_OFF = Y_BYTES, ZS_OFF = Z_OFF + Z_BYTES, H_OFF = ZS_OFF + ZSETS * Z_BYTES;
-  static constexpr int DEC_OFF = H_OFF + HSETS * H_BYTES, DEC_BYTES = kDecSets * C * 4;
+  static constexpr int DEC_OFF = H_OFF + HSETS * H_BYTES, DEC_BYTES = kDecFloats * 4;
   static constexpr int LDS_BYTES = DEC_OFF + 2 * DEC_BYTES;
   // Pieces of 16 bytes to copy, in units of one piece for each of 256 threads:
   // by the state waves, but for the first YO units of Y and ZO of Z of the
@@ -267,6 +268,41 @@ __device__ __forceinline__ void split_terms(const float* v, Frag* f) {
   }
 }
 
+// A slow decay of a chunk (or segment), applied again and again to a long memory,
+// has to keep its distance from 1: as a float near 1 it is off by 2^-24 and more
+// with every chunk, always to the same side where the decay is constant.  It is
+// held as 2^x - 1, a polynomial (the series of e^y - 1 up to y^7, |y| < 0.35, off by
+// 2e-8 of it), and applied by one multiply-add; 0 where 2^x itself will do.
+// (Decays of exactly 1 are 0 too.)
+__device__ __forceinline__ float decay_less_one(float x) {
+  const float y = x * 0.6931471805599453f;
+  float p = 1.f / 5040.f;
+  p = __builtin_fmaf(p, y, 1.f / 720.f);
+  p = __builtin_fmaf(p, y, 1.f / 120.f);
+  p = __builtin_fmaf(p, y, 1.f / 24.f);
+  p = __builtin_fmaf(p, y, 1.f / 6.f);
+  p = __builtin_fmaf(p, y, 0.5f);
+  p = __builtin_fmaf(p, y, 1.f);
+  return fabsf(x) < 0.5f ? p * y : 0.f;
+}
+// the decayed state: `end` and `less` of a chunk, the same for all lanes
+template <int TR, int TC>
+__device__ __forceinline__ void decay_step(f32x4 (&h)[TR][TC], float end, float less) {
+  if (__builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, less)) != 0) {
+#pragma unroll
+    for (int i = 0; i < TR; ++i)
+#pragma unroll
+      for (int j = 0; j < TC; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[i][j][e] = __builtin_fmaf(h[i][j][e], less, h[i][j][e]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < TR; ++i)
+#pragma unroll
+      for (int j = 0; j < TC; ++j) h[i][j] *= end;
+  }
+}
+
 // Decay factors of a chunk from the log decays g (one row a lane) into dec;
 // drop: the chunk's rows are to have no part in the state after it.
 __device__ __forceinline__ void decay_factors(float g, float* dec, int lane, bool drop = false) {
@@ -281,6 +317,7 @@ __device__ __forceinline__ void decay_factors(float g, float* dec, int lane, boo
   dec[2 * C + lane] = __builtin_amdgcn_exp2f(ch + cl);
   dec[3 * C + lane] = drop ? 0.f : __builtin_amdgcn_exp2f((th - ch) + (tl - cl));
   dec[4 * C + lane] = __builtin_amdgcn_exp2f((row_last(ch) - ch) + (row_last(cl) - cl));
+  if (lane == 0) dec[kDecSets * C] = decay_less_one(th + tl);
 }
 
 // The rows a workgroup works on: chunk row j of a segment is row row0 + j of
@@ -758,12 +795,9 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
     auto chunk = [&](int c, Units& next) __attribute__((always_inline)) {
       // ---- phase 1.  A operand: the columns of Y this wave's row tiles are;
       // B operand: the terms of G(C, s) z_s for its column tile
-      const float end = dec_of(c)[2 * C + C - 1];
+      const float end = dec_of(c)[2 * C + C - 1], less = dec_of(c)[kDecSets * C];
       if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane, A.drop_end && R.at_end(c + 1));
-#pragma unroll
-      for (int i = 0; i < TR; ++i)
-#pragma unroll
-        for (int j = 0; j < TC; ++j) h[i][j] *= end;
+      decay_step<TR, TC>(h, end, less);
       constexpr int KA = BF ? KBC : 1;   // K blocks read ahead of the products (fp32: one, for the registers)
       Frag zf[KA][TC][S::ZSETS], yf[KA][TR];
       auto read = [&](int kb) __attribute__((always_inline)) {
@@ -841,7 +875,7 @@ struct OwnCfg {
   static constexpr int RH = D1 / 16, RD = D2 / 16;
   static constexpr int TR = (RH + 1) / 2, TC = (RD + 3) / 4;   // tiles of one wave
   static constexpr int Y_BYTES = C * YROW, Z_BYTES = C * ZROW;
-  static constexpr int DEC_OFF = Y_BYTES + ZSETS * Z_BYTES, DEC_BYTES = kDecSets * C * 4;
+  static constexpr int DEC_OFF = Y_BYTES + ZSETS * Z_BYTES, DEC_BYTES = kDecFloats * 4;
   static constexpr int LDS_BYTES = DEC_OFF + 2 * DEC_BYTES;
   static constexpr int YPR = D1 * E / 16, ZPR = D2 * E / 16;
   static constexpr int NY = (C * YPR + 511) / 512, NZ = (C * ZPR + 511) / 512;
@@ -923,15 +957,13 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
   place(0);
   load(min(1, R.last));
   lds_barrier();
-  float decay = 1.f;   // product of the chunks' decays
+  float log_h = 0.f, log_l = 0.f;   // the segment's log2 decay, whole part and rest
   for (int c = 0; c < R.nch; ++c) {
     if (wave == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane, A.drop_end && R.at_end(c + 1));
-    const float end = dec_of(c)[2 * C + C - 1];
-    decay *= end;
-#pragma unroll
-    for (int i = 0; i < S::TR; ++i)
-#pragma unroll
-      for (int j = 0; j < S::TC; ++j) h[i][j] *= end;
+    const float end = dec_of(c)[2 * C + C - 1], less = dec_of(c)[kDecSets * C];
+    log_h += dec_of(c)[C - 1];
+    log_l += dec_of(c)[2 * C - 1];
+    decay_step<S::TR, S::TC>(h, end, less);
 #pragma unroll
     for (int kb = 0; kb < S::KBC; ++kb) {
       Frag yf[S::TR];
@@ -960,7 +992,10 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) out[(16 * (rt0 + i) + 4 * g + e) * D2 + 16 * (ct0 + j) + r] = h[i][j][e];
       }
-  if (tid == 0) A.seg_decay[(size_t)seg * L.units * L.group + bh] = decay;
+  if (tid == 0) {
+    const float x = log_h + log_l;
+    A.seg_decay[(size_t)seg * L.units * L.group + bh] = float2{__builtin_amdgcn_exp2f(x), decay_less_one(x)};
+  }
 }
 
 // Segment states, in place: segment i holds its own state (from zero) on entry
@@ -971,20 +1006,22 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
 // sub-segments, d128.
 struct ScanArgs {
   float* states;
-  const float *decay, *init;
+  const float2* decay;   // of every segment, and less 1 (as decay_step takes them)
+  const float* init;
 };
 __global__ __launch_bounds__(256) void segment_scan_kernel(ScanArgs one, ScanArgs two, int nseg, int heads,
                                                            long long elems, long long seg_stride) {
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= heads * elems) return;
   float* states = blockIdx.y ? two.states : one.states;
-  const float *decay = blockIdx.y ? two.decay : one.decay, *init = blockIdx.y ? two.init : one.init;
+  const float2* decay = blockIdx.y ? two.decay : one.decay;
+  const float* init = blockIdx.y ? two.init : one.init;
   const int bh = (int)(i / elems);
   f32x4 h = init ? *reinterpret_cast<const f32x4*>(init + i) : zero4();
   constexpr int AHEAD = 8;   // segments whose loads are in flight together
   for (int s0 = 0; s0 < nseg; s0 += AHEAD) {
     f32x4 mine[AHEAD];
-    float d[AHEAD];
+    float2 d[AHEAD];
 #pragma unroll
     for (int j = 0; j < AHEAD; ++j) {
       const int s = min(s0 + j, nseg - 2);   // (the last segment's own state is not formed)
@@ -995,7 +1032,9 @@ __global__ __launch_bounds__(256) void segment_scan_kernel(ScanArgs one, ScanArg
     for (int j = 0; j < AHEAD; ++j) {
       if (s0 + j >= nseg) break;
       *reinterpret_cast<f32x4*>(states + (s0 + j) * seg_stride + i) = h;
-      h = d[j] * h + mine[j];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        h[e] = (d[j].y != 0.f ? __builtin_fmaf(h[e], d[j].y, h[e]) : d[j].x * h[e]) + mine[j][e];
     }
   }
 }
@@ -1542,7 +1581,7 @@ static FwdPlan fwd_plan(int B, int H, int T, int dk, int dv, int dtype) {
   p.sp = plan_split((long long)bh, T, dk, dv, dtype, false);
   p.states = 0;
   p.decay = p.sp.nseg > 1 ? up256((size_t)p.sp.nsub * bh * dk * dv * 4) : 0;
-  p.bytes = p.sp.nseg > 1 ? p.decay + up256((size_t)p.sp.nsub * bh * 4) : 0;
+  p.bytes = p.sp.nseg > 1 ? p.decay + up256((size_t)p.sp.nsub * bh * 8) : 0;
   return p;
 }
 size_t linattn_fwd_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
@@ -1572,8 +1611,8 @@ static void set_split(SweepLaunch& L, const LinAttnArgs& a, const Split& sp) {
 // rstates, backward in time, both in the same launches (the whole backward, two
 // pairs of launches -> one: fp32 B1 H8 T1023 d64 38.6 -> 31.1 us, bf16 B1 H8
 // T4096 d128 98 -> 72, B1 H4 T8192 d64 63 -> 46)
-static hipError_t segment_starts(const LinAttnArgs& a, const Split& sp, float* states, float* decay, float* rstates,
-                                 float* rdecay) {
+static hipError_t segment_starts(const LinAttnArgs& a, const Split& sp, float* states, float2* decay, float* rstates,
+                                 float2* rdecay) {
   SweepLaunch L = sweep_base(a);
   set_split(L, a, sp);
   L.seg_rows = sp.sub_rows;
@@ -1607,7 +1646,7 @@ hipError_t launch_linattn_fwd(const LinAttnArgs& a) {
   unsigned char* ws = (unsigned char*)a.workspace;
   float* states = (float*)(ws + p.states);
   if (p.sp.nseg > 1) {
-    hipError_t e = segment_starts(a, p.sp, states, (float*)(ws + p.decay), nullptr, nullptr);
+    hipError_t e = segment_starts(a, p.sp, states, (float2*)(ws + p.decay), nullptr, nullptr);
     if (e != hipSuccess) return e;
   }
   SweepLaunch L = sweep_base(a);
@@ -1656,7 +1695,7 @@ static BwdPlan bwd_plan(int B, int H, int Hk, int T, int dk, int dv, int dtype) 
   p.head_sum = take(bh * 8);
   p.states = take(nsub * bh * elems * 4);
   p.rstates = take(nsub * bh * elems * 4);
-  p.decay = take(2 * nsub * bh * 4);   // of both directions
+  p.decay = take(2 * nsub * bh * 8);   // of both directions
   const bool grouped = H != Hk;
   p.dq = take(grouped ? bh * T * dk * 4 : 0);
   p.dk = take(grouped ? bh * T * dk * 4 : 0);
@@ -1717,7 +1756,7 @@ hipError_t launch_linattn_bwd(const LinAttnArgs& a) {
   float *states = (float*)(ws + p.states), *rstates = (float*)(ws + p.rstates);
   hipError_t e;
   if (p.sp.nseg > 1) {
-    float *decay = (float*)(ws + p.decay), *rdecay = decay + (size_t)p.sp.nsub * a.B * a.H;
+    float2 *decay = (float2*)(ws + p.decay), *rdecay = decay + (size_t)p.sp.nsub * a.B * a.H;
     if ((e = segment_starts(a, p.sp, states, decay, rstates, rdecay)) != hipSuccess) return e;
   }
   const bool grouped = a.H != a.Hk;
