@@ -92,11 +92,13 @@ struct SweepCfg {
   // by the state waves, but for the first YO units of Y and ZO of Z of the
   // widest slices, which the output waves copy (a unit of Z costs some ten
   // times one of Y, for its scaled terms).  Units are loaded NR chunks before
-  // they are copied; a chunk of a narrow slice takes less time than a load.
+  // they are copied; a chunk of a narrow slice takes less time than a load, and
+  // the widest have no registers for two (fp32 128 x 64, B8 H32 T512: forward 143
+  // us, 194 with two and 85 registers spilled; backward 432 and 567).
   static constexpr int YPR = D1 * E / 16, ZPR = ZROW / 16;
   static constexpr int NY = (C * YPR + 255) / 256, NZ = (C * ZPR + 255) / 256;
   static constexpr int YO = DS == 128 ? NY / 2 : 0, ZO = DS == 128 ? NZ / 4 : 0;
-  static constexpr int NR = DS == 128 ? 1 : 2;
+  static constexpr int NR = DS == 128 || D1 * DS * E >= 32768 ? 1 : 2;
 };
 
 // Byte offset of the 16-byte piece `piece` of row `row` in an LDS array of
@@ -798,6 +800,16 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       const float end = dec_of(c)[2 * C + C - 1], less = dec_of(c)[kDecSets * C];
       if (sw == 0) decay_factors(decay_of<T>(gv), dec_of(c + 1), lane, A.drop_end && R.at_end(c + 1));
       decay_step<TR, TC>(h, end, less);
+      // fp32: the chunk's products are summed apart and added to the state once;
+      // on top of it each of the 16 would round at the state's size (bf16: two,
+      // for which there are no registers in the widest slices)
+      f32x4 sum[BF ? 1 : TR][BF ? 1 : TC];
+      if constexpr (!BF) {
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+#pragma unroll
+          for (int j = 0; j < TC; ++j) sum[i][j] = zero4();
+      }
       constexpr int KA = BF ? KBC : 1;   // K blocks read ahead of the products (fp32: one, for the registers)
       Frag zf[KA][TC][S::ZSETS], yf[KA][TR];
       auto read = [&](int kb) __attribute__((always_inline)) {
@@ -814,7 +826,10 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
 #pragma unroll
           for (int j = 0; j < TC; ++j)
 #pragma unroll
-            for (int i = 0; i < TR; ++i) h[i][j] = mma<T>(h[i][j], yf[kb % KA][i], zf[kb % KA][j][n]);
+            for (int i = 0; i < TR; ++i) {
+              f32x4& to = BF ? h[i][j] : sum[BF ? 0 : i][BF ? 0 : j];
+              to = mma<T>(to, yf[kb % KA][i], zf[kb % KA][j][n]);
+            }
       };
 #pragma unroll
       for (int kb = 0; kb < KA; ++kb) read(kb);
@@ -825,6 +840,12 @@ __global__ __launch_bounds__(512, 2) void sweep_kernel(SweepLaunch L) {
       }
 #pragma unroll
       for (int kb = KBC - KA; kb < KBC; ++kb) multiply(kb);
+      if constexpr (!BF) {
+#pragma unroll
+        for (int i = 0; i < TR; ++i)
+#pragma unroll
+          for (int j = 0; j < TC; ++j) h[i][j] += sum[i][j];
+      }
       lds_barrier();
       // ---- phase 2
       place(next, c + 1, STATE);
@@ -964,6 +985,14 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
     log_h += dec_of(c)[C - 1];
     log_l += dec_of(c)[2 * C - 1];
     decay_step<S::TR, S::TC>(h, end, less);
+    constexpr bool APART = E == 4;   // (as in sweep_kernel)
+    f32x4 sum[APART ? S::TR : 1][APART ? S::TC : 1];
+    if constexpr (APART) {
+#pragma unroll
+      for (int i = 0; i < S::TR; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TC; ++j) sum[i][j] = zero4();
+    }
 #pragma unroll
     for (int kb = 0; kb < S::KBC; ++kb) {
       Frag yf[S::TR];
@@ -975,8 +1004,17 @@ __global__ __launch_bounds__(512, sizeof(T) == 2 ? 4 : 2) void own_state_kernel(
         for (int j = 0; j < S::TC; ++j) {
           const Frag zf = zcol[j].read(lds, kb, n * S::Z_BYTES);
 #pragma unroll
-          for (int i = 0; i < S::TR; ++i) h[i][j] = mma<T>(h[i][j], yf[i], zf);
+          for (int i = 0; i < S::TR; ++i) {
+            f32x4& to = APART ? sum[APART ? i : 0][APART ? j : 0] : h[i][j];
+            to = mma<T>(to, yf[i], zf);
+          }
         }
+    }
+    if constexpr (APART) {
+#pragma unroll
+      for (int i = 0; i < S::TR; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TC; ++j) h[i][j] += sum[i][j];
     }
     lds_barrier();
     place(c + 1);

@@ -71,3 +71,23 @@ def test_backward(heads, T, d, dtype):
     torch.cuda.synchronize()
     err = np.abs(mean_error(dh0, g, T, h0))
     assert (err <= bound(g, T)).all(), (err, bound(g, T))
+
+
+@pytest.mark.parametrize("heads,T,d", [(64, 2048, 64), (256, 1024, 128), (8, 4096, 64)])
+def test_fp32_state_is_rounded_once_a_chunk(heads, T, d):
+    """Without a decay, small writes to large states: an addition a chunk (and
+    segment), each off by 2^-24 / sqrt(3) of the state in the rms at most; a
+    fifth more is allowed for what is added.  (One for each matrix
+    instruction, 16 a chunk, would be four times that.)"""
+    r = np.random.default_rng(8)
+    t = lambda *s, f=1.0: torch.from_numpy((f * r.standard_normal(s)).astype(np.float32))  # noqa: E731
+    k, v, h0 = t(1, heads, T, d, f=d ** -0.5), t(1, heads, T, d), t(1, heads, d, d, f=8.0) + 64.0
+    g = torch.zeros(heads)
+    log(f"linattn_fwd fp32 states heads {heads} T {T} d {d}")
+    _, hT = ck.linattn_fwd(k.cuda(), k.cuda(), v.cuda(), g.cuda(), h0.cuda())
+    torch.cuda.synchronize()
+    few = [0, 1, heads - 1]
+    want = h0[:, few].double() + k[:, few].double().transpose(2, 3) @ v[:, few].double()
+    err = (hT.cpu()[:, few].double() - want) / want
+    rms = float((err ** 2).mean().sqrt())
+    assert rms <= 1.2 * 2.0 ** -24 / math.sqrt(3) * math.sqrt(T / 64), rms
