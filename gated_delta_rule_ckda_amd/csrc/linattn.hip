@@ -1432,14 +1432,20 @@ __global__ __launch_bounds__(kLaDecodeThreads) void linattn_decode_kernel(const 
   f32x4 vv;
 #pragma unroll
   for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[st * dv + col0 + 4 * cg + e]);
-  const float a = expf(to_f32(gate[head_decay ? st % heads : st]));
+  // a slow decay by its distance from 1, as in decay_less_one: rounded to fp32 it
+  // would move a long memory to one side, token by token
+  const float x = to_f32(gate[head_decay ? st % heads : st]);
+  const float a = expf(x), less = fabsf(x) < 0.35f ? expm1f(x) : 0.f;
   __syncthreads();
   f32x4 acc = zero4();
 #pragma unroll
   for (int j = 0; j < ITER; ++j) {
     const int row = rg + j * RPI;
     if (row < DK) {
-      const f32x4 hn = a * h[j] + s_k[row] * vv;
+      f32x4 hn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        hn[e] = (less != 0.f ? __builtin_fmaf(h[j][e], less, h[j][e]) : a * h[j][e]) + s_k[row] * vv[e];
       acc += s_q[row] * hn;
       // streaming store: the state is not read again in this step
       __builtin_nontemporal_store(hn, reinterpret_cast<f32x4*>(Hs + row * dv));

@@ -73,6 +73,21 @@ def test_backward(heads, T, d, dtype):
     assert (err <= bound(g, T)).all(), (err, bound(g, T))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_decode(dtype):
+    """4096 single tokens: one rounding each, to either side."""
+    steps, d = 4096, 64
+    g, h0 = case(len(RATES), steps, d, dtype)
+    log(f"linattn_decode_step slow decays steps {steps} d {d} {dtype}")
+    z = torch.zeros(1, len(RATES), d, dtype=dtype, device="cuda")
+    S, gd, o = h0.cuda(), g.cuda(), torch.empty_like(z)
+    for _ in range(steps):
+        ck.linattn_decode_step(z, z, z, gd, S, o=o)
+    torch.cuda.synchronize()
+    err = np.abs(mean_error(S, g, steps, h0))
+    assert (err <= bound(g, steps)).all(), (err, bound(g, steps))
+
+
 @pytest.mark.parametrize("heads,T,d", [(64, 2048, 64), (256, 1024, 128), (8, 4096, 64)])
 def test_fp32_state_is_rounded_once_a_chunk(heads, T, d):
     """Without a decay, small writes to large states: an addition a chunk (and
