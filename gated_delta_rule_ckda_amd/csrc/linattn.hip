@@ -40,11 +40,11 @@
 // vector-memory return path, 84% busy (TD_TD_BUSY) at some 11 bytes a cycle, as
 // every slice reads the chunk's x and y again (B4 H16 T4096, 256 workgroups: 104
 // us, 260 MB of HBM traffic); with whole states of 128 columns no unit by itself
-// (the backward's three sweeps of that size, 192 workgroups: 250 us, 790 MB;
+// (the backward's three sweeps of that size, 192 workgroups: 245 us, 810 MB;
 // return path 57%, matrix cores 21%, LDS 27% busy): one workgroup to a CU waits at
 // two barriers a chunk; in short calls the latency of the first loads and of a
 // chunk's two phases (77 rows: 6.8 us).  fp32: that latency too (B3 H8 T1000 dk64
-// dv128: 38 us, matrix cores 19%, return path 25% busy).
+// dv128: 38 us, matrix cores 18%, return path 24% busy).
 // Log decays are summed as two parts, whole multiples of 1/64 (whose sums are
 // exact) and the rest, so that differences of large sums keep fp32 accuracy.
 // (g log2 e itself is rounded once for each row, by 2^-24 of it: at most 4e-8 of
