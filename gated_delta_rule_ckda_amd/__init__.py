@@ -11,6 +11,10 @@ fails to load, every call raises.
     o, hT = linattn_fwd(q, k, v, g, h0=None)          # linear attention, a decay for each head
     y = head_norm_fwd(o, w, b, gate=z)                # norm and output gate, token-major
 
+    y, total = add_norm_fwd(x, residual, w)           # rms norm ahead of the projections (add_norm_quant_fwd: 8 bits)
+    q, sT = short_conv_fwd(x, w, heads=H)             # short causal convolution, head-major
+    y, hT = selective_scan_fwd(x, dt, A, Bm, Cm)      # diagonal recurrence, a decay for each channel and state
+
 With fuse=FUSE_GATES | FUSE_NORM_K (| FUSE_NORM_Q) the kernels first apply the
 per-token prologue: alpha and beta are logits, keys (queries) are normalised.
 """
@@ -32,6 +36,7 @@ FUSE_GATES, FUSE_NORM_K, FUSE_NORM_Q = 1, 2, 4       # CKDA_FUSE_*
 GATE_SCALAR = 8                                      # CKDA_GATE_SCALAR
 DECAY_HEAD = 16                                      # CKDA_DECAY_HEAD
 NORM_RMS, NORM_GATE_SILU, NORM_GATE_SIGMOID = 1, 2, 4   # CKDA_NORM_*
+CONV_SILU, SCAN_SOFTPLUS, PAD_ZERO = 1, 1, 32        # CKDA_CONV_SILU, CKDA_SCAN_SOFTPLUS, CKDA_PAD_ZERO
 EXPORTS = ("ckda_chunk_fwd_workspace_size", "ckda_chunk_fwd", "ckda_chunk_fwd_noalloc", "ckda_chunk_fwd_timed",
            "ckda_chunk_fwd_ex",
            "ckda_chunk_fwd_gather", "ckda_decode_step", "ckda_decode_step_ex", "ckda_decode_step_gather",
@@ -40,6 +45,10 @@ EXPORTS = ("ckda_chunk_fwd_workspace_size", "ckda_chunk_fwd", "ckda_chunk_fwd_no
            "ckda_deltaproduct2_bwd", "ckda_deltaproduct2_bwd_workspace_size",
            "ckda_linattn_fwd", "ckda_linattn_fwd_workspace_size", "ckda_linattn_bwd", "ckda_linattn_bwd_workspace_size",
            "ckda_linattn_decode_step", "ckda_head_norm_fwd", "ckda_head_norm_bwd", "ckda_head_norm_bwd_workspace_size",
+           "ckda_short_conv_fwd", "ckda_short_conv_bwd", "ckda_short_conv_bwd_workspace_size", "ckda_short_conv_decode_step",
+           "ckda_selective_scan_fwd", "ckda_selective_scan_fwd_workspace_size", "ckda_selective_scan_bwd",
+           "ckda_selective_scan_bwd_workspace_size", "ckda_selective_scan_decode_step",
+           "ckda_add_norm_fwd", "ckda_add_norm_bwd", "ckda_add_norm_bwd_workspace_size",
            "ckda_status_string", "ckda_last_error", "ckda_abi_version")
 
 _lib = None
@@ -111,6 +120,30 @@ def lib() -> ctypes.CDLL:
         L.ckda_head_norm_bwd_workspace_size.restype = sz
         L.ckda_head_norm_bwd.argtypes = [vp] * 9 + [i] * 7 + [f, vp, sz, vp]
         L.ckda_head_norm_bwd.restype = i
+        L.ckda_short_conv_fwd.argtypes = [vp] * 7 + [i] * 8 + [vp]
+        L.ckda_short_conv_fwd.restype = i
+        L.ckda_short_conv_bwd_workspace_size.argtypes = [i] * 5
+        L.ckda_short_conv_bwd_workspace_size.restype = sz
+        L.ckda_short_conv_bwd.argtypes = [vp] * 11 + [i] * 8 + [vp, sz, vp]
+        L.ckda_short_conv_bwd.restype = i
+        L.ckda_short_conv_decode_step.argtypes = [vp] * 5 + [i] * 6 + [vp]
+        L.ckda_short_conv_decode_step.restype = i
+        L.ckda_selective_scan_fwd_workspace_size.argtypes = [i] * 6
+        L.ckda_selective_scan_fwd_workspace_size.restype = sz
+        L.ckda_selective_scan_fwd.argtypes = [vp] * 12 + [i] * 9 + [vp, sz, vp]
+        L.ckda_selective_scan_fwd.restype = i
+        L.ckda_selective_scan_bwd_workspace_size.argtypes = [i] * 6
+        L.ckda_selective_scan_bwd_workspace_size.restype = sz
+        L.ckda_selective_scan_bwd.argtypes = [vp] * 21 + [i] * 9 + [vp, sz, vp]
+        L.ckda_selective_scan_bwd.restype = i
+        L.ckda_selective_scan_decode_step.argtypes = [vp] * 10 + [i] * 8 + [vp]
+        L.ckda_selective_scan_decode_step.restype = i
+        L.ckda_add_norm_fwd.argtypes = [vp] * 7 + [i] * 5 + [f, vp]
+        L.ckda_add_norm_fwd.restype = i
+        L.ckda_add_norm_bwd_workspace_size.argtypes = [i] * 4
+        L.ckda_add_norm_bwd_workspace_size.restype = sz
+        L.ckda_add_norm_bwd.argtypes = [vp] * 7 + [i] * 4 + [f, vp, sz, vp]
+        L.ckda_add_norm_bwd.restype = i
         L.ckda_status_string.argtypes = [i]
         L.ckda_status_string.restype = ctypes.c_char_p
         L.ckda_last_error.argtypes = []
@@ -687,3 +720,292 @@ def head_norm_bwd(x, dy, w=None, b=None, gate=None, act="silu", rms=False, eps=1
     _run(dev, stream, L.ckda_head_norm_bwd, x.data_ptr(), _ptr(gate), _ptr(w), _ptr(b), dy.data_ptr(), dx.data_ptr(),
          _ptr(dz), dw.data_ptr(), db.data_ptr(), B, H, T, D, wheads, code, flags, eps, *ws)
     return dx, dz, dw, db
+
+
+# ---------------------------------------------------------------- around the recurrence in a layer
+
+def _slice_of(device, name, t, shape, dtype, rows, width):
+    """Row stride of t, a column slice of a contiguous tensor: of `shape`, whose
+    first `rows` dimensions count rows and whose others are `width` elements next
+    to each other."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.is_contiguous():
+        return width
+    inner = 1
+    for size, stride in zip(reversed(t.shape[rows:]), reversed(t.stride()[rows:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"the columns of {name} must be contiguous")
+        inner *= size
+    ld = None
+    count = 1   # rows below the dimension
+    for size, stride in zip(reversed(t.shape[:rows]), reversed(t.stride()[:rows])):
+        if size != 1:
+            if ld is None and stride % count == 0:
+                ld = stride // count
+            if ld is None or stride != ld * count:
+                raise ValueError(f"{name} must be a column slice of a contiguous tensor")
+        count *= size
+    ld = width if ld is None else ld
+    if ld < width or ld > 2 ** 31 - 1:
+        raise ValueError(f"{name} must be a column slice of a contiguous tensor")
+    return ld
+
+
+def _conv_args(x, w, b, heads, act, lead):
+    """(lead sizes, C, K, flags, Dh) of short_conv_fwd's arguments."""
+    sx = _dims(x, lead + 1, "x")
+    C, K = sx[-1], _dims(w, 2, "w")[1]
+    if act not in (None, "silu"):
+        raise ValueError(f"act must be None or 'silu', got {act!r}")
+    if heads < 1 or C % heads:
+        raise ValueError(f"{heads} heads do not divide the {C} channels of x")
+    return sx[:lead], C, K, CONV_SILU if act else 0, C // heads
+
+
+def short_conv_fwd(x, w, b=None, s0=None, lens=None, heads=1, act="silu", y=None, sT=None, want_state=True, stream=None):
+    """Short causal convolution (ckda_short_conv_fwd): y_t = act(b + sum_j w_j
+    x_{t-K+1+j}) for each channel, K = 2, 3 or 4.
+
+    x [B,T,C], which may be a column slice of a wider projection; w [C,K] and b
+    [C] fp32, b or None; s0 [B,K-1,C] the inputs before the first row, or None;
+    lens [B] int32 GPU tensor of sequence lengths or None; act "silu" or None.
+    Returns (y [B,heads,T,C/heads], the last inputs sT [B,K-1,C] or None).  Rows
+    of y at or past a sequence's length are zero, or left as they were where y is
+    passed in."""
+    (B, T), C, K, flags, Dh = _conv_args(x, w, b, heads, act, 2)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("w", w, (C, K), f32), ("b", b, (C,), f32), ("s0", s0, (B, K - 1, C), dt), ("lens", lens, (B,), torch.int32),
+                   ("y", y, (B, heads, T, Dh), dt), ("sT", sT, (B, K - 1, C), dt)])
+    ldx = _slice_of(dev, "x", x, (B, T, C), dt, 2, C)
+    code = _dtype_code(x)
+    if y is None:
+        y = _fresh((B, heads, T, Dh), dt, dev, stream)
+        flags |= PAD_ZERO
+    if sT is None and want_state:
+        sT = _fresh((B, K - 1, C), dt, dev, stream)
+    _run(dev, stream, lib().ckda_short_conv_fwd, x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(s0), _ptr(lens), y.data_ptr(),
+         _ptr(sT), B, T, C, heads, K, ldx, code, flags)
+    return y, sT
+
+
+def short_conv_bwd(x, w, dy, b=None, s0=None, dsT=None, lens=None, act="silu", workspace=None, stream=None):
+    """Backward of short_conv_fwd (ckda_short_conv_bwd): given dy
+    [B,heads,T,C/heads] and dsT [B,K-1,C] or None, returns (dx [B,T,C], dw [C,K],
+    db [C], ds0 [B,K-1,C]): dx and ds0 in x's dtype, dw and db fp32.  Rows at or
+    past a sequence's length have zero gradients."""
+    heads = _dims(dy, 4, "dy")[1]
+    (B, T), C, K, flags, Dh = _conv_args(x, w, b, heads, act, 2)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("w", w, (C, K), f32), ("b", b, (C,), f32), ("s0", s0, (B, K - 1, C), dt), ("lens", lens, (B,), torch.int32),
+                   ("dy", dy, (B, heads, T, Dh), dt), ("dsT", dsT, (B, K - 1, C), dt)])
+    ldx = _slice_of(dev, "x", x, (B, T, C), dt, 2, C)
+    code = _dtype_code(x)
+    L = lib()
+    need = L.ckda_short_conv_bwd_workspace_size(B, T, C, K, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} K={K}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    dx, ds0 = _fresh((B, T, C), dt, dev, stream), _fresh((B, K - 1, C), dt, dev, stream)
+    dw, db = _fresh((C, K), f32, dev, stream), _fresh((C,), f32, dev, stream)
+    _run(dev, stream, L.ckda_short_conv_bwd, x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(s0), _ptr(lens), dy.data_ptr(),
+         _ptr(dsT), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ds0.data_ptr(), B, T, C, heads, K, ldx, code,
+         flags | PAD_ZERO, *ws)
+    return dx, dw, db, ds0
+
+
+def short_conv_decode_step(x, w, state, b=None, heads=1, act="silu", y=None, stream=None):
+    """One token of short_conv_fwd (ckda_short_conv_decode_step): x [N,C], which
+    may be a column slice; state [N,K-1,C] (the last inputs) updated in place.
+    Returns y [N,heads,C/heads]."""
+    (N,), C, K, flags, Dh = _conv_args(x, w, b, heads, act, 1)
+    dev, dt, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("w", w, (C, K), f32), ("b", b, (C,), f32), ("state", state, (N, K - 1, C), dt), ("y", y, (N, heads, Dh), dt)])
+    ldx = _slice_of(dev, "x", x, (N, C), dt, 1, C)
+    code = _dtype_code(x)
+    if y is None:
+        y = _fresh((N, heads, Dh), dt, dev, stream)
+    _run(dev, stream, lib().ckda_short_conv_decode_step, x.data_ptr(), w.data_ptr(), _ptr(b), state.data_ptr(), y.data_ptr(),
+         N, C, K, ldx, code, flags)
+    return y
+
+
+def selective_scan_workspace_size(B, T, C, G, N, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else _dtype_code(torch.empty(0, dtype=dtype))
+    return int(lib().ckda_selective_scan_fwd_workspace_size(B, T, C, G, N, code))
+
+
+def selective_scan_bwd_workspace_size(B, T, C, G, N, dtype) -> int:
+    code = dtype if isinstance(dtype, int) else _dtype_code(torch.empty(0, dtype=dtype))
+    return int(lib().ckda_selective_scan_bwd_workspace_size(B, T, C, G, N, code))
+
+
+def _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, more, lead):
+    """Checks of the selective scan's tensors; (lead sizes, C, G, N, ldbc, ldz)."""
+    sx, sb = _dims(x, lead + 1, "x"), _dims(Bm, lead + 2, "Bm")
+    rows, C, (G, N) = sx[:lead], sx[-1], sb[lead:]
+    if G < 1 or C % G:
+        raise ValueError(f"{G} groups of Bm do not divide the {C} channels of x")
+    dev, t, f32 = x.device, x.dtype, torch.float32
+    _tensors(dev, [("x", x, (*rows, C), t), ("dt", dt, (*rows, C), t), ("A", A, (C, N), f32), ("D", D, (C,), f32),
+                   ("dt_bias", dt_bias, (C,), f32), *more(rows, C, N)])
+    ldbc = _slice_of(dev, "Bm", Bm, (*rows, G, N), t, lead, G * N)
+    if _slice_of(dev, "Cm", Cm, (*rows, G, N), t, lead, G * N) != ldbc:
+        raise ValueError("Bm and Cm must have the same row stride")
+    ldz = C if z is None else _slice_of(dev, "z", z, (*rows, C), t, lead, C)
+    return rows, C, G, N, ldbc, ldz
+
+
+def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, lens=None, softplus=True, workspace=None,
+                       y=None, hT=None, want_state=True, stream=None):
+    """Selective scan (ckda_selective_scan_fwd): d = softplus(dt + dt_bias), h_t =
+    exp(d A) h_{t-1} + d x_t B_t for each channel and state, y_t = (C_t . h_t + D
+    x_t) silu(z_t).
+
+    x, dt [B,T,C]; A [C,N] fp32; Bm, Cm [B,T,G,N] (G dividing C; N up to 64);
+    D, dt_bias [C] fp32 or None; z [B,T,C] or None (no gate); h0 [B,C,N] fp32 or
+    None; lens [B] int32 GPU tensor of sequence lengths or None; Bm, Cm and z may
+    be column slices of a wider projection (Bm and Cm of the same).  Returns
+    (y [B,T,C], hT [B,C,N] fp32 or None).  Rows of y at or past a sequence's length
+    are zero, or left as they were where y is passed in.  hT may be h0."""
+    f32 = torch.float32
+    (B, T), C, G, N, ldbc, ldz = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lambda r, C, N: [
+        ("h0", h0, (r[0], C, N), f32), ("lens", lens, (r[0],), torch.int32), ("y", y, (*r, C), x.dtype),
+        ("hT", hT, (r[0], C, N), f32)], 2)
+    dev, code, flags = x.device, _dtype_code(x), SCAN_SOFTPLUS if softplus else 0
+    L = lib()
+    need = L.ckda_selective_scan_fwd_workspace_size(B, T, C, G, N, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} G={G} N={N}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    if y is None:
+        y = _fresh((B, T, C), x.dtype, dev, stream)
+        flags |= PAD_ZERO
+    if hT is None and want_state:
+        hT = _fresh((B, C, N), f32, dev, stream)
+    _run(dev, stream, L.ckda_selective_scan_fwd, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
+         _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), y.data_ptr(), _ptr(hT), B, T, C, G, N, ldbc, ldz, code,
+         flags, *ws)
+    return y, hT
+
+
+def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=None, dhT=None, lens=None, softplus=True,
+                       want_dh0=True, workspace=None, stream=None):
+    """Backward of selective_scan_fwd (ckda_selective_scan_bwd): given dy [B,T,C]
+    and dhT [B,C,N] fp32 or None, returns (dx, ddt, dA, dBm, dCm, dD, dz or None,
+    ddt_bias, dh0 or None): dx, ddt, dz [B,T,C] and dBm, dCm [B,T,G,N] in x's dtype,
+    the others fp32 (dD and ddt_bias also where D and dt_bias are None: the
+    gradients at zero).  Rows at or past a sequence's length have zero gradients."""
+    f32 = torch.float32
+    (B, T), C, G, N, ldbc, ldz = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lambda r, C, N: [
+        ("h0", h0, (r[0], C, N), f32), ("lens", lens, (r[0],), torch.int32), ("dy", dy, (*r, C), x.dtype),
+        ("dhT", dhT, (r[0], C, N), f32)], 2)
+    dev, t, code = x.device, x.dtype, _dtype_code(x)
+    L = lib()
+    need = L.ckda_selective_scan_bwd_workspace_size(B, T, C, G, N, code)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} G={G} N={N}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    dx, ddt = (_fresh((B, T, C), t, dev, stream) for _ in range(2))
+    dz = None if z is None else _fresh((B, T, C), t, dev, stream)
+    dBm, dCm = (_fresh((B, T, G, N), t, dev, stream) for _ in range(2))
+    dA, dD, dbias = (_fresh(s, f32, dev, stream) for s in ((C, N), (C,), (C,)))
+    dh0 = _fresh((B, C, N), f32, dev, stream) if want_dh0 else None
+    _run(dev, stream, L.ckda_selective_scan_bwd, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
+         _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), dy.data_ptr(), _ptr(dhT), dx.data_ptr(), ddt.data_ptr(),
+         dA.data_ptr(), dBm.data_ptr(), dCm.data_ptr(), dD.data_ptr(), _ptr(dz), dbias.data_ptr(), _ptr(dh0), B, T, C, G, N,
+         ldbc, ldz, code, (SCAN_SOFTPLUS if softplus else 0) | PAD_ZERO, *ws)
+    return dx, ddt, dA, dBm, dCm, dD, dz, dbias, dh0
+
+
+def selective_scan_decode_step(x, dt, A, Bm, Cm, H, D=None, z=None, dt_bias=None, softplus=True, y=None, stream=None):
+    """One token of selective_scan_fwd (ckda_selective_scan_decode_step): x, dt, z
+    [S,C]; Bm, Cm [S,G,N]; H [S,C,N] fp32 updated in place.  Returns y [S,C]."""
+    (S,), C, G, N, ldbc, ldz = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lambda r, C, N: [
+        ("H", H, (r[0], C, N), torch.float32), ("y", y, (r[0], C), x.dtype)], 1)
+    dev, code = x.device, _dtype_code(x)
+    if y is None:
+        y = _fresh((S, C), x.dtype, dev, stream)
+    _run(dev, stream, lib().ckda_selective_scan_decode_step, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
+         Cm.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), H.data_ptr(), y.data_ptr(), S, C, G, N, ldbc, ldz, code,
+         SCAN_SOFTPLUS if softplus else 0)
+    return y
+
+
+def _add_norm_args(x, res, w, total):
+    """(rows, D, residual's dtype) of x [..., D] with a residual of the same shape."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must have rows of at least one element, got shape {tuple(x.shape)}")
+    D = x.shape[-1]
+    rt = x.dtype if res is None and total is None else (res if res is not None else total).dtype
+    if rt not in (x.dtype, torch.float32):
+        raise TypeError(f"the residual must be {x.dtype} or float32, got {rt}")
+    _tensors(x.device, [("x", x, x.shape, x.dtype), ("res", res, x.shape, rt), ("w", w, (D,), torch.float32),
+                        ("total", total, x.shape, rt)])
+    return x.numel() // D, D, rt
+
+
+def add_norm_fwd(x, res=None, w=None, eps=1e-6, y=None, total=None, stream=None):
+    """Root-mean-square norm with the residual's addition (ckda_add_norm_fwd): r =
+    x + res, y = r / sqrt(mean r^2 + eps) w over the last dimension.
+
+    x [...,D]; res of the same shape, in x's dtype or fp32, or None; w [D] fp32 or
+    None.  Returns (y in x's dtype, r in the residual's dtype; None without res
+    unless `total` is passed in).  total may be res."""
+    R, D, rt = _add_norm_args(x, res, w, total)
+    dev, code = x.device, _dtype_code(x)
+    _tensors(dev, [("y", y, x.shape, x.dtype)])
+    if y is None:
+        y = _fresh(x.shape, x.dtype, dev, stream)
+    if total is None and res is not None:
+        total = _fresh(x.shape, rt, dev, stream)
+    _run(dev, stream, lib().ckda_add_norm_fwd, x.data_ptr(), _ptr(res), _ptr(w), y.data_ptr(), None, None, _ptr(total), R, D,
+         0, code, DTYPE_BF16 if rt == torch.bfloat16 else DTYPE_F32, eps)
+    return y, total
+
+
+def add_norm_quant_fwd(x, res=None, w=None, eps=1e-6, group=128, q=None, scales=None, total=None, stream=None):
+    """add_norm_fwd with its output in 8 bits: returns (q [...,D] float8_e4m3fn,
+    scales [..., groups] fp32, r or None), where q scales stands for y: one scale
+    for each 128 columns of a row (group=128; the last may have fewer) or for the
+    whole row (group=0), max |y| / 448."""
+    if group not in (0, 128):
+        raise ValueError(f"group must be 128 or 0 (a row), got {group}")
+    R, D, rt = _add_norm_args(x, res, w, total)
+    dev, code, e4m3 = x.device, _dtype_code(x), torch.float8_e4m3fn
+    sshape = (*x.shape[:-1], -(-D // group) if group else 1)
+    _tensors(dev, [("q", q, x.shape, e4m3), ("scales", scales, sshape, torch.float32)])
+    if q is None:
+        q = _fresh(x.shape, e4m3, dev, stream)
+    if scales is None:
+        scales = _fresh(sshape, torch.float32, dev, stream)
+    if total is None and res is not None:
+        total = _fresh(x.shape, rt, dev, stream)
+    _run(dev, stream, lib().ckda_add_norm_fwd, x.data_ptr(), _ptr(res), _ptr(w), None, q.data_ptr(), scales.data_ptr(),
+         _ptr(total), R, D, group, code, DTYPE_BF16 if rt == torch.bfloat16 else DTYPE_F32, eps)
+    return q, scales, total
+
+
+def add_norm_bwd(total, dy, w=None, dsum=None, eps=1e-6, workspace=None, stream=None):
+    """Backward of add_norm_fwd (ckda_add_norm_bwd) from its r (`total`), dy (x's
+    dtype) and dsum (the gradient of r from what follows, in r's dtype, or None).
+    Returns (dx in dy's dtype, dres in total's dtype, dw [D] fp32); where the dtypes
+    are the same dx and dres are one tensor."""
+    R, D, rt = _add_norm_args(dy, total, w, dsum)
+    dev, code, L = dy.device, _dtype_code(dy), lib()
+    rcode = DTYPE_BF16 if rt == torch.bfloat16 else DTYPE_F32
+    need = L.ckda_add_norm_bwd_workspace_size(R, D, code, rcode)
+    if need == 0:
+        raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes D={D}")
+    workspace, ws = _workspace_arg(workspace, need, dev, stream)
+    dx, dw = _fresh(dy.shape, dy.dtype, dev, stream), _fresh((D,), torch.float32, dev, stream)
+    dres = dx if rt == dy.dtype else _fresh(dy.shape, rt, dev, stream)
+    _run(dev, stream, L.ckda_add_norm_bwd, total.data_ptr(), _ptr(w), dy.data_ptr(), _ptr(dsum), dx.data_ptr(),
+         None if dres is dx else dres.data_ptr(), dw.data_ptr(), R, D, code, rcode, eps, *ws)
+    return dx, dres, dw

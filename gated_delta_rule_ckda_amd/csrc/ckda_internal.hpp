@@ -148,6 +148,87 @@ size_t head_norm_bwd_workspace_bytes(int B, int H, int T, int D, int wheads, int
 hipError_t launch_head_norm_fwd(const HeadNormArgs& a);
 hipError_t launch_head_norm_bwd(const HeadNormArgs& a);
 
+// ---- sums over parts, in a fixed order (part_sums.hip)
+// out[i] = sum over p of part[p * stride + i], for columns that lie side by side
+// in a part: up to three outputs (NULL: skipped) of cols[] columns each.
+struct PartSums {
+  const float* part;
+  int nparts;
+  size_t stride;
+  float* out[3];
+  size_t cols[3];
+};
+hipError_t launch_part_sums(const PartSums& s, hipStream_t stream);
+
+// ---- short causal convolution (short_conv.hip)
+struct ShortConvArgs {
+  const void* x;
+  const float *w, *b;
+  const void* s0;            // inputs before the first row (or NULL)
+  const int* lens;           // [B] or NULL
+  void *y, *sT;              // forward: outputs, last inputs (or NULL)
+  const void *dy, *dsT;      // backward
+  void* dx;
+  float *dw, *db;
+  void* ds0;
+  void* state;               // decode: state in place
+  int B, T, C, H, K, ldx, dtype, silu, pad_zero;
+  void* workspace;
+  hipStream_t stream;
+};
+size_t short_conv_bwd_workspace_bytes(int B, int T, int C, int K);
+bool short_conv_fits_grid(int B, int T, int C, int H);
+hipError_t launch_short_conv_fwd(const ShortConvArgs& a);
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a);
+hipError_t launch_short_conv_decode(const ShortConvArgs& a);
+
+// ---- selective scan (selective_scan.hip)
+struct SelScanArgs {
+  const void *x, *dt;
+  const float* A;
+  const void *Bm, *Cm;
+  const float* D;
+  const void* z;
+  const float* dt_bias;
+  const float* h0;
+  const int* lens;           // [B] or NULL
+  void* y;
+  float* hT;
+  const void* dy;            // backward
+  const float* dhT;
+  void *dx, *ddt, *dBm, *dCm, *dz;
+  float *dA, *dD, *dbias, *dh0;
+  float* H_inout;            // decode: state in place
+  int B, T, C, G, N, ldbc, ldz, dtype, softplus, pad_zero;
+  void* workspace;
+  hipStream_t stream;
+};
+size_t scan_fwd_workspace_bytes(int B, int T, int C, int G, int N);
+size_t scan_bwd_workspace_bytes(int B, int T, int C, int G, int N);
+bool scan_fits_grid(int B, int T, int C, int G, int N);
+hipError_t launch_scan_fwd(const SelScanArgs& a);
+hipError_t launch_scan_bwd(const SelScanArgs& a);
+hipError_t launch_scan_decode(const SelScanArgs& a);
+
+// ---- norm with the residual's addition (add_norm.hip)
+struct AddNormArgs {
+  const void *x, *res;
+  const float* w;
+  void *y, *q;
+  float* scales;
+  void* sum;                 // forward: stored sum (or NULL); backward: its input
+  const void *dy, *dsum;     // backward
+  void *dx, *dres;
+  float* dw;
+  int R, D, group, dtype, res_dtype;
+  float eps;
+  void* workspace;
+  hipStream_t stream;
+};
+size_t add_norm_bwd_workspace_bytes(int R, int D, int dtype);
+hipError_t launch_add_norm_fwd(const AddNormArgs& a);
+hipError_t launch_add_norm_bwd(const AddNormArgs& a);
+
 // Size of the fixed device scratch of ckda_chunk_fwd_noalloc (noalloc.hip),
 // and its device address on the current device (looked up on first use).
 constexpr size_t kNoallocScratchBytes = (size_t)64 << 20;

@@ -33,38 +33,6 @@ static bool linattn_planned(int B, int H, int T, int dk, int dv, size_t es) {
   return (size_t)B * H * 24 <= (size_t)INT32_MAX && linattn_rows_fit(T, dk, dv, es);
 }
 
-static int check_workspace(const char* fn, const void* workspace, size_t have, size_t need) {
-  if (!workspace) return fail(CKDA_ERR_WORKSPACE, "%s: workspace is NULL", fn);
-  if (have < need) return fail(CKDA_ERR_WORKSPACE, "%s: workspace of %zu bytes, need %zu", fn, have, need);
-  if (((uintptr_t)workspace & 255u) != 0) return fail(CKDA_ERR_WORKSPACE, "%s: workspace not 256-byte aligned", fn);
-  return CKDA_OK;
-}
-
-static int check_aligned(const char* fn, const Range* r, int n) {
-  for (int i = 0; i < n; ++i)
-    if (r[i].lo && misaligned((const void*)r[i].lo))
-      return fail(CKDA_ERR_DIM, "%s: %s is not 16-byte aligned", fn, r[i].name);
-  return CKDA_OK;
-}
-
-// no output overlaps an input or another output, and the workspace (among the
-// inputs, or NULL) no input; `same` may equal `with` exactly
-static int check_alias(const char* fn, const Range* in, int nin, const Range* out, int nout, const Range* ws,
-                       const Range* same = nullptr, const Range* with = nullptr) {
-  for (int j = 0; ws && j < nin; ++j)
-    if (&in[j] != ws && overlap(*ws, in[j])) return fail(CKDA_ERR_ALIAS, "%s: workspace overlaps %s", fn, in[j].name);
-  for (int i = 0; i < nout; ++i) {
-    for (int j = 0; j < nin; ++j) {
-      if (&out[i] == same && &in[j] == with && same->lo == with->lo) continue;
-      if (overlap(out[i], in[j])) return fail(CKDA_ERR_ALIAS, "%s: %s overlaps %s", fn, out[i].name, in[j].name);
-    }
-    for (int j = 0; j < nout; ++j)
-      if (j != i && overlap(out[i], out[j]))
-        return fail(CKDA_ERR_ALIAS, "%s: %s overlaps %s", fn, out[i].name, out[j].name);
-  }
-  return CKDA_OK;
-}
-
 // byte sizes of the linear attention's tensors
 struct LinAttnSizes {
   size_t qk, v, g, states, lens;

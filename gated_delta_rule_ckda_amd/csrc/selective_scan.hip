@@ -1,0 +1,824 @@
+// selective_scan.hip -- the selective scan: a diagonal recurrence whose decay
+// differs for every channel c and state n, forward, backward and decode step.
+//
+//   d_t = softplus(dt_t + bias),  a_t[n] = exp(d_t A[n])
+//   h_t[n] = a_t[n] h_{t-1}[n] + d_t x_t B_t[n],   s_t = sum_n C_t[n] h_t[n]
+//   y_t = (s_t + D x_t) silu(z_t)
+// and with ds = dy silu(z), R_t = a_{t+1} R_{t+1} + ds_t C_t (R behind the end: dhT):
+//   u_t = sum_n R_t B_t,  q_t[n] = a_t R_t h_{t-1},  v_t = sum_n q_t A
+//   dx = d u + D ds,  dd = x u + v,  dA = sum_t d q,  dD = sum_t ds x,
+//   dB_t[n] = sum_c d x R,  dC_t[n] = sum_c ds h,  dz = dy (s + D x) silu'(z).
+//
+// Bound by vector instructions: for every (row, channel, state) two products, an
+// exponential and two fused products, at about 22 cycles for 64 of them.  So the
+// layout is one that leaves nothing else to do for each of them:
+//  * A DPP row of 16 lanes is one channel, each lane a state (N > 16: NS = 2 or 4
+//    states a lane), the state in a register, time down a loop.
+//  * Rows go by chunks of 16.  What a row has for each channel (d, d x, ds) is
+//    made once, by the lane of that row, and handed to the channel's 16 lanes by
+//    the row broadcast of DPP, an operand modifier that costs no instruction.
+//  * Sums over the states (s, u, v) are made for 16 rows at once: a transposing
+//    reduction leaves row j's sum in lane j, 33 instructions for 16 sums instead
+//    of 64, and what follows them is again done once for each row and channel.
+//  * Sums over the channels (dB, dC) swap halves and quarters of a wave between
+//    the two and between two rows (3 instructions a row), then go through LDS.
+//  * A workgroup is 32 channels (8 waves), which share B_t and C_t in LDS, as
+//    fp32; its rows of x, dt, z, dy and y are read and written by whole rows of
+//    its channels and turned in LDS.
+// Few channels and many rows: the sequence runs in segments.  A first pass makes
+// each segment's own end state, a second joins them (a segment's decay is exp(A
+// sum d), closed), the main pass starts from the joined states.  The backward
+// needs the states in reverse: the forward pass stores them every 16 rows (of its
+// segment, joined when read), and the backward recomputes 16 rows in registers.
+#include <limits.h>
+
+#include <algorithm>
+#include <utility>
+
+#include "ckda_internal.hpp"
+#include "row_vec.hpp"
+
+namespace ckda {
+
+namespace {
+
+constexpr int kRows = 16;       // rows of a chunk, and lanes of a channel
+constexpr int kCh = 32;         // channels of a workgroup
+constexpr int kScanThreads = kRows * kCh;
+constexpr int kWaves = kScanThreads / 64;
+constexpr int kPad = kRows + 1;   // row of a turned tile in LDS
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266174e-8f, kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------- lanes
+
+template <int... J, typename F> __device__ __forceinline__ void each_row_impl(std::integer_sequence<int, J...>, F&& f) {
+  (f(std::integral_constant<int, J>{}), ...);
+}
+template <typename F> __device__ __forceinline__ void each_row(F&& f) {
+  each_row_impl(std::make_integer_sequence<int, kRows>{}, f);
+}
+
+// lane J's value of each DPP row, in all of its 16 lanes
+template <int J> __device__ __forceinline__ float row_bcast(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x150 + J, 0xF, 0xF, true));
+}
+template <int CTRL> __device__ __forceinline__ float dpp_mov(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
+// Sums over the 16 lanes of a DPP row of 16 values, value j's sum to lane j.  Each
+// step pairs lanes across one bit of the lane number: a lane keeps the half of the
+// values that has its bit and adds the partner's.  Where the bit selects whole
+// banks of four lanes the second sum is written over the first under a bank mask
+// (two instructions for two values), inside a bank it takes two selects and a sum.
+// (The wait states a DPP source needs behind its writer stand in the asm itself.)
+#define CKDA_PAIR(d, a, b, move, mask)                                      \
+  "v_add_f32_dpp " d ", " a ", " a " " move " row_mask:0xf bank_mask:0xf\n" \
+  "v_add_f32_dpp " d ", " b ", " b " " move " row_mask:0xf bank_mask:" mask "\n"
+__device__ __forceinline__ float turn_sums(const float (&v)[kRows], int lane) {
+  float a[8], b[4];
+  asm("s_nop 1\n"   //
+      CKDA_PAIR("%0", "%8", "%16", "row_ror:8", "0xc") CKDA_PAIR("%1", "%9", "%17", "row_ror:8", "0xc")
+      CKDA_PAIR("%2", "%10", "%18", "row_ror:8", "0xc") CKDA_PAIR("%3", "%11", "%19", "row_ror:8", "0xc")
+      CKDA_PAIR("%4", "%12", "%20", "row_ror:8", "0xc") CKDA_PAIR("%5", "%13", "%21", "row_ror:8", "0xc")
+      CKDA_PAIR("%6", "%14", "%22", "row_ror:8", "0xc") CKDA_PAIR("%7", "%15", "%23", "row_ror:8", "0xc")
+      : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2]), "=&v"(a[3]), "=&v"(a[4]), "=&v"(a[5]), "=&v"(a[6]), "=&v"(a[7])
+      : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]), "v"(v[7]), "v"(v[8]), "v"(v[9]),
+        "v"(v[10]), "v"(v[11]), "v"(v[12]), "v"(v[13]), "v"(v[14]), "v"(v[15]));
+  asm("s_nop 1\n"   //
+      CKDA_PAIR("%0", "%4", "%8", "row_half_mirror", "0xa") CKDA_PAIR("%1", "%5", "%9", "row_half_mirror", "0xa")
+      CKDA_PAIR("%2", "%6", "%10", "row_half_mirror", "0xa") CKDA_PAIR("%3", "%7", "%11", "row_half_mirror", "0xa")
+      : "=&v"(b[0]), "=&v"(b[1]), "=&v"(b[2]), "=&v"(b[3])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(a[4]), "v"(a[5]), "v"(a[6]), "v"(a[7]));
+  const bool two = lane & 2, one = lane & 1;
+  const float c0 = (two ? b[2] : b[0]) + dpp_mov<0x4E>(two ? b[0] : b[2]);   // quad_perm [2,3,0,1]
+  const float c1 = (two ? b[3] : b[1]) + dpp_mov<0x4E>(two ? b[1] : b[3]);
+  return (one ? c1 : c0) + dpp_mov<0xB1>(one ? c0 : c1);                     // quad_perm [1,0,3,2]
+}
+#undef CKDA_PAIR
+
+// lower half of the wave: a summed over the halves; upper half: b
+__device__ __forceinline__ float sum_halves(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// even DPP rows: a summed over the row and the next; odd ones: b
+__device__ __forceinline__ float sum_quarters(float a, float b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------- elements
+
+// exp(-|v|), to a few 2^-24 (the product with log2 e in two parts)
+__device__ __forceinline__ float exp_neg_abs(float v) {
+  const float m = fminf(fabsf(v), 200.f), t = -m * kLog2e;
+  const float lo = __builtin_fmaf(-m, kLog2eLo, __builtin_fmaf(-m, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, lo * kLn2, e);
+}
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), by the series of log((1 +
+// r) / (1 - r)) in r = e / (2 + e) <= 1/3 (next term 2^-26 of the first): small
+// steps keep their relative accuracy, which log(1 + e) does not.
+__device__ __forceinline__ float softplus(float v) {
+  const float e = exp_neg_abs(v), r = e * __builtin_amdgcn_rcpf(2.f + e), z = r * r;
+  float p = 1.f / 13.f;
+  p = __builtin_fmaf(p, z, 1.f / 11.f);
+  p = __builtin_fmaf(p, z, 1.f / 9.f);
+  p = __builtin_fmaf(p, z, 1.f / 7.f);
+  p = __builtin_fmaf(p, z, 1.f / 5.f);
+  p = __builtin_fmaf(p, z, 1.f / 3.f);
+  return (v < 0.f ? 0.f : v) + 2.f * __builtin_fmaf(r * z, p, r);   // (a NaN stays one)
+}
+__device__ __forceinline__ float softplus_slope(float v) {
+  const float e = exp_neg_abs(v), r = __builtin_amdgcn_rcpf(1.f + e);
+  return v >= 0.f ? r : e * r;
+}
+
+// A decay 2^x.  Where the inputs are bf16: itself, by the hardware's exponential
+// (mean error -0.12 of 2^-24 for small x, so a state that remembers M rows is off
+// by some 7e-9 M).  Where they are fp32: for -x < 1/16 its distance from 1, which
+// keeps slow decays to 2^-24 of their rate (degree 4: next term 2^-25); stronger
+// ones, of states that remember fewer than 24 rows, themselves.
+template <bool EXACT> struct Decay;
+template <> struct Decay<false> {
+  float m;
+  __device__ __forceinline__ explicit Decay(float x) : m(__builtin_amdgcn_exp2f(x)) {}
+  __device__ __forceinline__ Decay() {}
+  __device__ __forceinline__ float of(float h) const { return m * h; }
+  __device__ __forceinline__ float of(float h, float add) const { return __builtin_fmaf(m, h, add); }
+};
+template <> struct Decay<true> {
+  float m;
+  bool near;   // m is the distance from 1
+  __device__ __forceinline__ explicit Decay(float x) : near(fabsf(x) < 0.0625f) {
+    float p = 0.009618129107628477f;                        // ln2^4 / 24
+    p = __builtin_fmaf(p, x, 0.05550410866482158f);         // ln2^3 / 6
+    p = __builtin_fmaf(p, x, 0.2402265069591007f);          // ln2^2 / 2
+    p = __builtin_fmaf(p, x, kLn2);
+    m = near ? p * x : __builtin_amdgcn_exp2f(x);
+  }
+  __device__ __forceinline__ Decay() {}
+  __device__ __forceinline__ float of(float h) const { return __builtin_fmaf(m, h, near ? h : 0.f); }
+  __device__ __forceinline__ float of(float h, float add) const { return __builtin_fmaf(m, h, add) + (near ? h : 0.f); }
+};
+
+// ---------------------------------------------------------------- launches
+
+struct ScanGeom {
+  int B, T, C, G, N;
+  int Cg, cblocks;         // channels of a group, workgroups along them
+  int ldbc, ldz;
+  int nseg, seg_chunks;    // segments, chunks of each
+  int chunks;              // chunks of T rows
+  int softplus, pad_zero;
+};
+
+struct ScanWork {            // workspace of a call
+  float* ends;               // [B][nseg][C][N]: segments' own end states, then start states
+  float* steps;              // [B][nseg][C]: sums of d over the segments
+  float* back;               // [B][nseg][C][N]: backward in time
+  float* marks;              // [B][chunks][C][N]: states before each chunk, of their segment
+  float* mark_steps;         // [B][chunks][C]: sums of d from the segment's start to each chunk (nseg > 1)
+  float* bc;                 // [G cblocks][B T][2][N]: parts of dC, dB
+  float* weights;            // [B nseg][C N + 2 C]: parts of dA, dD, dbias
+};
+
+struct ScanLaunch {
+  SelScanArgs a;
+  ScanGeom G;
+  ScanWork w;
+  int segs;                  // segments of this launch
+};
+
+// Place of a workgroup: the channel blocks of one piece of rows next to each
+// other on one XCD, since they share lines of x, B and C.
+struct ScanPlace {
+  int b, seg, g, cb, len, ch0, ch1;
+};
+__device__ __forceinline__ bool scan_place(const ScanLaunch& L, ScanPlace& p) {
+  const ScanGeom& G = L.G;
+  const int total = G.B * L.segs * G.G * G.cblocks, per = (total + 7) / 8;
+  int i = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (i >= total || (int)(blockIdx.x / 8) >= per) return false;
+  p.cb = i % G.cblocks;
+  i /= G.cblocks;
+  p.g = i % G.G;
+  i /= G.G;
+  p.seg = i % L.segs;
+  p.b = i / L.segs;
+  p.len = L.a.lens ? min(max(L.a.lens[p.b], 0), G.T) : G.T;
+  const int all = (p.len + kRows - 1) / kRows;
+  p.ch0 = p.seg * G.seg_chunks;
+  p.ch1 = min(p.ch0 + G.seg_chunks, all);
+  return true;
+}
+
+// B and C of a chunk in LDS: [row][s][lane] pairs
+template <typename T, int NS> struct BcTile {
+  T raw[NS];
+  __device__ __forceinline__ void fetch(const ScanLaunch& L, const ScanPlace& p, int chunk) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int idx = (int)threadIdx.x + i * kScanThreads, n = idx % (16 * NS), which = idx / (16 * NS) % 2;
+      const int t = chunk * kRows + idx / (32 * NS);
+      raw[i] = from_f32<T>(0.f);
+      if (t < p.len && n < L.G.N) {
+        const T* src = which ? (const T*)L.a.Cm : (const T*)L.a.Bm;
+        raw[i] = src[((size_t)p.b * L.G.T + t) * L.G.ldbc + p.g * L.G.N + n];
+      }
+    }
+  }
+  __device__ __forceinline__ void stage(float* s) const {
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int idx = (int)threadIdx.x + i * kScanThreads, n = idx % (16 * NS), which = idx / (16 * NS) % 2;
+      const int row = idx / (32 * NS);
+      s[((row * NS + n / 16) * 16 + n % 16) * 2 + which] = to_f32(raw[i]);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- forward
+
+// MAIN: outputs (and the last state) from the segments' start states.  Else: the
+// segments' own end states and sums of steps, with MARK the states before each
+// chunk on the way.
+template <typename T, int NS, bool MAIN, bool MARK>
+__global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanLaunch L) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  __shared__ float2 s_d[2][kCh][kPad];
+  __shared__ float s_y[MAIN ? 2 : 1][MAIN ? kCh : 1][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][kRows * NS * 16 * 2];
+  const SelScanArgs& a = L.a;
+  const ScanGeom& G = L.G;
+  ScanPlace p;
+  if (!scan_place(L, p)) return;
+  const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;   // state and channel in the recurrence
+  const int r = tid >> 5, ch = tid & 31;                         // row and channel of the tiles
+  const int c0 = p.cb * kCh, first_c = p.g * G.Cg + c0;
+  const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
+  const int cm = first_c + mine, ct = first_c + ch;
+
+  float A2[NS], h[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const bool state = on && n + 16 * s < G.N;
+    const size_t at = (size_t)cm * G.N + n + 16 * s;
+    A2[s] = state ? a.A[at] * kLog2e : 0.f;
+    h[s] = 0.f;
+    if (state) {
+      if (MAIN && p.seg > 0) h[s] = L.w.ends[((size_t)p.b * G.nseg + p.seg) * G.C * G.N + at];
+      else if (p.seg == 0 && a.h0) h[s] = a.h0[(size_t)p.b * G.C * G.N + at];
+    }
+  }
+  const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
+  const float Dc = MAIN && tile_on && a.D ? a.D[ct] : 0.f;
+
+  T xr = from_f32<T>(0.f), dr = xr, zr = xr;
+  BcTile<T, NS> bc;
+  bool live = false;
+  auto fetch = [&](int chunk) {
+    const int t = chunk * kRows + r;
+    live = tile_on && t < p.len;
+    if (live) {
+      const size_t at = ((size_t)p.b * G.T + t);
+      xr = ((const T*)a.x)[at * G.C + ct];
+      dr = ((const T*)a.dt)[at * G.C + ct];
+      if (MAIN && a.z) zr = ((const T*)a.z)[at * G.ldz + ct];
+    }
+    bc.fetch(L, p, chunk);
+  };
+  auto stage = [&](int buf) {
+    float d = 0.f, x = 0.f;
+    if (live) {
+      x = to_f32(xr);
+      d = to_f32(dr) + bias;
+      if (G.softplus) d = softplus(d);
+    }
+    s_d[buf][ch][r] = float2{d, d * x};
+    bc.stage(s_bc[buf]);
+  };
+
+  float steps = 0.f;
+  if (p.ch0 < p.ch1) {
+    fetch(p.ch0);
+    stage(0);
+    __syncthreads();
+  }
+  for (int k = p.ch0; k < p.ch1; ++k) {
+    const int buf = (k - p.ch0) & 1;
+    const float xk = to_f32(xr), zk = to_f32(zr);
+    const bool live_k = live;
+    if (k + 1 < p.ch1) fetch(k + 1);
+    const float2 d = s_d[buf][mine][n];
+    if constexpr (MARK) {
+      if (on) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if (n + 16 * s < G.N) L.w.marks[(((size_t)p.b * G.chunks + k) * G.C + cm) * G.N + n + 16 * s] = h[s];
+        if (G.nseg > 1 && n == 0) L.w.mark_steps[((size_t)p.b * G.chunks + k) * G.C + cm] = steps;
+      }
+    }
+    if constexpr (!MAIN) steps += group_sum<16>(d.x);
+    float sums[kRows];
+    each_row([&](auto J) {
+      constexpr int j = J;
+      const float2* row = reinterpret_cast<const float2*>(s_bc[buf]) + j * NS * 16 + n;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const float2 f = row[s * 16];
+        h[s] = Decay<EXACT>(row_bcast<j>(d.x) * A2[s]).of(h[s], row_bcast<j>(d.y) * f.x);
+        if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(f.y, h[s], sums[j]) : f.y * h[s];
+      }
+    });
+    if constexpr (MAIN) s_y[buf][mine][n] = turn_sums(sums, n);
+    if (k + 1 < p.ch1) stage(buf ^ 1);
+    lds_barrier();
+    if constexpr (MAIN) {
+      if (live_k) {
+        float y = __builtin_fmaf(Dc, xk, s_y[buf][ch][r]);
+        if (a.z) y *= zk * row_sigmoid<T>(zk);
+        ((T*)a.y)[((size_t)p.b * G.T + k * kRows + r) * G.C + ct] = from_f32<T>(y);
+      }
+    }
+  }
+  if constexpr (MAIN) {
+    if (a.hT && p.seg == G.nseg - 1 && on) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        if (n + 16 * s < G.N) a.hT[((size_t)p.b * G.C + cm) * G.N + n + 16 * s] = h[s];
+    }
+    if (G.pad_zero && tile_on) {
+      const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
+      for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += kRows)
+        ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
+    }
+  } else if (on && G.nseg > 1) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      if (n + 16 * s < G.N) L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * G.N + n + 16 * s] = h[s];
+    if (n == 0) L.w.steps[((size_t)p.b * G.nseg + p.seg) * G.C + cm] = steps;
+  }
+}
+
+// Segments' own states joined in order, in place: each place gets the state that
+// its segment starts from (forward in time: the first is left as it is, backward:
+// the last).
+template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_join_kernel(const ScanLaunch L) {
+  const ScanGeom& G = L.G;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, CN = (long long)G.C * G.N;
+  if (i >= (long long)G.B * CN) return;
+  const int b = (int)(i / CN);
+  const long long cn = i - (long long)b * CN;
+  const float A2 = L.a.A[cn] * kLog2e;
+  float* own = (BACK ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CN + cn;
+  const float* steps = L.w.steps + (size_t)b * G.nseg * G.C + cn / G.N;
+  float h = own[(size_t)(BACK ? G.nseg - 1 : 0) * CN];
+  for (int k = 1; k < G.nseg; ++k) {
+    const int seg = BACK ? G.nseg - 1 - k : k;
+    // (the forward's launch of own states leaves out the last segment, whose end nobody starts from)
+    const bool last = k == G.nseg - 1;
+    const float next = last ? 0.f : own[(size_t)seg * CN], sum = last ? 0.f : steps[(size_t)seg * G.C];
+    own[(size_t)seg * CN] = h;
+    h = Decay<EXACT>(sum * A2).of(h) + next;
+  }
+}
+
+// ---------------------------------------------------------------- backward
+
+// MAIN: gradients.  Else: the segments' own states backward in time (the gradient
+// of the state before a segment, from its rows alone).
+template <typename T, int NS, bool MAIN>
+__global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch L) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  __shared__ float2 s_d[kCh][kPad];
+  __shared__ float s_ds[kCh][kPad];
+  __shared__ float s_out[MAIN ? 3 : 1][MAIN ? kCh : 1][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[kRows * NS * 16 * 2];
+  __shared__ float s_part[MAIN ? kWaves : 1][MAIN ? kRows / 2 * NS * 64 : 1];
+  const SelScanArgs& a = L.a;
+  const ScanGeom& G = L.G;
+  ScanPlace p;
+  if (!scan_place(L, p)) return;
+  if (!MAIN) p.seg += 1, p.ch0 += G.seg_chunks, p.ch1 = min(p.ch0 + G.seg_chunks, (p.len + kRows - 1) / kRows);
+  const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;
+  const int r = tid >> 5, ch = tid & 31;
+  const int c0 = p.cb * kCh, first_c = p.g * G.Cg + c0;
+  const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
+  const int cm = first_c + mine, ct = first_c + ch;
+  const size_t CN = (size_t)G.C * G.N;
+
+  float A2[NS], A[NS], Q[NS], start[NS], dA[NS];
+  bool state[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    state[s] = on && n + 16 * s < G.N;
+    const size_t at = (size_t)cm * G.N + n + 16 * s;
+    A[s] = state[s] ? a.A[at] : 0.f;
+    A2[s] = A[s] * kLog2e;
+    dA[s] = Q[s] = start[s] = 0.f;
+    if (state[s]) {
+      if (p.seg == G.nseg - 1) Q[s] = a.dhT ? a.dhT[(size_t)p.b * CN + at] : 0.f;
+      else if (MAIN) Q[s] = L.w.back[((size_t)p.b * G.nseg + p.seg) * CN + at];
+      if (MAIN && p.seg > 0) start[s] = L.w.ends[((size_t)p.b * G.nseg + p.seg) * CN + at];
+    }
+  }
+  const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
+  const float Dc = tile_on && a.D ? a.D[ct] : 0.f;
+  float dD = 0.f, dbias = 0.f;
+
+  const T zero = from_f32<T>(0.f);
+  T xr = zero, dr = zero, zr = zero, gr = zero;
+  float mark[NS], mark_steps = 0.f;
+  BcTile<T, NS> bc;
+  bool live = false;
+  auto fetch = [&](int chunk) {
+    const int t = chunk * kRows + r;
+    live = tile_on && t < p.len;
+    if (live) {
+      const size_t at = ((size_t)p.b * G.T + t);
+      if (MAIN) xr = ((const T*)a.x)[at * G.C + ct];
+      dr = ((const T*)a.dt)[at * G.C + ct];
+      gr = ((const T*)a.dy)[at * G.C + ct];
+      if (a.z) zr = ((const T*)a.z)[at * G.ldz + ct];
+    }
+    bc.fetch(L, p, chunk);
+    if constexpr (MAIN) {
+      const size_t at = ((size_t)p.b * G.chunks + chunk) * G.C + cm;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) mark[s] = state[s] ? L.w.marks[at * G.N + n + 16 * s] : 0.f;
+      if (p.seg > 0 && on) mark_steps = L.w.mark_steps[at];
+    }
+  };
+  if (p.ch0 < p.ch1) fetch(p.ch1 - 1);
+  for (int k = p.ch1 - 1; k >= p.ch0; --k) {
+    float x = 0.f, raw = 0.f, d = 0.f, z = 0.f, dy = 0.f, ds = 0.f;
+    const bool live_k = live;
+    if (live) {
+      x = to_f32(xr), raw = to_f32(dr) + bias, dy = to_f32(gr), z = to_f32(zr);
+      d = G.softplus ? softplus(raw) : raw;
+      ds = a.z ? dy * z * row_sigmoid<T>(z) : dy;
+    }
+    s_d[ch][r] = float2{d, d * x};
+    s_ds[ch][r] = ds;
+    bc.stage(s_bc);
+    float hc[NS];   // the state before the chunk
+    if constexpr (MAIN) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        hc[s] = p.seg > 0 ? mark[s] + Decay<EXACT>(mark_steps * A2[s]).of(start[s]) : mark[s];
+    }
+    lds_barrier();
+    if (k > p.ch0) fetch(k - 1);
+    const float2 dd = s_d[mine][n];
+    const float dsm = s_ds[mine][n];
+    const float2* rows = reinterpret_cast<const float2*>(s_bc) + n;
+    Decay<EXACT> e[MAIN ? kRows : 1][NS];
+    if constexpr (!MAIN) {
+      each_row([&](auto J) {
+        constexpr int j = kRows - 1 - J;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float R = __builtin_fmaf(row_bcast<j>(dsm), rows[(j * NS + s) * 16].y, Q[s]);
+          Q[s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]).of(R);
+        }
+      });
+      lds_barrier();
+    } else {
+      float h[kRows][NS];
+      {
+        float sums[kRows];
+        each_row([&](auto J) {
+          constexpr int j = J;
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const float2 f = rows[(j * NS + s) * 16];
+            e[j][s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]);
+            const float before = j ? h[j ? j - 1 : 0][s] : hc[s];
+            h[j][s] = e[j][s].of(before, row_bcast<j>(dd.y) * f.x);
+            sums[j] = s ? __builtin_fmaf(f.y, h[j][s], sums[j]) : f.y * h[j][s];
+          }
+        });
+        if (a.z) s_out[0][mine][n] = turn_sums(sums, n);
+      }
+      float u[kRows], v[kRows], pair[NS];
+      each_row([&](auto J) {
+        constexpr int j = kRows - 1 - J;
+        u[j] = v[j] = 0.f;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float2 f = rows[(j * NS + s) * 16];
+          const float R = __builtin_fmaf(row_bcast<j>(dsm), f.y, Q[s]);
+          const float both = sum_halves(row_bcast<j>(dsm) * h[j][s], row_bcast<j>(dd.y) * R);   // dC, dB
+          if constexpr (j % 2) pair[s] = both;
+          else s_part[tid >> 6][(j / 2 * NS + s) * 64 + (tid & 63)] = sum_quarters(both, pair[s]);
+          u[j] = __builtin_fmaf(R, f.x, u[j]);
+          Q[s] = e[j][s].of(R);
+          const float q = Q[s] * (j ? h[j ? j - 1 : 0][s] : hc[s]);
+          v[j] = __builtin_fmaf(q, A[s], v[j]);
+          dA[s] = __builtin_fmaf(q, row_bcast<j>(dd.x), dA[s]);
+        }
+      });
+      s_out[1][mine][n] = turn_sums(u, n);
+      s_out[2][mine][n] = turn_sums(v, n);
+      lds_barrier();
+      if (live_k) {
+        const size_t at = ((size_t)p.b * G.T + k * kRows + r) * G.C + ct;
+        const float uu = s_out[1][ch][r], dd_ = __builtin_fmaf(x, uu, s_out[2][ch][r]);
+        const float ddt = G.softplus ? dd_ * softplus_slope(raw) : dd_;
+        ((T*)a.dx)[at] = from_f32<T>(__builtin_fmaf(d, uu, Dc * ds));
+        ((T*)a.ddt)[at] = from_f32<T>(ddt);
+        if (a.z) {
+          const float pre = __builtin_fmaf(Dc, x, s_out[0][ch][r]);
+          ((T*)a.dz)[at] = from_f32<T>(dy * pre * silu_slope(z, row_sigmoid<T>(z)));
+        }
+        dD = __builtin_fmaf(ds, x, dD);
+        dbias += ddt;
+      }
+      // dC and dB of the workgroup's channels: place 64 (j / 2 NS + s) + lane of a wave's parts holds row j (odd
+      // DPP rows: j + 1) of state n + 16 s, dC in the lower half of the wave and dB in the upper one
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const int e_ = tid + i * kScanThreads, lane = e_ % 64, s = e_ / 64 % NS;
+        const int t = k * kRows + e_ / (64 * NS) * 2 + (lane / 16 & 1), m = lane % 16 + 16 * s;
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) sum += s_part[w][e_];
+        if (t < p.len && m < G.N)
+          L.w.bc[((((size_t)p.g * G.cblocks + p.cb) * G.B + p.b) * G.T + t) * 2 * G.N + (lane / 32) * G.N + m] = sum;
+      }
+      // (the next chunk's tiles, s_d, s_ds and s_bc, are not read in this phase; s_out and s_part are written
+      // behind its first barrier)
+    }
+  }
+  if constexpr (!MAIN) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+      if (state[s]) L.w.back[((size_t)p.b * G.nseg + p.seg) * CN + (size_t)cm * G.N + n + 16 * s] = Q[s];
+  } else {
+    float* part = L.w.weights + ((size_t)p.b * G.nseg + p.seg) * (CN + 2 * (size_t)G.C);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (!state[s]) continue;
+      part[(size_t)cm * G.N + n + 16 * s] = dA[s];
+      if (p.seg == 0 && a.dh0) a.dh0[(size_t)p.b * CN + (size_t)cm * G.N + n + 16 * s] = Q[s];
+    }
+    // over the tile's rows: thread (r, ch) holds the sums of rows r, r + 16, ...
+    __syncthreads();
+    s_out[0][ch][r] = dD;
+    s_out[1][ch][r] = dbias;
+    __syncthreads();
+    if (tid < 2 * kCh && c0 + (tid & 31) < G.Cg) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) sum += s_out[tid >> 5][tid & 31][i];
+      part[CN + (size_t)(tid >> 5) * G.C + first_c + (tid & 31)] = sum;
+    }
+    if (G.pad_zero && tile_on) {
+      const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
+      for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += kRows) {
+        const size_t at = ((size_t)p.b * G.T + t) * G.C + ct;
+        ((T*)a.dx)[at] = ((T*)a.ddt)[at] = zero;
+        if (a.z) ((T*)a.dz)[at] = zero;
+      }
+    }
+  }
+}
+
+// dBm and dCm: the sums of the channel blocks' parts
+template <typename T> __global__ __launch_bounds__(256) void scan_bc_kernel(const ScanLaunch L) {
+  const ScanGeom& G = L.G;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, GN = (long long)G.G * G.N;
+  const long long row = i / (2 * GN);
+  if (row >= (long long)G.B * G.T) return;
+  const int rest = (int)(i - row * 2 * GN), which = rest / (int)GN, gn = rest - which * (int)GN;
+  const int g = gn / G.N, m = gn - g * G.N, b = (int)(row / G.T), t = (int)(row - (long long)b * G.T);
+  const int len = L.a.lens ? min(max(L.a.lens[b], 0), G.T) : G.T;
+  T* out = (T*)(which ? L.a.dBm : L.a.dCm) + row * GN + gn;
+  if (t >= len) {
+    if (G.pad_zero) *out = from_f32<T>(0.f);
+    return;
+  }
+  const size_t stride = (size_t)G.B * G.T * 2 * G.N;
+  const float* part = L.w.bc + (size_t)g * G.cblocks * stride + ((size_t)row * 2 + which) * G.N + m;
+  float sum = 0.f;
+#pragma unroll 8
+  for (int k = 0; k < G.cblocks; ++k) sum += part[k * stride];
+  *out = from_f32<T>(sum);
+}
+
+// ---------------------------------------------------------------- decode
+
+// Four states a lane, LPC lanes a channel (a power of two, up to 16).  HBM-bound:
+// the state is read and written once.
+template <typename T, int LPC, bool WHOLE>
+__global__ __launch_bounds__(256) void scan_decode_kernel(const ScanLaunch L) {
+  constexpr bool EXACT = sizeof(T) == 4;
+  const SelScanArgs& a = L.a;
+  const ScanGeom& G = L.G;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long channel = i / LPC;
+  if (channel >= (long long)G.B * G.C) return;   // (a channel's lanes all leave or all stay)
+  const int l = (int)(i % LPC), n0 = 4 * l;
+  const int b = (int)(channel / G.C), c = (int)(channel - (long long)b * G.C), g = c / G.Cg;
+  float* hp = a.H_inout + (size_t)channel * G.N + n0;
+  const float* ap = a.A + (size_t)c * G.N + n0;
+  const size_t bc = (size_t)b * G.ldbc + (size_t)g * G.N + n0;
+  f32x4 h = zero4(), A = zero4();
+  float Bv[4], Cv[4];
+  const int left = G.N - n0;
+  if constexpr (WHOLE) {
+    if (left > 0) {
+      h = *reinterpret_cast<const f32x4*>(hp);
+      A = *reinterpret_cast<const f32x4*>(ap);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) h[e] = hp[e], A[e] = ap[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    Bv[e] = e < left ? to_f32(((const T*)a.Bm)[bc + e]) : 0.f;
+    Cv[e] = e < left ? to_f32(((const T*)a.Cm)[bc + e]) : 0.f;
+  }
+  const float x = to_f32(((const T*)a.x)[channel]);
+  float d = to_f32(((const T*)a.dt)[channel]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+  if (G.softplus) d = softplus(d);
+  const float dx = d * x;
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = Decay<EXACT>(d * (A[e] * kLog2e)).of(h[e], dx * Bv[e]);
+    s = __builtin_fmaf(Cv[e], h[e], s);
+  }
+  if constexpr (WHOLE) {
+    if (left > 0) *reinterpret_cast<f32x4*>(hp) = h;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < left) hp[e] = h[e];
+  }
+  if constexpr (LPC > 1) s = group_sum<LPC>(s);
+  if (l != 0) return;
+  float y = __builtin_fmaf(a.D ? a.D[c] : 0.f, x, s);
+  if (a.z) {
+    const float z = to_f32(((const T*)a.z)[(size_t)b * G.ldz + c]);
+    y *= z * row_sigmoid<T>(z);
+  }
+  ((T*)a.y)[channel] = from_f32<T>(y);
+}
+
+// ---------------------------------------------------------------- host
+
+ScanGeom scan_geom(int B, int T, int C, int G, int N) {
+  ScanGeom g = {};
+  g.B = B, g.T = T, g.C = C, g.G = G, g.N = N;
+  g.Cg = C / G;
+  g.cblocks = (g.Cg + kCh - 1) / kCh;
+  g.chunks = (int)(((long long)T + kRows - 1) / kRows);
+  // Segments where the channels leave CUs without a workgroup; of 128 rows at least.
+  const long long blocks = (long long)B * G * g.cblocks;
+  g.nseg = 1;
+  if (blocks > 0 && blocks < 192) g.nseg = (int)std::max(1LL, std::min((512 + blocks - 1) / blocks, (long long)g.chunks / 8));
+  g.seg_chunks = std::max(1, (g.chunks + g.nseg - 1) / g.nseg);
+  g.nseg = std::max(1, (g.chunks + g.seg_chunks - 1) / g.seg_chunks);
+  return g;
+}
+
+struct ScanSizes {
+  size_t ends, steps, back, marks, mark_steps, bc, weights;   // floats
+};
+ScanSizes scan_sizes(const ScanGeom& g, bool bwd) {
+  auto up = [](size_t n) { return (n + 63) / 64 * 64; };
+  const size_t CN = (size_t)g.C * g.N, segs = (size_t)g.B * g.nseg;
+  ScanSizes s = {};
+  if (g.nseg > 1) s.ends = up(segs * CN), s.steps = up(segs * g.C);
+  if (!bwd) return s;
+  if (g.nseg > 1) s.back = up(segs * CN), s.mark_steps = up((size_t)g.B * g.chunks * g.C);
+  s.marks = up((size_t)g.B * g.chunks * CN);
+  s.bc = up((size_t)g.G * g.cblocks * g.B * g.T * 2 * g.N);
+  s.weights = up(segs * (CN + 2 * (size_t)g.C));
+  return s;
+}
+size_t scan_bytes(const ScanSizes& s) {
+  return 4 * (s.ends + s.steps + s.back + s.marks + s.mark_steps + s.bc + s.weights);
+}
+
+ScanLaunch scan_launch(const SelScanArgs& a, bool bwd) {
+  ScanLaunch L;
+  L.a = a;
+  L.G = scan_geom(a.B, a.T, a.C, a.G, a.N);
+  L.G.ldbc = a.ldbc, L.G.ldz = a.ldz, L.G.softplus = a.softplus, L.G.pad_zero = a.pad_zero;
+  L.segs = L.G.nseg;
+  const ScanSizes s = scan_sizes(L.G, bwd);
+  float* p = (float*)a.workspace;
+  auto take = [&](size_t n) { float* q = n ? p : nullptr; p = n ? p + n : p; return q; };
+  L.w.ends = take(s.ends), L.w.steps = take(s.steps), L.w.back = take(s.back), L.w.marks = take(s.marks);
+  L.w.mark_steps = take(s.mark_steps), L.w.bc = take(s.bc), L.w.weights = take(s.weights);
+  return L;
+}
+
+unsigned scan_blocks(const ScanLaunch& L) {
+  const int total = L.G.B * L.segs * L.G.G * L.G.cblocks;
+  return (unsigned)((total + 7) / 8 * 8);
+}
+
+template <bool BACK> hipError_t launch_join(const ScanLaunch& L) {
+  const unsigned blocks = (unsigned)(((long long)L.G.B * L.G.C * L.G.N + 255) / 256);
+  if (L.a.dtype == CKDA_DTYPE_F32) hipLaunchKernelGGL((scan_join_kernel<true, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L);
+  else hipLaunchKernelGGL((scan_join_kernel<false, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L);
+  return hipGetLastError();
+}
+
+template <typename T, int NS> hipError_t launch_fwd_t(const SelScanArgs& a) {
+  ScanLaunch L = scan_launch(a, false);
+  if (L.G.nseg > 1) {
+    L.segs = L.G.nseg - 1;
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, false, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = launch_join<false>(L);
+    if (e != hipSuccess) return e;
+    L.segs = L.G.nseg;
+  }
+  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, true, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+  return hipGetLastError();
+}
+
+template <typename T, int NS> hipError_t launch_bwd_t(const SelScanArgs& a) {
+  ScanLaunch L = scan_launch(a, true);
+  hipError_t e = hipSuccess;
+  if (L.G.B > 0) {
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, false, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (L.G.nseg > 1) {
+      if ((e = launch_join<false>(L)) != hipSuccess) return e;
+      L.segs = L.G.nseg - 1;
+      hipLaunchKernelGGL((scan_bwd_kernel<T, NS, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      if ((e = launch_join<true>(L)) != hipSuccess) return e;
+      L.segs = L.G.nseg;
+    }
+    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
+    if (each > 0) {
+      hipLaunchKernelGGL((scan_bc_kernel<T>), dim3((unsigned)((each + 255) / 256)), dim3(256), 0, a.stream, L);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+  }
+  const size_t CN = (size_t)a.C * a.N, C = (size_t)a.C;
+  return launch_part_sums(PartSums{L.w.weights, L.G.B * L.G.nseg, CN + 2 * C, {a.dA, a.dD, a.dbias}, {CN, C, C}}, a.stream);
+}
+
+template <typename T, int LPC> hipError_t launch_decode_t(const SelScanArgs& a) {
+  const ScanLaunch L = scan_launch(a, false);
+  const unsigned blocks = (unsigned)(((long long)a.B * a.C * LPC + 255) / 256);
+  if (a.N % 4 == 0) hipLaunchKernelGGL((scan_decode_kernel<T, LPC, true>), dim3(blocks), dim3(256), 0, a.stream, L);
+  else hipLaunchKernelGGL((scan_decode_kernel<T, LPC, false>), dim3(blocks), dim3(256), 0, a.stream, L);
+  return hipGetLastError();
+}
+
+template <typename T> hipError_t launch_scan(const SelScanArgs& a, bool bwd) {
+  if (a.N <= 16) return bwd ? launch_bwd_t<T, 1>(a) : launch_fwd_t<T, 1>(a);
+  if (a.N <= 32) return bwd ? launch_bwd_t<T, 2>(a) : launch_fwd_t<T, 2>(a);
+  return bwd ? launch_bwd_t<T, 4>(a) : launch_fwd_t<T, 4>(a);
+}
+
+template <typename T> hipError_t launch_decode_n(const SelScanArgs& a) {
+  if (a.N <= 4) return launch_decode_t<T, 1>(a);
+  if (a.N <= 8) return launch_decode_t<T, 2>(a);
+  if (a.N <= 16) return launch_decode_t<T, 4>(a);
+  if (a.N <= 32) return launch_decode_t<T, 8>(a);
+  return launch_decode_t<T, 16>(a);
+}
+
+}  // namespace
+
+size_t scan_fwd_workspace_bytes(int B, int T, int C, int G, int N) {
+  return scan_bytes(scan_sizes(scan_geom(B, T, C, G, N), false));
+}
+size_t scan_bwd_workspace_bytes(int B, int T, int C, int G, int N) {
+  return scan_bytes(scan_sizes(scan_geom(B, T, C, G, N), true));
+}
+
+// fewer than 2^32 threads in every launch, and counts of workgroups in an int
+bool scan_fits_grid(int B, int T, int C, int G, int N) {
+  const ScanGeom g = scan_geom(B, T, C, G, N);
+  const long long blocks = (long long)B * g.nseg * G * g.cblocks;
+  return blocks < (1LL << 22) && (long long)B * C * N < (1LL << 31) && (long long)B * C * 16 < (1LL << 31) &&
+         (double)B * T * 2 * G * N < 4e9;
+}
+
+hipError_t launch_scan_fwd(const SelScanArgs& a) {
+  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan<bf16_t>(a, false) : launch_scan<float>(a, false);
+}
+hipError_t launch_scan_bwd(const SelScanArgs& a) {
+  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan<bf16_t>(a, true) : launch_scan<float>(a, true);
+}
+hipError_t launch_scan_decode(const SelScanArgs& a) {
+  return a.dtype == CKDA_DTYPE_BF16 ? launch_decode_n<bf16_t>(a) : launch_decode_n<float>(a);
+}
+
+}  // namespace ckda

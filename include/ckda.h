@@ -526,6 +526,155 @@ int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float
                        float* dw, float* db, int B, int H, int T, int D, int wheads, int dtype, int flags, float eps,
                        void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around a recurrence in a layer: the norm with the residual's
+ * addition ahead of the projections, the short causal convolution behind them,
+ * and the selective scan, a diagonal recurrence for layers without heads.
+ * Token-major rows ([B, T, C], as projections read and write them), dtype F32
+ * or BF16, all arithmetic, sums and states in fp32, outputs rounded once.
+ * Where a row stride `ld...` (in elements, at least the row's width) is taken,
+ * the input may be a column slice of a wider [B, T, ld] tensor, at any address
+ * that is a multiple of the element's size; all other tensors are contiguous
+ * and 16-byte aligned.
+ *
+ * lens: NULL, or [B] int32 (device), the rows of each batch entry that are part
+ * of its sequence (clamped into [0, T]); rows at or past it are never read, and
+ * those of the outputs are left as they were, or zeroed with CKDA_PAD_ZERO. */
+#define CKDA_PAD_ZERO 32
+
+/* Short causal convolution, one filter of K = 2, 3 or 4 taps for each channel:
+ *
+ *   u_t = b + sum_j w_j x_{t-K+1+j},   y_t = act(u_t)
+ *
+ * flags: CKDA_CONV_SILU   act(u) = u sigmoid(u), else act(u) = u
+ *        CKDA_PAD_ZERO    as above
+ *   x      : [B, T, C] dtype, row stride ldx
+ *   w, b   : [C, K], [C] fp32 (w_{K-1} is of the row itself); b NULL for zeros
+ *   s0     : [B, K-1, C] dtype, the inputs before the first row, oldest first,
+ *            or NULL for zeros
+ *   y      : [B, H, T, C/H] dtype, head-major: the queries, keys or values of
+ *            the attentions above (H divides C; H = 1 is token-major)
+ *   sT     : [B, K-1, C] dtype, the last K-1 inputs of each sequence (those of
+ *            s0 where it is shorter), or NULL to skip
+ * Outputs must not overlap each other or any input. */
+#define CKDA_CONV_SILU 1
+
+int ckda_short_conv_fwd(const void* x, const float* w, const float* b, const void* s0, const int* lens, void* y,
+                        void* sT, int B, int T, int C, int H, int K, int ldx, int dtype, int flags, void* stream);
+
+/* Bytes of device workspace ckda_short_conv_bwd needs, or 0 for invalid or
+ * unsupported sizes: K + 1 fp32 rows of width C for each workgroup that sums
+ * the weights' gradients. */
+size_t ckda_short_conv_bwd_workspace_size(int B, int T, int C, int K, int dtype);
+
+/* Backward of ckda_short_conv_fwd given dy [B, H, T, C/H] and, or NULL for
+ * zeros, dsT [B, K-1, C] (dtype): dx [B, T, C] and ds0 [B, K-1, C] (or NULL to
+ * skip) in dtype, dw [C, K] and db [C] fp32 (either may be NULL), summed over
+ * batch and time in a fixed order.  Outputs must not overlap each other, any
+ * input or the workspace, nor the workspace an input. */
+int ckda_short_conv_bwd(const void* x, const float* w, const float* b, const void* s0, const int* lens, const void* dy,
+                        const void* dsT, void* dx, float* dw, float* db, void* ds0, int B, int T, int C, int H, int K,
+                        int ldx, int dtype, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of N sequences: x [N, C] (row stride ldx), state_inout [N, K-1, C]
+ * dtype (the last K-1 inputs, oldest first), y [N, C] (head-major [N, H, C/H]
+ * is the same).  flags: CKDA_CONV_SILU. */
+int ckda_short_conv_decode_step(const void* x, const float* w, const float* b, void* state_inout, void* y, int N, int C,
+                                int K, int ldx, int dtype, int flags, void* stream);
+
+/* Selective scan, for every channel c with its N states n:
+ *
+ *   d_t = softplus(dt_t + dt_bias)        (CKDA_SCAN_SOFTPLUS; else dt_t + dt_bias)
+ *   h_t[n] = exp(d_t A[n]) h_{t-1}[n] + d_t x_t B_t[n]
+ *   y_t = (sum_n C_t[n] h_t[n] + D x_t) z_t sigmoid(z_t)
+ *
+ *   x, dt  : [B, T, C] dtype
+ *   A      : [C, N] fp32, finite (negative: the states decay)
+ *   Bm, Cm : [B, T, G, N] dtype, row stride ldbc (for both): channel c uses
+ *            those of group c / (C / G)
+ *   D      : [C] fp32, or NULL for zeros
+ *   z      : [B, T, C] dtype, row stride ldz, or NULL for no gate
+ *   dt_bias: [C] fp32, or NULL for zeros
+ *   h0, hT : [B, C, N] fp32, or NULL (zero states; skip); hT may equal h0
+ *   y      : [B, T, C] dtype
+ * Supported: 1 <= N <= 64, any C of which G is a divisor.  A decay is rounded
+ * to fp32 at every step (bf16: by the hardware's exponential, 2^-23); with F32
+ * a decay near 1 is applied by its distance from 1, so that slow states do not
+ * drift.  A non-finite input of a channel leaves that channel's rows from there
+ * on unspecified (in the backward all of it, and dBm and dCm of the rows where
+ * it is summed in). */
+#define CKDA_SCAN_SOFTPLUS 1
+
+/* Bytes of device workspace ckda_selective_scan_fwd needs, or 0 for invalid or
+ * unsupported sizes.  With few channels and many rows the sequence runs in
+ * segments, whose fp32 states and sums of steps it holds; else 256. */
+size_t ckda_selective_scan_fwd_workspace_size(int B, int T, int C, int G, int N, int dtype);
+
+int ckda_selective_scan_fwd(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                            const float* D, const void* z, const float* dt_bias, const float* h0, const int* lens,
+                            void* y, float* hT, int B, int T, int C, int G, int N, int ldbc, int ldz, int dtype,
+                            int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace ckda_selective_scan_bwd needs, or 0 for invalid or
+ * unsupported sizes: the fp32 states of every 16th row, and dBm and dCm (fp32)
+ * of every 32 channels. */
+size_t ckda_selective_scan_bwd_workspace_size(int B, int T, int C, int G, int N, int dtype);
+
+/* Backward given dy [B, T, C] (dtype) and dhT [B, C, N] fp32 (or NULL for
+ * zeros): dx, ddt (with respect to dt as given), dz (with z) [B, T, C] and dBm,
+ * dCm [B, T, G, N] in dtype, contiguous; dA [C, N], dD [C], ddt_bias [C] fp32
+ * (each may be NULL to skip); dh0 [B, C, N] fp32, or NULL to skip.  Nothing of
+ * the forward is needed but its inputs.  Sums run in a fixed order.  Outputs
+ * must not overlap each other, any input or the workspace, nor the workspace an
+ * input. */
+int ckda_selective_scan_bwd(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                            const float* D, const void* z, const float* dt_bias, const float* h0, const int* lens,
+                            const void* dy, const float* dhT, void* dx, void* ddt, float* dA, void* dBm, void* dCm,
+                            float* dD, void* dz, float* ddt_bias, float* dh0, int B, int T, int C, int G, int N,
+                            int ldbc, int ldz, int dtype, int flags, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* One token of S sequences, state in place: x, dt [S, C], Bm, Cm [S, G, N] (row
+ * stride ldbc), z [S, C] (row stride ldz) or NULL, H_inout [S, C, N] fp32,
+ * y [S, C].  One read and one write of the state.  flags: CKDA_SCAN_SOFTPLUS. */
+int ckda_selective_scan_decode_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
+                                    const float* D, const void* z, const float* dt_bias, float* H_inout, void* y, int S,
+                                    int C, int G, int N, int ldbc, int ldz, int dtype, int flags, void* stream);
+
+/* Root-mean-square norm with the residual's addition, rows of width D:
+ *
+ *   r = x + res,   y = r / sqrt(mean r^2 + eps) w
+ *
+ *   x      : [R, D] dtype
+ *   res    : [R, D] res_dtype (that of x, or F32), or NULL (r = x)
+ *   w      : [D] fp32, or NULL for ones
+ *   y      : [R, D] dtype, or NULL
+ *   q, scales : y in 8 bits (e4m3, largest value 448), or NULL: each row's
+ *            columns in groups of `group` (128, the last may be short; or 0: a
+ *            whole row), scales [R, groups] fp32 = max |y| / 448 of the group
+ *            (1 where that is 0), q [R, D] the codes of y / scale, rounded to
+ *            nearest even, from the unrounded y
+ *   sum    : [R, D] res_dtype, r rounded once (y is of the unrounded r), or
+ *            NULL; may equal res exactly
+ * One of y and q at least.  1 <= D <= 8192; eps finite, > 0.  A row with a NaN
+ * or an infinity has NaN outputs where the formula gives them. */
+int ckda_add_norm_fwd(const void* x, const void* res, const float* w, void* y, void* q, float* scales, void* sum, int R,
+                      int D, int group, int dtype, int res_dtype, float eps, void* stream);
+
+/* Bytes of device workspace ckda_add_norm_bwd needs, or 0 for invalid or
+ * unsupported sizes: one fp32 row of width D for each workgroup. */
+size_t ckda_add_norm_bwd_workspace_size(int R, int D, int dtype, int res_dtype);
+
+/* Backward: from sum = r [R, D] (res_dtype), dy [R, D] (dtype) and dsum [R, D]
+ * (res_dtype, the gradient of r from everything behind; NULL for zeros) the
+ * gradient of r, which is that of x and of res:
+ *   dr = dsum + (dy w - n mean(dy w n)) / sqrt(mean r^2 + eps),  n the norm of r
+ * in dx (dtype) and dres (res_dtype), either NULL but not both; dw [D] fp32 or
+ * NULL.  dres may equal dsum exactly. */
+int ckda_add_norm_bwd(const void* sum, const float* w, const void* dy, const void* dsum, void* dx, void* dres, float* dw,
+                      int R, int D, int dtype, int res_dtype, float eps, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /* Static description of a status code. */
 const char* ckda_status_string(int status);
 
