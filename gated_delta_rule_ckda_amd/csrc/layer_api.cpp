@@ -146,15 +146,17 @@ static int scan_check(const char* fn, int B, int T, int C, int G, int N, int ldb
   if (G < 1 || C % G != 0) return fail(CKDA_ERR_DIM, "%s: G=%d does not divide C=%d", fn, G, C);
   if (N < 1 || N > 64) return fail(CKDA_ERR_UNSUPPORTED, "%s: N=%d (supported: 1 .. 64)", fn, N);
   if (!supported_dtype(dtype)) return fail(CKDA_ERR_UNSUPPORTED, "%s: dtype %d is not F32(0) or BF16(1)", fn, dtype);
-  if (C > kMostChannels) return fail(CKDA_ERR_DIM, "%s: C=%d above 2^24", fn, C);
+  if (C >= kMostChannels) return fail(CKDA_ERR_DIM, "%s: C=%d not below 2^24", fn, C);
   if ((long long)ldbc < (long long)G * N) return fail(CKDA_ERR_DIM, "%s: row stride ldbc=%d below G*N=%d", fn, ldbc, G * N);
+  if (ldbc >= kMostChannels || (gate && ldz >= kMostChannels))
+    return fail(CKDA_ERR_DIM, "%s: row strides ldbc=%d, ldz=%d must be below 2^24", fn, ldbc, ldz);
   if (gate && ldz < C) return fail(CKDA_ERR_DIM, "%s: row stride ldz=%d below C=%d", fn, ldz, C);
   return CKDA_OK;
 }
 
 // sizes whose products the host's arithmetic holds and whose launches fit
 static bool scan_planned(int B, int T, int C, int G, int N) {
-  if (T > INT32_MAX - 64 || (long long)B * C >= 1LL << 31) return false;
+  if (T > INT32_MAX - 64 || (long long)B * C >= 1LL << 31 || (long long)C * N >= 1LL << 28) return false;
   return scan_fits_grid(B, T, C, G, N);
 }
 static int scan_grid(const char* fn, int B, int T, int C, int G, int N) {
@@ -164,7 +166,7 @@ static int scan_grid(const char* fn, int B, int T, int C, int G, int N) {
 
 static bool scan_sizes_ok(int B, int T, int C, int G, int N, int dtype) {
   return B >= 0 && T >= 0 && C >= 0 && G >= 1 && C % G == 0 && N >= 1 && N <= 64 && supported_dtype(dtype) &&
-         C <= kMostChannels && scan_planned(B, T, C, G, N);
+         C < kMostChannels && scan_planned(B, T, C, G, N);
 }
 
 size_t ckda_selective_scan_fwd_workspace_size(int B, int T, int C, int G, int N, int dtype) {

@@ -46,17 +46,20 @@ constexpr int kRows = 16;       // rows of a chunk, and lanes of a channel
 constexpr int kCh = 32;         // channels of a workgroup
 constexpr int kScanThreads = kRows * kCh;
 constexpr int kWaves = kScanThreads / 64;
+// registers for two to four waves on a SIMD: rows' operands are loaded ahead, not one after the other
+#define CKDA_SCAN_WAVES __attribute__((amdgpu_waves_per_eu(2, 4)))
 constexpr int kPad = kRows + 1;   // row of a turned tile in LDS
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266174e-8f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- lanes
 
-template <int... J, typename F> __device__ __forceinline__ void each_row_impl(std::integer_sequence<int, J...>, F&& f) {
+template <int... J, typename F> __device__ __forceinline__ void each_impl(std::integer_sequence<int, J...>, F&& f) {
   (f(std::integral_constant<int, J>{}), ...);
 }
-template <typename F> __device__ __forceinline__ void each_row(F&& f) {
-  each_row_impl(std::make_integer_sequence<int, kRows>{}, f);
+template <int N, typename F> __device__ __forceinline__ void each(F&& f) {
+  each_impl(std::make_integer_sequence<int, N>{}, f);
 }
+template <typename F> __device__ __forceinline__ void each_row(F&& f) { each<kRows>(f); }
 
 // lane J's value of each DPP row, in all of its 16 lanes
 template <int J> __device__ __forceinline__ float row_bcast(float x) {
@@ -214,51 +217,101 @@ __device__ __forceinline__ bool scan_place(const ScanLaunch& L, ScanPlace& p) {
   return true;
 }
 
-// B and C of a chunk in LDS: [row][s][lane] pairs
-template <typename T, int NS> struct BcTile {
-  T raw[NS];
-  __device__ __forceinline__ void fetch(const ScanLaunch& L, const ScanPlace& p, int chunk) {
+// Rows of a tensor through a buffer resource that covers the rows of one tile: a
+// thread's offset in the tile never changes, the resource moves (scalar registers),
+// and rows behind the end and columns that are none (kNowhere) read zero and are not
+// written, without a branch.
+constexpr int kNowhere = 0x7FFFFFFF;
+template <typename T> struct Rows {
+  const char* base;      // first row of the segment
+  uint32_t bytes;        // of a row
+  __device__ __forceinline__ Rows(const void* p, size_t first, int ld)
+      : base((const char*)p + first * ld * sizeof(T)), bytes((uint32_t)ld * sizeof(T)) {}
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile(int row, int rows) const {
+    row = __builtin_amdgcn_readfirstlane(row), rows = __builtin_amdgcn_readfirstlane(rows);   // (scalar registers)
+    return make_rsrc(base + (size_t)row * bytes, (uint32_t)max(rows, 0) * bytes);
+  }
+};
+template <typename T> __device__ __forceinline__ uint32_t load_raw(__amdgpu_buffer_rsrc_t r, int off) {
+  if constexpr (sizeof(T) == 2) return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+  else return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+}
+template <typename T> __device__ __forceinline__ void store_elem(__amdgpu_buffer_rsrc_t r, int off, float x) {
+  if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16((short)from_f32<bf16_t>(x).bits, r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
+}
+// A prefetched element, widened here and not where it was loaded (which would wait for it there).
+template <typename T> __device__ __forceinline__ float value_of(uint32_t raw) {
+  pin(raw);
+  return __uint_as_float(sizeof(T) == 2 ? raw << 16 : raw);
+}
+
+// B and C of SUBS chunks of rows in LDS: [row][s][lane] pairs.  Every wave moves
+// one of the two at a time.
+template <typename T, int NS, int SUBS, int THREADS> struct BcTile {
+  static constexpr int kEach = SUBS * NS * 32 * kRows / THREADS;   // elements a thread moves
+  static constexpr int kSpan = kEach > 1 ? THREADS : THREADS / 2;  // threads on one of the two
+  uint32_t raw[kEach];
+  int off[kEach];
+  // element of this thread, counted over the rows of one of the two
+  __device__ __forceinline__ static int place_of(int i) {
+    return (int)threadIdx.x % kSpan + (kEach > 1 ? i % (kEach / 2) : 0) * THREADS;
+  }
+  __device__ __forceinline__ static bool of_c(int i) {
+    return kEach > 1 ? i >= kEach / 2 : __builtin_amdgcn_readfirstlane((int)threadIdx.x) >= kSpan;
+  }
+  __device__ __forceinline__ void place(const ScanLaunch& L, const ScanPlace& p) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int idx = (int)threadIdx.x + i * kScanThreads, n = idx % (16 * NS), which = idx / (16 * NS) % 2;
-      const int t = chunk * kRows + idx / (32 * NS);
-      raw[i] = from_f32<T>(0.f);
-      if (t < p.len && n < L.G.N) {
-        const T* src = which ? (const T*)L.a.Cm : (const T*)L.a.Bm;
-        raw[i] = src[((size_t)p.b * L.G.T + t) * L.G.ldbc + p.g * L.G.N + n];
-      }
+    for (int i = 0; i < kEach; ++i) {
+      const int idx = place_of(i), n = idx % (16 * NS);
+      off[i] = n < L.G.N ? (idx / (16 * NS) * L.G.ldbc + p.g * L.G.N + n) * (int)sizeof(T) : kNowhere;
+    }
+  }
+  __device__ __forceinline__ void fetch(const Rows<T>& B, const Rows<T>& C, int row, int rows) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      Rows<T> src = B;
+      if (of_c(i)) src.base = C.base;
+      raw[i] = load_raw<T>(src.tile(row, rows), off[i]);
     }
   }
   __device__ __forceinline__ void stage(float* s) const {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int idx = (int)threadIdx.x + i * kScanThreads, n = idx % (16 * NS), which = idx / (16 * NS) % 2;
-      const int row = idx / (32 * NS);
-      s[((row * NS + n / 16) * 16 + n % 16) * 2 + which] = to_f32(raw[i]);
+    for (int i = 0; i < kEach; ++i) {
+      const int idx = place_of(i), n = idx % (16 * NS), row = idx / (16 * NS);
+      s[((row * NS + n / 16) * 16 + n % 16) * 2 + (of_c(i) ? 1 : 0)] = value_of<T>(raw[i]);
     }
   }
 };
+
+// block K of a tile's B and C: 16 / NS rows of NS states
+template <int NS, int K> __device__ __forceinline__ void load_rows(float2 (&f)[kRows], const float2* rows) {
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) f[i] = rows[(K * kRows + i) * 16];
+}
 
 // ---------------------------------------------------------------- forward
 
 // MAIN: outputs (and the last state) from the segments' start states.  Else: the
 // segments' own end states and sums of steps, with MARK the states before each
-// chunk on the way.
-template <typename T, int NS, bool MAIN, bool MARK>
-__global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanLaunch L) {
+// chunk on the way.  Two chunks of rows between barriers.
+template <typename T, int NS, int CH, bool MAIN, bool MARK>
+__global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(const ScanLaunch L) {
   constexpr bool EXACT = sizeof(T) == 4;
-  __shared__ float2 s_d[2][kCh][kPad];
-  __shared__ float s_y[MAIN ? 2 : 1][MAIN ? kCh : 1][kPad];
-  __shared__ __attribute__((aligned(16))) float s_bc[2][kRows * NS * 16 * 2];
+  constexpr int SUBS = 2, TILE = SUBS * kRows;
+  __shared__ float2 s_d[2][SUBS][CH][kPad];
+  __shared__ float s_y[MAIN ? 2 : 1][MAIN ? SUBS : 1][MAIN ? CH : 1][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][TILE * NS * 16 * 2];
   const SelScanArgs& a = L.a;
   const ScanGeom& G = L.G;
   ScanPlace p;
   if (!scan_place(L, p)) return;
   const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;   // state and channel in the recurrence
-  const int r = tid >> 5, ch = tid & 31;                         // row and channel of the tiles
-  const int c0 = p.cb * kCh, first_c = p.g * G.Cg + c0;
+  const int r = tid / CH, ch = tid % CH;                         // row and channel of the tiles
+  const int c0 = p.cb * CH, first_c = p.g * G.Cg + c0;
   const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
   const int cm = first_c + mine, ct = first_c + ch;
+  const int row0 = p.ch0 * kRows, end = min(p.ch1 * kRows, p.len);   // rows of the segment
 
   float A2[NS], h[NS];
 #pragma unroll
@@ -275,71 +328,100 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanLaunch
   const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
   const float Dc = MAIN && tile_on && a.D ? a.D[ct] : 0.f;
 
-  T xr = from_f32<T>(0.f), dr = xr, zr = xr;
-  BcTile<T, NS> bc;
-  bool live = false;
-  auto fetch = [&](int chunk) {
-    const int t = chunk * kRows + r;
-    live = tile_on && t < p.len;
-    if (live) {
-      const size_t at = ((size_t)p.b * G.T + t);
-      xr = ((const T*)a.x)[at * G.C + ct];
-      dr = ((const T*)a.dt)[at * G.C + ct];
-      if (MAIN && a.z) zr = ((const T*)a.z)[at * G.ldz + ct];
+  // this thread's rows of the tiles: row r, and every 16th from there
+  const size_t first = (size_t)p.b * G.T + row0;
+  const Rows<T> xs(a.x, first, G.C), ds(a.dt, first, G.C), ys(a.y, first, G.C), zs(a.z, first, G.ldz);
+  const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
+  int off[SUBS], zoff[SUBS];
+#pragma unroll
+  for (int i = 0; i < SUBS; ++i) {
+    off[i] = tile_on ? ((i * kRows + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
+    zoff[i] = tile_on ? ((i * kRows + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
+  }
+  uint32_t xr[SUBS], dr[SUBS], zr[SUBS] = {};
+  BcTile<T, NS, SUBS, kRows * CH> bc;
+  bc.place(L, p);
+  // Rows behind the segment read zero; no branch around the loads (values that meet behind one are copied there,
+  // and the copies wait for the loads).
+  auto fetch = [&](int t0) {
+    const int rows = min(end - t0, TILE), row = t0 - row0;
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      xr[i] = load_raw<T>(xs.tile(row, rows), off[i]);
+      dr[i] = load_raw<T>(ds.tile(row, rows), off[i]);
+      if (MAIN) zr[i] = load_raw<T>(zs.tile(row, a.z ? rows : 0), zoff[i]);
     }
-    bc.fetch(L, p, chunk);
+    bc.fetch(Bs, Cs, row, rows);
   };
-  auto stage = [&](int buf) {
-    float d = 0.f, x = 0.f;
-    if (live) {
-      x = to_f32(xr);
-      d = to_f32(dr) + bias;
+  auto stage = [&](int buf, int t0) {
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      float d = value_of<T>(dr[i]) + bias;
       if (G.softplus) d = softplus(d);
+      d = tile_on && t0 + i * kRows + r < end ? d : 0.f;   // a step of zero leaves the state
+      s_d[buf][i][ch][r] = float2{d, d * value_of<T>(xr[i])};
     }
-    s_d[buf][ch][r] = float2{d, d * x};
     bc.stage(s_bc[buf]);
   };
 
   float steps = 0.f;
-  if (p.ch0 < p.ch1) {
-    fetch(p.ch0);
-    stage(0);
+  if (row0 < end) {
+    fetch(row0);
+    stage(0, row0);
     __syncthreads();
   }
-  for (int k = p.ch0; k < p.ch1; ++k) {
-    const int buf = (k - p.ch0) & 1;
-    const float xk = to_f32(xr), zk = to_f32(zr);
-    const bool live_k = live;
-    if (k + 1 < p.ch1) fetch(k + 1);
-    const float2 d = s_d[buf][mine][n];
-    if constexpr (MARK) {
-      if (on) {
+  int buf = 0;
+  for (int t0 = row0; t0 < end; t0 += TILE, buf ^= 1) {
+    uint32_t xk[SUBS], zk[SUBS];
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if (n + 16 * s < G.N) L.w.marks[(((size_t)p.b * G.chunks + k) * G.C + cm) * G.N + n + 16 * s] = h[s];
-        if (G.nseg > 1 && n == 0) L.w.mark_steps[((size_t)p.b * G.chunks + k) * G.C + cm] = steps;
-      }
-    }
-    if constexpr (!MAIN) steps += group_sum<16>(d.x);
+    for (int i = 0; i < SUBS; ++i) xk[i] = xr[i], zk[i] = zr[i];
+    const bool more = t0 + TILE < end;
+    fetch(t0 + TILE);
+    // B and C of a block of rows are loaded while the block before is worked on
+    const float2* rows = reinterpret_cast<const float2*>(s_bc[buf]) + n;
+    float2 d[SUBS], f[2][kRows];
+    load_rows<NS, 0>(f[0], rows);
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) d[i] = s_d[buf][i][mine][n];
     float sums[kRows];
-    each_row([&](auto J) {
-      constexpr int j = J;
-      const float2* row = reinterpret_cast<const float2*>(s_bc[buf]) + j * NS * 16 + n;
+    each<SUBS * NS>([&](auto K) {
+      constexpr int k = K, i = k / NS, b = k % NS;   // block, its chunk and its place there
+      if constexpr (k + 1 < SUBS * NS) load_rows<NS, k + 1>(f[(k + 1) % 2], rows);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (b == 0) {
+        if constexpr (MARK) {
+          const int chunk = t0 / kRows + i;
+          if (on && chunk < p.ch1) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const float2 f = row[s * 16];
-        h[s] = Decay<EXACT>(row_bcast<j>(d.x) * A2[s]).of(h[s], row_bcast<j>(d.y) * f.x);
-        if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(f.y, h[s], sums[j]) : f.y * h[s];
+            for (int s = 0; s < NS; ++s)
+              if (n + 16 * s < G.N) L.w.marks[(((size_t)p.b * G.chunks + chunk) * G.C + cm) * G.N + n + 16 * s] = h[s];
+            if (G.nseg > 1 && n == 0) L.w.mark_steps[((size_t)p.b * G.chunks + chunk) * G.C + cm] = steps;
+          }
+        }
+        if constexpr (!MAIN) steps += group_sum<16>(d[i].x);
       }
+      each<kRows / NS>([&](auto J) {
+        constexpr int j = b * (kRows / NS) + J;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const float2 bc = f[k % 2][J * NS + s];
+          h[s] = Decay<EXACT>(row_bcast<j>(d[i].x) * A2[s]).of(h[s], row_bcast<j>(d[i].y) * bc.x);
+          if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(bc.y, h[s], sums[j]) : bc.y * h[s];
+        }
+      });
+      if constexpr (MAIN && b == NS - 1) s_y[buf][i][mine][n] = turn_sums(sums, n);
     });
-    if constexpr (MAIN) s_y[buf][mine][n] = turn_sums(sums, n);
-    if (k + 1 < p.ch1) stage(buf ^ 1);
+    if (more) stage(buf ^ 1, t0 + TILE);
     lds_barrier();
     if constexpr (MAIN) {
-      if (live_k) {
-        float y = __builtin_fmaf(Dc, xk, s_y[buf][ch][r]);
-        if (a.z) y *= zk * row_sigmoid<T>(zk);
-        ((T*)a.y)[((size_t)p.b * G.T + k * kRows + r) * G.C + ct] = from_f32<T>(y);
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i) {
+        float y = __builtin_fmaf(Dc, value_of<T>(xk[i]), s_y[buf][i][ch][r]);
+        if (a.z) {
+          const float z = value_of<T>(zk[i]);
+          y *= z * row_sigmoid<T>(z);
+        }
+        store_elem<T>(ys.tile(t0 - row0, min(end - t0, TILE)), off[i], y);
       }
     }
   }
@@ -351,8 +433,7 @@ __global__ __launch_bounds__(kScanThreads) void scan_fwd_kernel(const ScanLaunch
     }
     if (G.pad_zero && tile_on) {
       const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
-      for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += kRows)
-        ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
+      for (int t = max(p.len, row0) + r; t < to; t += kRows) ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
     }
   } else if (on && G.nseg > 1) {
 #pragma unroll
@@ -429,37 +510,37 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
   float dD = 0.f, dbias = 0.f;
 
   const T zero = from_f32<T>(0.f);
-  T xr = zero, dr = zero, zr = zero, gr = zero;
-  float mark[NS], mark_steps = 0.f;
-  BcTile<T, NS> bc;
-  bool live = false;
-  auto fetch = [&](int chunk) {
-    const int t = chunk * kRows + r;
-    live = tile_on && t < p.len;
-    if (live) {
-      const size_t at = ((size_t)p.b * G.T + t);
-      if (MAIN) xr = ((const T*)a.x)[at * G.C + ct];
-      dr = ((const T*)a.dt)[at * G.C + ct];
-      gr = ((const T*)a.dy)[at * G.C + ct];
-      if (a.z) zr = ((const T*)a.z)[at * G.ldz + ct];
-    }
-    bc.fetch(L, p, chunk);
+  const size_t first = (size_t)p.b * G.T;
+  const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
+  const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
+  const Rows<T> dxs(a.dx, first, G.C), ddts(a.ddt, first, G.C), dzs(a.dz, first, G.C);
+  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * G.N);
+  const Rows<float> mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  const int off = tile_on ? (r * G.C + ct) * (int)sizeof(T) : kNowhere;
+  const int zoff = tile_on ? (r * G.ldz + ct) * (int)sizeof(T) : kNowhere;
+  uint32_t xr = 0, dr = 0, zr = 0, gr = 0, mark[NS];
+  uint32_t mark_steps = 0;
+  BcTile<T, NS, 1, kScanThreads> bc;
+  bc.place(L, p);
+  auto fetch = [&](int chunk) {   // (before the segment's first chunk: nothing; no branch around the loads)
+    const int row = chunk * kRows, rows = chunk >= p.ch0 ? min(p.len - row, kRows) : 0;
+    if (MAIN) xr = load_raw<T>(xs.tile(row, rows), off);
+    dr = load_raw<T>(dts.tile(row, rows), off);
+    gr = load_raw<T>(dys.tile(row, rows), off);
+    zr = load_raw<T>(zs.tile(row, a.z ? rows : 0), zoff);
+    bc.fetch(Bs, Cs, row, rows);
     if constexpr (MAIN) {
-      const size_t at = ((size_t)p.b * G.chunks + chunk) * G.C + cm;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) mark[s] = state[s] ? L.w.marks[at * G.N + n + 16 * s] : 0.f;
-      if (p.seg > 0 && on) mark_steps = L.w.mark_steps[at];
+      for (int s = 0; s < NS; ++s)
+        mark[s] = load_raw<float>(marks.tile(chunk, rows > 0), state[s] ? (cm * G.N + n + 16 * s) * 4 : kNowhere);
+      mark_steps = load_raw<float>(mark_sums.tile(chunk, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
     }
   };
   if (p.ch0 < p.ch1) fetch(p.ch1 - 1);
   for (int k = p.ch1 - 1; k >= p.ch0; --k) {
-    float x = 0.f, raw = 0.f, d = 0.f, z = 0.f, dy = 0.f, ds = 0.f;
-    const bool live_k = live;
-    if (live) {
-      x = to_f32(xr), raw = to_f32(dr) + bias, dy = to_f32(gr), z = to_f32(zr);
-      d = G.softplus ? softplus(raw) : raw;
-      ds = a.z ? dy * z * row_sigmoid<T>(z) : dy;
-    }
+    const float x = value_of<T>(xr), raw = value_of<T>(dr) + bias, z = value_of<T>(zr), dy = value_of<T>(gr);
+    const float step = G.softplus ? softplus(raw) : raw, ds = a.z ? dy * z * row_sigmoid<T>(z) : dy;
+    const float d = tile_on && k * kRows + r < p.len ? step : 0.f;   // (dy, and so ds, is zero there)
     s_d[ch][r] = float2{d, d * x};
     s_ds[ch][r] = ds;
     bc.stage(s_bc);
@@ -467,10 +548,13 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
     if constexpr (MAIN) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        hc[s] = p.seg > 0 ? mark[s] + Decay<EXACT>(mark_steps * A2[s]).of(start[s]) : mark[s];
+        {
+        hc[s] = value_of<float>(mark[s]);
+        if (p.seg > 0) hc[s] += Decay<EXACT>(value_of<float>(mark_steps) * A2[s]).of(start[s]);
+      }
     }
     lds_barrier();
-    if (k > p.ch0) fetch(k - 1);
+    fetch(k - 1);
     const float2 dd = s_d[mine][n];
     const float dsm = s_ds[mine][n];
     const float2* rows = reinterpret_cast<const float2*>(s_bc) + n;
@@ -523,18 +607,18 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
       s_out[1][mine][n] = turn_sums(u, n);
       s_out[2][mine][n] = turn_sums(v, n);
       lds_barrier();
-      if (live_k) {
-        const size_t at = ((size_t)p.b * G.T + k * kRows + r) * G.C + ct;
+      {
+        const int row = k * kRows, rows = min(p.len - row, kRows);
         const float uu = s_out[1][ch][r], dd_ = __builtin_fmaf(x, uu, s_out[2][ch][r]);
         const float ddt = G.softplus ? dd_ * softplus_slope(raw) : dd_;
-        ((T*)a.dx)[at] = from_f32<T>(__builtin_fmaf(d, uu, Dc * ds));
-        ((T*)a.ddt)[at] = from_f32<T>(ddt);
+        store_elem<T>(dxs.tile(row, rows), off, __builtin_fmaf(d, uu, Dc * ds));
+        store_elem<T>(ddts.tile(row, rows), off, ddt);
         if (a.z) {
           const float pre = __builtin_fmaf(Dc, x, s_out[0][ch][r]);
-          ((T*)a.dz)[at] = from_f32<T>(dy * pre * silu_slope(z, row_sigmoid<T>(z)));
+          store_elem<T>(dzs.tile(row, rows), off, dy * pre * silu_slope(z, row_sigmoid<T>(z)));
         }
         dD = __builtin_fmaf(ds, x, dD);
-        dbias += ddt;
+        dbias += k * kRows + r < p.len ? ddt : 0.f;
       }
       // dC and dB of the workgroup's channels: place 64 (j / 2 NS + s) + lane of a wave's parts holds row j (odd
       // DPP rows: j + 1) of state n + 16 s, dC in the lower half of the wave and dB in the upper one
@@ -732,17 +816,22 @@ template <bool BACK> hipError_t launch_join(const ScanLaunch& L) {
   return hipGetLastError();
 }
 
+#ifndef FCH
+#define FCH 16
+#endif
+constexpr int kFwdCh = FCH;
 template <typename T, int NS> hipError_t launch_fwd_t(const SelScanArgs& a) {
   ScanLaunch L = scan_launch(a, false);
+  L.G.cblocks = (L.G.Cg + kFwdCh - 1) / kFwdCh;
   if (L.G.nseg > 1) {
     L.segs = L.G.nseg - 1;
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, false, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, false, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = launch_join<false>(L);
     if (e != hipSuccess) return e;
     L.segs = L.G.nseg;
   }
-  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, true, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, true, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
   return hipGetLastError();
 }
 
@@ -750,7 +839,7 @@ template <typename T, int NS> hipError_t launch_bwd_t(const SelScanArgs& a) {
   ScanLaunch L = scan_launch(a, true);
   hipError_t e = hipSuccess;
   if (L.G.B > 0) {
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, false, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (L.G.nseg > 1) {
       if ((e = launch_join<false>(L)) != hipSuccess) return e;
