@@ -59,7 +59,6 @@ template <int... J, typename F> __device__ __forceinline__ void each_impl(std::i
 template <int N, typename F> __device__ __forceinline__ void each(F&& f) {
   each_impl(std::make_integer_sequence<int, N>{}, f);
 }
-template <typename F> __device__ __forceinline__ void each_row(F&& f) { each<kRows>(f); }
 
 // lane J's value of each DPP row, in all of its 16 lanes
 template <int J> __device__ __forceinline__ float row_bcast(float x) {
@@ -99,6 +98,8 @@ __device__ __forceinline__ float turn_sums(const float (&v)[kRows], int lane) {
   return (one ? c1 : c0) + dpp_mov<0xB1>(one ? c0 : c1);                     // quad_perm [1,0,3,2]
 }
 #undef CKDA_PAIR
+
+__device__ __forceinline__ void pin_float(float& x) { asm volatile("" : "+v"(x)); }
 
 // lower half of the wave: a summed over the halves; upper half: b
 __device__ __forceinline__ float sum_halves(float a, float b) {
@@ -246,30 +247,32 @@ template <typename T> __device__ __forceinline__ float value_of(uint32_t raw) {
   return __uint_as_float(sizeof(T) == 2 ? raw << 16 : raw);
 }
 
-// B and C of SUBS chunks of rows in LDS: [row][s][lane] pairs.  Every wave moves
-// one of the two at a time.
-template <typename T, int NS, int SUBS, int THREADS> struct BcTile {
-  static constexpr int kEach = SUBS * NS * 32 * kRows / THREADS;   // elements a thread moves
-  static constexpr int kSpan = kEach > 1 ? THREADS : THREADS / 2;  // threads on one of the two
-  uint32_t raw[kEach];
-  int off[kEach];
-  // element of this thread, counted over the rows of one of the two
-  __device__ __forceinline__ static int place_of(int i) {
-    return (int)threadIdx.x % kSpan + (kEach > 1 ? i % (kEach / 2) : 0) * THREADS;
-  }
+// B and C (either alone: WHICH 1 or 2, both: 3) of SUBS chunks of rows in LDS, each
+// as [row / 4][s][lane][row % 4], so that a lane reads four rows at once.  Every wave
+// moves one of the two at a time.
+template <typename T, int NS, int SUBS, int THREADS, int WHICH> struct BcTile {
+  static constexpr int kOne = SUBS * kRows * 16 * NS;                  // elements of one of the two
+  static constexpr int kEach = (WHICH == 3 ? 2 : 1) * kOne / THREADS;  // elements a thread moves
+  static constexpr int kSpan = kOne < THREADS ? kOne : THREADS;        // threads on one of the two
+  static constexpr int kLoads = kEach > 0 ? kEach : 1;
+  uint32_t raw[kLoads];
+  int off[kLoads];
+  __device__ __forceinline__ static int place_of(int i) { return (int)threadIdx.x % kSpan + i % (kOne / kSpan) * kSpan; }
   __device__ __forceinline__ static bool of_c(int i) {
-    return kEach > 1 ? i >= kEach / 2 : __builtin_amdgcn_readfirstlane((int)threadIdx.x) >= kSpan;
+    if (WHICH != 3) return WHICH == 2;
+    return kSpan < THREADS ? __builtin_amdgcn_readfirstlane((int)threadIdx.x) >= kSpan : i >= kOne / kSpan;
   }
+  __device__ __forceinline__ static bool idle() { return WHICH != 3 && kSpan < THREADS && (int)threadIdx.x >= kSpan; }
   __device__ __forceinline__ void place(const ScanLaunch& L, const ScanPlace& p) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const int idx = place_of(i), n = idx % (16 * NS);
-      off[i] = n < L.G.N ? (idx / (16 * NS) * L.G.ldbc + p.g * L.G.N + n) * (int)sizeof(T) : kNowhere;
+      off[i] = n < L.G.N && !idle() ? (idx / (16 * NS) * L.G.ldbc + p.g * L.G.N + n) * (int)sizeof(T) : kNowhere;
     }
   }
   __device__ __forceinline__ void fetch(const Rows<T>& B, const Rows<T>& C, int row, int rows) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       Rows<T> src = B;
       if (of_c(i)) src.base = C.base;
       raw[i] = load_raw<T>(src.tile(row, rows), off[i]);
@@ -277,31 +280,38 @@ template <typename T, int NS, int SUBS, int THREADS> struct BcTile {
   }
   __device__ __forceinline__ void stage(float* s) const {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < kLoads; ++i) {
       const int idx = place_of(i), n = idx % (16 * NS), row = idx / (16 * NS);
-      s[((row * NS + n / 16) * 16 + n % 16) * 2 + (of_c(i) ? 1 : 0)] = value_of<T>(raw[i]);
+      if (!idle()) s[(of_c(i) && WHICH == 3 ? kOne : 0) + ((row / 4 * NS + n / 16) * 16 + n % 16) * 4 + row % 4] = value_of<T>(raw[i]);
     }
   }
 };
 
-// block K of a tile's B and C: 16 / NS rows of NS states
-template <int NS, int K> __device__ __forceinline__ void load_rows(float2 (&f)[kRows], const float2* rows) {
+// Block K of a tile's B or C: 16 / NS rows of NS states, f[row * NS + s].
+template <int NS, int K> __device__ __forceinline__ void load_block(float (&f)[kRows], const float* one) {
+  const f32x4* p = reinterpret_cast<const f32x4*>(one) + K * (4 / NS) * NS * 16 + (threadIdx.x & 15);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) f[i] = rows[(K * kRows + i) * 16];
+  for (int q = 0; q < 4 / NS; ++q)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const f32x4 v = p[(q * NS + s) * 16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[(4 * q + i) * NS + s] = v[i];
+    }
 }
 
 // ---------------------------------------------------------------- forward
 
 // MAIN: outputs (and the last state) from the segments' start states.  Else: the
 // segments' own end states and sums of steps, with MARK the states before each
-// chunk on the way.  Two chunks of rows between barriers.
-template <typename T, int NS, int CH, bool MAIN, bool MARK>
+// chunk on the way (SEGS: of several segments).  Two chunks of rows between barriers.
+template <typename T, int NS, int CH, bool MAIN, bool MARK, bool SEGS>
 __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(const ScanLaunch L) {
   constexpr bool EXACT = sizeof(T) == 4;
   constexpr int SUBS = 2, TILE = SUBS * kRows;
   __shared__ float2 s_d[2][SUBS][CH][kPad];
   __shared__ float s_y[MAIN ? 2 : 1][MAIN ? SUBS : 1][MAIN ? CH : 1][kPad];
-  __shared__ __attribute__((aligned(16))) float s_bc[2][TILE * NS * 16 * 2];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][TILE * NS * 16 * (MAIN ? 2 : 1)];
   const SelScanArgs& a = L.a;
   const ScanGeom& G = L.G;
   ScanPlace p;
@@ -339,7 +349,7 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
     zoff[i] = tile_on ? ((i * kRows + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
   }
   uint32_t xr[SUBS], dr[SUBS], zr[SUBS] = {};
-  BcTile<T, NS, SUBS, kRows * CH> bc;
+  BcTile<T, NS, SUBS, kRows * CH, MAIN ? 3 : 1> bc;
   bc.place(L, p);
   // Rows behind the segment read zero; no branch around the loads (values that meet behind one are copied there,
   // and the copies wait for the loads).
@@ -364,6 +374,11 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
     bc.stage(s_bc[buf]);
   };
 
+  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * G.N), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  int moff[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) moff[s] = on && n + 16 * s < G.N ? (cm * G.N + n + 16 * s) * 4 : kNowhere;
+
   float steps = 0.f;
   if (row0 < end) {
     fetch(row0);
@@ -378,35 +393,36 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
     const bool more = t0 + TILE < end;
     fetch(t0 + TILE);
     // B and C of a block of rows are loaded while the block before is worked on
-    const float2* rows = reinterpret_cast<const float2*>(s_bc[buf]) + n;
-    float2 d[SUBS], f[2][kRows];
-    load_rows<NS, 0>(f[0], rows);
+    const float* one = s_bc[buf];
+    float2 d[SUBS];
+    float Bv[2][kRows], Cv[2][kRows];
+    load_block<NS, 0>(Bv[0], one);
+    if constexpr (MAIN) load_block<NS, 0>(Cv[0], one + TILE * NS * 16);
 #pragma unroll
     for (int i = 0; i < SUBS; ++i) d[i] = s_d[buf][i][mine][n];
     float sums[kRows];
     each<SUBS * NS>([&](auto K) {
       constexpr int k = K, i = k / NS, b = k % NS;   // block, its chunk and its place there
-      if constexpr (k + 1 < SUBS * NS) load_rows<NS, k + 1>(f[(k + 1) % 2], rows);
+      if constexpr (k + 1 < SUBS * NS) {
+        load_block<NS, k + 1>(Bv[(k + 1) % 2], one);
+        if constexpr (MAIN) load_block<NS, k + 1>(Cv[(k + 1) % 2], one + TILE * NS * 16);
+      }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (b == 0) {
         if constexpr (MARK) {
           const int chunk = t0 / kRows + i;
-          if (on && chunk < p.ch1) {
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-              if (n + 16 * s < G.N) L.w.marks[(((size_t)p.b * G.chunks + chunk) * G.C + cm) * G.N + n + 16 * s] = h[s];
-            if (G.nseg > 1 && n == 0) L.w.mark_steps[((size_t)p.b * G.chunks + chunk) * G.C + cm] = steps;
-          }
+          for (int s = 0; s < NS; ++s) store_elem<float>(marks.tile(chunk, chunk < p.ch1), moff[s], h[s]);
+          if constexpr (SEGS) store_elem<float>(mark_sums.tile(chunk, chunk < p.ch1), on && n == 0 ? cm * 4 : kNowhere, steps);
         }
-        if constexpr (!MAIN) steps += group_sum<16>(d[i].x);
+        if constexpr (SEGS) steps += group_sum<16>(d[i].x);
       }
       each<kRows / NS>([&](auto J) {
         constexpr int j = b * (kRows / NS) + J;
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          const float2 bc = f[k % 2][J * NS + s];
-          h[s] = Decay<EXACT>(row_bcast<j>(d[i].x) * A2[s]).of(h[s], row_bcast<j>(d[i].y) * bc.x);
-          if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(bc.y, h[s], sums[j]) : bc.y * h[s];
+          h[s] = Decay<EXACT>(row_bcast<j>(d[i].x) * A2[s]).of(h[s], row_bcast<j>(d[i].y) * Bv[k % 2][J * NS + s]);
+          if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(Cv[k % 2][J * NS + s], h[s], sums[j]) : Cv[k % 2][J * NS] * h[s];
         }
       });
       if constexpr (MAIN && b == NS - 1) s_y[buf][i][mine][n] = turn_sums(sums, n);
@@ -435,7 +451,7 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
       const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
       for (int t = max(p.len, row0) + r; t < to; t += kRows) ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
     }
-  } else if (on && G.nseg > 1) {
+  } else if (SEGS && on) {
 #pragma unroll
     for (int s = 0; s < NS; ++s)
       if (n + 16 * s < G.N) L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * G.N + n + 16 * s] = h[s];
@@ -470,21 +486,23 @@ template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_joi
 
 // MAIN: gradients.  Else: the segments' own states backward in time (the gradient
 // of the state before a segment, from its rows alone).
-template <typename T, int NS, bool MAIN>
-__global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch L) {
+template <typename T, int NS, bool MAIN, bool GATE>
+__global__ __launch_bounds__(kScanThreads) CKDA_SCAN_WAVES void scan_bwd_kernel(const ScanLaunch L) {
   constexpr bool EXACT = sizeof(T) == 4;
-  __shared__ float2 s_d[kCh][kPad];
-  __shared__ float s_ds[kCh][kPad];
-  __shared__ float s_out[MAIN ? 3 : 1][MAIN ? kCh : 1][kPad];
-  __shared__ __attribute__((aligned(16))) float s_bc[kRows * NS * 16 * 2];
-  __shared__ float s_part[MAIN ? kWaves : 1][MAIN ? kRows / 2 * NS * 64 : 1];
+  constexpr int kPartBufs = NS <= 2 ? 2 : 1;   // (two do not fit with 64 states)
+  constexpr int kPart = kRows / 2 * NS * 64;   // a wave's dC and dB of a chunk: [row / 2][s][lane]
+  __shared__ float2 s_d[2][kCh][kPad];
+  __shared__ float s_ds[2][kCh][kPad];
+  __shared__ float s_out[MAIN ? 2 : 1][3][MAIN ? kCh : 1][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][kRows * NS * 16 * (MAIN ? 2 : 1)];
+  __shared__ __attribute__((aligned(16))) float s_part[MAIN ? kPartBufs : 1][MAIN ? kWaves : 1][MAIN ? kPart : 1];
   const SelScanArgs& a = L.a;
   const ScanGeom& G = L.G;
   ScanPlace p;
   if (!scan_place(L, p)) return;
   if (!MAIN) p.seg += 1, p.ch0 += G.seg_chunks, p.ch1 = min(p.ch0 + G.seg_chunks, (p.len + kRows - 1) / kRows);
   const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;
-  const int r = tid >> 5, ch = tid & 31;
+  const int r = tid / kCh, ch = tid % kCh;
   const int c0 = p.cb * kCh, first_c = p.g * G.Cg + c0;
   const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
   const int cm = first_c + mine, ct = first_c + ch;
@@ -509,7 +527,6 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
   const float Dc = tile_on && a.D ? a.D[ct] : 0.f;
   float dD = 0.f, dbias = 0.f;
 
-  const T zero = from_f32<T>(0.f);
   const size_t first = (size_t)p.b * G.T;
   const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
   const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
@@ -518,16 +535,15 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
   const Rows<float> mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
   const int off = tile_on ? (r * G.C + ct) * (int)sizeof(T) : kNowhere;
   const int zoff = tile_on ? (r * G.ldz + ct) * (int)sizeof(T) : kNowhere;
-  uint32_t xr = 0, dr = 0, zr = 0, gr = 0, mark[NS];
-  uint32_t mark_steps = 0;
-  BcTile<T, NS, 1, kScanThreads> bc;
+  uint32_t xr = 0, dr = 0, zr = 0, gr = 0, mark[NS], mark_steps = 0;
+  BcTile<T, NS, 1, kScanThreads, MAIN ? 3 : 2> bc;
   bc.place(L, p);
   auto fetch = [&](int chunk) {   // (before the segment's first chunk: nothing; no branch around the loads)
     const int row = chunk * kRows, rows = chunk >= p.ch0 ? min(p.len - row, kRows) : 0;
-    if (MAIN) xr = load_raw<T>(xs.tile(row, rows), off);
+    xr = load_raw<T>(xs.tile(row, MAIN ? rows : 0), off);
     dr = load_raw<T>(dts.tile(row, rows), off);
     gr = load_raw<T>(dys.tile(row, rows), off);
-    zr = load_raw<T>(zs.tile(row, a.z ? rows : 0), zoff);
+    zr = load_raw<T>(zs.tile(row, GATE ? rows : 0), zoff);
     bc.fetch(Bs, Cs, row, rows);
     if constexpr (MAIN) {
 #pragma unroll
@@ -536,104 +552,132 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
       mark_steps = load_raw<float>(mark_sums.tile(chunk, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
     }
   };
-  if (p.ch0 < p.ch1) fetch(p.ch1 - 1);
-  for (int k = p.ch1 - 1; k >= p.ch0; --k) {
-    const float x = value_of<T>(xr), raw = value_of<T>(dr) + bias, z = value_of<T>(zr), dy = value_of<T>(gr);
-    const float step = G.softplus ? softplus(raw) : raw, ds = a.z ? dy * z * row_sigmoid<T>(z) : dy;
-    const float d = tile_on && k * kRows + r < p.len ? step : 0.f;   // (dy, and so ds, is zero there)
-    s_d[ch][r] = float2{d, d * x};
-    s_ds[ch][r] = ds;
-    bc.stage(s_bc);
+  // what the tile's thread keeps of its row and channel from one chunk's staging to its outputs
+  struct Row {
+    float x, raw, z, dy, d, ds;
+  };
+  auto stage = [&](int buf, int chunk) {
+    Row t;
+    t.x = value_of<T>(xr), t.raw = value_of<T>(dr) + bias, t.z = value_of<T>(zr), t.dy = value_of<T>(gr);
+    const float step = G.softplus ? softplus(t.raw) : t.raw;
+    t.ds = GATE ? t.dy * t.z * row_sigmoid<T>(t.z) : t.dy;
+    t.d = tile_on && chunk * kRows + r < p.len ? step : 0.f;   // (dy, and so ds, is zero there)
+    s_d[buf][ch][r] = float2{t.d, t.d * t.x};
+    s_ds[buf][ch][r] = t.ds;
+    bc.stage(s_bc[buf]);
+    return t;
+  };
+  Row row = {};
+  if (p.ch0 < p.ch1) {
+    fetch(p.ch1 - 1);
+    row = stage(0, p.ch1 - 1);
+    __syncthreads();
+  }
+  int buf = 0;
+  for (int k = p.ch1 - 1; k >= p.ch0; --k, buf ^= 1) {
+    const int row0 = k * kRows, rows = min(p.len - row0, kRows);
     float hc[NS];   // the state before the chunk
     if constexpr (MAIN) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
-        {
+      for (int s = 0; s < NS; ++s) {
         hc[s] = value_of<float>(mark[s]);
         if (p.seg > 0) hc[s] += Decay<EXACT>(value_of<float>(mark_steps) * A2[s]).of(start[s]);
       }
     }
-    lds_barrier();
     fetch(k - 1);
-    const float2 dd = s_d[mine][n];
-    const float dsm = s_ds[mine][n];
-    const float2* rows = reinterpret_cast<const float2*>(s_bc) + n;
-    Decay<EXACT> e[MAIN ? kRows : 1][NS];
+    float2 dd = s_d[buf][mine][n];
+    const float dsm = s_ds[buf][mine][n];
+    const float *Bl = s_bc[buf], *Cl = s_bc[buf] + (MAIN ? kRows * NS * 16 : 0);
+    float Bv[kRows], Cv[kRows];   // of a block of rows
     if constexpr (!MAIN) {
-      each_row([&](auto J) {
-        constexpr int j = kRows - 1 - J;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const float R = __builtin_fmaf(row_bcast<j>(dsm), rows[(j * NS + s) * 16].y, Q[s]);
-          Q[s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]).of(R);
-        }
-      });
-      lds_barrier();
-    } else {
-      float h[kRows][NS];
-      {
-        float sums[kRows];
-        each_row([&](auto J) {
-          constexpr int j = J;
+      each<NS>([&](auto K) {
+        constexpr int b = NS - 1 - K;
+        load_block<NS, b>(Cv, Cl);
+        each<kRows / NS>([&](auto J) {
+          constexpr int i = kRows / NS - 1 - J, j = b * (kRows / NS) + i;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            const float2 f = rows[(j * NS + s) * 16];
-            e[j][s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]);
-            const float before = j ? h[j ? j - 1 : 0][s] : hc[s];
-            h[j][s] = e[j][s].of(before, row_bcast<j>(dd.y) * f.x);
-            sums[j] = s ? __builtin_fmaf(f.y, h[j][s], sums[j]) : f.y * h[j][s];
+            const float R = __builtin_fmaf(row_bcast<j>(dsm), Cv[i * NS + s], Q[s]);
+            Q[s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]).of(R);
           }
         });
-        if (a.z) s_out[0][mine][n] = turn_sums(sums, n);
-      }
-      float u[kRows], v[kRows], pair[NS];
-      each_row([&](auto J) {
-        constexpr int j = kRows - 1 - J;
-        u[j] = v[j] = 0.f;
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const float2 f = rows[(j * NS + s) * 16];
-          const float R = __builtin_fmaf(row_bcast<j>(dsm), f.y, Q[s]);
-          const float both = sum_halves(row_bcast<j>(dsm) * h[j][s], row_bcast<j>(dd.y) * R);   // dC, dB
-          if constexpr (j % 2) pair[s] = both;
-          else s_part[tid >> 6][(j / 2 * NS + s) * 64 + (tid & 63)] = sum_quarters(both, pair[s]);
-          u[j] = __builtin_fmaf(R, f.x, u[j]);
-          Q[s] = e[j][s].of(R);
-          const float q = Q[s] * (j ? h[j ? j - 1 : 0][s] : hc[s]);
-          v[j] = __builtin_fmaf(q, A[s], v[j]);
-          dA[s] = __builtin_fmaf(q, row_bcast<j>(dd.x), dA[s]);
-        }
       });
-      s_out[1][mine][n] = turn_sums(u, n);
-      s_out[2][mine][n] = turn_sums(v, n);
+      stage(buf ^ 1, k - 1);
+      lds_barrier();
+    } else {
+      Decay<EXACT> e[kRows][NS];
+      float h[kRows][NS], sums[kRows];
+      each<NS>([&](auto K) {
+        constexpr int b = K;
+        load_block<NS, b>(Bv, Bl);
+        load_block<NS, b>(Cv, Cl);
+        each<kRows / NS>([&](auto J) {
+          constexpr int j = b * (kRows / NS) + J;
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            e[j][s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]);
+            h[j][s] = e[j][s].of(j ? h[j ? j - 1 : 0][s] : hc[s], row_bcast<j>(dd.y) * Bv[J * NS + s]);
+            if constexpr (GATE) sums[j] = s ? __builtin_fmaf(Cv[J * NS + s], h[j][s], sums[j]) : Cv[J * NS] * h[j][s];
+          }
+        });
+      });
+      if constexpr (GATE) s_out[buf][0][mine][n] = turn_sums(sums, n);
+      // (so that the broadcasts below are operands of their products again, not values kept from above)
+      pin_float(dd.x), pin_float(dd.y);
+      float u[kRows], v[kRows], odd[NS];
+      float* part = s_part[buf % kPartBufs][tid >> 6] + (tid & 63);
+      each<NS>([&](auto K) {
+        constexpr int b = NS - 1 - K;
+        if constexpr (NS > 1) {   // (of one block they are still there)
+          load_block<NS, b>(Bv, Bl);
+          load_block<NS, b>(Cv, Cl);
+        }
+        each<kRows / NS>([&](auto J) {
+          constexpr int i = kRows / NS - 1 - J, j = b * (kRows / NS) + i;
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const float R = __builtin_fmaf(row_bcast<j>(dsm), Cv[i * NS + s], Q[s]);
+            // dC and dB of the wave's channels: in the halves of the wave, and two rows in their halves
+            const float both = sum_halves(row_bcast<j>(dsm) * h[j][s], row_bcast<j>(dd.y) * R);
+            if constexpr (j % 2) odd[s] = both;
+            else part[(j / 2 * NS + s) * 64] = sum_quarters(both, odd[s]);
+            u[j] = s ? __builtin_fmaf(R, Bv[i * NS + s], u[j]) : R * Bv[i * NS];
+            Q[s] = e[j][s].of(R);
+            const float q = Q[s] * (j ? h[j ? j - 1 : 0][s] : hc[s]);
+            v[j] = s ? __builtin_fmaf(q, A[s], v[j]) : q * A[0];
+            dA[s] = __builtin_fmaf(q, row_bcast<j>(dd.x), dA[s]);
+          }
+        });
+      });
+      s_out[buf][1][mine][n] = turn_sums(u, n);
+      s_out[buf][2][mine][n] = turn_sums(v, n);
+      const Row next = stage(buf ^ 1, k - 1);
       lds_barrier();
       {
-        const int row = k * kRows, rows = min(p.len - row, kRows);
-        const float uu = s_out[1][ch][r], dd_ = __builtin_fmaf(x, uu, s_out[2][ch][r]);
-        const float ddt = G.softplus ? dd_ * softplus_slope(raw) : dd_;
-        store_elem<T>(dxs.tile(row, rows), off, __builtin_fmaf(d, uu, Dc * ds));
-        store_elem<T>(ddts.tile(row, rows), off, ddt);
-        if (a.z) {
-          const float pre = __builtin_fmaf(Dc, x, s_out[0][ch][r]);
-          store_elem<T>(dzs.tile(row, rows), off, dy * pre * silu_slope(z, row_sigmoid<T>(z)));
+        const float uu = s_out[buf][1][ch][r], dd_ = __builtin_fmaf(row.x, uu, s_out[buf][2][ch][r]);
+        const float ddt = G.softplus ? dd_ * softplus_slope(row.raw) : dd_;
+        store_elem<T>(dxs.tile(row0, rows), off, __builtin_fmaf(row.d, uu, Dc * row.ds));
+        store_elem<T>(ddts.tile(row0, rows), off, ddt);
+        if constexpr (GATE) {
+          const float pre = __builtin_fmaf(Dc, row.x, s_out[buf][0][ch][r]);
+          store_elem<T>(dzs.tile(row0, rows), off, row.dy * pre * silu_slope(row.z, row_sigmoid<T>(row.z)));
         }
-        dD = __builtin_fmaf(ds, x, dD);
-        dbias += k * kRows + r < p.len ? ddt : 0.f;
+        dD = __builtin_fmaf(row.ds, row.x, dD);
+        dbias += r < rows ? ddt : 0.f;
       }
-      // dC and dB of the workgroup's channels: place 64 (j / 2 NS + s) + lane of a wave's parts holds row j (odd
-      // DPP rows: j + 1) of state n + 16 s, dC in the lower half of the wave and dB in the upper one
+      // dC (lower half of a wave's lanes) and dB of the workgroup's channels; odd DPP rows hold the second of two rows
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const int e_ = tid + i * kScanThreads, lane = e_ % 64, s = e_ / 64 % NS;
-        const int t = k * kRows + e_ / (64 * NS) * 2 + (lane / 16 & 1), m = lane % 16 + 16 * s;
+        const int at = tid + i * kScanThreads, lane = at % 64, which = lane / 32;
+        const int t = at / (64 * NS) * 2 + (lane / 16 & 1), m = lane % 16 + 16 * (at / 64 % NS);
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += s_part[w][e_];
-        if (t < p.len && m < G.N)
-          L.w.bc[((((size_t)p.g * G.cblocks + p.cb) * G.B + p.b) * G.T + t) * 2 * G.N + (lane / 32) * G.N + m] = sum;
+        for (int w = 0; w < kWaves; ++w) sum += s_part[buf % kPartBufs][w][at];
+        if (t < rows && m < G.N)
+          L.w.bc[((((size_t)p.g * G.cblocks + p.cb) * G.B + p.b) * G.T + row0 + t) * 2 * G.N + which * G.N + m] = sum;
       }
-      // (the next chunk's tiles, s_d, s_ds and s_bc, are not read in this phase; s_out and s_part are written
-      // behind its first barrier)
+      row = next;
+      if constexpr (kPartBufs == 1) lds_barrier();   // the next chunk writes the same parts
     }
   }
   if constexpr (!MAIN) {
@@ -650,21 +694,22 @@ __global__ __launch_bounds__(kScanThreads) void scan_bwd_kernel(const ScanLaunch
     }
     // over the tile's rows: thread (r, ch) holds the sums of rows r, r + 16, ...
     __syncthreads();
-    s_out[0][ch][r] = dD;
-    s_out[1][ch][r] = dbias;
+    s_out[0][0][ch][r] = dD;
+    s_out[0][1][ch][r] = dbias;
     __syncthreads();
-    if (tid < 2 * kCh && c0 + (tid & 31) < G.Cg) {
+    if (tid < 2 * kCh && c0 + tid % kCh < G.Cg) {
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) sum += s_out[tid >> 5][tid & 31][i];
-      part[CN + (size_t)(tid >> 5) * G.C + first_c + (tid & 31)] = sum;
+      for (int i = 0; i < kRows; ++i) sum += s_out[0][tid / kCh][tid % kCh][i];
+      part[CN + (size_t)(tid / kCh) * G.C + first_c + tid % kCh] = sum;
     }
     if (G.pad_zero && tile_on) {
+      const T zero = from_f32<T>(0.f);
       const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
       for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += kRows) {
         const size_t at = ((size_t)p.b * G.T + t) * G.C + ct;
         ((T*)a.dx)[at] = ((T*)a.ddt)[at] = zero;
-        if (a.z) ((T*)a.dz)[at] = zero;
+        if (GATE) ((T*)a.dz)[at] = zero;
       }
     }
   }
@@ -816,40 +861,50 @@ template <bool BACK> hipError_t launch_join(const ScanLaunch& L) {
   return hipGetLastError();
 }
 
-#ifndef FCH
-#define FCH 16
-#endif
-constexpr int kFwdCh = FCH;
+// Channels of the forward's workgroups: 16 rather than the backward's 32 (which share one part of dB and dC), for
+// barriers among fewer waves (MI355X, us, 16 and 32 channels: B4 T4096 C2048 N16 233 and 243, B16 T1024 C4096 339
+// and 357, B2 T2048 C2048 N64 221 and 270; 8 channels are slower again, 237, 367 and 261).
+constexpr int kFwdCh = 16;
 template <typename T, int NS> hipError_t launch_fwd_t(const SelScanArgs& a) {
   ScanLaunch L = scan_launch(a, false);
   L.G.cblocks = (L.G.Cg + kFwdCh - 1) / kFwdCh;
   if (L.G.nseg > 1) {
     L.segs = L.G.nseg - 1;
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, false, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, false, false, true>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess) e = launch_join<false>(L);
     if (e != hipSuccess) return e;
     L.segs = L.G.nseg;
   }
-  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, true, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
+  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, true, false, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
   return hipGetLastError();
+}
+
+template <typename T, int NS, bool MAIN> void launch_bwd_kernel(const ScanLaunch& L) {
+  if (L.a.z)
+    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, MAIN, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, L.a.stream, L);
+  else
+    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, MAIN, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, L.a.stream, L);
 }
 
 template <typename T, int NS> hipError_t launch_bwd_t(const SelScanArgs& a) {
   ScanLaunch L = scan_launch(a, true);
   hipError_t e = hipSuccess;
   if (L.G.B > 0) {
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    if (L.G.nseg > 1)
+      hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    else
+      hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (L.G.nseg > 1) {
       if ((e = launch_join<false>(L)) != hipSuccess) return e;
       L.segs = L.G.nseg - 1;
-      hipLaunchKernelGGL((scan_bwd_kernel<T, NS, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+      launch_bwd_kernel<T, NS, false>(L);
       if ((e = hipGetLastError()) != hipSuccess) return e;
       if ((e = launch_join<true>(L)) != hipSuccess) return e;
       L.segs = L.G.nseg;
     }
-    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
+    launch_bwd_kernel<T, NS, true>(L);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
     if (each > 0) {
