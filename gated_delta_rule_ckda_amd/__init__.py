@@ -728,6 +728,8 @@ def _slice_of(device, name, t, shape, dtype, rows, width):
     """Row stride of t, a column slice of a contiguous tensor: of `shape`, whose
     first `rows` dimensions count rows and whose others are `width` elements next
     to each other."""
+    if t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.get_device() == device.index:
+        return width
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:

@@ -6,9 +6,10 @@
 //   dx_s = sum_j w_j g_{s+K-1-j},  dw_j = sum_t g_t x_{t-K+1+j},  db = sum_t g_t.
 //
 // HBM-bound: x is read and y written once (backward: x, dy, dx).  A thread owns
-// one 16-byte piece of channels and walks down a slab of rows with the last
+// a piece of four channels and walks down a slab of rows with the last
 // K - 1 rows (and, in the backward, the last K - 1 g) in registers, so that every
-// row is loaded once but for the K - 1 rows around a slab; LPR threads cover a
+// row is loaded once but for the K - 1 rows around a slab, and four rows' loads are
+// in flight while four are worked on; LPR threads cover a
 // row's piece of channels and the workgroup's other threads other slabs.  y (and
 // dy) is head-major, the layout of the attentions: the transposition is an
 // address.  The weights' gradients stay in registers down the slab, are summed
@@ -50,14 +51,44 @@ int conv_rows(int B, int T, int C) {
   return rows;
 }
 
-template <typename T, int VEC, int K> struct ConvTaps {
+// Weights of a thread's channels: K VEC floats next to each other (16-byte loads: one by one they would be as
+// many loads as a slab has rows).
+template <int VEC, int K> struct ConvTaps {
   float w[K][VEC], b[VEC];
   __device__ __forceinline__ void load(const float* wp, const float* bp, int c0, int left) {
+    float raw[K * VEC];
+    wp += (size_t)c0 * K;
+    if (VEC > 1 && left >= VEC) {
+#pragma unroll
+      for (int i = 0; i < K * VEC; i += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(wp + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < K * VEC) raw[i + e] = v[e];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < K * VEC; ++i) raw[i] = i < left * K ? wp[i] : 0.f;
+    }
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) w[j][e] = e < left ? wp[(size_t)(c0 + e) * K + j] : 0.f;
-      b[e] = bp && e < left ? bp[c0 + e] : 0.f;
+      for (int j = 0; j < K; ++j) w[j][e] = raw[e * K + j];
+    }
+    if (!bp) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) b[e] = 0.f;
+    } else if (VEC > 1 && left >= VEC) {
+#pragma unroll
+      for (int e = 0; e < VEC; e += 4) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(bp + c0 + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i < VEC) b[e + i] = v[i];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) b[e] = e < left ? bp[c0 + e] : 0.f;
     }
   }
 };
@@ -95,7 +126,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const T* x, cons
   const int h = c0 / G.Dh;
   T* yb = y + ((size_t)batch * G.H + h) * G.T * G.Dh + (c0 - h * G.Dh);
   if (r0 < live) {
-    ConvTaps<T, VEC, K> taps;
+    ConvTaps<VEC, K> taps;
     taps.load(w, b, c0, left);
     float win[K - 1 + kUnroll][VEC];
     {
@@ -105,15 +136,17 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const T* x, cons
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) v[i].widen(win[i]);
     }
-    for (int t = r0; t < live; t += kUnroll) {
-      RowVec<T, VEC> v[kUnroll];
+    RowVec<T, VEC> v[kUnroll];
+    // rows behind the slab: its last row once more (no branch around the loads, so that they stay in flight)
+    auto fetch = [&](int t) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        if (t + u < live) v[u].load(xb + (size_t)(t + u) * G.ldx, left);
-        else v[u].clear();
-      }
+      for (int u = 0; u < kUnroll; ++u) v[u].load(xb + (size_t)min(t + u, live - 1) * G.ldx, left);
+    };
+    fetch(r0);
+    for (int t = r0; t < live; t += kUnroll) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) v[u].widen(win[K - 1 + u]);
+      fetch(t + kUnroll);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         float o[VEC];
@@ -124,8 +157,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const T* x, cons
           for (int j = 0; j < K; ++j) a = __builtin_fmaf(taps.w[j][e], win[u + j][e], a);
           o[e] = SILU ? a * row_sigmoid<T>(a) : a;
         }
-        v[u].round(o);
-        if (t + u < live) v[u].store(yb + (size_t)(t + u) * G.Dh, left);
+        RowVec<T, VEC> q;
+        q.round(o);
+        if (t + u < live) q.store(yb + (size_t)(t + u) * G.Dh, left);
       }
 #pragma unroll
       for (int i = 0; i < K - 1; ++i)
@@ -147,7 +181,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const T* x, cons
   const int tx = threadIdx.x & (G.lpr - 1), sub = threadIdx.x / G.lpr, nsub = kConvThreads / G.lpr;
   const int cb = blockIdx.x % G.cblocks, p = blockIdx.x / G.cblocks;
   const int c0 = (cb * G.lpr + tx) * VEC, left = G.C - c0;
-  ConvTaps<T, VEC, K> taps;
+  ConvTaps<VEC, K> taps;
   taps.load(w, b, c0, left);
   float dw[K][VEC], db[VEC];
 #pragma unroll
@@ -178,23 +212,30 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const T* x, cons
       for (int e = 0; e < VEC; ++e) gw[i][e] = 0.f;
     }
     // row t makes g_t, and with it dx_{t-K+1}; of the slab's last K - 1 rows by the rows behind it
-    for (int t = r0; t < r1 + K - 1; t += kUnroll) {
-      RowVec<T, VEC> v[kUnroll], q[kUnroll];
+    RowVec<T, VEC> v[kUnroll], q[kUnroll];
+    const int last = min(len, r1 + K - 1) - 1;
+    // rows behind the last one: that one once more, masked below
+    auto fetch = [&](int t) {
+      if (last < r0) return;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        if (t + u < len && t + u < r1 + K - 1) {
-          v[u].load(xb + (size_t)(t + u) * G.ldx, left);
-          q[u].load(gb + (size_t)(t + u) * G.Dh, left);
-        } else {
-          v[u].clear();
-          q[u].clear();
-        }
+        v[u].load(xb + (size_t)min(t + u, last) * G.ldx, left);
+        q[u].load(gb + (size_t)min(t + u, last) * G.Dh, left);
       }
+    };
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u].clear(), q[u].clear();
+    fetch(r0);
+    for (int t = r0; t < r1 + K - 1; t += kUnroll) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         v[u].widen(win[K - 1 + u]);
+        q[u].widen(gw[K - 1 + u]);
+      }
+      fetch(t + kUnroll);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
         float* g = gw[K - 1 + u];
-        q[u].widen(g);
         const bool live = t + u < len && t + u < r1 + K - 1, mine = live && t + u < r1;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -269,36 +310,40 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const T* x, cons
   }
 }
 
+// A thread owns a piece of channels of `each` sequences (the weights are read once).
 template <typename T, int VEC, int K, bool SILU>
 __global__ __launch_bounds__(kConvThreads) void conv_decode_kernel(const T* x, const float* w, const float* b, T* state,
-                                                                   T* y, int N, int C, int pieces, int ldx) {
+                                                                   T* y, int N, int C, int pieces, int ldx, int each) {
   const long long i = (long long)blockIdx.x * kConvThreads + threadIdx.x;
-  const long long n = i / pieces;
-  const int c0 = (int)(i - n * pieces) * VEC, left = C - c0;
-  if (n >= N) return;
-  RowVec<T, VEC> v[K];
-  T* sb = state + (size_t)n * (K - 1) * C + c0;
-#pragma unroll
-  for (int j = 0; j < K - 1; ++j) v[j].load(sb + (size_t)j * C, left);
-  v[K - 1].load(x + (size_t)n * ldx + c0, left);
-  ConvTaps<T, VEC, K> taps;
+  const long long first = i / pieces * each;
+  const int c0 = (int)(i % pieces) * VEC, left = C - c0;
+  if (first >= N) return;
+  ConvTaps<VEC, K> taps;
   taps.load(w, b, c0, left);
+  for (int m = 0; m < each && first + m < N; ++m) {
+    const size_t n = first + m;
+    RowVec<T, VEC> v[K];
+    T* sb = state + n * (K - 1) * C + c0;
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) v[j + 1].store(sb + (size_t)j * C, left);
-  float o[VEC];
+    for (int j = 0; j < K - 1; ++j) v[j].load(sb + (size_t)j * C, left);
+    v[K - 1].load(x + n * ldx + c0, left);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = taps.b[e];
+    for (int j = 0; j < K - 1; ++j) v[j + 1].store(sb + (size_t)j * C, left);
+    float o[VEC];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    float r[VEC];
-    v[j].widen(r);
+    for (int e = 0; e < VEC; ++e) o[e] = taps.b[e];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) o[e] = __builtin_fmaf(taps.w[j][e], r[e], o[e]);
+    for (int j = 0; j < K; ++j) {
+      float r[VEC];
+      v[j].widen(r);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) o[e] = __builtin_fmaf(taps.w[j][e], r[e], o[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) o[e] = SILU ? o[e] * row_sigmoid<T>(o[e]) : o[e];
+    v[0].round(o);
+    v[0].store(y + n * C + c0, left);
   }
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) o[e] = SILU ? o[e] * row_sigmoid<T>(o[e]) : o[e];
-  v[0].round(o);
-  v[0].store(y + (size_t)n * C + c0, left);
 }
 
 ConvGeom conv_geom(const ShortConvArgs& a, int vec) {
@@ -318,52 +363,54 @@ ConvGeom conv_geom(const ShortConvArgs& a, int vec) {
 
 enum class ConvOp { fwd, bwd, decode };
 
-template <typename T, int VEC, int K, bool SILU> hipError_t launch_conv_t(const ShortConvArgs& a, ConvOp op) {
-  if (op == ConvOp::decode) {
+template <ConvOp OP, typename T, int VEC, int K, bool SILU> hipError_t launch_conv_t(const ShortConvArgs& a) {
+  if constexpr (OP == ConvOp::decode) {
     const int pieces = (a.C + VEC - 1) / VEC;
-    const long long blocks = ((long long)a.B * pieces + kConvThreads - 1) / kConvThreads;
+    const int each = (int)std::max(1LL, std::min(4LL, (long long)a.B * pieces / 65536));
+    const long long blocks = ((long long)(a.B + each - 1) / each * pieces + kConvThreads - 1) / kConvThreads;
     hipLaunchKernelGGL((conv_decode_kernel<T, VEC, K, SILU>), dim3((unsigned)blocks), dim3(kConvThreads), 0, a.stream,
-                       (const T*)a.x, a.w, a.b, (T*)a.state, (T*)a.y, a.B, a.C, pieces, a.ldx);
+                       (const T*)a.x, a.w, a.b, (T*)a.state, (T*)a.y, a.B, a.C, pieces, a.ldx, each);
     return hipGetLastError();
+  } else {
+    const ConvGeom G = conv_geom(a, VEC);
+    if constexpr (OP == ConvOp::fwd) {
+      hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, K, SILU>), dim3((unsigned)G.items * G.cblocks), dim3(kConvThreads), 0,
+                         a.stream, (const T*)a.x, a.w, a.b, (const T*)a.s0, a.lens, (T*)a.y, (T*)a.sT, G);
+      return hipGetLastError();
+    }
+    const bool weights = a.dw || a.db;
+    if (G.items > 0) {
+      hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, K, SILU>), dim3((unsigned)G.parts * G.cblocks), dim3(kConvThreads), 0,
+                         a.stream, (const T*)a.x, a.w, a.b, (const T*)a.s0, a.lens, (const T*)a.dy, (const T*)a.dsT, (T*)a.dx,
+                         (T*)a.ds0, weights ? (float*)a.workspace : nullptr, G);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess || !weights) return e;
+    }
+    const size_t C = (size_t)a.C;
+    return launch_part_sums(PartSums{(const float*)a.workspace, G.parts, C * (K + 1), {a.dw, a.db, nullptr}, {C * K, C, 0}},
+                            a.stream);
   }
-  const ConvGeom G = conv_geom(a, VEC);
-  if (op == ConvOp::fwd) {
-    hipLaunchKernelGGL((conv_fwd_kernel<T, VEC, K, SILU>), dim3((unsigned)G.items * G.cblocks), dim3(kConvThreads), 0,
-                       a.stream, (const T*)a.x, a.w, a.b, (const T*)a.s0, a.lens, (T*)a.y, (T*)a.sT, G);
-    return hipGetLastError();
-  }
-  const bool weights = a.dw || a.db;
-  if (G.items > 0) {
-    hipLaunchKernelGGL((conv_bwd_kernel<T, VEC, K, SILU>), dim3((unsigned)G.parts * G.cblocks), dim3(kConvThreads), 0,
-                       a.stream, (const T*)a.x, a.w, a.b, (const T*)a.s0, a.lens, (const T*)a.dy, (const T*)a.dsT, (T*)a.dx,
-                       (T*)a.ds0, weights ? (float*)a.workspace : nullptr, G);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !weights) return e;
-  }
-  const size_t C = (size_t)a.C;
-  return launch_part_sums(PartSums{(const float*)a.workspace, G.parts, C * (K + 1), {a.dw, a.db, nullptr}, {C * K, C, 0}},
-                          a.stream);
 }
 
-template <typename T, int VEC> hipError_t launch_conv_v(const ShortConvArgs& a, ConvOp op) {
+template <ConvOp OP, typename T, int VEC> hipError_t launch_conv_v(const ShortConvArgs& a) {
   switch (a.K * 2 + (a.silu ? 1 : 0)) {
-    case 4: return launch_conv_t<T, VEC, 2, false>(a, op);
-    case 5: return launch_conv_t<T, VEC, 2, true>(a, op);
-    case 6: return launch_conv_t<T, VEC, 3, false>(a, op);
-    case 7: return launch_conv_t<T, VEC, 3, true>(a, op);
-    case 8: return launch_conv_t<T, VEC, 4, false>(a, op);
-    case 9: return launch_conv_t<T, VEC, 4, true>(a, op);
+    case 4: return launch_conv_t<OP, T, VEC, 2, false>(a);
+    case 5: return launch_conv_t<OP, T, VEC, 2, true>(a);
+    case 6: return launch_conv_t<OP, T, VEC, 3, false>(a);
+    case 7: return launch_conv_t<OP, T, VEC, 3, true>(a);
+    case 8: return launch_conv_t<OP, T, VEC, 4, false>(a);
+    case 9: return launch_conv_t<OP, T, VEC, 4, true>(a);
   }
   return hipErrorInvalidValue;
 }
 
-// whole pieces of 16 bytes, unless a piece would lie across two heads
-bool conv_pieces(const ShortConvArgs& a, int vec) { return a.H == 1 || (a.C / a.H) % vec == 0; }
-
-hipError_t launch_conv(const ShortConvArgs& a, ConvOp op) {
-  if (a.dtype == CKDA_DTYPE_BF16)
-    return conv_pieces(a, 8) ? launch_conv_v<bf16_t, 8>(a, op) : launch_conv_v<bf16_t, 1>(a, op);
-  return conv_pieces(a, 4) ? launch_conv_v<float, 4>(a, op) : launch_conv_v<float, 1>(a, op);
+// Pieces of four channels (with bf16 8 bytes: half the registers of 16, so twice the waves; MI355X, us, four and
+// eight: forward B4 T4096 C2048 31.5 and 39, backward 66 and 143), or single ones where a piece would lie across
+// two heads.
+template <ConvOp OP> hipError_t launch_conv(const ShortConvArgs& a) {
+  const bool pieces = a.H == 1 || (a.C / a.H) % 4 == 0;
+  if (a.dtype == CKDA_DTYPE_BF16) return pieces ? launch_conv_v<OP, bf16_t, 4>(a) : launch_conv_v<OP, bf16_t, 1>(a);
+  return pieces ? launch_conv_v<OP, float, 4>(a) : launch_conv_v<OP, float, 1>(a);
 }
 
 }  // namespace
@@ -382,8 +429,8 @@ bool short_conv_fits_grid(int B, int T, int C, int H) {
   return (long long)B * slabs <= INT_MAX && (long long)B * slabs * pieces < (1LL << 24) && H > 0;
 }
 
-hipError_t launch_short_conv_fwd(const ShortConvArgs& a) { return launch_conv(a, ConvOp::fwd); }
-hipError_t launch_short_conv_bwd(const ShortConvArgs& a) { return launch_conv(a, ConvOp::bwd); }
-hipError_t launch_short_conv_decode(const ShortConvArgs& a) { return launch_conv(a, ConvOp::decode); }
+hipError_t launch_short_conv_fwd(const ShortConvArgs& a) { return launch_conv<ConvOp::fwd>(a); }
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a) { return launch_conv<ConvOp::bwd>(a); }
+hipError_t launch_short_conv_decode(const ShortConvArgs& a) { return launch_conv<ConvOp::decode>(a); }
 
 }  // namespace ckda
