@@ -10,26 +10,34 @@
 //   dB_t[n] = sum_c d x R,  dC_t[n] = sum_c ds h,  dz = dy (s + D x) silu'(z).
 //
 // Bound by vector instructions: for every (row, channel, state) two products, an
-// exponential and two fused products, at about 22 cycles for 64 of them.  So the
-// layout is one that leaves nothing else to do for each of them:
-//  * A DPP row of 16 lanes is one channel, each lane a state (N > 16: NS = 2 or 4
-//    states a lane), the state in a register, time down a loop.
-//  * Rows go by chunks of 16.  What a row has for each channel (d, d x, ds) is
-//    made once, by the lane of that row, and handed to the channel's 16 lanes by
-//    the row broadcast of DPP, an operand modifier that costs no instruction.
-//  * Sums over the states (s, u, v) are made for 16 rows at once: a transposing
-//    reduction leaves row j's sum in lane j, 33 instructions for 16 sums instead
-//    of 64, and what follows them is again done once for each row and channel.
-//  * Sums over the channels (dB, dC) swap halves and quarters of a wave between
-//    the two and between two rows (3 instructions a row), then go through LDS.
-//  * A workgroup is 32 channels (8 waves), which share B_t and C_t in LDS, as
-//    fp32; its rows of x, dt, z, dy and y are read and written by whole rows of
-//    its channels and turned in LDS.
+// exponential and two fused products (MI355X, ns a wave of 64 and a SIMD with waves
+// enough: product 1.0, fused 1.25, exponential 3.5; with a DPP operand 1.9, a select
+// 1.9, a swap of halves 3.4).  So the layout leaves little else to do for each:
+//  * LN neighbouring lanes are one channel, each with NS states in registers, time
+//    down a loop.  4 x 4 for up to 16 states; 16 x 2 and 16 x 4 for up to 32 and 64;
+//    16 x 1 where 4 lanes a channel would leave SIMDs idle and the sequence would
+//    have to be cut (see scan_geom).
+//  * Rows go by chunks of 16.  What a row has for each channel (d, d x, ds) is made
+//    once, by one lane, and handed to the channel's lanes by a DPP broadcast inside a
+//    row of 16 lanes or a quad.
+//  * Sums over the states (s, u, v) are made for LN rows at once by a transposing
+//    reduction, which leaves each row's sum in a lane of its own (16 sums of 16
+//    lanes: 33 instructions instead of 64), and what follows is again done once for
+//    each row and channel.
+//  * Sums over the channels (dB, dC) go the same way: values of different states and
+//    rows are paired, each half of the lanes keeps one of the two.  The waves' sums
+//    meet in LDS.  (On the fp32 matrix cores, 16x16x4, each masked row's product
+//    takes 32 cycles in which the SIMD issues nothing else: slower, 1058 us against
+//    830 at B4 T4096 C2048 N16.)
+//  * Workgroups share B_t and C_t in LDS, as fp32; rows of x, dt, z, dy and y are
+//    read and written by whole rows of the workgroup's channels and turned in LDS.
 // Few channels and many rows: the sequence runs in segments.  A first pass makes
 // each segment's own end state, a second joins them (a segment's decay is exp(A
-// sum d), closed), the main pass starts from the joined states.  The backward
-// needs the states in reverse: the forward pass stores them every 16 rows (of its
-// segment, joined when read), and the backward recomputes 16 rows in registers.
+// sum d), closed), the main pass starts from the joined states.  The backward needs
+// the states in reverse: a pass forward in time stores them every 16 rows (of its
+// segment, joined when read), and the main pass recomputes 16 rows in registers.  The
+// segments' own gradient states, sum_t (a_1 .. a_t) ds_t C_t, take no second
+// exponential: the same pass sums them with the running product of its decays.
 #include <limits.h>
 
 #include <algorithm>
@@ -42,13 +50,12 @@ namespace ckda {
 
 namespace {
 
-constexpr int kRows = 16;       // rows of a chunk, and lanes of a channel
-constexpr int kCh = 32;         // channels of a workgroup
-constexpr int kScanThreads = kRows * kCh;
-constexpr int kWaves = kScanThreads / 64;
-// registers for two to four waves on a SIMD: rows' operands are loaded ahead, not one after the other
-#define CKDA_SCAN_WAVES __attribute__((amdgpu_waves_per_eu(2, 4)))
+constexpr int kRows = 16;       // rows of a chunk
 constexpr int kPad = kRows + 1;   // row of a turned tile in LDS
+// Registers: for four waves on a SIMD with 4 lanes a channel, for two to four with 16 (rows' operands are loaded
+// ahead, not one after the other); the backward's main pass with 4 lanes for three, without spills.
+#define CKDA_SCAN_WAVES(LN) __attribute__((amdgpu_waves_per_eu((LN) == 4 ? 4 : 2, 4)))
+#define CKDA_SCAN_BWD_WAVES(LN) __attribute__((amdgpu_waves_per_eu((LN) == 4 ? 3 : 2, 4)))
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266174e-8f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- lanes
@@ -59,6 +66,16 @@ template <int... J, typename F> __device__ __forceinline__ void each_impl(std::i
 template <int N, typename F> __device__ __forceinline__ void each(F&& f) {
   each_impl(std::make_integer_sequence<int, N>{}, f);
 }
+
+// LN lanes a channel with NS states each
+template <int LN, int NS> struct Layout {
+  static constexpr int kStates = LN * NS;       // of a channel, the last ones possibly none
+  static constexpr int kRegs = kRows / LN;      // registers that hold one value for each row of a chunk: row i LN + l in lane l of i
+  static constexpr int kPack = 4 / NS;          // rows of B or C in one 16-byte LDS read
+  static constexpr int kBlockRows = NS == 4 ? 1 : kRows / NS;   // rows whose B and C are read together,
+  static constexpr int kBlock = kBlockRows * NS;                // and the values of a lane in them
+  static constexpr int kBlocks = kRows / kBlockRows;            // of a chunk
+};
 
 // lane J's value of each DPP row, in all of its 16 lanes
 template <int J> __device__ __forceinline__ float row_bcast(float x) {
@@ -100,6 +117,34 @@ __device__ __forceinline__ float turn_sums(const float (&v)[kRows], int lane) {
 #undef CKDA_PAIR
 
 __device__ __forceinline__ void pin_float(float& x) { asm volatile("" : "+v"(x)); }
+// Values that the next chunk takes over are pinned where they are made: the compiler would move the arithmetic
+// behind the branches that follow, and keep every operand until then.
+template <int N> __device__ __forceinline__ void pin_floats(float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) pin_float(x[i]);
+}
+
+// The channel's value of row J, in all of its lanes.  Used by one state it is the DPP operand of its product; by
+// several, a register of its own (kept apart from the products: each with a DPP operand would cost more).
+template <int LN, int NS, int J> __device__ __forceinline__ float row_value(const float (&x)[kRows / LN]) {
+  float v;
+  if constexpr (LN == 16) v = row_bcast<J>(x[0]);
+  else v = dpp_mov<(J % 4) * 0x55>(x[J / 4]);   // quad_perm [j,j,j,j]
+  if constexpr (NS > 1) pin_float(v);
+  return v;
+}
+
+// Sums over a channel's lanes of LN values, value j's sum to lane j
+__device__ __forceinline__ float turn_quad(const float (&v)[4], int lane) {
+  const bool two = lane & 2, one = lane & 1;
+  const float c0 = (two ? v[2] : v[0]) + dpp_mov<0x4E>(two ? v[0] : v[2]);
+  const float c1 = (two ? v[3] : v[1]) + dpp_mov<0x4E>(two ? v[1] : v[3]);
+  return (one ? c1 : c0) + dpp_mov<0xB1>(one ? c0 : c1);
+}
+template <int LN> __device__ __forceinline__ float turn_lanes(const float (&v)[LN], int l) {
+  if constexpr (LN == 16) return turn_sums(v, l);
+  else return turn_quad(v, l);
+}
 
 // lower half of the wave: a summed over the halves; upper half: b
 __device__ __forceinline__ float sum_halves(float a, float b) {
@@ -111,6 +156,23 @@ __device__ __forceinline__ float sum_quarters(float a, float b) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
+
+// Sums over the 4 quads of a DPP row of 4 states of two quantities: quad b gets the sum of state (b & 1) 2 + b / 2
+// of each.  Pairs across quads two apart (row_ror:8), then next ones (from the quad behind, row_ror:12, where the
+// first of a pair is kept, from the one before, row_ror:4, where the second is).
+#define CKDA_QUADS(d, a, b, low, high, mask)                               \
+  "v_add_f32_dpp " d ", " a ", " a " " low " row_mask:0xf bank_mask:0xf\n" \
+  "v_add_f32_dpp " d ", " b ", " b " " high " row_mask:0xf bank_mask:" mask "\n"
+__device__ __forceinline__ void sum_quads(const float (&x)[4], const float (&y)[4], float& sx, float& sy) {
+  float a0, a1, a2, a3;
+  asm("s_nop 1\n"   //
+      CKDA_QUADS("%2", "%6", "%7", "row_ror:8", "row_ror:8", "0xc") CKDA_QUADS("%3", "%8", "%9", "row_ror:8", "row_ror:8", "0xc")
+      CKDA_QUADS("%4", "%10", "%11", "row_ror:8", "row_ror:8", "0xc") CKDA_QUADS("%5", "%12", "%13", "row_ror:8", "row_ror:8", "0xc")
+      CKDA_QUADS("%0", "%2", "%3", "row_ror:12", "row_ror:4", "0xa") CKDA_QUADS("%1", "%4", "%5", "row_ror:12", "row_ror:4", "0xa")
+      : "=&v"(sx), "=&v"(sy), "=&v"(a0), "=&v"(a1), "=&v"(a2), "=&v"(a3)
+      : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]), "v"(y[2]), "v"(y[3]));
+}
+#undef CKDA_QUADS
 
 // ---------------------------------------------------------------- elements
 
@@ -178,11 +240,11 @@ struct ScanGeom {
   int softplus, pad_zero;
 };
 
-struct ScanWork {            // workspace of a call
-  float* ends;               // [B][nseg][C][N]: segments' own end states, then start states
+struct ScanWork {            // workspace of a call; P = a layout's states
+  float* ends;               // [B][nseg][C][P]: segments' own end states, then start states
   float* steps;              // [B][nseg][C]: sums of d over the segments
-  float* back;               // [B][nseg][C][N]: backward in time
-  float* marks;              // [B][chunks][C][N]: states before each chunk, of their segment
+  float* back;               // [B][nseg][C][P]: backward in time
+  float* marks;              // [B][chunks][C][P]: states before each chunk, of their segment
   float* mark_steps;         // [B][chunks][C]: sums of d from the segment's start to each chunk (nseg > 1)
   float* bc;                 // [G cblocks][B T][2][N]: parts of dC, dB
   float* weights;            // [B nseg][C N + 2 C]: parts of dA, dD, dbias
@@ -241,6 +303,25 @@ template <typename T> __device__ __forceinline__ void store_elem(__amdgpu_buffer
   if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16((short)from_f32<bf16_t>(x).bits, r, off, 0, 0);
   else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, 0);
 }
+// states of a lane, next to each other
+template <int NS> __device__ __forceinline__ void load_states(uint32_t (&v)[NS], __amdgpu_buffer_rsrc_t r, int off) {
+  if constexpr (NS == 4) {
+    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0);
+    v[0] = w[0], v[1] = w[1], v[2] = w[2], v[3] = w[3];
+  } else if constexpr (NS == 2) {
+    const u32x2 w = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+    v[0] = w[0], v[1] = w[1];
+  } else {
+    v[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+  }
+}
+template <int NS> __device__ __forceinline__ void store_states(__amdgpu_buffer_rsrc_t r, int off, const float (&h)[NS]) {
+  if constexpr (NS == 4)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(h[0]), __float_as_uint(h[1]), __float_as_uint(h[2]), __float_as_uint(h[3])}, r, off, 0, 0);
+  else if constexpr (NS == 2)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(h[0]), __float_as_uint(h[1])}, r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(h[0]), r, off, 0, 0);
+}
 // A prefetched element, widened here and not where it was loaded (which would wait for it there).
 template <typename T> __device__ __forceinline__ float value_of(uint32_t raw) {
   pin(raw);
@@ -248,10 +329,11 @@ template <typename T> __device__ __forceinline__ float value_of(uint32_t raw) {
 }
 
 // B and C (either alone: WHICH 1 or 2, both: 3) of SUBS chunks of rows in LDS, each
-// as [row / 4][s][lane][row % 4], so that a lane reads four rows at once.  Every wave
-// moves one of the two at a time.
-template <typename T, int NS, int SUBS, int THREADS, int WHICH> struct BcTile {
-  static constexpr int kOne = SUBS * kRows * 16 * NS;                  // elements of one of the two
+// as [row / kPack][lane][row % kPack][state], 16 bytes a lane.  Every wave moves one of
+// the two at a time.
+template <typename T, int LN, int NS, int SUBS, int THREADS, int WHICH> struct BcTile {
+  using Lay = Layout<LN, NS>;
+  static constexpr int kOne = SUBS * kRows * Lay::kStates;             // elements of one of the two
   static constexpr int kEach = (WHICH == 3 ? 2 : 1) * kOne / THREADS;  // elements a thread moves
   static constexpr int kSpan = kOne < THREADS ? kOne : THREADS;        // threads on one of the two
   static constexpr int kLoads = kEach > 0 ? kEach : 1;
@@ -266,8 +348,8 @@ template <typename T, int NS, int SUBS, int THREADS, int WHICH> struct BcTile {
   __device__ __forceinline__ void place(const ScanLaunch& L, const ScanPlace& p) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int idx = place_of(i), n = idx % (16 * NS);
-      off[i] = n < L.G.N && !idle() ? (idx / (16 * NS) * L.G.ldbc + p.g * L.G.N + n) * (int)sizeof(T) : kNowhere;
+      const int idx = place_of(i), n = idx % Lay::kStates;
+      off[i] = n < L.G.N && !idle() ? (idx / Lay::kStates * L.G.ldbc + p.g * L.G.N + n) * (int)sizeof(T) : kNowhere;
     }
   }
   __device__ __forceinline__ void fetch(const Rows<T>& B, const Rows<T>& C, int row, int rows) {
@@ -281,43 +363,44 @@ template <typename T, int NS, int SUBS, int THREADS, int WHICH> struct BcTile {
   __device__ __forceinline__ void stage(float* s) const {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int idx = place_of(i), n = idx % (16 * NS), row = idx / (16 * NS);
-      if (!idle()) s[(of_c(i) && WHICH == 3 ? kOne : 0) + ((row / 4 * NS + n / 16) * 16 + n % 16) * 4 + row % 4] = value_of<T>(raw[i]);
+      const int idx = place_of(i), n = idx % Lay::kStates, row = idx / Lay::kStates;
+      const int at = (row / Lay::kPack * LN + n / NS) * 4 + row % Lay::kPack * NS + n % NS;
+      if (!idle()) s[(of_c(i) && WHICH == 3 ? kOne : 0) + at] = value_of<T>(raw[i]);
     }
   }
 };
 
-// Block K of a tile's B or C: 16 / NS rows of NS states, f[row * NS + s].
-template <int NS, int K> __device__ __forceinline__ void load_block(float (&f)[kRows], const float* one) {
-  const f32x4* p = reinterpret_cast<const f32x4*>(one) + K * (4 / NS) * NS * 16 + (threadIdx.x & 15);
+// Block K of a tile's B or C: f[row * NS + s] of this lane's states.
+template <int LN, int NS, int K, int VALUES> __device__ __forceinline__ void load_block(float (&f)[VALUES], const float* one) {
+  static_assert(VALUES == Layout<LN, NS>::kBlock, "values of a block");
+  constexpr int Q = VALUES / 4;
+  const f32x4* p = reinterpret_cast<const f32x4*>(one) + K * Q * LN + threadIdx.x % LN;
 #pragma unroll
-  for (int q = 0; q < 4 / NS; ++q)
+  for (int q = 0; q < Q; ++q) {
+    const f32x4 v = p[q * LN];
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const f32x4 v = p[(q * NS + s) * 16];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[(4 * q + i) * NS + s] = v[i];
-    }
+    for (int i = 0; i < 4; ++i) f[4 * q + i] = v[i];
+  }
 }
 
 // ---------------------------------------------------------------- forward
 
 // MAIN: outputs (and the last state) from the segments' start states.  Else: the
-// segments' own end states and sums of steps, with MARK the states before each
-// chunk on the way (SEGS: of several segments).  Two chunks of rows between barriers.
-template <typename T, int NS, int CH, bool MAIN, bool MARK, bool SEGS>
-__global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(const ScanLaunch L) {
+// segments' own end states and sums of steps.  SUBS chunks of rows between barriers.
+template <typename T, int LN, int NS, int THREADS, int SUBS, bool MAIN>
+__global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_fwd_kernel(const ScanLaunch L) {
+  using Lay = Layout<LN, NS>;
   constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int SUBS = 2, TILE = SUBS * kRows;
+  constexpr int CH = THREADS / LN, REGS = Lay::kRegs, TILE = SUBS * kRows, EACH = SUBS * REGS, P = Lay::kStates;
   __shared__ float2 s_d[2][SUBS][CH][kPad];
   __shared__ float s_y[MAIN ? 2 : 1][MAIN ? SUBS : 1][MAIN ? CH : 1][kPad];
-  __shared__ __attribute__((aligned(16))) float s_bc[2][TILE * NS * 16 * (MAIN ? 2 : 1)];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][TILE * P * (MAIN ? 2 : 1)];
   const SelScanArgs& a = L.a;
   const ScanGeom& G = L.G;
   ScanPlace p;
   if (!scan_place(L, p)) return;
-  const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;   // state and channel in the recurrence
-  const int r = tid / CH, ch = tid % CH;                         // row and channel of the tiles
+  const int tid = threadIdx.x, l = tid % LN, mine = tid / LN;   // lane and channel in the recurrence
+  const int r = tid / CH, ch = tid % CH;                         // row (i LN + r) and channel of the tiles
   const int c0 = p.cb * CH, first_c = p.g * G.Cg + c0;
   const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
   const int cm = first_c + mine, ct = first_c + ch;
@@ -326,37 +409,36 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
   float A2[NS], h[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    const bool state = on && n + 16 * s < G.N;
-    const size_t at = (size_t)cm * G.N + n + 16 * s;
-    A2[s] = state ? a.A[at] * kLog2e : 0.f;
+    const int n = l * NS + s;
+    const bool state = on && n < G.N;
+    A2[s] = state ? a.A[(size_t)cm * G.N + n] * kLog2e : 0.f;
     h[s] = 0.f;
     if (state) {
-      if (MAIN && p.seg > 0) h[s] = L.w.ends[((size_t)p.b * G.nseg + p.seg) * G.C * G.N + at];
-      else if (p.seg == 0 && a.h0) h[s] = a.h0[(size_t)p.b * G.C * G.N + at];
+      if (MAIN && p.seg > 0) h[s] = L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + n];
+      else if (p.seg == 0 && a.h0) h[s] = a.h0[((size_t)p.b * G.C + cm) * G.N + n];
     }
   }
   const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
   const float Dc = MAIN && tile_on && a.D ? a.D[ct] : 0.f;
 
-  // this thread's rows of the tiles: row r, and every 16th from there
   const size_t first = (size_t)p.b * G.T + row0;
   const Rows<T> xs(a.x, first, G.C), ds(a.dt, first, G.C), ys(a.y, first, G.C), zs(a.z, first, G.ldz);
   const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
-  int off[SUBS], zoff[SUBS];
+  int off[EACH], zoff[EACH];
 #pragma unroll
-  for (int i = 0; i < SUBS; ++i) {
-    off[i] = tile_on ? ((i * kRows + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
-    zoff[i] = tile_on ? ((i * kRows + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
+  for (int i = 0; i < EACH; ++i) {
+    off[i] = tile_on ? ((i * LN + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
+    zoff[i] = tile_on ? ((i * LN + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
   }
-  uint32_t xr[SUBS], dr[SUBS], zr[SUBS] = {};
-  BcTile<T, NS, SUBS, kRows * CH, MAIN ? 3 : 1> bc;
+  uint32_t xr[EACH], dr[EACH], zr[EACH] = {};
+  BcTile<T, LN, NS, SUBS, THREADS, MAIN ? 3 : 1> bc;
   bc.place(L, p);
   // Rows behind the segment read zero; no branch around the loads (values that meet behind one are copied there,
   // and the copies wait for the loads).
   auto fetch = [&](int t0) {
     const int rows = min(end - t0, TILE), row = t0 - row0;
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) {
+    for (int i = 0; i < EACH; ++i) {
       xr[i] = load_raw<T>(xs.tile(row, rows), off[i]);
       dr[i] = load_raw<T>(ds.tile(row, rows), off[i]);
       if (MAIN) zr[i] = load_raw<T>(zs.tile(row, a.z ? rows : 0), zoff[i]);
@@ -365,19 +447,14 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
   };
   auto stage = [&](int buf, int t0) {
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) {
+    for (int i = 0; i < EACH; ++i) {
       float d = value_of<T>(dr[i]) + bias;
       if (G.softplus) d = softplus(d);
-      d = tile_on && t0 + i * kRows + r < end ? d : 0.f;   // a step of zero leaves the state
-      s_d[buf][i][ch][r] = float2{d, d * value_of<T>(xr[i])};
+      d = tile_on && t0 + i * LN + r < end ? d : 0.f;   // a step of zero leaves the state
+      s_d[buf][i / REGS][ch][i % REGS * LN + r] = float2{d, d * value_of<T>(xr[i])};
     }
     bc.stage(s_bc[buf]);
   };
-
-  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * G.N), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
-  int moff[NS];
-#pragma unroll
-  for (int s = 0; s < NS; ++s) moff[s] = on && n + 16 * s < G.N ? (cm * G.N + n + 16 * s) * 4 : kNowhere;
 
   float steps = 0.f;
   if (row0 < end) {
@@ -387,52 +464,55 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
   }
   int buf = 0;
   for (int t0 = row0; t0 < end; t0 += TILE, buf ^= 1) {
-    uint32_t xk[SUBS], zk[SUBS];
+    uint32_t xk[EACH], zk[EACH];
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) xk[i] = xr[i], zk[i] = zr[i];
+    for (int i = 0; i < EACH; ++i) xk[i] = xr[i], zk[i] = zr[i];
     const bool more = t0 + TILE < end;
     fetch(t0 + TILE);
     // B and C of a block of rows are loaded while the block before is worked on
     const float* one = s_bc[buf];
-    float2 d[SUBS];
-    float Bv[2][kRows], Cv[2][kRows];
-    load_block<NS, 0>(Bv[0], one);
-    if constexpr (MAIN) load_block<NS, 0>(Cv[0], one + TILE * NS * 16);
+    float d[SUBS][REGS], dx[SUBS][REGS], Bv[2][Lay::kBlock], Cv[2][Lay::kBlock];
+    load_block<LN, NS, 0>(Bv[0], one);
+    if constexpr (MAIN) load_block<LN, NS, 0>(Cv[0], one + TILE * P);
 #pragma unroll
-    for (int i = 0; i < SUBS; ++i) d[i] = s_d[buf][i][mine][n];
-    float sums[kRows];
-    each<SUBS * NS>([&](auto K) {
-      constexpr int k = K, i = k / NS, b = k % NS;   // block, its chunk and its place there
-      if constexpr (k + 1 < SUBS * NS) {
-        load_block<NS, k + 1>(Bv[(k + 1) % 2], one);
-        if constexpr (MAIN) load_block<NS, k + 1>(Cv[(k + 1) % 2], one + TILE * NS * 16);
+    for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+      for (int q = 0; q < REGS; ++q) {
+        const float2 v = s_d[buf][i][mine][q * LN + l];
+        d[i][q] = v.x, dx[i][q] = v.y;
+      }
+    float sums[LN];
+    each<SUBS * Lay::kBlocks>([&](auto K) {
+      constexpr int k = K, i = k / Lay::kBlocks, b = k % Lay::kBlocks, R = Lay::kBlockRows;   // a block, its chunk and its place there
+      if constexpr (k + 1 < SUBS * Lay::kBlocks) {
+        load_block<LN, NS, k + 1>(Bv[(k + 1) % 2], one);
+        if constexpr (MAIN) load_block<LN, NS, k + 1>(Cv[(k + 1) % 2], one + TILE * P);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (b == 0) {
-        if constexpr (MARK) {
-          const int chunk = t0 / kRows + i;
+      if constexpr (!MAIN && b == 0) {
+        float sum = d[i][0];
 #pragma unroll
-          for (int s = 0; s < NS; ++s) store_elem<float>(marks.tile(chunk, chunk < p.ch1), moff[s], h[s]);
-          if constexpr (SEGS) store_elem<float>(mark_sums.tile(chunk, chunk < p.ch1), on && n == 0 ? cm * 4 : kNowhere, steps);
-        }
-        if constexpr (SEGS) steps += group_sum<16>(d[i].x);
+        for (int q = 1; q < REGS; ++q) sum += d[i][q];
+        steps += group_sum<LN>(sum);
       }
-      each<kRows / NS>([&](auto J) {
-        constexpr int j = b * (kRows / NS) + J;
+      each<R>([&](auto J) {
+        constexpr int j = b * R + J;
+        const float dj = row_value<LN, NS, j>(d[i]), dxj = row_value<LN, NS, j>(dx[i]);
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          h[s] = Decay<EXACT>(row_bcast<j>(d[i].x) * A2[s]).of(h[s], row_bcast<j>(d[i].y) * Bv[k % 2][J * NS + s]);
-          if constexpr (MAIN) sums[j] = s ? __builtin_fmaf(Cv[k % 2][J * NS + s], h[s], sums[j]) : Cv[k % 2][J * NS] * h[s];
+          h[s] = Decay<EXACT>(dj * A2[s]).of(h[s], dxj * Bv[k % 2][J * NS + s]);
+          if constexpr (MAIN) sums[j % LN] = s ? __builtin_fmaf(Cv[k % 2][J * NS + s], h[s], sums[j % LN]) : Cv[k % 2][J * NS] * h[s];
         }
       });
-      if constexpr (MAIN && b == NS - 1) s_y[buf][i][mine][n] = turn_sums(sums, n);
+      pin_floats(h);
+      if constexpr (MAIN && (b + 1) * R % LN == 0) s_y[buf][i][mine][(b + 1) * R - LN + l] = turn_lanes<LN>(sums, l);
     });
     if (more) stage(buf ^ 1, t0 + TILE);
     lds_barrier();
     if constexpr (MAIN) {
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i) {
-        float y = __builtin_fmaf(Dc, value_of<T>(xk[i]), s_y[buf][i][ch][r]);
+      for (int i = 0; i < EACH; ++i) {
+        float y = __builtin_fmaf(Dc, value_of<T>(xk[i]), s_y[buf][i / REGS][ch][i % REGS * LN + r]);
         if (a.z) {
           const float z = value_of<T>(zk[i]);
           y *= z * row_sigmoid<T>(z);
@@ -445,82 +525,234 @@ __global__ __launch_bounds__(kRows* CH) CKDA_SCAN_WAVES void scan_fwd_kernel(con
     if (a.hT && p.seg == G.nseg - 1 && on) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        if (n + 16 * s < G.N) a.hT[((size_t)p.b * G.C + cm) * G.N + n + 16 * s] = h[s];
+        if (l * NS + s < G.N) a.hT[((size_t)p.b * G.C + cm) * G.N + l * NS + s] = h[s];
     }
     if (G.pad_zero && tile_on) {
       const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
-      for (int t = max(p.len, row0) + r; t < to; t += kRows) ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
+      for (int t = max(p.len, row0) + r; t < to; t += LN) ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
     }
-  } else if (SEGS && on) {
+  } else if (on) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
-      if (n + 16 * s < G.N) L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * G.N + n + 16 * s] = h[s];
-    if (n == 0) L.w.steps[((size_t)p.b * G.nseg + p.seg) * G.C + cm] = steps;
+    for (int s = 0; s < NS; ++s) L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + l * NS + s] = h[s];
+    if (l == 0) L.w.steps[((size_t)p.b * G.nseg + p.seg) * G.C + cm] = steps;
   }
 }
 
 // Segments' own states joined in order, in place: each place gets the state that
-// its segment starts from (forward in time: the first is left as it is, backward:
-// the last).
-template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_join_kernel(const ScanLaunch L) {
+// its segment starts from (BACK: the gradient of its last state, from dhT on).
+template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_join_kernel(const ScanLaunch L, int P) {
   const ScanGeom& G = L.G;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, CN = (long long)G.C * G.N;
-  if (i >= (long long)G.B * CN) return;
-  const int b = (int)(i / CN);
-  const long long cn = i - (long long)b * CN;
-  const float A2 = L.a.A[cn] * kLog2e;
-  float* own = (BACK ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CN + cn;
-  const float* steps = L.w.steps + (size_t)b * G.nseg * G.C + cn / G.N;
-  float h = own[(size_t)(BACK ? G.nseg - 1 : 0) * CN];
-  for (int k = 1; k < G.nseg; ++k) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, CP = (long long)G.C * P;
+  if (i >= (long long)G.B * CP) return;
+  const int b = (int)(i / CP), c = (int)(i % CP / P), n = (int)(i % P);
+  if (n >= G.N) return;
+  const float A2 = L.a.A[(size_t)c * G.N + n] * kLog2e;
+  float* own = (BACK ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CP + i % CP;
+  const float* steps = L.w.steps + (size_t)b * G.nseg * G.C + c;
+  float h = BACK && L.a.dhT ? L.a.dhT[((size_t)b * G.C + c) * G.N + n] : 0.f;
+  for (int k = 0; k < G.nseg; ++k) {
     const int seg = BACK ? G.nseg - 1 - k : k;
-    // (the forward's launch of own states leaves out the last segment, whose end nobody starts from)
+    // (of the last one nobody needs the end, and the forward does not make it)
     const bool last = k == G.nseg - 1;
-    const float next = last ? 0.f : own[(size_t)seg * CN], sum = last ? 0.f : steps[(size_t)seg * G.C];
-    own[(size_t)seg * CN] = h;
-    h = Decay<EXACT>(sum * A2).of(h) + next;
+    const float next = last ? 0.f : own[(size_t)seg * CP], sum = last ? 0.f : steps[(size_t)seg * G.C];
+    own[(size_t)seg * CP] = h;
+    // (the first segment's own state has the initial one in it already)
+    h = BACK || k ? Decay<EXACT>(sum * A2).of(h) + next : next;
   }
 }
 
 // ---------------------------------------------------------------- backward
 
-// MAIN: gradients.  Else: the segments' own states backward in time (the gradient
-// of the state before a segment, from its rows alone).
-template <typename T, int NS, bool MAIN, bool GATE>
-__global__ __launch_bounds__(kScanThreads) CKDA_SCAN_WAVES void scan_bwd_kernel(const ScanLaunch L) {
+// What the main pass needs from a pass forward in time: the states before each chunk
+// and, of several segments (SEGS), each segment's own end state, its sum of steps, and
+// its own gradient state (of the state before it, from its rows alone).
+template <typename T, int LN, int NS, int THREADS, bool SEGS>
+__global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(const ScanLaunch L) {
+  using Lay = Layout<LN, NS>;
   constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int kPartBufs = NS <= 2 ? 2 : 1;   // (two do not fit with 64 states)
-  constexpr int kPart = kRows / 2 * NS * 64;   // a wave's dC and dB of a chunk: [row / 2][s][lane]
-  __shared__ float2 s_d[2][kCh][kPad];
-  __shared__ float s_ds[2][kCh][kPad];
-  __shared__ float s_out[MAIN ? 2 : 1][3][MAIN ? kCh : 1][kPad];
-  __shared__ __attribute__((aligned(16))) float s_bc[2][kRows * NS * 16 * (MAIN ? 2 : 1)];
-  __shared__ __attribute__((aligned(16))) float s_part[MAIN ? kPartBufs : 1][MAIN ? kWaves : 1][MAIN ? kPart : 1];
+  constexpr int CH = THREADS / LN, REGS = Lay::kRegs, P = Lay::kStates;
+  __shared__ float2 s_d[2][CH][kPad];
+  __shared__ float s_ds[SEGS ? 2 : 1][SEGS ? CH : 1][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[2][kRows * P * (SEGS ? 2 : 1)];
   const SelScanArgs& a = L.a;
   const ScanGeom& G = L.G;
   ScanPlace p;
   if (!scan_place(L, p)) return;
-  if (!MAIN) p.seg += 1, p.ch0 += G.seg_chunks, p.ch1 = min(p.ch0 + G.seg_chunks, (p.len + kRows - 1) / kRows);
-  const int tid = threadIdx.x, n = tid & 15, mine = tid >> 4;
-  const int r = tid / kCh, ch = tid % kCh;
-  const int c0 = p.cb * kCh, first_c = p.g * G.Cg + c0;
+  const int tid = threadIdx.x, l = tid % LN, mine = tid / LN;
+  const int r = tid / CH, ch = tid % CH;
+  const int c0 = p.cb * CH, first_c = p.g * G.Cg + c0;
+  const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
+  const int cm = first_c + mine, ct = first_c + ch;
+
+  float A2[NS], h[NS], Q[NS], product[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int n = l * NS + s;
+    const bool state = on && n < G.N;
+    A2[s] = state ? a.A[(size_t)cm * G.N + n] * kLog2e : 0.f;
+    h[s] = state && p.seg == 0 && a.h0 ? a.h0[((size_t)p.b * G.C + cm) * G.N + n] : 0.f;
+    Q[s] = 0.f, product[s] = 1.f;
+  }
+  const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
+  const size_t first = (size_t)p.b * G.T;
+  const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
+  const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
+  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * P), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  const int moff = on ? (cm * P + l * NS) * 4 : kNowhere;
+  int off[REGS], zoff[REGS];
+#pragma unroll
+  for (int i = 0; i < REGS; ++i) {
+    off[i] = tile_on ? ((i * LN + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
+    zoff[i] = tile_on ? ((i * LN + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
+  }
+  uint32_t xr[REGS], dr[REGS], gr[REGS] = {}, zr[REGS] = {};
+  BcTile<T, LN, NS, 1, THREADS, SEGS ? 3 : 1> bc;
+  bc.place(L, p);
+  auto fetch = [&](int chunk) {
+    const int row = chunk * kRows, rows = chunk < p.ch1 ? min(p.len - row, kRows) : 0;
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      xr[i] = load_raw<T>(xs.tile(row, rows), off[i]);
+      dr[i] = load_raw<T>(dts.tile(row, rows), off[i]);
+      if (SEGS) {
+        gr[i] = load_raw<T>(dys.tile(row, rows), off[i]);
+        zr[i] = load_raw<T>(zs.tile(row, a.z ? rows : 0), zoff[i]);
+      }
+    }
+    bc.fetch(Bs, Cs, row, rows);
+  };
+  auto stage = [&](int buf, int chunk) {
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      float d = value_of<T>(dr[i]) + bias;
+      if (G.softplus) d = softplus(d);
+      d = tile_on && chunk * kRows + i * LN + r < p.len ? d : 0.f;
+      s_d[buf][ch][i * LN + r] = float2{d, d * value_of<T>(xr[i])};
+      if constexpr (SEGS) {
+        const float z = value_of<T>(zr[i]);
+        s_ds[buf][ch][i * LN + r] = value_of<T>(gr[i]) * (a.z ? z * row_sigmoid<T>(z) : 1.f);   // (dy is zero behind the rows)
+      }
+    }
+    bc.stage(s_bc[buf]);
+  };
+  float steps = 0.f;
+  if (p.ch0 < p.ch1) {
+    fetch(p.ch0);
+    stage(0, p.ch0);
+    __syncthreads();
+  }
+  int buf = 0;
+  for (int k = p.ch0; k < p.ch1; ++k, buf ^= 1) {
+    fetch(k + 1);
+    store_states<NS>(marks.tile(k, 1), moff, h);
+    if constexpr (SEGS) store_elem<float>(mark_sums.tile(k, 1), on && l == 0 ? cm * 4 : kNowhere, steps);
+    const float* one = s_bc[buf];
+    float d[REGS], dx[REGS], ds[REGS], Bv[2][Lay::kBlock], Cv[2][Lay::kBlock];
+    load_block<LN, NS, 0>(Bv[0], one);
+    if constexpr (SEGS) load_block<LN, NS, 0>(Cv[0], one + kRows * P);
+#pragma unroll
+    for (int q = 0; q < REGS; ++q) {
+      const float2 v = s_d[buf][mine][q * LN + l];
+      d[q] = v.x, dx[q] = v.y;
+      if constexpr (SEGS) ds[q] = s_ds[buf][mine][q * LN + l];
+    }
+    each<Lay::kBlocks>([&](auto K) {
+      constexpr int b = K, R = Lay::kBlockRows;
+      if constexpr (b + 1 < Lay::kBlocks) {
+        load_block<LN, NS, b + 1>(Bv[(b + 1) % 2], one);
+        if constexpr (SEGS) load_block<LN, NS, b + 1>(Cv[(b + 1) % 2], one + kRows * P);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (SEGS && b == 0) {
+        float sum = d[0];
+#pragma unroll
+        for (int q = 1; q < REGS; ++q) sum += d[q];
+        steps += group_sum<LN>(sum);
+      }
+      each<R>([&](auto J) {
+        constexpr int j = b * R + J;
+        const float dj = row_value<LN, NS, j>(d), dxj = row_value<LN, NS, j>(dx);
+        float dsj = 0.f;
+        if constexpr (SEGS) dsj = row_value<LN, NS, j>(ds);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const Decay<EXACT> e(dj * A2[s]);
+          h[s] = e.of(h[s], dxj * Bv[b % 2][J * NS + s]);
+          if constexpr (SEGS) {
+            product[s] = e.of(product[s]);
+            Q[s] = __builtin_fmaf(product[s], dsj * Cv[b % 2][J * NS + s], Q[s]);
+          }
+        }
+      });
+      pin_floats(h);
+      if constexpr (SEGS) pin_floats(product), pin_floats(Q);
+    });
+    stage(buf ^ 1, k + 1);
+    lds_barrier();
+  }
+  if (SEGS && on) {
+    const size_t at = (((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + l * NS;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) L.w.ends[at + s] = h[s], L.w.back[at + s] = Q[s];
+    if (l == 0) L.w.steps[((size_t)p.b * G.nseg + p.seg) * G.C + cm] = steps;
+  }
+}
+
+// two elements that a thread keeps, of bf16 in one register
+template <typename T> struct Kept;
+template <> struct Kept<bf16_t> {
+  uint32_t w;
+  __device__ __forceinline__ Kept() {}
+  __device__ __forceinline__ Kept(uint32_t a, uint32_t b) : w(a | b << 16) {}
+  __device__ __forceinline__ float first() const { return bf16_lo_half(w); }
+  __device__ __forceinline__ float second() const { return bf16_hi_half(w); }
+};
+template <> struct Kept<float> {
+  uint32_t a, b;
+  __device__ __forceinline__ Kept() {}
+  __device__ __forceinline__ Kept(uint32_t a, uint32_t b) : a(a), b(b) {}
+  __device__ __forceinline__ float first() const { return __uint_as_float(a); }
+  __device__ __forceinline__ float second() const { return __uint_as_float(b); }
+};
+
+// The gradients, chunk by chunk from the last one.
+template <typename T, int LN, int NS, int THREADS, bool GATE>
+__global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kernel(const ScanLaunch L) {
+  using Lay = Layout<LN, NS>;
+  constexpr bool EXACT = sizeof(T) == 4;
+  constexpr bool AHEAD = LN != 4;   // the next chunk's rows are loaded ahead (with 4 lanes other waves fill the wait)
+  constexpr bool KEEP = NS <= 2;   // the decays of a chunk stay in registers; else they are formed twice
+  constexpr int HALVES = LN == 4 ? 2 : 1, HR = kRows / HALVES;
+  constexpr int CH = THREADS / LN, REGS = Lay::kRegs, P = Lay::kStates, WAVES = THREADS / 64;
+  constexpr int PR = P / 16, kPart = kRows / 2 * PR * 64;   // a wave's dC and dB of a chunk: [row / 2][PR][lane]
+  // (d, d x), then (d u, u), of the same row and channel, which one wave reads and writes; ds, then s
+  __shared__ float2 s_d[CH][kPad];
+  __shared__ float s_ds[CH][kPad], s_v[CH][kPad];
+  __shared__ __attribute__((aligned(16))) float s_bc[kRows * P * 2];
+  __shared__ float s_part[WAVES][kPart];
+  const SelScanArgs& a = L.a;
+  const ScanGeom& G = L.G;
+  ScanPlace p;
+  if (!scan_place(L, p)) return;
+  const int tid = threadIdx.x, l = tid % LN, mine = tid / LN;
+  const int r = tid / CH, ch = tid % CH;
+  const int c0 = p.cb * CH, first_c = p.g * G.Cg + c0;
   const bool on = c0 + mine < G.Cg, tile_on = c0 + ch < G.Cg;
   const int cm = first_c + mine, ct = first_c + ch;
   const size_t CN = (size_t)G.C * G.N;
 
-  float A2[NS], A[NS], Q[NS], start[NS], dA[NS];
-  bool state[NS];
+  float A2[NS], Q[NS], start[NS], dA[NS];   // (A itself is A2 ln 2)
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
-    state[s] = on && n + 16 * s < G.N;
-    const size_t at = (size_t)cm * G.N + n + 16 * s;
-    A[s] = state[s] ? a.A[at] : 0.f;
-    A2[s] = A[s] * kLog2e;
+    const int n = l * NS + s;
+    const bool state = on && n < G.N;
+    const size_t seg = (((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + n;
+    A2[s] = state ? a.A[(size_t)cm * G.N + n] * kLog2e : 0.f;
     dA[s] = Q[s] = start[s] = 0.f;
-    if (state[s]) {
-      if (p.seg == G.nseg - 1) Q[s] = a.dhT ? a.dhT[(size_t)p.b * CN + at] : 0.f;
-      else if (MAIN) Q[s] = L.w.back[((size_t)p.b * G.nseg + p.seg) * CN + at];
-      if (MAIN && p.seg > 0) start[s] = L.w.ends[((size_t)p.b * G.nseg + p.seg) * CN + at];
+    if (state) {
+      if (G.nseg > 1) Q[s] = L.w.back[seg];
+      else if (a.dhT) Q[s] = a.dhT[((size_t)p.b * G.C + cm) * G.N + n];
+      if (p.seg > 0) start[s] = L.w.ends[seg];
     }
   }
   const float bias = tile_on && a.dt_bias ? a.dt_bias[ct] : 0.f;
@@ -531,186 +763,213 @@ __global__ __launch_bounds__(kScanThreads) CKDA_SCAN_WAVES void scan_bwd_kernel(
   const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
   const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
   const Rows<T> dxs(a.dx, first, G.C), ddts(a.ddt, first, G.C), dzs(a.dz, first, G.C);
-  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * G.N);
-  const Rows<float> mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
-  const int off = tile_on ? (r * G.C + ct) * (int)sizeof(T) : kNowhere;
-  const int zoff = tile_on ? (r * G.ldz + ct) * (int)sizeof(T) : kNowhere;
-  uint32_t xr = 0, dr = 0, zr = 0, gr = 0, mark[NS], mark_steps = 0;
-  BcTile<T, NS, 1, kScanThreads, MAIN ? 3 : 2> bc;
+  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * P), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  int off[REGS], zoff[REGS];
+#pragma unroll
+  for (int i = 0; i < REGS; ++i) {
+    off[i] = tile_on ? ((i * LN + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
+    zoff[i] = tile_on ? ((i * LN + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
+  }
+  uint32_t xr[REGS], dr[REGS], zr[REGS] = {}, gr[REGS], mark[NS], mark_steps;
+  BcTile<T, LN, NS, 1, THREADS, 3> bc;
   bc.place(L, p);
   auto fetch = [&](int chunk) {   // (before the segment's first chunk: nothing; no branch around the loads)
     const int row = chunk * kRows, rows = chunk >= p.ch0 ? min(p.len - row, kRows) : 0;
-    xr = load_raw<T>(xs.tile(row, MAIN ? rows : 0), off);
-    dr = load_raw<T>(dts.tile(row, rows), off);
-    gr = load_raw<T>(dys.tile(row, rows), off);
-    zr = load_raw<T>(zs.tile(row, GATE ? rows : 0), zoff);
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      xr[i] = load_raw<T>(xs.tile(row, rows), off[i]);
+      dr[i] = load_raw<T>(dts.tile(row, rows), off[i]);
+      gr[i] = load_raw<T>(dys.tile(row, rows), off[i]);
+      if (GATE) zr[i] = load_raw<T>(zs.tile(row, rows), zoff[i]);
+    }
     bc.fetch(Bs, Cs, row, rows);
-    if constexpr (MAIN) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
-        mark[s] = load_raw<float>(marks.tile(chunk, rows > 0), state[s] ? (cm * G.N + n + 16 * s) * 4 : kNowhere);
-      mark_steps = load_raw<float>(mark_sums.tile(chunk, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
-    }
+    load_states<NS>(mark, marks.tile(chunk, rows > 0), on ? (cm * P + l * NS) * 4 : kNowhere);
+    mark_steps = load_raw<float>(mark_sums.tile(chunk, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
   };
-  // what the tile's thread keeps of its row and channel from one chunk's staging to its outputs
-  struct Row {
-    float x, raw, z, dy, d, ds;
-  };
-  auto stage = [&](int buf, int chunk) {
-    Row t;
-    t.x = value_of<T>(xr), t.raw = value_of<T>(dr) + bias, t.z = value_of<T>(zr), t.dy = value_of<T>(gr);
-    const float step = G.softplus ? softplus(t.raw) : t.raw;
-    t.ds = GATE ? t.dy * t.z * row_sigmoid<T>(t.z) : t.dy;
-    t.d = tile_on && chunk * kRows + r < p.len ? step : 0.f;   // (dy, and so ds, is zero there)
-    s_d[buf][ch][r] = float2{t.d, t.d * t.x};
-    s_ds[buf][ch][r] = t.ds;
-    bc.stage(s_bc[buf]);
-    return t;
-  };
-  Row row = {};
-  if (p.ch0 < p.ch1) {
-    fetch(p.ch1 - 1);
-    row = stage(0, p.ch1 - 1);
-    __syncthreads();
-  }
-  int buf = 0;
-  for (int k = p.ch1 - 1; k >= p.ch0; --k, buf ^= 1) {
+  if (AHEAD && p.ch0 < p.ch1) fetch(p.ch1 - 1);
+  for (int k = p.ch1 - 1; k >= p.ch0; --k) {
     const int row0 = k * kRows, rows = min(p.len - row0, kRows);
+    if (!AHEAD) fetch(k);
+    // the tile, and what its thread keeps of its rows for their outputs
+    Kept<T> xd[REGS], zg[REGS];
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      xd[i] = Kept<T>(xr[i], dr[i]), zg[i] = Kept<T>(zr[i], gr[i]);
+      float d = value_of<T>(dr[i]) + bias;
+      if (G.softplus) d = softplus(d);
+      d = tile_on && i * LN + r < rows ? d : 0.f;   // (dy, and so ds, is zero behind the rows)
+      const float z = value_of<T>(zr[i]);
+      s_d[ch][i * LN + r] = float2{d, d * value_of<T>(xr[i])};
+      s_ds[ch][i * LN + r] = value_of<T>(gr[i]) * (GATE ? z * row_sigmoid<T>(z) : 1.f);
+    }
+    bc.stage(s_bc);
     float hc[NS];   // the state before the chunk
-    if constexpr (MAIN) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        hc[s] = value_of<float>(mark[s]);
-        if (p.seg > 0) hc[s] += Decay<EXACT>(value_of<float>(mark_steps) * A2[s]).of(start[s]);
-      }
-    }
-    fetch(k - 1);
-    float2 dd = s_d[buf][mine][n];
-    const float dsm = s_ds[buf][mine][n];
-    const float *Bl = s_bc[buf], *Cl = s_bc[buf] + (MAIN ? kRows * NS * 16 : 0);
-    float Bv[kRows], Cv[kRows];   // of a block of rows
-    if constexpr (!MAIN) {
-      each<NS>([&](auto K) {
-        constexpr int b = NS - 1 - K;
-        load_block<NS, b>(Cv, Cl);
-        each<kRows / NS>([&](auto J) {
-          constexpr int i = kRows / NS - 1 - J, j = b * (kRows / NS) + i;
-#pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const float R = __builtin_fmaf(row_bcast<j>(dsm), Cv[i * NS + s], Q[s]);
-            Q[s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]).of(R);
-          }
-        });
-      });
-      stage(buf ^ 1, k - 1);
-      lds_barrier();
-    } else {
-      Decay<EXACT> e[kRows][NS];
-      float h[kRows][NS], sums[kRows];
-      each<NS>([&](auto K) {
-        constexpr int b = K;
-        load_block<NS, b>(Bv, Bl);
-        load_block<NS, b>(Cv, Cl);
-        each<kRows / NS>([&](auto J) {
-          constexpr int j = b * (kRows / NS) + J;
-#pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            e[j][s] = Decay<EXACT>(row_bcast<j>(dd.x) * A2[s]);
-            h[j][s] = e[j][s].of(j ? h[j ? j - 1 : 0][s] : hc[s], row_bcast<j>(dd.y) * Bv[J * NS + s]);
-            if constexpr (GATE) sums[j] = s ? __builtin_fmaf(Cv[J * NS + s], h[j][s], sums[j]) : Cv[J * NS] * h[j][s];
-          }
-        });
-      });
-      if constexpr (GATE) s_out[buf][0][mine][n] = turn_sums(sums, n);
-      // (so that the broadcasts below are operands of their products again, not values kept from above)
-      pin_float(dd.x), pin_float(dd.y);
-      float u[kRows], v[kRows], odd[NS];
-      float* part = s_part[buf % kPartBufs][tid >> 6] + (tid & 63);
-      each<NS>([&](auto K) {
-        constexpr int b = NS - 1 - K;
-        if constexpr (NS > 1) {   // (of one block they are still there)
-          load_block<NS, b>(Bv, Bl);
-          load_block<NS, b>(Cv, Cl);
-        }
-        each<kRows / NS>([&](auto J) {
-          constexpr int i = kRows / NS - 1 - J, j = b * (kRows / NS) + i;
-#pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const float R = __builtin_fmaf(row_bcast<j>(dsm), Cv[i * NS + s], Q[s]);
-            // dC and dB of the wave's channels: in the halves of the wave, and two rows in their halves
-            const float both = sum_halves(row_bcast<j>(dsm) * h[j][s], row_bcast<j>(dd.y) * R);
-            if constexpr (j % 2) odd[s] = both;
-            else part[(j / 2 * NS + s) * 64] = sum_quarters(both, odd[s]);
-            u[j] = s ? __builtin_fmaf(R, Bv[i * NS + s], u[j]) : R * Bv[i * NS];
-            Q[s] = e[j][s].of(R);
-            const float q = Q[s] * (j ? h[j ? j - 1 : 0][s] : hc[s]);
-            v[j] = s ? __builtin_fmaf(q, A[s], v[j]) : q * A[0];
-            dA[s] = __builtin_fmaf(q, row_bcast<j>(dd.x), dA[s]);
-          }
-        });
-      });
-      s_out[buf][1][mine][n] = turn_sums(u, n);
-      s_out[buf][2][mine][n] = turn_sums(v, n);
-      const Row next = stage(buf ^ 1, k - 1);
-      lds_barrier();
-      {
-        const float uu = s_out[buf][1][ch][r], dd_ = __builtin_fmaf(row.x, uu, s_out[buf][2][ch][r]);
-        const float ddt = G.softplus ? dd_ * softplus_slope(row.raw) : dd_;
-        store_elem<T>(dxs.tile(row0, rows), off, __builtin_fmaf(row.d, uu, Dc * row.ds));
-        store_elem<T>(ddts.tile(row0, rows), off, ddt);
-        if constexpr (GATE) {
-          const float pre = __builtin_fmaf(Dc, row.x, s_out[buf][0][ch][r]);
-          store_elem<T>(dzs.tile(row0, rows), off, row.dy * pre * silu_slope(row.z, row_sigmoid<T>(row.z)));
-        }
-        dD = __builtin_fmaf(row.ds, row.x, dD);
-        dbias += r < rows ? ddt : 0.f;
-      }
-      // dC (lower half of a wave's lanes) and dB of the workgroup's channels; odd DPP rows hold the second of two rows
-#pragma unroll
-      for (int i = 0; i < NS; ++i) {
-        const int at = tid + i * kScanThreads, lane = at % 64, which = lane / 32;
-        const int t = at / (64 * NS) * 2 + (lane / 16 & 1), m = lane % 16 + 16 * (at / 64 % NS);
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) sum += s_part[buf % kPartBufs][w][at];
-        if (t < rows && m < G.N)
-          L.w.bc[((((size_t)p.g * G.cblocks + p.cb) * G.B + p.b) * G.T + row0 + t) * 2 * G.N + which * G.N + m] = sum;
-      }
-      row = next;
-      if constexpr (kPartBufs == 1) lds_barrier();   // the next chunk writes the same parts
-    }
-  }
-  if constexpr (!MAIN) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-      if (state[s]) L.w.back[((size_t)p.b * G.nseg + p.seg) * CN + (size_t)cm * G.N + n + 16 * s] = Q[s];
-  } else {
-    float* part = L.w.weights + ((size_t)p.b * G.nseg + p.seg) * (CN + 2 * (size_t)G.C);
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      if (!state[s]) continue;
-      part[(size_t)cm * G.N + n + 16 * s] = dA[s];
-      if (p.seg == 0 && a.dh0) a.dh0[(size_t)p.b * CN + (size_t)cm * G.N + n + 16 * s] = Q[s];
+      hc[s] = value_of<float>(mark[s]);
+      if (p.seg > 0) hc[s] += Decay<EXACT>(value_of<float>(mark_steps) * A2[s]).of(start[s]);
     }
-    // over the tile's rows: thread (r, ch) holds the sums of rows r, r + 16, ...
-    __syncthreads();
-    s_out[0][0][ch][r] = dD;
-    s_out[0][1][ch][r] = dbias;
-    __syncthreads();
-    if (tid < 2 * kCh && c0 + tid % kCh < G.Cg) {
+    lds_barrier();
+    if (AHEAD) fetch(k - 1);
+    float d[REGS], dx[REGS], ds[REGS];
+#pragma unroll
+    for (int q = 0; q < REGS; ++q) {
+      const float2 v = s_d[mine][q * LN + l];
+      d[q] = v.x, dx[q] = v.y;
+      ds[q] = s_ds[mine][q * LN + l];
+    }
+    const float *Bl = s_bc, *Cl = s_bc + kRows * P;
+    constexpr int BLK = Lay::kBlocks, R = Lay::kBlockRows;
+    float Bv[2][Lay::kBlock], Cv[2][Lay::kBlock];   // of a block of rows, and of the next
+    // The chunk's last half first, from the state in its middle: the states of HR rows are in registers at a time.
+    float hm[NS];
+    if constexpr (HALVES == 2) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) hm[s] = hc[s];
+      load_block<LN, NS, 0>(Bv[0], Bl);
+      each<BLK / 2>([&](auto K) {
+        constexpr int b = K;
+        if constexpr (b + 1 < BLK / 2) load_block<LN, NS, b + 1>(Bv[(b + 1) % 2], Bl);
+        __builtin_amdgcn_sched_barrier(0);
+        each<R>([&](auto J) {
+          constexpr int j = b * R + J;
+          const float dj = row_value<LN, NS, j>(d), dxj = row_value<LN, NS, j>(dx);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) hm[s] = Decay<EXACT>(dj * A2[s]).of(hm[s], dxj * Bv[b % 2][J * NS + s]);
+        });
+        pin_floats(hm);
+      });
+    }
+    float* part = s_part[tid >> 6] + (tid & 63);
+    each<HALVES>([&](auto Half) {
+      constexpr int half = HALVES - 1 - Half, j0 = half * HR, b0 = half * BLK / HALVES, b1 = b0 + BLK / HALVES;
+      Decay<EXACT> e[KEEP ? HR : 1][NS];
+      float h[HR][NS], sums[LN], u[LN], v[LN], odd[PR];
+      auto before = [&](int j, int s) { return j > j0 ? h[j - 1 - j0][s] : half ? hm[s] : hc[s]; };
+      load_block<LN, NS, b0>(Bv[b0 % 2], Bl);
+      if constexpr (GATE) load_block<LN, NS, b0>(Cv[b0 % 2], Cl);
+      each<BLK / HALVES>([&](auto K) {
+        constexpr int b = b0 + K;
+        if constexpr (b + 1 < b1) {
+          load_block<LN, NS, b + 1>(Bv[(b + 1) % 2], Bl);
+          if constexpr (GATE) load_block<LN, NS, b + 1>(Cv[(b + 1) % 2], Cl);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        each<R>([&](auto J) {
+          constexpr int j = b * R + J;
+          const float dj = row_value<LN, NS, j>(d), dxj = row_value<LN, NS, j>(dx);
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const Decay<EXACT> now(dj * A2[s]);
+            h[j - j0][s] = now.of(before(j, s), dxj * Bv[b % 2][J * NS + s]);
+            if constexpr (KEEP) e[j - j0][s] = now;
+            if constexpr (GATE) sums[j % LN] = s ? __builtin_fmaf(Cv[b % 2][J * NS + s], h[j - j0][s], sums[j % LN]) : Cv[b % 2][J * NS] * h[j - j0][s];
+          }
+        });
+        if constexpr (GATE && (b + 1) * R % LN == 0) s_ds[mine][(b + 1) * R - LN + l] = turn_lanes<LN>(sums, l);
+      });
+      pin_floats(d), pin_floats(dx);   // (the broadcasts below are made again where they are used, not kept from above)
+      load_block<LN, NS, b1 - 1>(Bv[(b1 - 1) % 2], Bl);
+      load_block<LN, NS, b1 - 1>(Cv[(b1 - 1) % 2], Cl);
+      each<BLK / HALVES>([&](auto K) {
+        constexpr int b = b1 - 1 - K;
+        if constexpr (b > b0) {
+          load_block<LN, NS, b - 1>(Bv[(b + 1) % 2], Bl);
+          load_block<LN, NS, b - 1>(Cv[(b + 1) % 2], Cl);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        each<R>([&](auto J) {
+          constexpr int i = R - 1 - J, j = b * R + i;
+          const float dj = row_value<LN, NS, j>(d), dxj = row_value<LN, NS, j>(dx), dsj = row_value<LN, NS, j>(ds);
+          float dC[NS], dB[NS];
+#pragma unroll
+          for (int s = 0; s < NS; ++s) {
+            const float R_ = __builtin_fmaf(dsj, Cv[b % 2][i * NS + s], Q[s]);
+            dC[s] = dsj * h[j - j0][s], dB[s] = dxj * R_;
+            u[j % LN] = s ? __builtin_fmaf(R_, Bv[b % 2][i * NS + s], u[j % LN]) : R_ * Bv[b % 2][i * NS];
+            Q[s] = KEEP ? e[KEEP ? j - j0 : 0][s].of(R_) : Decay<EXACT>(dj * A2[s]).of(R_);
+            const float q = Q[s] * before(j, s);
+            v[j % LN] = s ? __builtin_fmaf(q, A2[s], v[j % LN]) : q * A2[0];
+            dA[s] = __builtin_fmaf(q, dj, dA[s]);
+          }
+          // dC and dB of the wave's channels: in the halves of the wave, two rows in their halves, states in the quads
+          float both[PR];
+          if constexpr (LN == 4) {
+            float sc, sb;
+            sum_quads(dC, dB, sc, sb);
+            both[0] = sum_halves(sc, sb);
+          } else {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) both[s] = sum_halves(dC[s], dB[s]);
+          }
+#pragma unroll
+          for (int s = 0; s < PR; ++s) {
+            if constexpr (j % 2) odd[s] = both[s];
+            else part[(j / 2 * PR + s) * 64] = sum_quarters(both[s], odd[s]);
+          }
+        });
+        pin_floats(Q), pin_floats(dA);
+        if constexpr (b * R % LN == 0) {   // LN rows done: lane l has those of row b R + l
+          const float uu = turn_lanes<LN>(u, l);
+          s_d[mine][b * R + l] = float2{uu * d[b * R / LN], uu};
+          s_v[mine][b * R + l] = turn_lanes<LN>(v, l) * kLn2;
+        }
+      });
+    });
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < REGS; ++i) {
+      const float2 du = s_d[ch][i * LN + r];
+      const float x = xd[i].first(), dy = zg[i].second(), z = zg[i].first();
+      const float sg = GATE ? row_sigmoid<T>(z) : 0.f, dsr = GATE ? dy * z * sg : dy;
+      const float dd = __builtin_fmaf(x, du.y, s_v[ch][i * LN + r]);
+      const float ddt = G.softplus ? dd * softplus_slope(xd[i].second() + bias) : dd;
+      store_elem<T>(dxs.tile(row0, rows), off[i], __builtin_fmaf(Dc, dsr, du.x));
+      store_elem<T>(ddts.tile(row0, rows), off[i], ddt);
+      if constexpr (GATE)
+        store_elem<T>(dzs.tile(row0, rows), off[i], dy * __builtin_fmaf(Dc, x, s_ds[ch][i * LN + r]) * silu_slope(z, sg));
+      dD = __builtin_fmaf(dsr, x, dD);
+      dbias += i * LN + r < rows ? ddt : 0.f;
+    }
+    // dC (lower half of a wave's lanes) and dB of the workgroup's channels; odd DPP rows hold the second of two rows
+#pragma unroll
+    for (int i = 0; i < kPart / THREADS; ++i) {
+      const int at = tid + i * THREADS, lane = at % 64, which = lane / 32, t = at / (64 * PR) * 2 + (lane / 16 & 1);
+      const int bank = lane / 4 % 4;
+      const int n = LN == 4 ? lane % 4 * 4 + (bank & 1) * 2 + bank / 2 : lane % 16 * NS + at / 64 % PR;
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) sum += s_out[0][tid / kCh][tid % kCh][i];
-      part[CN + (size_t)(tid / kCh) * G.C + first_c + tid % kCh] = sum;
+      for (int w = 0; w < WAVES; ++w) sum += s_part[w][at];
+      if (t < rows && n < G.N)
+        L.w.bc[((((size_t)p.g * G.cblocks + p.cb) * G.B + p.b) * G.T + row0 + t) * 2 * G.N + which * G.N + n] = sum;
     }
-    if (G.pad_zero && tile_on) {
-      const T zero = from_f32<T>(0.f);
-      const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
-      for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += kRows) {
-        const size_t at = ((size_t)p.b * G.T + t) * G.C + ct;
-        ((T*)a.dx)[at] = ((T*)a.ddt)[at] = zero;
-        if (GATE) ((T*)a.dz)[at] = zero;
-      }
+    lds_barrier();   // the next chunk's tile goes to the same place
+  }
+  float* part = L.w.weights + ((size_t)p.b * G.nseg + p.seg) * (CN + 2 * (size_t)G.C);
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int n = l * NS + s;
+    if (!on || n >= G.N) continue;
+    part[(size_t)cm * G.N + n] = dA[s];
+    if (p.seg == 0 && a.dh0) a.dh0[((size_t)p.b * G.C + cm) * G.N + n] = Q[s];
+  }
+  // over the tile's rows: thread (r, ch) holds the sums of rows r, r + LN, ...
+  s_ds[ch][r] = dD;
+  s_v[ch][r] = dbias;
+  __syncthreads();
+  if (tid < 2 * CH && c0 + tid % CH < G.Cg) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < LN; ++i) sum += tid < CH ? s_ds[tid % CH][i] : s_v[tid % CH][i];
+    part[CN + (size_t)(tid / CH) * G.C + first_c + tid % CH] = sum;
+  }
+  if (G.pad_zero && tile_on) {
+    const T zero = from_f32<T>(0.f);
+    const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
+    for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += LN) {
+      const size_t at = ((size_t)p.b * G.T + t) * G.C + ct;
+      ((T*)a.dx)[at] = ((T*)a.ddt)[at] = zero;
+      if (GATE) ((T*)a.dz)[at] = zero;
     }
   }
 }
@@ -825,47 +1084,68 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(const ScanLaunch L) {
 
 // ---------------------------------------------------------------- host
 
-ScanGeom scan_geom(int B, int T, int C, int G, int N) {
-  ScanGeom g = {};
+constexpr int kFwdThreads = 256;                       // of every layout
+constexpr int kQuadThreads = 256, kWideThreads = 512;   // of the backward's passes
+
+// How a call runs: lanes and states a channel, channels of a workgroup, segments.
+struct ScanPlan {
+  ScanGeom G;
+  int ln, ns;
+};
+ScanPlan scan_plan(int B, int T, int C, int G, int N, bool bwd) {
+  ScanPlan plan = {};
+  ScanGeom& g = plan.G;
   g.B = B, g.T = T, g.C = C, g.G = G, g.N = N;
   g.Cg = C / G;
-  g.cblocks = (g.Cg + kCh - 1) / kCh;
   g.chunks = (int)(((long long)T + kRows - 1) / kRows);
-  // Segments where the channels leave CUs without a workgroup; of 128 rows at least.
-  const long long blocks = (long long)B * G * g.cblocks;
+  // 4 lanes a channel where that can fill three waves of every SIMD, by segments of 128 rows or more; but in the
+  // forward not where 16 lanes fill two without segments and 4 lanes would need them, which cost a pass of their own
+  // (MI355X, us, 4 and 16 lanes: forward B4 T4096 C2048 290 and 224, B16 T1024 C4096 297 and 325, B1 T32768 C1024 280
+  // and 340, B1 T1024 C1024 40 and 24; backward B4 T4096 C2048 697 and 826, fp32 B3 T777 C500 160 and 117).
+  const long long channels = (long long)B * C, blocks4 = (long long)B * G * ((g.Cg + 63) / 64);
+  const bool fills = blocks4 * std::max(1, g.chunks / 8) >= 768, alone = !bwd && channels >= 8192 && channels < 49152;
+  const bool quad = N <= 16 && fills && !alone;
+  plan.ln = quad ? 4 : 16;
+  plan.ns = quad ? 4 : N <= 16 ? 1 : N <= 32 ? 2 : 4;
+  const int ch = (quad ? kQuadThreads : bwd ? kWideThreads : kFwdThreads) / plan.ln;
+  g.cblocks = (g.Cg + ch - 1) / ch;
+  // Segments where the channels leave SIMDs without waves (fewer than three with 4 lanes, two with 16): four then.
+  const long long blocks = (long long)B * G * g.cblocks, full = quad ? 1024 : 16384 / ch;
   g.nseg = 1;
-  if (blocks > 0 && blocks < 192) g.nseg = (int)std::max(1LL, std::min((512 + blocks - 1) / blocks, (long long)g.chunks / 8));
+  if (blocks > 0 && blocks < (quad ? full * 3 / 4 : full * 3 / 8))
+    g.nseg = (int)std::max(1LL, std::min((full + blocks - 1) / blocks, (long long)g.chunks / 8));
   g.seg_chunks = std::max(1, (g.chunks + g.nseg - 1) / g.nseg);
   g.nseg = std::max(1, (g.chunks + g.seg_chunks - 1) / g.seg_chunks);
-  return g;
+  return plan;
 }
 
 struct ScanSizes {
   size_t ends, steps, back, marks, mark_steps, bc, weights;   // floats
 };
-ScanSizes scan_sizes(const ScanGeom& g, bool bwd) {
+ScanSizes scan_sizes(const ScanPlan& plan, bool bwd) {
   auto up = [](size_t n) { return (n + 63) / 64 * 64; };
-  const size_t CN = (size_t)g.C * g.N, segs = (size_t)g.B * g.nseg;
+  const ScanGeom& g = plan.G;
+  const size_t CP = (size_t)g.C * plan.ln * plan.ns, segs = (size_t)g.B * g.nseg;
   ScanSizes s = {};
-  if (g.nseg > 1) s.ends = up(segs * CN), s.steps = up(segs * g.C);
+  if (g.nseg > 1) s.ends = up(segs * CP), s.steps = up(segs * g.C);
   if (!bwd) return s;
-  if (g.nseg > 1) s.back = up(segs * CN), s.mark_steps = up((size_t)g.B * g.chunks * g.C);
-  s.marks = up((size_t)g.B * g.chunks * CN);
+  if (g.nseg > 1) s.back = up(segs * CP), s.mark_steps = up((size_t)g.B * g.chunks * g.C);
+  s.marks = up((size_t)g.B * g.chunks * CP);
   s.bc = up((size_t)g.G * g.cblocks * g.B * g.T * 2 * g.N);
-  s.weights = up(segs * (CN + 2 * (size_t)g.C));
+  s.weights = up(segs * ((size_t)g.C * g.N + 2 * (size_t)g.C));
   return s;
 }
 size_t scan_bytes(const ScanSizes& s) {
   return 4 * (s.ends + s.steps + s.back + s.marks + s.mark_steps + s.bc + s.weights);
 }
 
-ScanLaunch scan_launch(const SelScanArgs& a, bool bwd) {
+ScanLaunch scan_launch(const SelScanArgs& a, const ScanPlan& plan, bool bwd) {
   ScanLaunch L;
   L.a = a;
-  L.G = scan_geom(a.B, a.T, a.C, a.G, a.N);
+  L.G = plan.G;
   L.G.ldbc = a.ldbc, L.G.ldz = a.ldz, L.G.softplus = a.softplus, L.G.pad_zero = a.pad_zero;
   L.segs = L.G.nseg;
-  const ScanSizes s = scan_sizes(L.G, bwd);
+  const ScanSizes s = scan_sizes(plan, bwd);
   float* p = (float*)a.workspace;
   auto take = [&](size_t n) { float* q = n ? p : nullptr; p = n ? p + n : p; return q; };
   L.w.ends = take(s.ends), L.w.steps = take(s.steps), L.w.back = take(s.back), L.w.marks = take(s.marks);
@@ -878,57 +1158,44 @@ unsigned scan_blocks(const ScanLaunch& L) {
   return (unsigned)((total + 7) / 8 * 8);
 }
 
-template <bool BACK> hipError_t launch_join(const ScanLaunch& L) {
-  const unsigned blocks = (unsigned)(((long long)L.G.B * L.G.C * L.G.N + 255) / 256);
-  if (L.a.dtype == CKDA_DTYPE_F32) hipLaunchKernelGGL((scan_join_kernel<true, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L);
-  else hipLaunchKernelGGL((scan_join_kernel<false, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L);
+template <bool BACK> hipError_t launch_join(const ScanLaunch& L, int P) {
+  const unsigned blocks = (unsigned)(((long long)L.G.B * L.G.C * P + 255) / 256);
+  if (L.a.dtype == CKDA_DTYPE_F32) hipLaunchKernelGGL((scan_join_kernel<true, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L, P);
+  else hipLaunchKernelGGL((scan_join_kernel<false, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L, P);
   return hipGetLastError();
 }
 
-// Channels of the forward's workgroups: 16 rather than the backward's 32 (which share one part of dB and dC), for
-// barriers among fewer waves (MI355X, us, 16 and 32 channels: B4 T4096 C2048 N16 233 and 243, B16 T1024 C4096 339
-// and 357, B2 T2048 C2048 N64 221 and 270; 8 channels are slower again, 237, 367 and 261).
-constexpr int kFwdCh = 16;
-template <typename T, int NS> hipError_t launch_fwd_t(const SelScanArgs& a) {
-  ScanLaunch L = scan_launch(a, false);
-  L.G.cblocks = (L.G.Cg + kFwdCh - 1) / kFwdCh;
+template <typename T, int LN, int NS> hipError_t launch_fwd_t(const SelScanArgs& a, const ScanPlan& plan) {
+  constexpr int SUBS = LN == 4 ? 1 : 2;   // a tile of 64 channels and 16 rows, or 16 and 32
+  ScanLaunch L = scan_launch(a, plan, false);
   if (L.G.nseg > 1) {
     L.segs = L.G.nseg - 1;
-    hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, false, false, true>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
+    hipLaunchKernelGGL((scan_fwd_kernel<T, LN, NS, kFwdThreads, SUBS, false>), dim3(scan_blocks(L)), dim3(kFwdThreads), 0, a.stream, L);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess) e = launch_join<false>(L);
+    if (e == hipSuccess) e = launch_join<false>(L, LN * NS);
     if (e != hipSuccess) return e;
     L.segs = L.G.nseg;
   }
-  hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kFwdCh, true, false, false>), dim3(scan_blocks(L)), dim3(kRows * kFwdCh), 0, a.stream, L);
+  hipLaunchKernelGGL((scan_fwd_kernel<T, LN, NS, kFwdThreads, SUBS, true>), dim3(scan_blocks(L)), dim3(kFwdThreads), 0, a.stream, L);
   return hipGetLastError();
 }
 
-template <typename T, int NS, bool MAIN> void launch_bwd_kernel(const ScanLaunch& L) {
-  if (L.a.z)
-    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, MAIN, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, L.a.stream, L);
-  else
-    hipLaunchKernelGGL((scan_bwd_kernel<T, NS, MAIN, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, L.a.stream, L);
-}
-
-template <typename T, int NS> hipError_t launch_bwd_t(const SelScanArgs& a) {
-  ScanLaunch L = scan_launch(a, true);
+template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs& a, const ScanPlan& plan) {
+  constexpr int THREADS = LN == 4 ? kQuadThreads : kWideThreads;
+  const ScanLaunch L = scan_launch(a, plan, true);
+  const dim3 grid(scan_blocks(L)), block(THREADS);
   hipError_t e = hipSuccess;
   if (L.G.B > 0) {
-    if (L.G.nseg > 1)
-      hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true, true>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
-    else
-      hipLaunchKernelGGL((scan_fwd_kernel<T, NS, kCh, false, true, false>), dim3(scan_blocks(L)), dim3(kScanThreads), 0, a.stream, L);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
     if (L.G.nseg > 1) {
-      if ((e = launch_join<false>(L)) != hipSuccess) return e;
-      L.segs = L.G.nseg - 1;
-      launch_bwd_kernel<T, NS, false>(L);
+      hipLaunchKernelGGL((scan_prep_kernel<T, LN, NS, THREADS, true>), grid, block, 0, a.stream, L);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      if ((e = launch_join<true>(L)) != hipSuccess) return e;
-      L.segs = L.G.nseg;
+      if ((e = launch_join<false>(L, LN * NS)) != hipSuccess || (e = launch_join<true>(L, LN * NS)) != hipSuccess) return e;
+    } else {
+      hipLaunchKernelGGL((scan_prep_kernel<T, LN, NS, THREADS, false>), grid, block, 0, a.stream, L);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    launch_bwd_kernel<T, NS, true>(L);
+    if (a.z) hipLaunchKernelGGL((scan_bwd_kernel<T, LN, NS, THREADS, true>), grid, block, 0, a.stream, L);
+    else hipLaunchKernelGGL((scan_bwd_kernel<T, LN, NS, THREADS, false>), grid, block, 0, a.stream, L);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
     if (each > 0) {
@@ -943,7 +1210,7 @@ template <typename T, int NS> hipError_t launch_bwd_t(const SelScanArgs& a) {
 // Two sequences a thread where that leaves threads enough (MI355X, us, one and two: 256 sequences of 4096 channels
 // with 16 states 32.5 and 28, 64 of 2048 with 64 states 19.1 and 17).
 template <typename T, int LPC, bool WHOLE> hipError_t launch_decode_t(const SelScanArgs& a) {
-  const ScanLaunch L = scan_launch(a, false);
+  const ScanLaunch L = scan_launch(a, scan_plan(a.B, a.T, a.C, a.G, a.N, false), false);
   const bool many = (long long)a.B * a.C * LPC >= 1 << 20;
   const long long groups = many ? (a.B + 1) / 2 : a.B;
   const unsigned blocks = (unsigned)((groups * a.C * LPC + 255) / 256);
@@ -952,10 +1219,17 @@ template <typename T, int LPC, bool WHOLE> hipError_t launch_decode_t(const SelS
   return hipGetLastError();
 }
 
-template <typename T> hipError_t launch_scan(const SelScanArgs& a, bool bwd) {
-  if (a.N <= 16) return bwd ? launch_bwd_t<T, 1>(a) : launch_fwd_t<T, 1>(a);
-  if (a.N <= 32) return bwd ? launch_bwd_t<T, 2>(a) : launch_fwd_t<T, 2>(a);
-  return bwd ? launch_bwd_t<T, 4>(a) : launch_fwd_t<T, 4>(a);
+template <typename T> hipError_t launch_scan_fwd_t(const SelScanArgs& a) {
+  const ScanPlan plan = scan_plan(a.B, a.T, a.C, a.G, a.N, false);
+  if (plan.ln == 4) return launch_fwd_t<T, 4, 4>(a, plan);
+  if (plan.ns == 1) return launch_fwd_t<T, 16, 1>(a, plan);
+  return plan.ns == 2 ? launch_fwd_t<T, 16, 2>(a, plan) : launch_fwd_t<T, 16, 4>(a, plan);
+}
+template <typename T> hipError_t launch_scan_bwd_t(const SelScanArgs& a) {
+  const ScanPlan plan = scan_plan(a.B, a.T, a.C, a.G, a.N, true);
+  if (plan.ln == 4) return launch_bwd_t<T, 4, 4>(a, plan);
+  if (plan.ns == 1) return launch_bwd_t<T, 16, 1>(a, plan);
+  return plan.ns == 2 ? launch_bwd_t<T, 16, 2>(a, plan) : launch_bwd_t<T, 16, 4>(a, plan);
 }
 
 template <typename T, bool WHOLE> hipError_t launch_decode_n(const SelScanArgs& a) {
@@ -972,25 +1246,25 @@ template <typename T> hipError_t launch_decode(const SelScanArgs& a) {
 }  // namespace
 
 size_t scan_fwd_workspace_bytes(int B, int T, int C, int G, int N) {
-  return scan_bytes(scan_sizes(scan_geom(B, T, C, G, N), false));
+  return scan_bytes(scan_sizes(scan_plan(B, T, C, G, N, false), false));
 }
 size_t scan_bwd_workspace_bytes(int B, int T, int C, int G, int N) {
-  return scan_bytes(scan_sizes(scan_geom(B, T, C, G, N), true));
+  return scan_bytes(scan_sizes(scan_plan(B, T, C, G, N, true), true));
 }
 
 // fewer than 2^32 threads in every launch, and counts of workgroups in an int
 bool scan_fits_grid(int B, int T, int C, int G, int N) {
-  const ScanGeom g = scan_geom(B, T, C, G, N);
-  const long long blocks = (long long)B * g.nseg * G * g.cblocks;
-  return blocks < (1LL << 22) && (long long)B * C * N < (1LL << 31) && (long long)B * C * 16 < (1LL << 31) &&
-         (double)B * T * 2 * G * N < 4e9;
+  const ScanGeom g = scan_plan(B, T, C, G, N, true).G, f = scan_plan(B, T, C, G, N, false).G;
+  const long long groups = (long long)B * G;
+  return groups * g.nseg * g.cblocks < (1LL << 22) && groups * f.nseg * f.cblocks < (1LL << 22) &&
+         (long long)B * C * 64 < (1LL << 32) && (double)B * T * 2 * G * N < 4e9;
 }
 
 hipError_t launch_scan_fwd(const SelScanArgs& a) {
-  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan<bf16_t>(a, false) : launch_scan<float>(a, false);
+  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan_fwd_t<bf16_t>(a) : launch_scan_fwd_t<float>(a);
 }
 hipError_t launch_scan_bwd(const SelScanArgs& a) {
-  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan<bf16_t>(a, true) : launch_scan<float>(a, true);
+  return a.dtype == CKDA_DTYPE_BF16 ? launch_scan_bwd_t<bf16_t>(a) : launch_scan_bwd_t<float>(a);
 }
 hipError_t launch_scan_decode(const SelScanArgs& a) {
   return a.dtype == CKDA_DTYPE_BF16 ? launch_decode<bf16_t>(a) : launch_decode<float>(a);

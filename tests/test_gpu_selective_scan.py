@@ -142,6 +142,20 @@ def test_many_workgroups(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,T,C,G,N,kw", [(1000, 20, 50, 1, 16, {}), (1000, 33, 50, 2, 5, dict(lens=True)),
+                                          (1000, 18, 51, 1, 12, dict(gate=False, state=False)), (16, 2060, 130, 1, 16, {}),
+                                          (16, 2100, 130, 2, 7, dict(lens=True, gate=False, D=False)),
+                                          (48, 700, 70, 1, 15, dict(lens=True, state=False))])
+def test_many_channels_or_long_sequences(B, T, C, G, N, kw, dtype):
+    """Four lanes a channel (enough channels and rows for every SIMD), with one segment and with several."""
+    if kw.get("lens"):
+        lens = np.random.default_rng(T).integers(0, T + 1, B)
+        lens[:3] = T, 0, 1
+        kw = dict(kw, lens=lens.tolist())
+    run(T, B, T, C, G, N, dtype, **kw)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("C,G,N", [(1, 1, 16), (40, 2, 16), (33, 1, 1), (5, 5, 3), (12, 1, 8), (7, 1, 17), (9, 3, 64), (4, 1, 33)])
 def test_decode_continues_the_forward(C, G, N, dtype):
     T, S = 9, 3
