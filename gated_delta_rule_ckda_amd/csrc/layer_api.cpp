@@ -228,8 +228,9 @@ int ckda_selective_scan_bwd(const void* x, const void* dt, const float* A, const
   const bool rows_there = B > 0 && T > 0;
   // gradients of the weights exist (as zeros) without rows, and so does the initial state's; dBm and dCm are
   // zero where there are rows but no channels
-  if (C == 0 || (!rows_there && !dA && !dD && !ddt_bias && (B == 0 || !dh0))) return ok();
-  if (!A || (rows_there && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || !dBm || !dCm || (z && !dz))))
+  if (!rows_there && (C == 0 || (!dA && !dD && !ddt_bias && (B == 0 || !dh0)))) return ok();
+  if ((C > 0 && !A) || (rows_there && (!dBm || !dCm)) ||
+      (rows_there && C > 0 && (!x || !dt || !Bm || !Cm || !dy || !dx || !ddt || (z && !dz))))
     return fail(CKDA_ERR_NULL, "%s: x, dt, A, Bm, Cm, dy and the gradients of x, dt, Bm, Cm (and z) are required", fn);
   if ((st = scan_grid(fn, B, T, C, G, N)) != CKDA_OK) return st;
   const size_t need = ckda_selective_scan_bwd_workspace_size(B, T, C, G, N, dtype);

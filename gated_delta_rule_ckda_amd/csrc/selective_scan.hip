@@ -1185,7 +1185,7 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
   const ScanLaunch L = scan_launch(a, plan, true);
   const dim3 grid(scan_blocks(L)), block(THREADS);
   hipError_t e = hipSuccess;
-  if (L.G.B > 0) {
+  if (L.G.B > 0 && L.G.C > 0) {
     if (L.G.nseg > 1) {
       hipLaunchKernelGGL((scan_prep_kernel<T, LN, NS, THREADS, true>), grid, block, 0, a.stream, L);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1197,11 +1197,11 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
     if (a.z) hipLaunchKernelGGL((scan_bwd_kernel<T, LN, NS, THREADS, true>), grid, block, 0, a.stream, L);
     else hipLaunchKernelGGL((scan_bwd_kernel<T, LN, NS, THREADS, false>), grid, block, 0, a.stream, L);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
-    if (each > 0) {
-      hipLaunchKernelGGL((scan_bc_kernel<T>), dim3((unsigned)((each + 255) / 256)), dim3(256), 0, a.stream, L);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+  }
+  const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
+  if (each > 0) {   // (without channels: zeros)
+    hipLaunchKernelGGL((scan_bc_kernel<T>), dim3((unsigned)((each + 255) / 256)), dim3(256), 0, a.stream, L);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const size_t CN = (size_t)a.C * a.N, C = (size_t)a.C;
   return launch_part_sums(PartSums{L.w.weights, L.G.B * L.G.nseg, CN + 2 * C, {a.dA, a.dD, a.dbias}, {CN, C, C}}, a.stream);

@@ -189,9 +189,13 @@ def test_empty_calls_are_ok():
     assert conv_bwd(B=0, **none) == 0 and conv_bwd(T=0, **none) == 0 and conv_dec(B=0, **none) == 0
     empty = dict.fromkeys(BWD + ("hT", "H", "y"))
     assert scan(B=0, **empty) == 0 and scan(C=0, ldz=0, **empty) == 0 and scan(T=0, **empty) == 0
-    assert scan_bwd(B=0, **empty) == 0 and scan_dec(B=0, **empty) == 0
+    assert scan_bwd(B=0, **empty) == 0 and scan_bwd(C=0, T=0, ldz=0, **empty) == 0 and scan_dec(B=0, **empty) == 0
     assert norm(R=0, x=None, y=None, q=None, scales=None) == 0 and norm_bwd(R=0, dw=None) == 0
     assert ck.lib().ckda_last_error() == b""
+
+
+def test_scan_bwd_without_channels_needs_the_sums_over_them():
+    assert scan_bwd(C=0, ldz=0, dBm=None) == ck.ERR_NULL and scan_bwd(C=0, ldz=0, dCm=None) == ck.ERR_NULL
 
 
 def test_workspace_sizes():
