@@ -147,7 +147,7 @@ static int scan_check(const char* fn, int B, int T, int C, int G, int N, int ldb
   if (N < 1 || N > 64) return fail(CKDA_ERR_UNSUPPORTED, "%s: N=%d (supported: 1 .. 64)", fn, N);
   if (!supported_dtype(dtype)) return fail(CKDA_ERR_UNSUPPORTED, "%s: dtype %d is not F32(0) or BF16(1)", fn, dtype);
   if (C >= kMostChannels) return fail(CKDA_ERR_DIM, "%s: C=%d not below 2^24", fn, C);
-  if ((long long)ldbc < (long long)G * N) return fail(CKDA_ERR_DIM, "%s: row stride ldbc=%d below G*N=%d", fn, ldbc, G * N);
+  if ((long long)ldbc < (long long)G * N) return fail(CKDA_ERR_DIM, "%s: row stride ldbc=%d below G*N=%lld", fn, ldbc, (long long)G * N);
   if (ldbc >= kMostChannels || (gate && ldz >= kMostChannels))
     return fail(CKDA_ERR_DIM, "%s: row strides ldbc=%d, ldz=%d must be below 2^24", fn, ldbc, ldz);
   if (gate && ldz < C) return fail(CKDA_ERR_DIM, "%s: row stride ldz=%d below C=%d", fn, ldz, C);

@@ -1212,7 +1212,7 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
 template <typename T, int LPC, bool WHOLE> hipError_t launch_decode_t(const SelScanArgs& a) {
   const ScanLaunch L = scan_launch(a, scan_plan(a.B, a.T, a.C, a.G, a.N, false), false);
   const bool many = (long long)a.B * a.C * LPC >= 1 << 20;
-  const long long groups = many ? (a.B + 1) / 2 : a.B;
+  const long long groups = many ? ((long long)a.B + 1) / 2 : a.B;
   const unsigned blocks = (unsigned)((groups * a.C * LPC + 255) / 256);
   if (many) hipLaunchKernelGGL((scan_decode_kernel<T, LPC, WHOLE, 2>), dim3(blocks), dim3(256), 0, a.stream, L);
   else hipLaunchKernelGGL((scan_decode_kernel<T, LPC, WHOLE, 1>), dim3(blocks), dim3(256), 0, a.stream, L);

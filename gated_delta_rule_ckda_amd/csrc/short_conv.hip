@@ -45,9 +45,9 @@ struct ConvGeom {
 // CUs; by the pieces of 512 channels, so that the sums' parts do not depend on
 // how the channels can be read.
 int conv_rows(int B, int T, int C) {
-  const long long pieces = (C + 511) / 512;
+  const double pieces = (double)B * ((C + 511) / 512);   // (of sizes that are refused too)
   int rows = 32;
-  while (rows > 4 && (long long)B * ((T + rows - 1) / rows) * pieces < 2048) rows /= 2;
+  while (rows > 4 && pieces * ((T + rows - 1) / rows) < 2048) rows /= 2;
   return rows;
 }
 
@@ -367,7 +367,7 @@ template <ConvOp OP, typename T, int VEC, int K, bool SILU> hipError_t launch_co
   if constexpr (OP == ConvOp::decode) {
     const int pieces = (a.C + VEC - 1) / VEC;
     const int each = (int)std::max(1LL, std::min(4LL, (long long)a.B * pieces / 65536));
-    const long long blocks = ((long long)(a.B + each - 1) / each * pieces + kConvThreads - 1) / kConvThreads;
+    const long long blocks = (((long long)a.B + each - 1) / each * pieces + kConvThreads - 1) / kConvThreads;
     hipLaunchKernelGGL((conv_decode_kernel<T, VEC, K, SILU>), dim3((unsigned)blocks), dim3(kConvThreads), 0, a.stream,
                        (const T*)a.x, a.w, a.b, (T*)a.state, (T*)a.y, a.B, a.C, pieces, a.ldx, each);
     return hipGetLastError();
