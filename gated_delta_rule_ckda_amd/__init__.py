@@ -724,12 +724,23 @@ def head_norm_bwd(x, dy, w=None, b=None, gate=None, act="silu", rms=False, eps=1
 
 # ---------------------------------------------------------------- around the recurrence in a layer
 
+def _like(t, stream):
+    """_fresh in the shape and type of `t`, which is contiguous (0.5 us less than by shape, dtype and device)."""
+    return torch.empty_like(t) if stream is None else _fresh(t.shape, t.dtype, t.device, stream)
+
+
 def _slice_of(device, name, t, shape, dtype, rows, width):
     """Row stride of t, a column slice of a contiguous tensor: of `shape`, whose
     first `rows` dimensions count rows and whose others are `width` elements next
     to each other."""
-    if t.shape == shape and t.dtype == dtype and t.is_contiguous() and t.get_device() == device.index:
-        return width
+    if t.shape == shape and t.dtype == dtype and t.get_device() == device.index:   # the usual ones first
+        if t.is_contiguous():
+            return width
+        st = t.stride()
+        ld = st[rows - 1]
+        if (st[-1] == 1 and width <= ld < 2 ** 31 and (rows == 1 or st[0] == ld * shape[1])
+                and (len(st) == rows + 1 or st[-2] == shape[-1])):
+            return ld
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda:
@@ -832,7 +843,7 @@ def short_conv_decode_step(x, w, state, b=None, heads=1, act="silu", y=None, str
     ldx = _slice_of(dev, "x", x, (N, C), dt, 1, C)
     code = _dtype_code(x)
     if y is None:
-        y = _fresh((N, heads, Dh), dt, dev, stream)
+        y = x.new_empty((N, heads, Dh)) if stream is None else _fresh((N, heads, Dh), dt, dev, stream)
     _run(dev, stream, lib().ckda_short_conv_decode_step, x.data_ptr(), w.data_ptr(), _ptr(b), state.data_ptr(), y.data_ptr(),
          N, C, K, ldx, code, flags)
     return y
@@ -887,7 +898,7 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, 
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} G={G} N={N}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     if y is None:
-        y = _fresh((B, T, C), x.dtype, dev, stream)
+        y = _like(x, stream)
         flags |= PAD_ZERO
     if hT is None and want_state:
         hT = _fresh((B, C, N), f32, dev, stream)
@@ -933,23 +944,24 @@ def selective_scan_decode_step(x, dt, A, Bm, Cm, H, D=None, z=None, dt_bias=None
         ("H", H, (r[0], C, N), torch.float32), ("y", y, (r[0], C), x.dtype)], 1)
     dev, code = x.device, _dtype_code(x)
     if y is None:
-        y = _fresh((S, C), x.dtype, dev, stream)
+        y = _like(x, stream)
     _run(dev, stream, lib().ckda_selective_scan_decode_step, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(),
          Cm.data_ptr(), _ptr(D), _ptr(z), _ptr(dt_bias), H.data_ptr(), y.data_ptr(), S, C, G, N, ldbc, ldz, code,
          SCAN_SOFTPLUS if softplus else 0)
     return y
 
 
-def _add_norm_args(x, res, w, total):
+def _add_norm_args(x, res, w, total, more=lambda shape, D: ()):
     """(rows, D, residual's dtype) of x [..., D] with a residual of the same shape."""
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"x must have rows of at least one element, got shape {tuple(x.shape)}")
-    D = x.shape[-1]
-    rt = x.dtype if res is None and total is None else (res if res is not None else total).dtype
-    if rt not in (x.dtype, torch.float32):
-        raise TypeError(f"the residual must be {x.dtype} or float32, got {rt}")
-    _tensors(x.device, [("x", x, x.shape, x.dtype), ("res", res, x.shape, rt), ("w", w, (D,), torch.float32),
-                        ("total", total, x.shape, rt)])
+    shape, t = x.shape, x.dtype
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError(f"x must have rows of at least one element, got shape {tuple(shape)}")
+    D = shape[-1]
+    rt = res.dtype if res is not None else t if total is None else total.dtype
+    if rt != t and rt != torch.float32:
+        raise TypeError(f"the residual must be {t} or float32, got {rt}")
+    _tensors(x.device, [("x", x, shape, t), ("res", res, shape, rt), ("w", w, (D,), torch.float32), ("total", total, shape, rt),
+                        *more(shape, D)])
     return x.numel() // D, D, rt
 
 
@@ -960,13 +972,12 @@ def add_norm_fwd(x, res=None, w=None, eps=1e-6, y=None, total=None, stream=None)
     x [...,D]; res of the same shape, in x's dtype or fp32, or None; w [D] fp32 or
     None.  Returns (y in x's dtype, r in the residual's dtype; None without res
     unless `total` is passed in).  total may be res."""
-    R, D, rt = _add_norm_args(x, res, w, total)
+    R, D, rt = _add_norm_args(x, res, w, total, lambda shape, D: [("y", y, shape, x.dtype)])
     dev, code = x.device, _dtype_code(x)
-    _tensors(dev, [("y", y, x.shape, x.dtype)])
     if y is None:
-        y = _fresh(x.shape, x.dtype, dev, stream)
+        y = _like(x, stream)
     if total is None and res is not None:
-        total = _fresh(x.shape, rt, dev, stream)
+        total = _like(res, stream)
     _run(dev, stream, lib().ckda_add_norm_fwd, x.data_ptr(), _ptr(res), _ptr(w), y.data_ptr(), None, None, _ptr(total), R, D,
          0, code, DTYPE_BF16 if rt == torch.bfloat16 else DTYPE_F32, eps)
     return y, total
@@ -979,16 +990,16 @@ def add_norm_quant_fwd(x, res=None, w=None, eps=1e-6, group=128, q=None, scales=
     whole row (group=0), max |y| / 448."""
     if group not in (0, 128):
         raise ValueError(f"group must be 128 or 0 (a row), got {group}")
-    R, D, rt = _add_norm_args(x, res, w, total)
-    dev, code, e4m3 = x.device, _dtype_code(x), torch.float8_e4m3fn
-    sshape = (*x.shape[:-1], -(-D // group) if group else 1)
-    _tensors(dev, [("q", q, x.shape, e4m3), ("scales", scales, sshape, torch.float32)])
+    e4m3 = torch.float8_e4m3fn
+    groups = lambda shape, D: (*shape[:-1], -(-D // group) if group else 1)  # noqa: E731
+    R, D, rt = _add_norm_args(x, res, w, total, lambda shape, D: [("q", q, shape, e4m3), ("scales", scales, groups(shape, D), torch.float32)])
+    dev, code = x.device, _dtype_code(x)
     if q is None:
         q = _fresh(x.shape, e4m3, dev, stream)
     if scales is None:
-        scales = _fresh(sshape, torch.float32, dev, stream)
+        scales = _fresh(groups(x.shape, D), torch.float32, dev, stream)
     if total is None and res is not None:
-        total = _fresh(x.shape, rt, dev, stream)
+        total = _like(res, stream)
     _run(dev, stream, lib().ckda_add_norm_fwd, x.data_ptr(), _ptr(res), _ptr(w), None, q.data_ptr(), scales.data_ptr(),
          _ptr(total), R, D, group, code, DTYPE_BF16 if rt == torch.bfloat16 else DTYPE_F32, eps)
     return q, scales, total
@@ -1006,8 +1017,8 @@ def add_norm_bwd(total, dy, w=None, dsum=None, eps=1e-6, workspace=None, stream=
     if need == 0:
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes D={D}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
-    dx, dw = _fresh(dy.shape, dy.dtype, dev, stream), _fresh((D,), torch.float32, dev, stream)
-    dres = dx if rt == dy.dtype else _fresh(dy.shape, rt, dev, stream)
+    dx, dw = _like(dy, stream), _fresh((D,), torch.float32, dev, stream)
+    dres = dx if rt == dy.dtype else _like(total, stream)
     _run(dev, stream, L.ckda_add_norm_bwd, total.data_ptr(), _ptr(w), dy.data_ptr(), _ptr(dsum), dx.data_ptr(),
          None if dres is dx else dres.data_ptr(), dw.data_ptr(), R, D, code, rcode, eps, *ws)
     return dx, dres, dw
