@@ -34,8 +34,8 @@
 // Few channels and many rows: the sequence runs in segments.  A first pass makes
 // each segment's own end state, a second joins them (a segment's decay is exp(A
 // sum d), closed), the main pass starts from the joined states.  The backward needs
-// the states in reverse: a pass forward in time stores them every 16 rows (of its
-// segment, joined when read), and the main pass recomputes 16 rows in registers.  The
+// the states in reverse: a pass forward in time stores them every 16 rows (8 with 4
+// lanes; of its segment, joined when read), and the main pass recomputes the others in registers.  The
 // segments' own gradient states, sum_t (a_1 .. a_t) ds_t C_t, take no second
 // exponential: the same pass sums them with the running product of its decays.
 #include <limits.h>
@@ -75,6 +75,7 @@ template <int LN, int NS> struct Layout {
   static constexpr int kBlockRows = NS == 4 ? 1 : kRows / NS;   // rows whose B and C are read together,
   static constexpr int kBlock = kBlockRows * NS;                // and the values of a lane in them
   static constexpr int kBlocks = kRows / kBlockRows;            // of a chunk
+  static constexpr int kMarks = LN == 4 ? 2 : 1;                // states of a chunk that the backward's first pass leaves
 };
 
 // lane J's value of each DPP row, in all of its 16 lanes
@@ -176,28 +177,36 @@ __device__ __forceinline__ void sum_quads(const float (&x)[4], const float (&y)[
 
 // ---------------------------------------------------------------- elements
 
-// exp(-|v|), to a few 2^-24 (the product with log2 e in two parts)
-__device__ __forceinline__ float exp_neg_abs(float v) {
+// exp(-|v|): with fp32 inputs to a few 2^-24 (the product with log2 e in two parts),
+// with bf16 ones to (|v| + 2) 2^-24.
+template <bool EXACT> __device__ __forceinline__ float exp_neg_abs(float v) {
+  if constexpr (!EXACT) return __builtin_amdgcn_exp2f(fabsf(v) * -kLog2e);
   const float m = fminf(fabsf(v), 200.f), t = -m * kLog2e;
   const float lo = __builtin_fmaf(-m, kLog2eLo, __builtin_fmaf(-m, kLog2e, -t));
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, lo * kLn2, e);
 }
-// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), by the series of log((1 +
-// r) / (1 - r)) in r = e / (2 + e) <= 1/3 (next term 2^-26 of the first): small
-// steps keep their relative accuracy, which log(1 + e) does not.
-__device__ __forceinline__ float softplus(float v) {
-  const float e = exp_neg_abs(v), r = e * __builtin_amdgcn_rcpf(2.f + e), z = r * r;
-  float p = 1.f / 13.f;
-  p = __builtin_fmaf(p, z, 1.f / 11.f);
-  p = __builtin_fmaf(p, z, 1.f / 9.f);
-  p = __builtin_fmaf(p, z, 1.f / 7.f);
-  p = __builtin_fmaf(p, z, 1.f / 5.f);
-  p = __builtin_fmaf(p, z, 1.f / 3.f);
-  return (v < 0.f ? 0.f : v) + 2.f * __builtin_fmaf(r * z, p, r);   // (a NaN stays one)
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|), with log((1 + r) / (1 - r)) =
+// 2 r (1 + z f(z)), r = e / (2 + e) <= 1/3, z = r^2: small steps keep their relative
+// accuracy, which log(1 + e) does not.  f is a polynomial fitted to least largest error
+// over z <= 1/9: 2^-27 of the whole for fp32 inputs, 2^-22 for bf16.
+template <bool EXACT> __device__ __forceinline__ float softplus(float v) {
+  const float e = exp_neg_abs<EXACT>(v), r = e * __builtin_amdgcn_rcpf(2.f + e), z = r * r;
+  float p, most;
+  if constexpr (EXACT) {
+    p = __builtin_fmaf(0.14005993f, z, 0.14000903f);
+    p = __builtin_fmaf(p, z, 0.20010763f);
+    p = __builtin_fmaf(p, z, 0.33333209f);
+    most = v < 0.f ? 0.f : v;   // (a NaN stays one)
+  } else {
+    p = __builtin_fmaf(0.16991776f, z, 0.19817986f);
+    p = __builtin_fmaf(p, z, 0.33336741f);
+    most = fmaxf(v, 0.f);       // (a NaN stays one in e)
+  }
+  return __builtin_fmaf(2.f, __builtin_fmaf(r * z, p, r), most);
 }
-__device__ __forceinline__ float softplus_slope(float v) {
-  const float e = exp_neg_abs(v), r = __builtin_amdgcn_rcpf(1.f + e);
+template <bool EXACT> __device__ __forceinline__ float softplus_slope(float v) {
+  const float e = exp_neg_abs<EXACT>(v), r = __builtin_amdgcn_rcpf(1.f + e);
   return v >= 0.f ? r : e * r;
 }
 
@@ -244,8 +253,8 @@ struct ScanWork {            // workspace of a call; P = a layout's states
   float* ends;               // [B][nseg][C][P]: segments' own end states, then start states
   float* steps;              // [B][nseg][C]: sums of d over the segments
   float* back;               // [B][nseg][C][P]: backward in time
-  float* marks;              // [B][chunks][C][P]: states before each chunk, of their segment
-  float* mark_steps;         // [B][chunks][C]: sums of d from the segment's start to each chunk (nseg > 1)
+  float* marks;              // [B][chunks kMarks][C][P]: states before each chunk (and in its middle), of their segment
+  float* mark_steps;         // [B][chunks kMarks][C]: sums of d from the segment's start to each of those (nseg > 1)
   float* bc;                 // [G cblocks][B T][2][N]: parts of dC, dB
   float* weights;            // [B nseg][C N + 2 C]: parts of dA, dD, dbias
 };
@@ -449,7 +458,7 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_fwd_kernel(c
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       float d = value_of<T>(dr[i]) + bias;
-      if (G.softplus) d = softplus(d);
+      if (G.softplus) d = softplus<EXACT>(d);
       d = tile_on && t0 + i * LN + r < end ? d : 0.f;   // a step of zero leaves the state
       s_d[buf][i / REGS][ch][i % REGS * LN + r] = float2{d, d * value_of<T>(xr[i])};
     }
@@ -564,7 +573,7 @@ template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_joi
 // ---------------------------------------------------------------- backward
 
 // What the main pass needs from a pass forward in time: the states before each chunk
-// and, of several segments (SEGS), each segment's own end state, its sum of steps, and
+// (with 4 lanes also in its middle: the main pass has registers for the states of 8 rows) and, of several segments (SEGS), each segment's own end state, its sum of steps, and
 // its own gradient state (of the state before it, from its rows alone).
 template <typename T, int LN, int NS, int THREADS, bool SEGS>
 __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(const ScanLaunch L) {
@@ -597,7 +606,9 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(
   const size_t first = (size_t)p.b * G.T;
   const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
   const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
-  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * P), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  constexpr int MARKS = Lay::kMarks;
+  const size_t first_mark = (size_t)p.b * G.chunks * MARKS;
+  const Rows<float> marks(L.w.marks, first_mark, G.C * P), mark_sums(L.w.mark_steps, first_mark, G.C);
   const int moff = on ? (cm * P + l * NS) * 4 : kNowhere;
   int off[REGS], zoff[REGS];
 #pragma unroll
@@ -625,7 +636,7 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(
 #pragma unroll
     for (int i = 0; i < REGS; ++i) {
       float d = value_of<T>(dr[i]) + bias;
-      if (G.softplus) d = softplus(d);
+      if (G.softplus) d = softplus<EXACT>(d);
       d = tile_on && chunk * kRows + i * LN + r < p.len ? d : 0.f;
       s_d[buf][ch][i * LN + r] = float2{d, d * value_of<T>(xr[i])};
       if constexpr (SEGS) {
@@ -644,8 +655,6 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(
   int buf = 0;
   for (int k = p.ch0; k < p.ch1; ++k, buf ^= 1) {
     fetch(k + 1);
-    store_states<NS>(marks.tile(k, 1), moff, h);
-    if constexpr (SEGS) store_elem<float>(mark_sums.tile(k, 1), on && l == 0 ? cm * 4 : kNowhere, steps);
     const float* one = s_bc[buf];
     float d[REGS], dx[REGS], ds[REGS], Bv[2][Lay::kBlock], Cv[2][Lay::kBlock];
     load_block<LN, NS, 0>(Bv[0], one);
@@ -663,11 +672,16 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_prep_kernel(
         if constexpr (SEGS) load_block<LN, NS, b + 1>(Cv[(b + 1) % 2], one + kRows * P);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (SEGS && b == 0) {
-        float sum = d[0];
+      if constexpr (b % (Lay::kBlocks / MARKS) == 0) {
+        constexpr int m = b / (Lay::kBlocks / MARKS), q0 = m * REGS / MARKS;
+        store_states<NS>(marks.tile(k * MARKS + m, 1), moff, h);
+        if constexpr (SEGS) {
+          store_elem<float>(mark_sums.tile(k * MARKS + m, 1), on && l == 0 ? cm * 4 : kNowhere, steps);
+          float sum = d[q0];
 #pragma unroll
-        for (int q = 1; q < REGS; ++q) sum += d[q];
-        steps += group_sum<LN>(sum);
+          for (int q = 1; q < REGS / MARKS; ++q) sum += d[q0 + q];
+          steps += group_sum<LN>(sum);
+        }
       }
       each<R>([&](auto J) {
         constexpr int j = b * R + J;
@@ -722,10 +736,10 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
   constexpr bool EXACT = sizeof(T) == 4;
   constexpr bool AHEAD = LN != 4;   // the next chunk's rows are loaded ahead (with 4 lanes other waves fill the wait)
   constexpr bool KEEP = NS <= 2;   // the decays of a chunk stay in registers; else they are formed twice
-  constexpr int HALVES = LN == 4 ? 2 : 1, HR = kRows / HALVES;
+  constexpr int HALVES = Lay::kMarks, HR = kRows / HALVES;   // rows whose states are in registers at a time
   constexpr int CH = THREADS / LN, REGS = Lay::kRegs, P = Lay::kStates, WAVES = THREADS / 64;
   constexpr int PR = P / 16, kPart = kRows / 2 * PR * 64;   // a wave's dC and dB of a chunk: [row / 2][PR][lane]
-  // (d, d x), then (d u, u), of the same row and channel, which one wave reads and writes; ds, then s
+  // (d, d x), then (d, u), of the same row and channel, which one wave reads and writes; ds, then s
   __shared__ float2 s_d[CH][kPad];
   __shared__ float s_ds[CH][kPad], s_v[CH][kPad];
   __shared__ __attribute__((aligned(16))) float s_bc[kRows * P * 2];
@@ -763,14 +777,15 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
   const Rows<T> xs(a.x, first, G.C), dts(a.dt, first, G.C), dys(a.dy, first, G.C), zs(a.z, first, G.ldz);
   const Rows<T> Bs(a.Bm, first, G.ldbc), Cs(a.Cm, first, G.ldbc);
   const Rows<T> dxs(a.dx, first, G.C), ddts(a.ddt, first, G.C), dzs(a.dz, first, G.C);
-  const Rows<float> marks(L.w.marks, (size_t)p.b * G.chunks, G.C * P), mark_sums(L.w.mark_steps, (size_t)p.b * G.chunks, G.C);
+  const size_t first_mark = (size_t)p.b * G.chunks * HALVES;
+  const Rows<float> marks(L.w.marks, first_mark, G.C * P), mark_sums(L.w.mark_steps, first_mark, G.C);
   int off[REGS], zoff[REGS];
 #pragma unroll
   for (int i = 0; i < REGS; ++i) {
     off[i] = tile_on ? ((i * LN + r) * G.C + ct) * (int)sizeof(T) : kNowhere;
     zoff[i] = tile_on ? ((i * LN + r) * G.ldz + ct) * (int)sizeof(T) : kNowhere;
   }
-  uint32_t xr[REGS], dr[REGS], zr[REGS] = {}, gr[REGS], mark[NS], mark_steps;
+  uint32_t xr[REGS], dr[REGS], zr[REGS] = {}, gr[REGS], mark[HALVES][NS], mark_steps[HALVES];
   BcTile<T, LN, NS, 1, THREADS, 3> bc;
   bc.place(L, p);
   auto fetch = [&](int chunk) {   // (before the segment's first chunk: nothing; no branch around the loads)
@@ -783,8 +798,11 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
       if (GATE) zr[i] = load_raw<T>(zs.tile(row, rows), zoff[i]);
     }
     bc.fetch(Bs, Cs, row, rows);
-    load_states<NS>(mark, marks.tile(chunk, rows > 0), on ? (cm * P + l * NS) * 4 : kNowhere);
-    mark_steps = load_raw<float>(mark_sums.tile(chunk, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
+#pragma unroll
+    for (int m = 0; m < HALVES; ++m) {
+      load_states<NS>(mark[m], marks.tile(chunk * HALVES + m, rows > 0), on ? (cm * P + l * NS) * 4 : kNowhere);
+      mark_steps[m] = load_raw<float>(mark_sums.tile(chunk * HALVES + m, p.seg > 0 && rows > 0), on ? cm * 4 : kNowhere);
+    }
   };
   if (AHEAD && p.ch0 < p.ch1) fetch(p.ch1 - 1);
   for (int k = p.ch1 - 1; k >= p.ch0; --k) {
@@ -796,19 +814,21 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
     for (int i = 0; i < REGS; ++i) {
       xd[i] = Kept<T>(xr[i], dr[i]), zg[i] = Kept<T>(zr[i], gr[i]);
       float d = value_of<T>(dr[i]) + bias;
-      if (G.softplus) d = softplus(d);
+      if (G.softplus) d = softplus<EXACT>(d);
       d = tile_on && i * LN + r < rows ? d : 0.f;   // (dy, and so ds, is zero behind the rows)
       const float z = value_of<T>(zr[i]);
       s_d[ch][i * LN + r] = float2{d, d * value_of<T>(xr[i])};
       s_ds[ch][i * LN + r] = value_of<T>(gr[i]) * (GATE ? z * row_sigmoid<T>(z) : 1.f);
     }
     bc.stage(s_bc);
-    float hc[NS];   // the state before the chunk
+    float hc[HALVES][NS];   // the states before the chunk and its halves
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      hc[s] = value_of<float>(mark[s]);
-      if (p.seg > 0) hc[s] += Decay<EXACT>(value_of<float>(mark_steps) * A2[s]).of(start[s]);
-    }
+    for (int m = 0; m < HALVES; ++m)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        hc[m][s] = value_of<float>(mark[m][s]);
+        if (p.seg > 0) hc[m][s] += Decay<EXACT>(value_of<float>(mark_steps[m]) * A2[s]).of(start[s]);
+      }
     lds_barrier();
     if (AHEAD) fetch(k - 1);
     float d[REGS], dx[REGS], ds[REGS];
@@ -821,31 +841,12 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
     const float *Bl = s_bc, *Cl = s_bc + kRows * P;
     constexpr int BLK = Lay::kBlocks, R = Lay::kBlockRows;
     float Bv[2][Lay::kBlock], Cv[2][Lay::kBlock];   // of a block of rows, and of the next
-    // The chunk's last half first, from the state in its middle: the states of HR rows are in registers at a time.
-    float hm[NS];
-    if constexpr (HALVES == 2) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s) hm[s] = hc[s];
-      load_block<LN, NS, 0>(Bv[0], Bl);
-      each<BLK / 2>([&](auto K) {
-        constexpr int b = K;
-        if constexpr (b + 1 < BLK / 2) load_block<LN, NS, b + 1>(Bv[(b + 1) % 2], Bl);
-        __builtin_amdgcn_sched_barrier(0);
-        each<R>([&](auto J) {
-          constexpr int j = b * R + J;
-          const float dj = row_value<LN, NS, j>(d), dxj = row_value<LN, NS, j>(dx);
-#pragma unroll
-          for (int s = 0; s < NS; ++s) hm[s] = Decay<EXACT>(dj * A2[s]).of(hm[s], dxj * Bv[b % 2][J * NS + s]);
-        });
-        pin_floats(hm);
-      });
-    }
     float* part = s_part[tid >> 6] + (tid & 63);
     each<HALVES>([&](auto Half) {
       constexpr int half = HALVES - 1 - Half, j0 = half * HR, b0 = half * BLK / HALVES, b1 = b0 + BLK / HALVES;
       Decay<EXACT> e[KEEP ? HR : 1][NS];
       float h[HR][NS], sums[LN], u[LN], v[LN], odd[PR];
-      auto before = [&](int j, int s) { return j > j0 ? h[j - 1 - j0][s] : half ? hm[s] : hc[s]; };
+      auto before = [&](int j, int s) { return j > j0 ? h[j - 1 - j0][s] : hc[half][s]; };
       load_block<LN, NS, b0>(Bv[b0 % 2], Bl);
       if constexpr (GATE) load_block<LN, NS, b0>(Cv[b0 % 2], Cl);
       each<BLK / HALVES>([&](auto K) {
@@ -910,8 +911,7 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
         });
         pin_floats(Q), pin_floats(dA);
         if constexpr (b * R % LN == 0) {   // LN rows done: lane l has those of row b R + l
-          const float uu = turn_lanes<LN>(u, l);
-          s_d[mine][b * R + l] = float2{uu * d[b * R / LN], uu};
+          s_d[mine][b * R + l].y = turn_lanes<LN>(u, l);
           s_v[mine][b * R + l] = turn_lanes<LN>(v, l) * kLn2;
         }
       });
@@ -923,8 +923,8 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
       const float x = xd[i].first(), dy = zg[i].second(), z = zg[i].first();
       const float sg = GATE ? row_sigmoid<T>(z) : 0.f, dsr = GATE ? dy * z * sg : dy;
       const float dd = __builtin_fmaf(x, du.y, s_v[ch][i * LN + r]);
-      const float ddt = G.softplus ? dd * softplus_slope(xd[i].second() + bias) : dd;
-      store_elem<T>(dxs.tile(row0, rows), off[i], __builtin_fmaf(Dc, dsr, du.x));
+      const float ddt = G.softplus ? dd * softplus_slope<EXACT>(xd[i].second() + bias) : dd;
+      store_elem<T>(dxs.tile(row0, rows), off[i], __builtin_fmaf(Dc, dsr, du.x * du.y));
       store_elem<T>(ddts.tile(row0, rows), off[i], ddt);
       if constexpr (GATE)
         store_elem<T>(dzs.tile(row0, rows), off[i], dy * __builtin_fmaf(Dc, x, s_ds[ch][i * LN + r]) * silu_slope(z, sg));
@@ -1057,7 +1057,7 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(const ScanLaunch L) {
     Cr[m].widen(Cv);
     const float x = to_f32(xr[m]);
     float d = to_f32(dr[m]) + bias;
-    if (G.softplus) d = softplus(d);
+    if (G.softplus) d = softplus<EXACT>(d);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       h[m][e] = Decay<EXACT>(d * A2[e]).of(h[m][e], d * x * Bv[e]);
@@ -1110,9 +1110,11 @@ ScanPlan scan_plan(int B, int T, int C, int G, int N, bool bwd) {
   const int ch = (quad ? kQuadThreads : bwd ? kWideThreads : kFwdThreads) / plan.ln;
   g.cblocks = (g.Cg + ch - 1) / ch;
   // Segments where the channels leave SIMDs without waves (fewer than three with 4 lanes, two with 16): four then.
-  const long long blocks = (long long)B * G * g.cblocks, full = quad ? 1024 : 16384 / ch;
+  // The backward's main pass with 4 lanes keeps three: two rounds of those (B4 T4096 C2048: 647, and with 1024
+  // workgroups, a round and a third, 661).
+  const long long blocks = (long long)B * G * g.cblocks, full = !quad ? 16384 / ch : bwd ? 1536 : 1024;
   g.nseg = 1;
-  if (blocks > 0 && blocks < (quad ? full * 3 / 4 : full * 3 / 8))
+  if (blocks > 0 && blocks < (quad ? 768 : full * 3 / 8))
     g.nseg = (int)std::max(1LL, std::min((full + blocks - 1) / blocks, (long long)g.chunks / 8));
   g.seg_chunks = std::max(1, (g.chunks + g.nseg - 1) / g.nseg);
   g.nseg = std::max(1, (g.chunks + g.seg_chunks - 1) / g.seg_chunks);
@@ -1129,8 +1131,9 @@ ScanSizes scan_sizes(const ScanPlan& plan, bool bwd) {
   ScanSizes s = {};
   if (g.nseg > 1) s.ends = up(segs * CP), s.steps = up(segs * g.C);
   if (!bwd) return s;
-  if (g.nseg > 1) s.back = up(segs * CP), s.mark_steps = up((size_t)g.B * g.chunks * g.C);
-  s.marks = up((size_t)g.B * g.chunks * CP);
+  const size_t marks = (size_t)g.chunks * (plan.ln == 4 ? Layout<4, 4>::kMarks : 1);
+  if (g.nseg > 1) s.back = up(segs * CP), s.mark_steps = up((size_t)g.B * marks * g.C);
+  s.marks = up((size_t)g.B * marks * CP);
   s.bc = up((size_t)g.G * g.cblocks * g.B * g.T * 2 * g.N);
   s.weights = up(segs * ((size_t)g.C * g.N + 2 * (size_t)g.C));
   return s;
