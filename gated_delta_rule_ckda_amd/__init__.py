@@ -826,7 +826,7 @@ def short_conv_bwd(x, w, dy, b=None, s0=None, dsT=None, lens=None, act="silu", w
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} K={K}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     dx, ds0 = _fresh((B, T, C), dt, dev, stream), _fresh((B, K - 1, C), dt, dev, stream)
-    dw, db = _fresh((C, K), f32, dev, stream), _fresh((C,), f32, dev, stream)
+    dw, db = _like(w, stream), _fresh((C,), f32, dev, stream)
     _run(dev, stream, L.ckda_short_conv_bwd, x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(s0), _ptr(lens), dy.data_ptr(),
          _ptr(dsT), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ds0.data_ptr(), B, T, C, heads, K, ldx, code,
          flags | PAD_ZERO, *ws)
@@ -925,10 +925,12 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=No
     if need == 0:
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} G={G} N={N}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
-    dx, ddt = (_fresh((B, T, C), t, dev, stream) for _ in range(2))
-    dz = None if z is None else _fresh((B, T, C), t, dev, stream)
-    dBm, dCm = (_fresh((B, T, G, N), t, dev, stream) for _ in range(2))
-    dA, dD, dbias = (_fresh(s, f32, dev, stream) for s in ((C, N), (C,), (C,)))
+    dx, ddt, dA = _like(x, stream), _like(dt, stream), _like(A, stream)
+    dz = None if z is None else _like(x, stream)
+    dBm = _fresh((B, T, G, N), t, dev, stream)
+    dCm = _like(dBm, stream)
+    dD = _fresh((C,), f32, dev, stream)
+    dbias = _like(dD, stream)
     dh0 = _fresh((B, C, N), f32, dev, stream) if want_dh0 else None
     _run(dev, stream, L.ckda_selective_scan_bwd, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
          _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), dy.data_ptr(), _ptr(dhT), dx.data_ptr(), ddt.data_ptr(),

@@ -15,6 +15,10 @@
 // this one; w stays in registers.  In the backward dw does too; a workgroup
 // leaves one part and a second kernel adds them in a fixed order.  All arithmetic
 // is fp32; y, the codes, sum and dr are rounded once, from unrounded values.
+//
+// MI355X, 16384 x 2048 bf16 with an fp32 residual: forward to 8 bits with the sum 89 us
+// (4.2 TB/s of 370 MB; a copy of 2 GiB moves 4.9), backward 118 (114 and 4 for the parts'
+// sums; 4.6 TB/s of 537 MB).  One row: 2.4 us, the rest of its 9 is the call.
 #include <algorithm>
 
 #include "ckda_internal.hpp"

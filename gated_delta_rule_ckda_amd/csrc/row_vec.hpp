@@ -1,6 +1,6 @@
 // row_vec.hpp -- pieces of token-major rows in registers: VEC consecutive
-// elements (16 bytes) at any address that is a multiple of the element's size
-// (global memory takes 16-byte accesses at 2-byte boundaries), the last piece of
+// elements (16 or 8 bytes, or one) at any address that is a multiple of the element's
+// size (global memory takes wide accesses at 2-byte boundaries), the last piece of
 // a row possibly short.  Device code.
 #pragma once
 

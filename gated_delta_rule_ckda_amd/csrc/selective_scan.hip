@@ -10,9 +10,13 @@
 //   dB_t[n] = sum_c d x R,  dC_t[n] = sum_c ds h,  dz = dy (s + D x) silu'(z).
 //
 // Bound by vector instructions: for every (row, channel, state) two products, an
-// exponential and two fused products (MI355X, ns a wave of 64 and a SIMD with waves
-// enough: product 1.0, fused 1.25, exponential 3.5; with a DPP operand 1.9, a select
-// 1.9, a swap of halves 3.4).  So the layout leaves little else to do for each:
+// exponential and two fused products, and whatever else runs for each.  MI355X, B4 T4096
+// C2048 N16 bf16 with the gate: forward 214 us (9.7 instructions for each state of a row,
+// the vector units busy 72% of the time at the two waves a SIMD gets from 8192 channels),
+// backward 647 (a pass forward 181, 10 instructions, and the main pass 440, 27; both with
+// the vector units busy all the time).  Eight issue slots of 16 lanes for a state
+// (the exponential takes four) would be 109 us, HBM 55.  The layout leaves little else to
+// do for each:
 //  * LN neighbouring lanes are one channel, each with NS states in registers, time
 //    down a loop.  4 x 4 for up to 16 states; 16 x 2 and 16 x 4 for up to 32 and 64;
 //    16 x 1 where 4 lanes a channel would leave SIMDs idle and the sequence would
@@ -1084,6 +1088,8 @@ __global__ __launch_bounds__(256) void scan_decode_kernel(const ScanLaunch L) {
 
 // ---------------------------------------------------------------- host
 
+// (the forward with 16 lanes: 16 channels a workgroup; MI355X, us, with 8, 16 and 32: B4 T4096 C2048 237, 233 and
+// 243, of 64 states 261, 221 and 270)
 constexpr int kFwdThreads = 256;                       // of every layout
 constexpr int kQuadThreads = 256, kWideThreads = 512;   // of the backward's passes
 
@@ -1101,7 +1107,7 @@ ScanPlan scan_plan(int B, int T, int C, int G, int N, bool bwd) {
   // 4 lanes a channel where that can fill three waves of every SIMD, by segments of 128 rows or more; but in the
   // forward not where 16 lanes fill two without segments and 4 lanes would need them, which cost a pass of their own
   // (MI355X, us, 4 and 16 lanes: forward B4 T4096 C2048 290 and 224, B16 T1024 C4096 297 and 325, B1 T32768 C1024 280
-  // and 340, B1 T1024 C1024 40 and 24; backward B4 T4096 C2048 697 and 826, fp32 B3 T777 C500 160 and 117).
+  // and 340, B1 T1024 C1024 40 and 24; backward B4 T4096 C2048 697 and 785, fp32 B3 T777 C500 160 and 100).
   const long long channels = (long long)B * C, blocks4 = (long long)B * G * ((g.Cg + 63) / 64);
   const bool fills = blocks4 * std::max(1, g.chunks / 8) >= 768, alone = !bwd && channels >= 8192 && channels < 49152;
   const bool quad = N <= 16 && fills && !alone;

@@ -15,6 +15,13 @@
 // address.  The weights' gradients stay in registers down the slab, are summed
 // over the workgroup's slabs through LDS, and leave one part for each workgroup
 // (at most kMostParts), which a second kernel adds in a fixed order.
+//
+// MI355X, B4 T4096 C2048 K4 bf16 with SiLU: forward 30 us (4.4 TB/s of 134 MB), backward
+// 67 (62 and 5 for the parts' sums; 3.2 TB/s of 201 MB).  The backward has the vector
+// units busy for two thirds of its time (three waves on a SIMD) and still no unit full;
+// shorter slabs, slabs that fill the SIMDs exactly once, an order of the workgroups by
+// L2 and an inner loop without the masks (177 registers instead of 164) gave nothing or
+// lost.  Decode, 256 sequences of 4096 channels: 7 us, of which the launch is most.
 #include <limits.h>
 
 #include <algorithm>

@@ -600,9 +600,9 @@ int ckda_short_conv_decode_step(const void* x, const float* w, const float* b, v
  * Supported: 1 <= N <= 64, any C of which G is a divisor.  A decay is rounded
  * to fp32 at every step (bf16: by the hardware's exponential, 2^-23); with F32
  * a decay near 1 is applied by its distance from 1, so that slow states do not
- * drift.  A non-finite input of a channel leaves that channel's rows from there
+ * drift.  C and both row strides below 2^24, C N below 2^28.  A non-finite input of a channel leaves that channel's rows from there
  * on unspecified (in the backward all of it, and dBm and dCm of the rows where
- * it is summed in). */
+ * it is summed in); one in Bm or Cm does so for its group's channels. */
 #define CKDA_SCAN_SOFTPLUS 1
 
 /* Bytes of device workspace ckda_selective_scan_fwd needs, or 0 for invalid or
@@ -616,8 +616,9 @@ int ckda_selective_scan_fwd(const void* x, const void* dt, const float* A, const
                             int flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace ckda_selective_scan_bwd needs, or 0 for invalid or
- * unsupported sizes: the fp32 states of every 16th row, and dBm and dCm (fp32)
- * of every 32 channels. */
+ * unsupported sizes: fp32 states of every 16th row (every 8th where there are
+ * channels and rows enough for 4 lanes a channel), and dBm and dCm (fp32) of
+ * every 32 (64) channels. */
 size_t ckda_selective_scan_bwd_workspace_size(int B, int T, int C, int G, int N, int dtype);
 
 /* Backward given dy [B, T, C] (dtype) and dhT [B, C, N] fp32 (or NULL for
