@@ -427,7 +427,8 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_fwd_kernel(c
     A2[s] = state ? a.A[(size_t)cm * G.N + n] * kLog2e : 0.f;
     h[s] = 0.f;
     if (state) {
-      if (MAIN && p.seg > 0) h[s] = L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + n];
+      // (of several segments the first one's start too: its h0 may be the hT that the last one writes)
+      if (MAIN && G.nseg > 1) h[s] = L.w.ends[(((size_t)p.b * G.nseg + p.seg) * G.C + cm) * P + n];
       else if (p.seg == 0 && a.h0) h[s] = a.h0[((size_t)p.b * G.C + cm) * G.N + n];
     }
   }
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_fwd_kernel(c
         if (l * NS + s < G.N) a.hT[((size_t)p.b * G.C + cm) * G.N + l * NS + s] = h[s];
     }
     if (G.pad_zero && tile_on) {
-      const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
+      const int to = (int)min(((long long)p.ch0 + G.seg_chunks) * kRows, (long long)G.T);
       for (int t = max(p.len, row0) + r; t < to; t += LN) ((T*)a.y)[((size_t)p.b * G.T + t) * G.C + ct] = from_f32<T>(0.f);
     }
   } else if (on) {
@@ -562,15 +563,25 @@ template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_joi
   const float A2 = L.a.A[(size_t)c * G.N + n] * kLog2e;
   float* own = (BACK ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CP + i % CP;
   const float* steps = L.w.steps + (size_t)b * G.nseg * G.C + c;
-  float h = BACK && L.a.dhT ? L.a.dhT[((size_t)b * G.C + c) * G.N + n] : 0.f;
-  for (int k = 0; k < G.nseg; ++k) {
-    const int seg = BACK ? G.nseg - 1 - k : k;
-    // (of the last one nobody needs the end, and the forward does not make it)
-    const bool last = k == G.nseg - 1;
-    const float next = last ? 0.f : own[(size_t)seg * CP], sum = last ? 0.f : steps[(size_t)seg * G.C];
-    own[(size_t)seg * CP] = h;
-    // (the first segment's own state has the initial one in it already)
-    h = BACK || k ? Decay<EXACT>(sum * A2).of(h) + next : next;
+  const float* first = BACK ? L.a.dhT : L.a.h0;
+  float h = first ? first[((size_t)b * G.C + c) * G.N + n] : 0.f;
+  constexpr int EACH = 8;   // segments whose loads are in flight together (64 segments: 20 us one after the other, 8 so)
+  for (int k0 = 0; k0 < G.nseg; k0 += EACH) {
+    float next[EACH], sum[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      // (of the last one nobody needs the end, and the forward does not make it)
+      const int k = min(k0 + i, G.nseg - 2), seg = BACK ? G.nseg - 1 - k : k;
+      next[i] = own[(size_t)seg * CP], sum[i] = steps[(size_t)seg * G.C];
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int k = k0 + i;
+      if (k >= G.nseg) break;
+      own[(size_t)(BACK ? G.nseg - 1 - k : k) * CP] = h;
+      // (the first segment's own state has the initial one in it already)
+      h = BACK || k ? Decay<EXACT>(sum[i] * A2).of(h) + next[i] : next[i];
+    }
   }
 }
 
@@ -969,7 +980,7 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
   }
   if (G.pad_zero && tile_on) {
     const T zero = from_f32<T>(0.f);
-    const int to = min((p.ch0 + G.seg_chunks) * kRows, G.T);
+    const int to = (int)min(((long long)p.ch0 + G.seg_chunks) * kRows, (long long)G.T);
     for (int t = max(p.len, p.ch0 * kRows) + r; t < to; t += LN) {
       const size_t at = ((size_t)p.b * G.T + t) * G.C + ct;
       ((T*)a.dx)[at] = ((T*)a.ddt)[at] = zero;

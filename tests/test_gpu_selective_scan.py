@@ -215,6 +215,19 @@ def test_no_rows():
     assert all((out[k] == 0).all() for k in (2, 5, 7))
 
 
+@pytest.mark.parametrize("B,T,C,N", [(1, 1500, 20, 16), (1, 1500, 20, 40), (16, 2060, 130, 16), (40, 2060, 130, 16), (2, 30, 24, 16)])
+def test_final_state_in_place_of_the_initial_one(B, T, C, N):
+    a, _, _ = make(9, B, T, C, 1, N, BF)
+    d = cuda(a)
+    want = ck.selective_scan_fwd(**d)
+    h0 = d["h0"].clone()
+    for _ in range(3):
+        d["h0"].copy_(h0)
+        y, hT = ck.selective_scan_fwd(**d, hT=d["h0"])
+        torch.cuda.synchronize()
+        assert hT is d["h0"] and torch.equal(y, want[0]) and torch.equal(hT, want[1])
+
+
 def test_a_channel_with_nan_leaves_the_others():
     """A non-finite input of one channel: the others' outputs, and its own rows before, stay as they were."""
     a, _, _ = make(8, 1, 40, 36, 1, 16, BF)
