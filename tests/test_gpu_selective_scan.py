@@ -171,6 +171,26 @@ def test_decode_continues_the_forward(C, G, N, dtype):
     check("H", H, want["hT"], k * want["shT"])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("S,C,N", [(515, 512, 16), (517, 510, 13), (129, 512, 64), (515, 2052, 3)])
+def test_decode_of_many_sequences(S, C, N, dtype):
+    """Two sequences a thread, their number odd: the same bytes as with the sequences in small calls."""
+    a, _, _ = make(N, S, 1, C, 1, N, dtype)
+    d = {n: t if n in ("A", "D", "dt_bias", "h0") or t is None else t[:, 0].contiguous() for n, t in cuda(a).items() if n != "lens"}
+    H = d.pop("h0")
+    one = H.clone()
+    rest = ("A", "D", "dt_bias")
+    want = torch.cat([ck.selective_scan_decode_step(**{n: t if n in rest else t[i:i + 64] for n, t in d.items()}, H=one[i:i + 64])
+                      for i in range(0, S, 64)])   # (16-byte aligned pieces)
+    y = ck.selective_scan_decode_step(**d, H=H)
+    ref_y = ref.selective_scan(**a)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(H, one)
+    half, k = torch.finfo(dtype).eps / 2, 65 * 2.0 ** -21
+    check("y", y, ref_y["y"][:, 0], half * np.abs(ref_y["y"][:, 0]) + (k + N * 2.0 ** -24) * ref_y["sy"][:, 0])
+    check("H", H, ref_y["hT"], k * ref_y["shT"])
+
+
 def test_state_continues_in_place():
     """Two halves, the second from the first's state, hT in the place of h0, as the whole."""
     a, _, _ = make(2, 2, 64, 40, 1, 16, F32)

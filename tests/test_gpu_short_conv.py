@@ -136,6 +136,23 @@ def test_decode_continues_the_forward(K, H, C, dtype):
     assert torch.equal(torch.stack(rows, 2), y) and torch.equal(state, sT)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("N,C,K", [(601, 1024, 4), (1203, 1024, 3), (2407, 511, 2)])
+def test_decode_of_many_sequences(N, C, K, dtype):
+    """Several sequences a thread, the last thread with fewer: the same bytes as with the sequences in small calls."""
+    a, _, _ = make(C, N, 1, C, K, dtype, True, None)
+    x, w, b, state = dev(a["x"])[:, 0].contiguous(), dev(a["w"]), dev(a["b"]), dev(a["s0"])
+    one = state.clone()
+    want = torch.cat([ck.short_conv_decode_step(x[i:i + 64], w, one[i:i + 64], b) for i in range(0, N, 64)])   # (16-byte aligned pieces)
+    y = ck.short_conv_decode_step(x, w, state, b)
+    z = ref.short_conv(**a)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and torch.equal(state, one) and torch.equal(state[:, -1], x)
+    e, u = 2.0 ** -24, z["u"]
+    off = 1.1 * (K + 1) * e * z["su"] + (8 + 2 * np.abs(u)) * 2 * e * np.abs(u)
+    check("y", y[:, 0], z["y"][:, 0, 0], torch.finfo(dtype).eps / 2 * np.abs(z["y"][:, 0, 0]) + off[:, 0])
+
+
 def test_rows_behind_a_sequence_are_left():
     """Outputs passed in keep their rows at or past a length; NaN there is not read."""
     a, dy, _ = make(1, 2, 20, 24, 4, BF, False, [7, 0])
