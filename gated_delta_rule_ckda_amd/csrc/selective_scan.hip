@@ -48,6 +48,7 @@
 #include <utility>
 
 #include "ckda_internal.hpp"
+#include "part_sums.hpp"
 #include "row_vec.hpp"
 
 namespace ckda {
@@ -552,18 +553,20 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_WAVES(LN) void scan_fwd_kernel(c
   }
 }
 
-// Segments' own states joined in order, in place: each place gets the state that
-// its segment starts from (BACK: the gradient of its last state, from dhT on).
-template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_join_kernel(const ScanLaunch L, int P) {
+// Segments' own states joined in order, in place: each place gets the state that its
+// segment starts from.  Backward in time the gradients of their last states, from dhT
+// on, by the second half of the workgroups (one launch: 5 us less than two).
+template <bool EXACT> __global__ __launch_bounds__(256) void scan_join_kernel(const ScanLaunch L, int P, unsigned half) {
   const ScanGeom& G = L.G;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x, CP = (long long)G.C * P;
+  const bool back = blockIdx.x >= half;
+  const long long i = (long long)(blockIdx.x - (back ? half : 0)) * 256 + threadIdx.x, CP = (long long)G.C * P;
   if (i >= (long long)G.B * CP) return;
   const int b = (int)(i / CP), c = (int)(i % CP / P), n = (int)(i % P);
   if (n >= G.N) return;
   const float A2 = L.a.A[(size_t)c * G.N + n] * kLog2e;
-  float* own = (BACK ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CP + i % CP;
+  float* own = (back ? L.w.back : L.w.ends) + (size_t)b * G.nseg * CP + i % CP;
   const float* steps = L.w.steps + (size_t)b * G.nseg * G.C + c;
-  const float* first = BACK ? L.a.dhT : L.a.h0;
+  const float* first = back ? L.a.dhT : L.a.h0;
   float h = first ? first[((size_t)b * G.C + c) * G.N + n] : 0.f;
   constexpr int EACH = 8;   // segments whose loads are in flight together (64 segments: 20 us one after the other, 8 so)
   for (int k0 = 0; k0 < G.nseg; k0 += EACH) {
@@ -571,16 +574,16 @@ template <bool EXACT, bool BACK> __global__ __launch_bounds__(256) void scan_joi
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       // (of the last one nobody needs the end, and the forward does not make it)
-      const int k = min(k0 + i, G.nseg - 2), seg = BACK ? G.nseg - 1 - k : k;
+      const int k = min(k0 + i, G.nseg - 2), seg = back ? G.nseg - 1 - k : k;
       next[i] = own[(size_t)seg * CP], sum[i] = steps[(size_t)seg * G.C];
     }
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const int k = k0 + i;
       if (k >= G.nseg) break;
-      own[(size_t)(BACK ? G.nseg - 1 - k : k) * CP] = h;
+      own[(size_t)(back ? G.nseg - 1 - k : k) * CP] = h;
       // (the first segment's own state has the initial one in it already)
-      h = BACK || k ? Decay<EXACT>(sum[i] * A2).of(h) + next[i] : next[i];
+      h = back || k ? Decay<EXACT>(sum[i] * A2).of(h) + next[i] : next[i];
     }
   }
 }
@@ -989,8 +992,14 @@ __global__ __launch_bounds__(THREADS) CKDA_SCAN_BWD_WAVES(LN) void scan_bwd_kern
   }
 }
 
-// dBm and dCm: the sums of the channel blocks' parts
-template <typename T> __global__ __launch_bounds__(256) void scan_bc_kernel(const ScanLaunch L) {
+// dBm and dCm, the sums of the channel blocks' parts, by the first workgroups, and the
+// weights' gradients by the others (one launch: 4 us less than two)
+template <typename T>
+__global__ __launch_bounds__(256) void scan_sums_kernel(const ScanLaunch L, const SumOuts weights, unsigned first) {
+  if (blockIdx.x >= first) {
+    sum_parts<256 / kSumCols>(weights, blockIdx.x - first);
+    return;
+  }
   const ScanGeom& G = L.G;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x, GN = (long long)G.G * G.N;
   const long long row = i / (2 * GN);
@@ -1178,10 +1187,10 @@ unsigned scan_blocks(const ScanLaunch& L) {
   return (unsigned)((total + 7) / 8 * 8);
 }
 
-template <bool BACK> hipError_t launch_join(const ScanLaunch& L, int P) {
-  const unsigned blocks = (unsigned)(((long long)L.G.B * L.G.C * P + 255) / 256);
-  if (L.a.dtype == CKDA_DTYPE_F32) hipLaunchKernelGGL((scan_join_kernel<true, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L, P);
-  else hipLaunchKernelGGL((scan_join_kernel<false, BACK>), dim3(blocks), dim3(256), 0, L.a.stream, L, P);
+hipError_t launch_join(const ScanLaunch& L, int P, bool bwd) {
+  const unsigned half = (unsigned)(((long long)L.G.B * L.G.C * P + 255) / 256), blocks = bwd ? 2 * half : half;
+  if (L.a.dtype == CKDA_DTYPE_F32) hipLaunchKernelGGL(scan_join_kernel<true>, dim3(blocks), dim3(256), 0, L.a.stream, L, P, half);
+  else hipLaunchKernelGGL(scan_join_kernel<false>, dim3(blocks), dim3(256), 0, L.a.stream, L, P, half);
   return hipGetLastError();
 }
 
@@ -1192,7 +1201,7 @@ template <typename T, int LN, int NS> hipError_t launch_fwd_t(const SelScanArgs&
     L.segs = L.G.nseg - 1;
     hipLaunchKernelGGL((scan_fwd_kernel<T, LN, NS, kFwdThreads, SUBS, false>), dim3(scan_blocks(L)), dim3(kFwdThreads), 0, a.stream, L);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess) e = launch_join<false>(L, LN * NS);
+    if (e == hipSuccess) e = launch_join(L, LN * NS, false);
     if (e != hipSuccess) return e;
     L.segs = L.G.nseg;
   }
@@ -1209,7 +1218,7 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
     if (L.G.nseg > 1) {
       hipLaunchKernelGGL((scan_prep_kernel<T, LN, NS, THREADS, true>), grid, block, 0, a.stream, L);
       if ((e = hipGetLastError()) != hipSuccess) return e;
-      if ((e = launch_join<false>(L, LN * NS)) != hipSuccess || (e = launch_join<true>(L, LN * NS)) != hipSuccess) return e;
+      if ((e = launch_join(L, LN * NS, true)) != hipSuccess) return e;
     } else {
       hipLaunchKernelGGL((scan_prep_kernel<T, LN, NS, THREADS, false>), grid, block, 0, a.stream, L);
       if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -1219,12 +1228,13 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const long long each = (long long)a.B * a.T * 2 * a.G * a.N;
-  if (each > 0) {   // (without channels: zeros)
-    hipLaunchKernelGGL((scan_bc_kernel<T>), dim3((unsigned)((each + 255) / 256)), dim3(256), 0, a.stream, L);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
+  const unsigned first = (unsigned)((each + 255) / 256);
   const size_t CN = (size_t)a.C * a.N, C = (size_t)a.C;
-  return launch_part_sums(PartSums{L.w.weights, L.G.B * L.G.nseg, CN + 2 * C, {a.dA, a.dD, a.dbias}, {CN, C, C}}, a.stream);
+  const SumOuts weights = sum_outs(PartSums{L.w.weights, L.G.B * L.G.nseg, CN + 2 * C, {a.dA, a.dD, a.dbias}, {CN, C, C}});
+  const unsigned blocks = first + (wanted(weights) ? sum_blocks(weights) : 0);   // (without channels dB and dC are zeros)
+  if (blocks == 0) return e;
+  hipLaunchKernelGGL((scan_sums_kernel<T>), dim3(blocks), dim3(256), 0, a.stream, L, weights, first);
+  return hipGetLastError();
 }
 
 // Two sequences a thread where that leaves threads enough (MI355X, us, one and two: 256 sequences of 4096 channels
@@ -1277,7 +1287,7 @@ bool scan_fits_grid(int B, int T, int C, int G, int N) {
   const ScanGeom g = scan_plan(B, T, C, G, N, true).G, f = scan_plan(B, T, C, G, N, false).G;
   const long long groups = (long long)B * G;
   return groups * g.nseg * g.cblocks < (1LL << 22) && groups * f.nseg * f.cblocks < (1LL << 22) &&
-         (long long)B * C * 64 < (1LL << 32) && (double)B * T * 2 * G * N < 4e9;
+         (long long)B * C * 64 < (1LL << 31) && (double)B * T * 2 * G * N + 256.0 / kSumCols * (N + 2.0) * C < 4e9;
 }
 
 hipError_t launch_scan_fwd(const SelScanArgs& a) {

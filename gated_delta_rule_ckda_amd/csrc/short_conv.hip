@@ -429,11 +429,12 @@ size_t short_conv_bwd_workspace_bytes(int B, int T, int C, int K) {
   return (size_t)std::min<long long>(items, kMostParts) * C * (K + 1) * 4;
 }
 
-// fewer than 2^24 workgroups of 256 threads, however the channels are read
+// fewer than 2^24 workgroups of 256 threads, however the channels are read, and 2^22 of 1024 for the parts' sums
 bool short_conv_fits_grid(int B, int T, int C, int H) {
   const long long rows = 4 * (long long)conv_rows(B, T, C), pieces = (C + 63) / 64;
   const long long slabs = std::max(1LL, (T + rows - 1) / rows);
-  return (long long)B * slabs <= INT_MAX && (long long)B * slabs * pieces < (1LL << 24) && H > 0;
+  return (long long)B * slabs <= INT_MAX && (long long)B * slabs * pieces < (1LL << 24) && H > 0 &&
+         (long long)C * 5 < (1LL << 26);
 }
 
 hipError_t launch_short_conv_fwd(const ShortConvArgs& a) { return launch_conv<ConvOp::fwd>(a); }
