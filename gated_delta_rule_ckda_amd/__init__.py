@@ -729,6 +729,11 @@ def _like(t, stream):
     return torch.empty_like(t) if stream is None else _fresh(t.shape, t.dtype, t.device, stream)
 
 
+def _beside(t, shape, stream):
+    """_fresh in the type of `t`, on its device."""
+    return t.new_empty(shape) if stream is None else _fresh(shape, t.dtype, t.device, stream)
+
+
 def _slice_of(device, name, t, shape, dtype, rows, width):
     """Row stride of t, a column slice of a contiguous tensor: of `shape`, whose
     first `rows` dimensions count rows and whose others are `width` elements next
@@ -799,10 +804,10 @@ def short_conv_fwd(x, w, b=None, s0=None, lens=None, heads=1, act="silu", y=None
     ldx = _slice_of(dev, "x", x, (B, T, C), dt, 2, C)
     code = _dtype_code(x)
     if y is None:
-        y = _fresh((B, heads, T, Dh), dt, dev, stream)
+        y = _beside(x, (B, heads, T, Dh), stream)
         flags |= PAD_ZERO
     if sT is None and want_state:
-        sT = _fresh((B, K - 1, C), dt, dev, stream)
+        sT = _beside(x, (B, K - 1, C), stream) if s0 is None else _like(s0, stream)
     _run(dev, stream, lib().ckda_short_conv_fwd, x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(s0), _ptr(lens), y.data_ptr(),
          _ptr(sT), B, T, C, heads, K, ldx, code, flags)
     return y, sT
@@ -825,8 +830,8 @@ def short_conv_bwd(x, w, dy, b=None, s0=None, dsT=None, lens=None, act="silu", w
     if need == 0:
         raise CkdaError(ERR_UNSUPPORTED, f"unsupported sizes B={B} T={T} C={C} K={K}")
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
-    dx, ds0 = _fresh((B, T, C), dt, dev, stream), _fresh((B, K - 1, C), dt, dev, stream)
-    dw, db = _like(w, stream), _fresh((C,), f32, dev, stream)
+    dx, ds0 = _beside(x, (B, T, C), stream), _beside(x, (B, K - 1, C), stream)
+    dw, db = _like(w, stream), _beside(w, (C,), stream)
     _run(dev, stream, L.ckda_short_conv_bwd, x.data_ptr(), w.data_ptr(), _ptr(b), _ptr(s0), _ptr(lens), dy.data_ptr(),
          _ptr(dsT), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ds0.data_ptr(), B, T, C, heads, K, ldx, code,
          flags | PAD_ZERO, *ws)
@@ -843,7 +848,7 @@ def short_conv_decode_step(x, w, state, b=None, heads=1, act="silu", y=None, str
     ldx = _slice_of(dev, "x", x, (N, C), dt, 1, C)
     code = _dtype_code(x)
     if y is None:
-        y = x.new_empty((N, heads, Dh)) if stream is None else _fresh((N, heads, Dh), dt, dev, stream)
+        y = _beside(x, (N, heads, Dh), stream)
     _run(dev, stream, lib().ckda_short_conv_decode_step, x.data_ptr(), w.data_ptr(), _ptr(b), state.data_ptr(), y.data_ptr(),
          N, C, K, ldx, code, flags)
     return y
@@ -901,7 +906,7 @@ def selective_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, 
         y = _like(x, stream)
         flags |= PAD_ZERO
     if hT is None and want_state:
-        hT = _fresh((B, C, N), f32, dev, stream)
+        hT = _beside(A, (B, C, N), stream) if h0 is None else _like(h0, stream)
     _run(dev, stream, L.ckda_selective_scan_fwd, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
          _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), y.data_ptr(), _ptr(hT), B, T, C, G, N, ldbc, ldz, code,
          flags, *ws)
@@ -919,7 +924,7 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=No
     (B, T), C, G, N, ldbc, ldz = _scan_args(x, dt, A, Bm, Cm, D, z, dt_bias, lambda r, C, N: [
         ("h0", h0, (r[0], C, N), f32), ("lens", lens, (r[0],), torch.int32), ("dy", dy, (*r, C), x.dtype),
         ("dhT", dhT, (r[0], C, N), f32)], 2)
-    dev, t, code = x.device, x.dtype, _dtype_code(x)
+    dev, code = x.device, _dtype_code(x)
     L = lib()
     need = L.ckda_selective_scan_bwd_workspace_size(B, T, C, G, N, code)
     if need == 0:
@@ -927,11 +932,11 @@ def selective_scan_bwd(x, dt, A, Bm, Cm, dy, D=None, z=None, dt_bias=None, h0=No
     workspace, ws = _workspace_arg(workspace, need, dev, stream)
     dx, ddt, dA = _like(x, stream), _like(dt, stream), _like(A, stream)
     dz = None if z is None else _like(x, stream)
-    dBm = _fresh((B, T, G, N), t, dev, stream)
+    dBm = _beside(x, (B, T, G, N), stream)
     dCm = _like(dBm, stream)
-    dD = _fresh((C,), f32, dev, stream)
+    dD = _beside(A, (C,), stream)
     dbias = _like(dD, stream)
-    dh0 = _fresh((B, C, N), f32, dev, stream) if want_dh0 else None
+    dh0 = _beside(A, (B, C, N), stream) if want_dh0 else None
     _run(dev, stream, L.ckda_selective_scan_bwd, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(),
          _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(h0), _ptr(lens), dy.data_ptr(), _ptr(dhT), dx.data_ptr(), ddt.data_ptr(),
          dA.data_ptr(), dBm.data_ptr(), dCm.data_ptr(), dD.data_ptr(), _ptr(dz), dbias.data_ptr(), _ptr(dh0), B, T, C, G, N,

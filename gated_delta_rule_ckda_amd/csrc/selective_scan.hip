@@ -13,14 +13,14 @@
 // exponential and two fused products, and whatever else runs for each.  MI355X, B4 T4096
 // C2048 N16 bf16 with the gate: forward 214 us (9.7 instructions for each state of a row,
 // the vector units busy 72% of the time at the two waves a SIMD gets from 8192 channels),
-// backward 643 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
+// backward 642 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
 // the vector units busy all the time).  Eight issue slots of 16 lanes for a state
 // (the exponential takes four) would be 109 us, HBM 55.  The layout leaves little else to
 // do for each:
 //  * LN neighbouring lanes are one channel, each with NS states in registers, time
 //    down a loop.  4 x 4 for up to 16 states; 16 x 2 and 16 x 4 for up to 32 and 64;
 //    16 x 1 where 4 lanes a channel would leave SIMDs idle and the sequence would
-//    have to be cut (see scan_geom).
+//    have to be cut (see scan_plan).
 //  * Rows go by chunks of 16.  What a row has for each channel (d, d x, ds) is made
 //    once, by one lane, and handed to the channel's lanes by a DPP broadcast inside a
 //    row of 16 lanes or a quad.
