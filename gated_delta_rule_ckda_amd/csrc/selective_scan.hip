@@ -11,9 +11,9 @@
 //
 // Bound by vector instructions: for every (row, channel, state) two products, an
 // exponential and two fused products, and whatever else runs for each.  MI355X, B4 T4096
-// C2048 N16 bf16 with the gate: forward 214 us (9.7 instructions for each state of a row,
+// C2048 N16 bf16 with the gate: forward 212 us (9.7 instructions for each state of a row,
 // the vector units busy 72% of the time at the two waves a SIMD gets from 8192 channels),
-// backward 642 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
+// backward 638 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
 // the vector units busy all the time).  Eight issue slots of 16 lanes for a state
 // (the exponential takes four) would be 109 us, HBM 55.  The layout leaves little else to
 // do for each:
