@@ -96,7 +96,9 @@ template <int CTRL> __device__ __forceinline__ float dpp_mov(float x) {
 // values that has its bit and adds the partner's.  Where the bit selects whole
 // banks of four lanes the second sum is written over the first under a bank mask
 // (two instructions for two values), inside a bank it takes two selects and a sum.
-// (The wait states a DPP source needs behind its writer stand in the asm itself.)
+// (The compiler does not see what the asm reads and writes by vector instructions: the two wait states that a DPP
+// source needs behind its writer stand at its start, and where a result goes to a DPP operand or a lane swap, two
+// stand at its end.  Of turn_sums none does: the selects read them.)
 #define CKDA_PAIR(d, a, b, move, mask)                                      \
   "v_add_f32_dpp " d ", " a ", " a " " move " row_mask:0xf bank_mask:0xf\n" \
   "v_add_f32_dpp " d ", " b ", " b " " move " row_mask:0xf bank_mask:" mask "\n"
@@ -165,7 +167,8 @@ __device__ __forceinline__ float sum_quarters(float a, float b) {
 
 // Sums over the 4 quads of a DPP row of 4 states of two quantities: quad b gets the sum of state (b & 1) 2 + b / 2
 // of each.  Pairs across quads two apart (row_ror:8), then next ones (from the quad behind, row_ror:12, where the
-// first of a pair is kept, from the one before, row_ror:4, where the second is).
+// first of a pair is kept, from the one before, row_ror:4, where the second is).  The lane swap of sum_halves reads
+// the results: its two wait states are the last instruction.
 #define CKDA_QUADS(d, a, b, low, high, mask)                               \
   "v_add_f32_dpp " d ", " a ", " a " " low " row_mask:0xf bank_mask:0xf\n" \
   "v_add_f32_dpp " d ", " b ", " b " " high " row_mask:0xf bank_mask:" mask "\n"
@@ -175,6 +178,7 @@ __device__ __forceinline__ void sum_quads(const float (&x)[4], const float (&y)[
       CKDA_QUADS("%2", "%6", "%7", "row_ror:8", "row_ror:8", "0xc") CKDA_QUADS("%3", "%8", "%9", "row_ror:8", "row_ror:8", "0xc")
       CKDA_QUADS("%4", "%10", "%11", "row_ror:8", "row_ror:8", "0xc") CKDA_QUADS("%5", "%12", "%13", "row_ror:8", "row_ror:8", "0xc")
       CKDA_QUADS("%0", "%2", "%3", "row_ror:12", "row_ror:4", "0xa") CKDA_QUADS("%1", "%4", "%5", "row_ror:12", "row_ror:4", "0xa")
+      "s_nop 1"
       : "=&v"(sx), "=&v"(sy), "=&v"(a0), "=&v"(a1), "=&v"(a2), "=&v"(a3)
       : "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]), "v"(y[0]), "v"(y[1]), "v"(y[2]), "v"(y[3]));
 }
