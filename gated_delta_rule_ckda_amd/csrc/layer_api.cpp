@@ -148,9 +148,14 @@ static int scan_check(const char* fn, int B, int T, int C, int G, int N, int ldb
   if (!supported_dtype(dtype)) return fail(CKDA_ERR_UNSUPPORTED, "%s: dtype %d is not F32(0) or BF16(1)", fn, dtype);
   if (C >= kMostChannels) return fail(CKDA_ERR_DIM, "%s: C=%d not below 2^24", fn, C);
   if ((long long)ldbc < (long long)G * N) return fail(CKDA_ERR_DIM, "%s: row stride ldbc=%d below G*N=%lld", fn, ldbc, (long long)G * N);
+  if (gate && ldz < C) return fail(CKDA_ERR_DIM, "%s: row stride ldz=%d below C=%d", fn, ldz, C);
+  return CKDA_OK;
+}
+
+// the forward's and the backward's tiles of rows take 31-bit offsets; a step's rows, any int
+static int scan_strides(const char* fn, int ldbc, int ldz, bool gate) {
   if (ldbc >= kMostChannels || (gate && ldz >= kMostChannels))
     return fail(CKDA_ERR_DIM, "%s: row strides ldbc=%d, ldz=%d must be below 2^24", fn, ldbc, ldz);
-  if (gate && ldz < C) return fail(CKDA_ERR_DIM, "%s: row stride ldz=%d below C=%d", fn, ldz, C);
   return CKDA_OK;
 }
 
@@ -187,7 +192,7 @@ int ckda_selective_scan_fwd(const void* x, const void* dt, const float* A, const
                             int flags, void* workspace, size_t workspace_bytes, void* stream) {
   const char* fn = "ckda_selective_scan_fwd";
   int st = scan_check(fn, B, T, C, G, N, ldbc, ldz, z != nullptr, dtype, flags, CKDA_SCAN_SOFTPLUS | CKDA_PAD_ZERO);
-  if (st != CKDA_OK) return st;
+  if (st != CKDA_OK || (st = scan_strides(fn, ldbc, ldz, z != nullptr)) != CKDA_OK) return st;
   if (B == 0 || C == 0 || (T == 0 && !hT)) return ok();
   if (!A || (T > 0 && (!x || !dt || !Bm || !Cm || !y)))
     return fail(CKDA_ERR_NULL, "%s: x, dt, A, Bm, Cm and y are required", fn);
@@ -224,7 +229,7 @@ int ckda_selective_scan_bwd(const void* x, const void* dt, const float* A, const
                             void* stream) {
   const char* fn = "ckda_selective_scan_bwd";
   int st = scan_check(fn, B, T, C, G, N, ldbc, ldz, z != nullptr, dtype, flags, CKDA_SCAN_SOFTPLUS | CKDA_PAD_ZERO);
-  if (st != CKDA_OK) return st;
+  if (st != CKDA_OK || (st = scan_strides(fn, ldbc, ldz, z != nullptr)) != CKDA_OK) return st;
   const bool rows_there = B > 0 && T > 0;
   // gradients of the weights exist (as zeros) without rows, and so does the initial state's; dBm and dCm are
   // zero where there are rows but no channels

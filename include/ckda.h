@@ -600,9 +600,11 @@ int ckda_short_conv_decode_step(const void* x, const float* w, const float* b, v
  * Supported: 1 <= N <= 64, any C of which G is a divisor.  A decay is rounded
  * to fp32 at every step (bf16: by the hardware's exponential, 2^-23); with F32
  * a decay near 1 is applied by its distance from 1, so that slow states do not
- * drift.  C and both row strides below 2^24, C N below 2^28.  A non-finite input of a channel leaves that channel's rows from there
- * on unspecified (in the backward all of it, and dBm and dCm of the rows where
- * it is summed in); one in Bm or Cm does so for its group's channels. */
+ * drift.  C below 2^24; forward and backward also both row strides below 2^24
+ * and C N below 2^28.  A non-finite input of a channel leaves that channel's
+ * rows from there on unspecified (in the backward all of it, and dBm and dCm of
+ * the rows where it is summed in); one in Bm or Cm does so for its group's
+ * channels. */
 #define CKDA_SCAN_SOFTPLUS 1
 
 /* Bytes of device workspace ckda_selective_scan_fwd needs, or 0 for invalid or
@@ -637,7 +639,9 @@ int ckda_selective_scan_bwd(const void* x, const void* dt, const float* A, const
 
 /* One token of S sequences, state in place: x, dt [S, C], Bm, Cm [S, G, N] (row
  * stride ldbc), z [S, C] (row stride ldz) or NULL, H_inout [S, C, N] fp32,
- * y [S, C].  One read and one write of the state.  flags: CKDA_SCAN_SOFTPLUS. */
+ * y [S, C].  The row strides may be those of one token's rows in a [S, T, W]
+ * tensor, T W of any int.  One read and one write of the state.  flags:
+ * CKDA_SCAN_SOFTPLUS. */
 int ckda_selective_scan_decode_step(const void* x, const void* dt, const float* A, const void* Bm, const void* Cm,
                                     const float* D, const void* z, const float* dt_bias, float* H_inout, void* y, int S,
                                     int C, int G, int N, int ldbc, int ldz, int dtype, int flags, void* stream);
