@@ -197,10 +197,16 @@ def _shapes(expect):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+INT_MAX = 2 ** 31 - 1   # of the C ABI's sizes; ctypes would wrap a larger one around
+
+
 def _dims(t, n, name):
-    if t.dim() != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(t.shape)}")
-    return tuple(t.shape)
+    shape = tuple(t.shape)
+    if len(shape) != n:
+        raise ValueError(f"{name} must have {n} dimensions, got shape {shape}")
+    if max(shape) > INT_MAX:
+        raise ValueError(f"{name} has shape {shape}, with more than 2^31 - 1 of a dimension")
+    return shape
 
 
 def _scratch(nbytes, device, stream):
@@ -743,7 +749,7 @@ def _slice_of(device, name, t, shape, dtype, rows, width):
             return width
         st = t.stride()
         ld = st[rows - 1]
-        if (st[-1] == 1 and width <= ld < 2 ** 31 and (rows == 1 or st[0] == ld * shape[1])
+        if (st[-1] == 1 and width <= ld <= INT_MAX and (rows == 1 or st[0] == ld * shape[1])
                 and (len(st) == rows + 1 or st[-2] == shape[-1])):
             return ld
     if t.shape != shape:
@@ -771,7 +777,7 @@ def _slice_of(device, name, t, shape, dtype, rows, width):
                 raise ValueError(f"{name} must be a column slice of a contiguous tensor")
         count *= size
     ld = width if ld is None else ld
-    if ld < width or ld > 2 ** 31 - 1:
+    if ld < width or ld > INT_MAX:
         raise ValueError(f"{name} must be a column slice of a contiguous tensor")
     return ld
 
@@ -964,12 +970,15 @@ def _add_norm_args(x, res, w, total, more=lambda shape, D: ()):
     if len(shape) < 1 or shape[-1] < 1:
         raise ValueError(f"x must have rows of at least one element, got shape {tuple(shape)}")
     D = shape[-1]
+    R = x.numel() // D
+    if R > INT_MAX:
+        raise ValueError(f"x has {R} rows (shape {tuple(shape)}), more than 2^31 - 1")
     rt = res.dtype if res is not None else t if total is None else total.dtype
     if rt != t and rt != torch.float32:
         raise TypeError(f"the residual must be {t} or float32, got {rt}")
     _tensors(x.device, [("x", x, shape, t), ("res", res, shape, rt), ("w", w, (D,), torch.float32), ("total", total, shape, rt),
                         *more(shape, D)])
-    return x.numel() // D, D, rt
+    return R, D, rt
 
 
 def add_norm_fwd(x, res=None, w=None, eps=1e-6, y=None, total=None, stream=None):
