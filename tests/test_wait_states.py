@@ -129,6 +129,7 @@ def test_the_count_follows_jumps():
                           "s_endpgm"))[0] == []
 
 
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="llvm-objdump not installed")
 def test_lane_swaps_and_dpp_operands_wait_for_their_registers(tmp_path):
     if not os.path.exists(ck.LIB_PATH):
         libbuild.build()
