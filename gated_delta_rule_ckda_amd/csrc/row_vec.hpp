@@ -11,7 +11,8 @@ namespace ckda {
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);   // elements in 16 bytes
 
 // VEC elements as loaded.  `left` is how many of them the row still has (<= 0:
-// none, and nothing is read); the others are zero.
+// none, and nothing is read); the others are zero.  Every load and store is a branch
+// on the piece being whole, with the elements of a short one beside it.
 template <typename T, int VEC> struct RowVec {
   static_assert(VEC * sizeof(T) == 16 || VEC * sizeof(T) == 8 || VEC == 1, "piece of a row");
   T e[VEC];

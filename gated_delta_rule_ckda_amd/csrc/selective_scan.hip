@@ -11,10 +11,10 @@
 //
 // Bound by vector instructions: for every (row, channel, state) two products, an
 // exponential and two fused products, and whatever else runs for each.  MI355X, B4 T4096
-// C2048 N16 bf16 with the gate: forward 212 us (9.7 instructions for each state of a row,
+// C2048 N16 bf16 with the gate: forward 213 us (9.7 instructions for each state of a row,
 // the vector units busy 72% of the time at the two waves a SIMD gets from 8192 channels),
-// backward 638 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
-// the vector units busy all the time).  Eight issue slots of 16 lanes for a state
+// backward 632 (a pass forward 175, 10 instructions, and the main pass 435, 27; both with
+// the vector units busy all the time).  fp32 367 and 983: its decays branch (see Decay).  Eight issue slots of 16 lanes for a state
 // (the exponential takes four) would be 109 us, HBM 55.  The layout leaves little else to
 // do for each:
 //  * LN neighbouring lanes are one channel, each with NS states in registers, time
@@ -58,7 +58,8 @@ namespace {
 constexpr int kRows = 16;       // rows of a chunk
 constexpr int kPad = kRows + 1;   // row of a turned tile in LDS
 // Registers: for four waves on a SIMD with 4 lanes a channel, for two to four with 16 (rows' operands are loaded
-// ahead, not one after the other); the backward's main pass with 4 lanes for three, without spills.
+// ahead, not one after the other); the backward's main pass with 4 lanes for three, which bf16 has without spills (fp32
+// keeps 21 registers in memory with the gate and 6 without; with 16 lanes of four states 54 and 48).
 #define CKDA_SCAN_WAVES(LN) __attribute__((amdgpu_waves_per_eu((LN) == 4 ? 4 : 2, 4)))
 #define CKDA_SCAN_BWD_WAVES(LN) __attribute__((amdgpu_waves_per_eu((LN) == 4 ? 3 : 2, 4)))
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLo = 1.9259629911266174e-8f, kLn2 = 0.6931471805599453f;
@@ -223,7 +224,9 @@ template <bool EXACT> __device__ __forceinline__ float softplus_slope(float v) {
 // (mean error -0.12 of 2^-24 for small x, so a state that remembers M rows is off
 // by some 7e-9 M).  Where they are fp32: for -x < 1/16 its distance from 1, which
 // keeps slow decays to 2^-24 of their rate (degree 4: next term 2^-25); stronger
-// ones, of states that remember fewer than 24 rows, themselves.
+// ones, of states that remember fewer than 24 rows, themselves.  The choice becomes
+// branches, not selects: 147 regions under a mask in the 4-lane forward where bf16 has
+// 20; both sides run where a wave's lanes differ, and nothing moves across them.
 template <bool EXACT> struct Decay;
 template <> struct Decay<false> {
   float m;
@@ -1130,8 +1133,11 @@ ScanPlan scan_plan(int B, int T, int C, int G, int N, bool bwd) {
   g.chunks = (int)(((long long)T + kRows - 1) / kRows);
   // 4 lanes a channel where that can fill three waves of every SIMD, by segments of 128 rows or more; but in the
   // forward not where 16 lanes fill two without segments and 4 lanes would need them, which cost a pass of their own
-  // (MI355X, us, 4 and 16 lanes: forward B4 T4096 C2048 290 and 224, B16 T1024 C4096 297 and 325, B1 T32768 C1024 280
-  // and 340, B1 T1024 C1024 40 and 24; backward B4 T4096 C2048 697 and 785, fp32 B3 T777 C500 160 and 100).
+  // (MI355X, us, 4 and 16 lanes: forward B4 T4096 C2048 257 and 213, B16 T1024 C4096 279 and 315, B1 T32768 C1024 257
+  // and 299, B1 T1024 C1024 36 and 22; backward B4 T4096 C2048 632 and 855, fp32 B3 T777 C500 149 and 90).  The two
+  // meet at some 6000 channels, below the 8192 that fill two waves (forward B4 T4096, 4 and 16 lanes: C1920 258 and
+  // 213, C1536 216 and 212, C1024 134 and 143, C512 76 and 82; fp32 C2048 443 and 367, C1920 458 and 365, C1024 231
+  // and 243): between, the rule takes the slower one.
   const long long channels = (long long)B * C, blocks4 = (long long)B * G * ((g.Cg + 63) / 64);
   const bool fills = blocks4 * std::max(1, g.chunks / 8) >= 768, alone = !bwd && channels >= 8192 && channels < 49152;
   const bool quad = N <= 16 && fills && !alone;
@@ -1140,8 +1146,8 @@ ScanPlan scan_plan(int B, int T, int C, int G, int N, bool bwd) {
   const int ch = (quad ? kQuadThreads : bwd ? kWideThreads : kFwdThreads) / plan.ln;
   g.cblocks = (g.Cg + ch - 1) / ch;
   // Segments where the channels leave SIMDs without waves (fewer than three with 4 lanes, two with 16): four then.
-  // The backward's main pass with 4 lanes keeps three: two rounds of those (B4 T4096 C2048: 647, and with 1024
-  // workgroups, a round and a third, 661).
+  // The backward's main pass with 4 lanes keeps three: two rounds of those (B4 T4096 C2048: 632, and with 1024
+  // workgroups, a round and a third, 644).
   const long long blocks = (long long)B * G * g.cblocks, full = !quad ? 16384 / ch : bwd ? 1536 : 1024;
   g.nseg = 1;
   if (blocks > 0 && blocks < (quad ? 768 : full * 3 / 8))
@@ -1242,7 +1248,7 @@ template <typename T, int LN, int NS> hipError_t launch_bwd_t(const SelScanArgs&
 }
 
 // Two sequences a thread where that leaves threads enough (MI355X, us, one and two: 256 sequences of 4096 channels
-// with 16 states 32.5 and 28, 64 of 2048 with 64 states 19.1 and 17).
+// with 16 states 32.5 and 28, 64 of 2048 with 64 states 18.6 and 16).
 template <typename T, int LPC, bool WHOLE> hipError_t launch_decode_t(const SelScanArgs& a) {
   const ScanLaunch L = scan_launch(a, scan_plan(a.B, a.T, a.C, a.G, a.N, false), false);
   const bool many = (long long)a.B * a.C * LPC >= 1 << 20;

@@ -8,20 +8,25 @@
 // HBM-bound: x is read and y written once (backward: x, dy, dx).  A thread owns
 // a piece of four channels and walks down a slab of rows with the last
 // K - 1 rows (and, in the backward, the last K - 1 g) in registers, so that every
-// row is loaded once but for the K - 1 rows around a slab, and four rows' loads are
-// in flight while four are worked on; LPR threads cover a
-// row's piece of channels and the workgroup's other threads other slabs.  y (and
+// row is loaded once but for the K - 1 rows around a slab, and four rows' loads of
+// whole pieces are in flight while four are worked on (each load is a branch on the
+// piece being whole; the rows ahead of a slab, which may be the state's, are waited
+// for one after the other); LPR threads cover a row's piece of channels and the
+// workgroup's other threads other slabs.  y (and
 // dy) is head-major, the layout of the attentions: the transposition is an
 // address.  The weights' gradients stay in registers down the slab, are summed
 // over the workgroup's slabs through LDS, and leave one part for each workgroup
 // (at most kMostParts), which a second kernel adds in a fixed order.
 //
-// MI355X, B4 T4096 C2048 K4 bf16 with SiLU: forward 30 us (4.4 TB/s of 134 MB), backward
-// 67 (62 and 5 for the parts' sums; 3.2 TB/s of 201 MB).  The backward has the vector
-// units busy for two thirds of its time (three waves on a SIMD) and still no unit full;
+// MI355X, B4 T4096 C2048 K4 bf16 with SiLU: forward 33 us (4.1 TB/s of 134 MB), backward
+// 67 (62 and 5 for the parts' sums; 3.0 TB/s of 201 MB); fp32 69 and 102 (3.9 and 4.0
+// TB/s).  The backward in bf16 has the vector units busy for two thirds of its time
+// (164 registers, three waves on a SIMD) and still no unit full;
 // shorter slabs, slabs that fill the SIMDs exactly once, an order of the workgroups by
 // L2 and an inner loop without the masks (177 registers instead of 164) gave nothing or
-// lost.  Decode, 256 sequences of 4096 channels: 7 us, of which the launch is most.
+// lost.  Decode, 256 sequences of 4096 channels: a kernel of 7.4 us for 17 MB (3.4 at the
+// copy's rate): a thread's sequences go one after the other, each one's loads behind the
+// stores of the one before.
 #include <limits.h>
 
 #include <algorithm>
@@ -144,7 +149,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const T* x, cons
       for (int i = 0; i < K - 1; ++i) v[i].widen(win[i]);
     }
     RowVec<T, VEC> v[kUnroll];
-    // rows behind the slab: its last row once more (no branch around the loads, so that they stay in flight)
+    // rows behind the slab: its last row once more (no branch on the row, so that whole pieces' loads stay in flight)
     auto fetch = [&](int t) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) v[u].load(xb + (size_t)min(t + u, live - 1) * G.ldx, left);

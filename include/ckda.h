@@ -556,7 +556,8 @@ int ckda_head_norm_bwd(const void* x, const void* z, const float* w, const float
  *            the attentions above (H divides C; H = 1 is token-major)
  *   sT     : [B, K-1, C] dtype, the last K-1 inputs of each sequence (those of
  *            s0 where it is shorter), or NULL to skip
- * Outputs must not overlap each other or any input. */
+ * Outputs must not overlap each other or any input.  Refused beside bad arguments:
+ * B ceil(T / 128) ceil(C / 64) of 2^24 and more, 5 C of 2^26 and more. */
 #define CKDA_CONV_SILU 1
 
 int ckda_short_conv_fwd(const void* x, const float* w, const float* b, const void* s0, const int* lens, void* y,
@@ -578,7 +579,7 @@ int ckda_short_conv_bwd(const void* x, const float* w, const float* b, const voi
 
 /* One token of N sequences: x [N, C] (row stride ldx), state_inout [N, K-1, C]
  * dtype (the last K-1 inputs, oldest first), y [N, C] (head-major [N, H, C/H]
- * is the same).  flags: CKDA_CONV_SILU. */
+ * is the same); N C below 2^31.  flags: CKDA_CONV_SILU. */
 int ckda_short_conv_decode_step(const void* x, const float* w, const float* b, void* state_inout, void* y, int N, int C,
                                 int K, int ldx, int dtype, int flags, void* stream);
 
@@ -597,14 +598,18 @@ int ckda_short_conv_decode_step(const void* x, const float* w, const float* b, v
  *   dt_bias: [C] fp32, or NULL for zeros
  *   h0, hT : [B, C, N] fp32, or NULL (zero states; skip); hT may equal h0
  *   y      : [B, T, C] dtype
+ * y and hT must not overlap each other, any other input or the workspace.
  * Supported: 1 <= N <= 64, any C of which G is a divisor.  A decay is rounded
  * to fp32 at every step (bf16: by the hardware's exponential, 2^-23); with F32
  * a decay near 1 is applied by its distance from 1, so that slow states do not
- * drift.  C below 2^24; forward and backward also both row strides below 2^24
- * and C N below 2^28.  A non-finite input of a channel leaves that channel's
- * rows from there on unspecified (in the backward all of it, and dBm and dCm of
- * the rows where it is summed in); one in Bm or Cm does so for its group's
- * channels. */
+ * drift.  C below 2^24.  Forward and backward (either refuses what only the
+ * other could not run): both row strides below 2^24, C N below 2^28, B C below
+ * 2^25, 2 B T G N + 16 C (N + 2) below 4e9, and no more than 2^22 workgroups,
+ * each of 16 to 64 channels of one of the B G groups.  The step: S C below 2^27.
+ * A non-finite input of a channel leaves that channel's rows from there on
+ * unspecified (in the backward all of it, and dBm and dCm of the rows where it is
+ * summed in); one in Bm or Cm does so for its group's channels, and decays that
+ * grow (d A > 0) until their product over the rows passes fp32 for theirs. */
 #define CKDA_SCAN_SOFTPLUS 1
 
 /* Bytes of device workspace ckda_selective_scan_fwd needs, or 0 for invalid or
@@ -620,7 +625,9 @@ int ckda_selective_scan_fwd(const void* x, const void* dt, const float* A, const
 /* Bytes of device workspace ckda_selective_scan_bwd needs, or 0 for invalid or
  * unsupported sizes: fp32 states of every 16th row (every 8th where there are
  * channels and rows enough for 4 lanes a channel), and dBm and dCm (fp32) of
- * every 32 (64) channels. */
+ * every 32 (64) channels.  For each row and channel that is 4, 8 or 16 bytes with
+ * up to 16, 32 or 64 states (8 with 4 lanes, which are for up to 16), and for each
+ * row and 32 (64) channels of a group 8 N: B16 T4096 C8192 N16 takes 5.4 GB. */
 size_t ckda_selective_scan_bwd_workspace_size(int B, int T, int C, int G, int N, int dtype);
 
 /* Backward given dy [B, T, C] (dtype) and dhT [B, C, N] fp32 (or NULL for
@@ -661,8 +668,10 @@ int ckda_selective_scan_decode_step(const void* x, const void* dt, const float* 
  *            nearest even, from the unrounded y
  *   sum    : [R, D] res_dtype, r rounded once (y is of the unrounded r), or
  *            NULL; may equal res exactly
- * One of y and q at least.  1 <= D <= 8192; eps finite, > 0.  A row with a NaN
- * or an infinity has NaN outputs where the formula gives them. */
+ * One of y and q at least.  Outputs must not overlap each other or any other
+ * input.  1 <= D <= 8192; eps finite, > 0.  A row with a NaN or an infinity has
+ * NaN outputs where the formula gives them.  The squares are summed in fp32: of a
+ * row where that passes 3.4e38 (values of 1.8e19 and more) y is 0. */
 int ckda_add_norm_fwd(const void* x, const void* res, const float* w, void* y, void* q, float* scales, void* sum, int R,
                       int D, int group, int dtype, int res_dtype, float eps, void* stream);
 
@@ -675,7 +684,8 @@ size_t ckda_add_norm_bwd_workspace_size(int R, int D, int dtype, int res_dtype);
  * gradient of r, which is that of x and of res:
  *   dr = dsum + (dy w - n mean(dy w n)) / sqrt(mean r^2 + eps),  n the norm of r
  * in dx (dtype) and dres (res_dtype), either NULL but not both; dw [D] fp32 or
- * NULL.  dres may equal dsum exactly. */
+ * NULL.  dres may equal dsum exactly; else outputs must not overlap each other,
+ * any input or the workspace, nor the workspace an input. */
 int ckda_add_norm_bwd(const void* sum, const float* w, const void* dy, const void* dsum, void* dx, void* dres, float* dw,
                       int R, int D, int dtype, int res_dtype, float eps, void* workspace, size_t workspace_bytes,
                       void* stream);
