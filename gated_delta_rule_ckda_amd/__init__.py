@@ -201,11 +201,11 @@ INT_MAX = 2 ** 31 - 1   # of the C ABI's sizes; ctypes would wrap a larger one a
 
 
 def _dims(t, n, name):
-    shape = tuple(t.shape)
+    shape = t.shape
     if len(shape) != n:
-        raise ValueError(f"{name} must have {n} dimensions, got shape {shape}")
-    if max(shape) > INT_MAX:
-        raise ValueError(f"{name} has shape {shape}, with more than 2^31 - 1 of a dimension")
+        raise ValueError(f"{name} must have {n} dimensions, got shape {tuple(shape)}")
+    if t.numel() > INT_MAX and max(shape) > INT_MAX:   # (the count first: small calls wait for the host)
+        raise ValueError(f"{name} has shape {tuple(shape)}, with more than 2^31 - 1 of a dimension")
     return shape
 
 
